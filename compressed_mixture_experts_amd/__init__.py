@@ -1,7 +1,8 @@
 """ButterflyMoE expert layer on AMD MI355X (gfx950): Python binding.
 
 The computation runs in ``libbmoe.so`` (hand-written HIP kernels behind the C
-ABI of ``include/bmoe.h``, ``bmoe_trace.h`` and ``bmoe_grad.h``).  The test
+ABI of ``include/bmoe.h``, ``bmoe_trace.h``, ``bmoe_grad.h``, ``bmoe_train.h``,
+``bmoe_norm.h`` and ``bmoe_update.h``).  The test
 hooks of ``include/bmoe_debug.h`` live only in ``libbmoe_debug.so`` (the same
 kernels, built with -DBMOE_DEBUG_EXPORTS), loaded on first use of a
 ``dbg_*`` function.  This module only marshals arguments: torch tensors
@@ -17,6 +18,8 @@ CPU ABI tests use it for the sanitized host build).
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from typing import List, Optional, Sequence, Tuple
 
@@ -25,7 +28,8 @@ import numpy as np
 __all__ = [
     "BmoeError", "lib", "library_path", "pack_ternary", "packed_words", "Layer",
     "dbg_butterfly", "dbg_ternary_gemm", "dbg_ternary_gemm_fp4", "butterfly_backward", "substrate_grad",
-    "combine_backward", "router_backward", "gelu_backward", "substrate_input_grad", "STATUS",
+    "combine_backward", "router_backward", "gelu_backward", "substrate_input_grad",
+    "layer_norm_forward", "layer_norm_backward", "orthogonalize", "substrate_step", "STATUS",
     "EXPORTED_SYMBOLS", "DEBUG_SYMBOLS", "debug_lib",
 ]
 
@@ -42,7 +46,8 @@ F32, BF16 = 0, 1
 NOALLOC_SCRATCH_BYTES = 64 << 20   # BMOE_NOALLOC_SCRATCH_BYTES of include/bmoe.h
 ACT_NONE, ACT_GELU_ERF = 0, 1
 
-# exports of libbmoe.so (include/bmoe.h, bmoe_trace.h, bmoe_grad.h)
+# exports of libbmoe.so (include/bmoe.h, bmoe_trace.h, bmoe_grad.h, bmoe_train.h,
+# bmoe_norm.h, bmoe_update.h)
 EXPORTED_SYMBOLS = [
     "bmoe_packed_words", "bmoe_pack_ternary", "bmoe_workspace_size", "bmoe_prepared_bytes",
     "bmoe_prepare", "bmoe_route", "bmoe_forward", "bmoe_forward_noalloc", "bmoe_status_string",
@@ -53,6 +58,9 @@ EXPORTED_SYMBOLS = [
     "bmoe_substrate_input_grad",
     "bmoe_train_state_size", "bmoe_forward_train_workspace", "bmoe_forward_train",
     "bmoe_layer_backward_workspace", "bmoe_layer_backward",
+    "bmoe_layer_norm_forward", "bmoe_layer_norm_backward_workspace", "bmoe_layer_norm_backward",
+    "bmoe_orthogonalize_workspace", "bmoe_orthogonalize",
+    "bmoe_substrate_step_workspace", "bmoe_substrate_step",
 ]
 # exported by libbmoe_debug.so only (include/bmoe_debug.h)
 DEBUG_SYMBOLS = ["bmoe_dbg_butterfly", "bmoe_dbg_ternary_gemm", "bmoe_dbg_ternary_gemm_fp4"]
@@ -137,6 +145,15 @@ def _load(path: str, debug: bool) -> ctypes.CDLL:
     L.bmoe_layer_backward_workspace.argtypes = [pL, c_i32, ctypes.POINTER(c_sz)]
     L.bmoe_layer_backward.argtypes = [pL, c_vp, c_i32, c_vp, c_vp, c_sz, ctypes.POINTER(LayerGrads), c_vp, c_sz,
                                       c_vp]
+    c_d = ctypes.c_double
+    L.bmoe_layer_norm_forward.argtypes = [c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_f, c_vp, c_vp, c_vp, c_vp, c_vp]
+    L.bmoe_layer_norm_backward_workspace.argtypes = [c_i32, c_i32, ctypes.POINTER(c_sz)]
+    L.bmoe_layer_norm_backward.argtypes = [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                           c_vp, c_vp, c_sz, c_vp]
+    L.bmoe_orthogonalize_workspace.argtypes = [c_i32, c_i32, ctypes.POINTER(c_sz)]
+    L.bmoe_orthogonalize.argtypes = [c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_f, c_i32, c_vp, c_vp, c_sz, c_vp]
+    L.bmoe_substrate_step_workspace.argtypes = [c_i32, c_i32, ctypes.POINTER(c_sz)]
+    L.bmoe_substrate_step.argtypes = [c_i32, c_i32, c_vp, c_vp, c_d, c_d, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]
     ret = [n for n in EXPORTED_SYMBOLS if n not in ("bmoe_packed_words", "bmoe_prepared_bytes",
                                                     "bmoe_status_string", "bmoe_last_error")]
     if debug:
@@ -518,6 +535,168 @@ def substrate_input_grad(dz, wt_packed, d_in: int, alpha: float = 1.0):
     _check(lib().bmoe_substrate_input_grad(rows, d_out, d_in, BF16 if dz.dtype == torch.bfloat16 else F32, _ptr(dz),
                                            _ptr(wt_packed), float(alpha), _ptr(du), _stream_handle()))
     return du
+
+
+def _operand(name: str, t, shape, dtypes, device):
+    """Check one tensor of a training-step operator: dense, on `device`, of the
+    given shape and one of the dtypes."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected a GPU tensor on {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _on_device(fn):
+    """Run fn(tensor, ...) with the first tensor's GPU as the current
+    device, so that the launches go to that device's current stream."""
+    name = next(iter(inspect.signature(fn).parameters))
+
+    @functools.wraps(fn)
+    def run(*args, **kw):
+        torch = _torch()
+        first = args[0] if args else kw[name]
+        if not first.is_cuda:
+            raise ValueError(f"{fn.__name__} needs GPU tensors, got one on {first.device}")
+        if first.dim() != 2:
+            raise ValueError(f"{fn.__name__} expects a 2-D tensor, got {tuple(first.shape)}")
+        if first.device.index == torch.cuda.current_device():
+            return fn(*args, **kw)
+        with torch.cuda.device(first.device):
+            return fn(*args, **kw)
+    return run
+
+
+def _scratch(nbytes: int, device):
+    return _torch().empty(max(nbytes, 16), dtype=_torch().uint8, device=device)
+
+
+@_on_device
+def layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, stats: bool = True, y=None,
+                       sum_out=None):
+    """Row norm of s = x (+ residual): y = (s - mean) rstd gamma + beta.
+    x, residual [rows][width] fp32 or bf16; gamma, beta [width] fp32 or None
+    (ones, zeros).  Returns (y, s, mean, rstd): s is x itself without a
+    residual, mean and rstd ([rows] fp32) are None with stats=False."""
+    torch = _torch()
+    dev, kinds, f32 = x.device, (torch.float32, torch.bfloat16), (torch.float32,)
+    rows, width = x.shape
+    _operand("x", x, x.shape, kinds, dev)
+    for name, t in (("gamma", gamma), ("beta", beta)):
+        if t is not None:
+            _operand(name, t, (width,), f32, dev)
+    same = (x.dtype,)
+    if residual is None:
+        if sum_out is not None:
+            raise ValueError("sum_out needs a residual")
+    else:
+        _operand("residual", residual, x.shape, same, dev)
+        sum_out = torch.empty_like(x) if sum_out is None else _operand("sum_out", sum_out, x.shape, same, dev)
+    y = torch.empty_like(x) if y is None else _operand("y", y, x.shape, same, dev)
+    mean = rstd = None
+    if stats:
+        mean, rstd = torch.empty(rows, dtype=torch.float32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev)
+    _check(lib().bmoe_layer_norm_forward(rows, width, BF16 if x.dtype == torch.bfloat16 else F32, _ptr(x), _ptr(residual),
+                                         _ptr(gamma), _ptr(beta), float(eps), _ptr(sum_out), _ptr(y), _ptr(mean),
+                                         _ptr(rstd), _stream_handle()))
+    return y, x if residual is None else sum_out, mean, rstd
+
+
+@_on_device
+def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None, weight_grads: bool = True, dx=None):
+    """Backward of layer_norm_forward at its s, mean and rstd: dy [rows][width]
+    fp32 or of s's dtype, d_sum [rows][width] like s or None (gradient that
+    reaches s past the norm, added into dx).  Returns (dx like s, dgamma,
+    dbeta [width] fp32; None with weight_grads=False)."""
+    torch = _torch()
+    dev, f32 = dy.device, (torch.float32,)
+    rows, width = dy.shape
+    _operand("s", s, dy.shape, (torch.float32, torch.bfloat16), dev)
+    _operand("dy", dy, dy.shape, (torch.float32, s.dtype), dev)
+    if gamma is not None:
+        _operand("gamma", gamma, (width,), f32, dev)
+    _operand("mean", mean, (rows,), f32, dev)
+    _operand("rstd", rstd, (rows,), f32, dev)
+    if d_sum is not None:
+        _operand("d_sum", d_sum, dy.shape, (s.dtype,), dev)
+    dx = torch.empty_like(s) if dx is None else _operand("dx", dx, dy.shape, (s.dtype,), dev)
+    dgamma = dbeta = ws = None
+    nbytes = 0
+    if weight_grads:
+        dgamma, dbeta = torch.empty((2, width), dtype=torch.float32, device=dev).unbind(0)
+        nb = ctypes.c_size_t(0)
+        _check(lib().bmoe_layer_norm_backward_workspace(rows, width, ctypes.byref(nb)))
+        nbytes = int(nb.value)
+        ws = _scratch(nbytes, dev)
+    _check(lib().bmoe_layer_norm_backward(rows, width, BF16 if s.dtype == torch.bfloat16 else F32,
+                                          BF16 if dy.dtype == torch.bfloat16 else F32, _ptr(dy), _ptr(s), _ptr(gamma),
+                                          _ptr(mean), _ptr(rstd), _ptr(d_sum), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
+                                          _ptr(ws), nbytes, _stream_handle()))
+    return dx, dgamma, dbeta
+
+
+@_on_device
+def orthogonalize(grad, momentum=None, mu: float = 0.95, nesterov: bool = True, momentum_out=None, out=None):
+    """Orthogonalised update of a matrix gradient [rows][cols] (fp32 or bf16):
+    momentum step M' = mu M + G (fp32, when momentum is given) and five
+    Newton-Schulz steps on G + mu M' (or M', or G).  Returns (out bf16
+    [rows][cols], M' or None); momentum_out may be momentum itself."""
+    torch = _torch()
+    dev, f32 = grad.device, (torch.float32,)
+    rows, cols = grad.shape
+    _operand("grad", grad, grad.shape, (torch.float32, torch.bfloat16), dev)
+    if momentum is None:
+        if momentum_out is not None:
+            raise ValueError("momentum_out needs a momentum")
+    else:
+        _operand("momentum", momentum, grad.shape, f32, dev)
+        momentum_out = (torch.empty_like(momentum) if momentum_out is None else
+                        _operand("momentum_out", momentum_out, grad.shape, f32, dev))
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    else:
+        _operand("out", out, grad.shape, (torch.bfloat16,), dev)
+    nb = ctypes.c_size_t(0)
+    _check(lib().bmoe_orthogonalize_workspace(rows, cols, ctypes.byref(nb)))
+    ws = _scratch(int(nb.value), dev)
+    _check(lib().bmoe_orthogonalize(rows, cols, BF16 if grad.dtype == torch.bfloat16 else F32, _ptr(grad),
+                                    _ptr(momentum), _ptr(momentum_out), float(mu), 1 if nesterov else 0, _ptr(out),
+                                    _ptr(ws), int(nb.value), _stream_handle()))
+    return out, momentum_out
+
+
+@_on_device
+def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None, packed=None):
+    """Latent substrate step W' = (1 - decay) W - step O (W [rows][cols] fp32, O
+    bf16; W' = W without O) and its ternary codes at threshold mean |W'| / 2.
+    Returns (W', packed [rows][cols / 16] int32 in pack_ternary's format,
+    scale: 0-d fp32 tensor mean |W'|).  w_out may be w itself; packed may be a
+    layer's w_base tensor (call Layer.prepare again afterwards where used)."""
+    torch = _torch()
+    dev = w.device
+    rows, cols = w.shape
+    _operand("w", w, w.shape, (torch.float32,), dev)
+    if o is None:
+        if w_out is not None:
+            raise ValueError("w_out needs an update o")
+    else:
+        _operand("o", o, w.shape, (torch.bfloat16,), dev)
+        w_out = torch.empty_like(w) if w_out is None else _operand("w_out", w_out, w.shape, (torch.float32,), dev)
+    if packed is None:
+        packed = torch.empty((rows, cols // 16), dtype=torch.int32, device=dev)
+    else:
+        _operand("packed", packed, (rows, cols // 16), (torch.int32,), dev)
+    scale = torch.empty((), dtype=torch.float32, device=dev)
+    nb = ctypes.c_size_t(0)
+    _check(lib().bmoe_substrate_step_workspace(rows, cols, ctypes.byref(nb)))
+    ws = _scratch(int(nb.value), dev)
+    _check(lib().bmoe_substrate_step(rows, cols, _ptr(w), _ptr(o), float(step), float(decay), _ptr(w_out), _ptr(packed),
+                                     _ptr(scale), _ptr(ws), int(nb.value), _stream_handle()))
+    return w if o is None else w_out, packed, scale
 
 
 def dbg_ternary_gemm(a, w_packed, n_out: int, alpha: float = 1.0):

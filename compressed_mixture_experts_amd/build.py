@@ -4,7 +4,7 @@
 
 Outputs, next to this file:
   libbmoe.so          the product library (include/bmoe.h, bmoe_trace.h, bmoe_grad.h,
-                      bmoe_train.h)
+                      bmoe_train.h, bmoe_norm.h, bmoe_update.h)
   libbmoe_debug.so    the same plus the test hooks of include/bmoe_debug.h
                       (api.hip compiled with -DBMOE_DEBUG_EXPORTS)
   libbmoe_hostsan.so  the debug library with its host code (argument checks,
@@ -33,7 +33,8 @@ LIB_HOSTSAN = os.path.join(PKG, "libbmoe_hostsan.so")
 KERNEL_SOURCES = ["route.hip", "gemm.hip", "butterfly.hip", "butterfly_in.hip", "butterfly_mid.hip",
                   "butterfly_out.hip", "fused.hip", "fused_mfma.hip", "prep.hip", "gemm_fp4.hip",
                   "butterfly_split.hip", "butterfly_bwd.hip", "substrate_grad.hip", "combine_bwd.hip",
-                  "router_bwd.hip", "gelu_bwd.hip", "butterfly_rot.hip", "train.hip"]
+                  "router_bwd.hip", "gelu_bwd.hip", "butterfly_rot.hip", "train.hip",
+                  "layer_norm.hip", "substrate_step.hip", "orthogonalize.hip"]
 DEBUG_SOURCES = ["butterfly_dbg.hip"]   # kernels reached only from the test hooks
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

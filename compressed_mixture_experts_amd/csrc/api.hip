@@ -1,20 +1,25 @@
 // Host side of the C ABI declared in include/bmoe.h, include/bmoe_trace.h,
-// include/bmoe_grad.h and (built with -DBMOE_DEBUG_EXPORTS only)
+// include/bmoe_grad.h, include/bmoe_norm.h, include/bmoe_train.h,
+// include/bmoe_update.h and (built with -DBMOE_DEBUG_EXPORTS only)
 // include/bmoe_debug.h: argument validation (all before any enqueue),
 // workspace planning, and the launch sequence of the forward pass on the
 // caller's stream.
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <string>
 #include <vector>
 
 #include "bmoe.h"
 #include "bmoe_debug.h"
 #include "bmoe_grad.h"
+#include "bmoe_norm.h"
 #include "bmoe_trace.h"
 #include "bmoe_train.h"
+#include "bmoe_update.h"
 #include "common.hpp"
 
 using namespace bmoe;
@@ -1492,6 +1497,198 @@ bmoe_status bmoe_layer_backward(const bmoe_layer* layer, const void* x, int32_t 
   BMOE_HIP(launch_router_bwd(x, layer->w_gate, idx, dgate, dxr, g->d_w_gate, at<char>(workspace, bw.rb), T, d, N, k,
                              layer->renorm_gates, act, stream));
   BMOE_HIP(launch_token_sum(dU, qpos, nullptr, dxr, g->dx, true, T, d, k, act, stream));
+  return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- layer norm, substrate updates
+namespace {
+
+constexpr int32_t kMaxNormWidth = 16384, kMaxUpdateSide = 16384;
+
+bmoe_status check_norm_shape(int32_t rows, int32_t width) {
+  if (rows < 0 || rows > kMaxTokens || width < 1 || width > kMaxNormWidth)
+    return fail(BMOE_ERR_SHAPE, "rows=%d must be in [0, %d], width=%d in [1, %d]", rows, kMaxTokens, width,
+                kMaxNormWidth);
+  return BMOE_OK;
+}
+
+bmoe_status check_ortho_shape(int32_t rows, int32_t cols) {
+  if (rows < 1 || rows > kMaxUpdateSide || cols < 1 || cols > kMaxUpdateSide)
+    return fail(BMOE_ERR_SHAPE, "rows=%d and cols=%d must be in [1, %d]", rows, cols, kMaxUpdateSide);
+  return BMOE_OK;
+}
+
+bmoe_status check_step_shape(int32_t rows, int32_t cols) {
+  if (rows < 1 || cols < 16 || cols % 16 != 0 || int64_t(rows) * cols > (int64_t(1) << 31) - 1)
+    return fail(BMOE_ERR_SHAPE, "rows=%d, cols=%d: need rows >= 1, cols a positive multiple of 16, rows * cols below 2^31",
+                rows, cols);
+  return BMOE_OK;
+}
+
+// Whether range r overlaps any of the others (same_ok: one that starts at the
+// same address is the same buffer and allowed).
+bool overlaps_any(Range r, std::initializer_list<Range> others, bool same_ok = false) {
+  for (const Range& o : others)
+    if (overlap(r, o) && !(same_ok && r.p == o.p)) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+bmoe_status bmoe_layer_norm_forward(int32_t rows, int32_t width, int32_t dtype, const void* x, const void* residual,
+                                    const float* gamma, const float* beta, float eps, void* sum, void* y, float* mean,
+                                    float* rstd, hipStream_t stream) {
+  bmoe_status st = check_norm_shape(rows, width);
+  if (st != BMOE_OK) return st;
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(BMOE_ERR_SHAPE, "eps=%g must be finite and not negative", double(eps));
+  if (dtype != BMOE_F32 && dtype != BMOE_BF16) return fail(BMOE_ERR_DTYPE, "dtype=%d is unknown", dtype);
+  if (rows == 0) return ok();
+  if (!x || !y) return fail(BMOE_ERR_NULL, "x / y is NULL");
+  if (!residual != !sum) return fail(BMOE_ERR_NULL, "residual and sum go together");
+  if (!mean != !rstd) return fail(BMOE_ERR_NULL, "mean and rstd go together");
+  const size_t es = act_size(dtype);
+  if (!aligned(x, es) || !aligned(residual, es) || !aligned(sum, es) || !aligned(y, es))
+    return fail(BMOE_ERR_ALIGN, "x, residual, sum and y must be aligned to their element size");
+  if (!aligned(gamma, 4) || !aligned(beta, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return fail(BMOE_ERR_ALIGN, "gamma, beta, mean and rstd must be 4-byte aligned");
+  const size_t nb = size_t(rows) * width * es, wb = size_t(width) * 4, rb = size_t(rows) * 4;
+  const Range rx{x, nb}, rr{residual, nb}, rg{gamma, wb}, rbt{beta, wb}, rs{sum, nb}, ry{y, nb}, rm{mean, rb}, rd{rstd, rb};
+  if (overlaps_any(ry, {rx, rr}, true) || overlaps_any(ry, {rg, rbt, rs, rm, rd}))
+    return fail(BMOE_ERR_ALIAS, "y overlaps another array (it may be x or residual itself)");
+  if (overlaps_any(rs, {rx, rr}, true) || overlaps_any(rs, {rg, rbt, rm, rd}))
+    return fail(BMOE_ERR_ALIAS, "sum overlaps another array (it may be x or residual itself)");
+  if (overlaps_any(rm, {rx, rr, rg, rbt, rd}) || overlaps_any(rd, {rx, rr, rg, rbt}))
+    return fail(BMOE_ERR_ALIAS, "mean / rstd overlaps another array");
+  st = check_device();
+  if (st != BMOE_OK) return st;
+  const LnFwdArgs a{x, residual, gamma, beta, sum, y, mean, rstd, eps, rows, width};
+  BMOE_HIP(launch_ln_fwd(a, dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, stream));
+  return ok();
+}
+
+bmoe_status bmoe_layer_norm_backward_workspace(int32_t rows, int32_t width, size_t* bytes) {
+  if (!bytes) return fail(BMOE_ERR_NULL, "bytes is NULL");
+  const bmoe_status st = check_norm_shape(rows, width);
+  if (st != BMOE_OK) return st;
+  *bytes = ln_bwd_workspace(rows, width);
+  return ok();
+}
+
+bmoe_status bmoe_layer_norm_backward(int32_t rows, int32_t width, int32_t dtype, int32_t dy_dtype, const void* dy,
+                                     const void* s, const float* gamma, const float* mean, const float* rstd,
+                                     const void* d_sum, void* dx, float* dgamma, float* dbeta, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream) {
+  bmoe_status st = check_norm_shape(rows, width);
+  if (st != BMOE_OK) return st;
+  if (dtype != BMOE_F32 && dtype != BMOE_BF16) return fail(BMOE_ERR_DTYPE, "dtype=%d is unknown", dtype);
+  if (dy_dtype != BMOE_F32 && dy_dtype != dtype) return fail(BMOE_ERR_DTYPE, "dy_dtype=%d must be fp32 or dtype", dy_dtype);
+  if (!dgamma != !dbeta) return fail(BMOE_ERR_NULL, "dgamma and dbeta go together");
+  if (rows == 0 && !dgamma) return ok();
+  if (rows > 0 && (!dy || !s || !mean || !rstd || !dx)) return fail(BMOE_ERR_NULL, "dy / s / mean / rstd / dx is NULL");
+  const size_t need = dgamma ? ln_bwd_workspace(rows, width) : 0;
+  if (need > 0 && !workspace) return fail(BMOE_ERR_NULL, "workspace is NULL");
+  const size_t es = act_size(dtype), ds = act_size(dy_dtype);
+  if (rows > 0 && (!aligned(dy, ds) || !aligned(s, es) || !aligned(d_sum, es) || !aligned(dx, es)))
+    return fail(BMOE_ERR_ALIGN, "dy, s, d_sum and dx must be aligned to their element size");
+  if (!aligned(gamma, 4) || !aligned(dgamma, 4) || !aligned(dbeta, 4) ||
+      (rows > 0 && (!aligned(mean, 4) || !aligned(rstd, 4))))
+    return fail(BMOE_ERR_ALIGN, "gamma, mean, rstd, dgamma and dbeta must be 4-byte aligned");
+  if (need > 0 && !aligned(workspace, 16)) return fail(BMOE_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (workspace_bytes < need)
+    return fail(BMOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  const size_t n = size_t(rows) * width, wb = size_t(width) * 4, rb = size_t(rows) * 4;
+  const Range rdy{dy, n * ds}, rs{s, n * es}, rg{gamma, wb}, rm{mean, rb}, rr{rstd, rb}, rd{d_sum, n * es}, rdx{dx, n * es},
+      rdg{dgamma, wb}, rdb{dbeta, wb}, rws{workspace, need};
+  if (overlaps_any(rdx, {rs, rd}, true) || overlaps_any(rdx, {rdy}, ds == es) ||
+      overlaps_any(rdx, {rg, rm, rr, rdg, rdb, rws}))
+    return fail(BMOE_ERR_ALIAS, "dx overlaps another array (it may be s, d_sum or a dy of its dtype itself)");
+  if (overlaps_any(rdg, {rdy, rs, rg, rm, rr, rd, rdb, rws}) || overlaps_any(rdb, {rdy, rs, rg, rm, rr, rd, rws}))
+    return fail(BMOE_ERR_ALIAS, "dgamma / dbeta overlaps another array");
+  if (overlaps_any(rws, {rdy, rs, rg, rm, rr, rd})) return fail(BMOE_ERR_ALIAS, "the workspace overlaps an input");
+  st = check_device();
+  if (st != BMOE_OK) return st;
+  const LnBwdArgs a{dy, s, gamma, mean, rstd, d_sum, dx, dgamma ? static_cast<float*>(workspace) : nullptr, rows, width};
+  BMOE_HIP(launch_ln_bwd(a, dgamma, dbeta, dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32,
+                         dy_dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, stream));
+  return ok();
+}
+
+bmoe_status bmoe_orthogonalize_workspace(int32_t rows, int32_t cols, size_t* bytes) {
+  if (!bytes) return fail(BMOE_ERR_NULL, "bytes is NULL");
+  const bmoe_status st = check_ortho_shape(rows, cols);
+  if (st != BMOE_OK) return st;
+  *bytes = ortho_workspace(rows, cols);
+  return ok();
+}
+
+bmoe_status bmoe_orthogonalize(int32_t rows, int32_t cols, int32_t grad_dtype, const void* grad, const float* momentum,
+                               float* momentum_out, float mu, int32_t nesterov, void* out, void* workspace,
+                               size_t workspace_bytes, hipStream_t stream) {
+  bmoe_status st = check_ortho_shape(rows, cols);
+  if (st != BMOE_OK) return st;
+  if (grad_dtype != BMOE_F32 && grad_dtype != BMOE_BF16) return fail(BMOE_ERR_DTYPE, "grad_dtype=%d is unknown", grad_dtype);
+  if (!grad || !out || !workspace) return fail(BMOE_ERR_NULL, "grad / out / workspace is NULL");
+  if (!momentum != !momentum_out) return fail(BMOE_ERR_NULL, "momentum and momentum_out go together");
+  if (momentum && !(mu >= 0.f && mu <= 1.f)) return fail(BMOE_ERR_SHAPE, "mu=%g must be in [0, 1]", double(mu));
+  if (momentum && nesterov != 0 && nesterov != 1) return fail(BMOE_ERR_SHAPE, "nesterov=%d must be 0 or 1", nesterov);
+  const size_t es = act_size(grad_dtype);
+  if (!aligned(grad, es) || !aligned(momentum, 4) || !aligned(momentum_out, 4) || !aligned(out, 2))
+    return fail(BMOE_ERR_ALIGN, "grad, momentum, momentum_out and out must be aligned to their element size");
+  if (!aligned(workspace, 256)) return fail(BMOE_ERR_ALIGN, "workspace is not 256-byte aligned");
+  const size_t need = ortho_workspace(rows, cols), n = size_t(rows) * cols;
+  if (workspace_bytes < need)
+    return fail(BMOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  const Range rg{grad, n * es}, rm{momentum, n * 4}, rn{momentum_out, n * 4}, ro{out, n * 2}, rws{workspace, need};
+  if (overlaps_any(rn, {rm}, true) || overlaps_any(rn, {rg, ro, rws}))
+    return fail(BMOE_ERR_ALIAS, "momentum_out overlaps another array (it may be momentum itself)");
+  if (overlaps_any(ro, {rg, rm, rws})) return fail(BMOE_ERR_ALIAS, "out overlaps another array");
+  if (overlaps_any(rws, {rg, rm})) return fail(BMOE_ERR_ALIAS, "the workspace overlaps an input");
+  st = check_device();
+  if (st != BMOE_OK) return st;
+  const OrthoArgs a{grad, momentum, momentum_out, static_cast<uint16_t*>(out), mu, rows, cols, nesterov,
+                    grad_dtype == BMOE_BF16, workspace};
+  BMOE_HIP(launch_orthogonalize(a, stream));
+  return ok();
+}
+
+bmoe_status bmoe_substrate_step_workspace(int32_t rows, int32_t cols, size_t* bytes) {
+  if (!bytes) return fail(BMOE_ERR_NULL, "bytes is NULL");
+  const bmoe_status st = check_step_shape(rows, cols);
+  if (st != BMOE_OK) return st;
+  *bytes = sub_step_workspace(size_t(rows) * cols);
+  return ok();
+}
+
+bmoe_status bmoe_substrate_step(int32_t rows, int32_t cols, const float* w, const void* o, double step, double decay,
+                                float* w_out, uint32_t* packed, float* scale, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream) {
+  bmoe_status st = check_step_shape(rows, cols);
+  if (st != BMOE_OK) return st;
+  if (!std::isfinite(step) || !std::isfinite(decay))
+    return fail(BMOE_ERR_SHAPE, "step=%g and decay=%g must be finite", step, decay);
+  if (!w || !packed || !workspace) return fail(BMOE_ERR_NULL, "w / packed / workspace is NULL");
+  if (!o != !w_out) return fail(BMOE_ERR_NULL, "o and w_out go together");
+  if (!aligned(w, 16) || !aligned(o, 16) || !aligned(w_out, 16) || !aligned(packed, 16))
+    return fail(BMOE_ERR_ALIGN, "w, o, w_out and packed must be 16-byte aligned");
+  if (!aligned(scale, 4) || !aligned(workspace, 16))
+    return fail(BMOE_ERR_ALIGN, "scale must be 4-byte aligned, the workspace 16-byte aligned");
+  const size_t n = size_t(rows) * cols, need = sub_step_workspace(n);
+  if (workspace_bytes < need)
+    return fail(BMOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  const Range rw{w, n * 4}, ro{o, n * 2}, rwo{w_out, n * 4}, rp{packed, n / 4}, rs{scale, 4}, rws{workspace, need};
+  if (overlaps_any(rwo, {rw}, true) || overlaps_any(rwo, {ro, rp, rs, rws}))
+    return fail(BMOE_ERR_ALIAS, "w_out overlaps another array (it may be w itself)");
+  if (overlaps_any(rp, {rw, ro, rs, rws}) || overlaps_any(rs, {rw, ro, rws}) || overlaps_any(rws, {rw, ro}))
+    return fail(BMOE_ERR_ALIAS, "packed, scale or the workspace overlaps another array");
+  st = check_device();
+  if (st != BMOE_OK) return st;
+  const SubStepArgs a{w, static_cast<const uint16_t*>(o), w_out, packed, scale, static_cast<double*>(workspace), step,
+                      1.0 - decay, n};
+  BMOE_HIP(launch_sub_step(a, stream));
   return ok();
 }
 

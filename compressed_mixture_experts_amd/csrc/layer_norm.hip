@@ -1,0 +1,417 @@
+// Layer norm over rows, forward and backward (include/bmoe_norm.h).
+//
+// Both passes are bound by HBM: a few operations per element read once and
+// written once.  A row is held in registers between its loads and its stores:
+// TPR threads (one wave up to 2048 columns with 16-byte loads, else a whole
+// workgroup) hold NV groups of GE consecutive elements each, group v of thread
+// t being group t + TPR v of the row, so every load is contiguous over the
+// wave.  One wave per row needs no LDS and no barrier.  Workgroups loop over
+// rows, which keeps gamma, beta and the backward's column sums of the
+// thread's columns in registers.
+//
+// GE = 8 (16-byte vectors) needs a width that is a multiple of 8 and 16-byte
+// aligned arrays; GE = 2 an even width; else GE = 1.
+#include "common.hpp"
+
+namespace bmoe {
+
+// Sum over a wave's 64 lanes, the same value in every lane (fixed order).
+__device__ __forceinline__ float ln_wave_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// Sums of N values over the TPR threads of a row, the same in each of them.
+template <int TPR, int N>
+__device__ __forceinline__ void ln_row_sum(float (&v)[N], float2* red) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = ln_wave_sum(v[k]);
+  if constexpr (TPR > 64) {
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();  // the previous use of red is over
+    if ((threadIdx.x & 63) == 0) red[wave] = make_float2(v[0], v[N - 1]);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < TPR / 64; ++w) {
+      v[0] += red[w].x;
+      if constexpr (N == 2) v[1] += red[w].y;
+    }
+  }
+}
+
+template <int ACT, int GE>
+__device__ __forceinline__ void ln_load(const void* p, size_t i, float* v) {
+  if constexpr (GE == 8) {
+    load8<ACT>(p, i, v);
+  } else if constexpr (GE == 2 && ACT == ACT_BF16) {
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i);
+    v[0] = bf16lo(u);
+    v[1] = bf16hi(u);
+  } else if constexpr (GE == 2) {
+    const float2 u = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
+    v[0] = u.x;
+    v[1] = u.y;
+  } else {
+    v[0] = load1<ACT>(p, i);
+  }
+}
+
+template <int ACT, int GE>
+__device__ __forceinline__ void ln_store(void* p, size_t i, const float* v) {
+  if constexpr (GE == 8) {
+    store8<ACT>(p, i, v);
+  } else if constexpr (GE == 2 && ACT == ACT_BF16) {
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + i) = pack_bf16x2(v[0], v[1]);
+  } else if constexpr (GE == 2) {
+    *reinterpret_cast<float2*>(static_cast<float*>(p) + i) = make_float2(v[0], v[1]);
+  } else if constexpr (ACT == ACT_BF16) {
+    static_cast<uint16_t*>(p)[i] = uint16_t(pack_bf16x2(v[0], v[0]));
+  } else {
+    static_cast<float*>(p)[i] = v[0];
+  }
+}
+
+// The values as the activation dtype stores them.
+template <int ACT, int GE>
+__device__ __forceinline__ void ln_round(float* v) {
+  if constexpr (ACT == ACT_BF16) {
+#pragma unroll
+    for (int j = 0; j < GE; ++j) v[j] = float(__bf16(v[j]));
+  }
+}
+
+template <int ACT, int GE, int TPR, int NV>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(LnFwdArgs a) {
+  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;  // rows per workgroup
+  __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int groups = a.width / GE;
+  const float inv = 1.0f / float(a.width);
+  float ga[NV][GE], be[NV][GE];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int g = t + TPR * v;
+#pragma unroll
+    for (int j = 0; j < GE; ++j) {
+      ga[v][j] = 1.f;
+      be[v][j] = 0.f;
+    }
+    if (g < groups && a.gamma) ln_load<ACT_F32, GE>(a.gamma, size_t(g) * GE, ga[v]);
+    if (g < groups && a.beta) ln_load<ACT_F32, GE>(a.beta, size_t(g) * GE, be[v]);
+  }
+  for (int row = blockIdx.x * RPW + sub; row < a.rows; row += gridDim.x * RPW) {
+    const size_t at = size_t(row) * a.width;
+    float x[NV][GE];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int g = t + TPR * v;
+#pragma unroll
+      for (int j = 0; j < GE; ++j) x[v][j] = 0.f;
+      if (g < groups) ln_load<ACT, GE>(a.x, at + size_t(g) * GE, x[v]);
+    }
+    if (a.res) {
+      float r[NV][GE];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int g = t + TPR * v;
+#pragma unroll
+        for (int j = 0; j < GE; ++j) r[v][j] = 0.f;
+        if (g < groups) ln_load<ACT, GE>(a.res, at + size_t(g) * GE, r[v]);
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int g = t + TPR * v;
+#pragma unroll
+        for (int j = 0; j < GE; ++j) x[v][j] += r[v][j];
+        ln_round<ACT, GE>(x[v]);
+        if (g < groups) ln_store<ACT, GE>(a.sum, at + size_t(g) * GE, x[v]);
+      }
+    }
+    float s[1] = {0.f}, q[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < GE; ++j) s[0] += x[v][j];
+    ln_row_sum<TPR>(s, red);
+    const float mean = s[0] * inv;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if (t + TPR * v < groups) {
+#pragma unroll
+        for (int j = 0; j < GE; ++j) {
+          const float c = x[v][j] - mean;
+          q[0] = fmaf(c, c, q[0]);
+        }
+      }
+    }
+    ln_row_sum<TPR>(q, red);
+    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, a.eps));
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int g = t + TPR * v;
+      float y[GE];
+#pragma unroll
+      for (int j = 0; j < GE; ++j) y[j] = fmaf((x[v][j] - mean) * rstd, ga[v][j], be[v][j]);
+      if (g < groups) ln_store<ACT, GE>(a.y, at + size_t(g) * GE, y);
+    }
+    if (t == 0 && a.mean) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+  }
+}
+
+// Backward.  Each thread keeps its columns' sums of dy xhat and dy over the
+// rows of its workgroup; at the end the workgroup adds its waves' sums in
+// order (through LDS) and writes one partial row [dgamma | dbeta].
+template <int ACT, int DACT, int GE, int TPR, int NV>
+__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_kernel(LnBwdArgs a) {
+  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;
+  __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
+  __shared__ float cols[RPW > 1 ? RPW : 1][RPW > 1 ? TPR * NV * GE : 1];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int groups = a.width / GE;
+  const float inv = 1.0f / float(a.width);
+  float ga[NV][GE], dg[NV][GE], db[NV][GE];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int g = t + TPR * v;
+#pragma unroll
+    for (int j = 0; j < GE; ++j) {
+      ga[v][j] = 1.f;
+      dg[v][j] = db[v][j] = 0.f;
+    }
+    if (g < groups && a.gamma) ln_load<ACT_F32, GE>(a.gamma, size_t(g) * GE, ga[v]);
+  }
+  for (int row = blockIdx.x * RPW + sub; row < a.rows; row += gridDim.x * RPW) {
+    const size_t at = size_t(row) * a.width;
+    float x[NV][GE], d[NV][GE];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int g = t + TPR * v;
+#pragma unroll
+      for (int j = 0; j < GE; ++j) x[v][j] = d[v][j] = 0.f;
+      if (g < groups) {
+        ln_load<ACT, GE>(a.s, at + size_t(g) * GE, x[v]);
+        ln_load<DACT, GE>(a.dy, at + size_t(g) * GE, d[v]);
+      }
+    }
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float c[2] = {0.f, 0.f};  // sums of v and v xhat
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      // groups past the row: dy is zero there and xhat is made zero, so that
+      // an infinite rstd or mean reaches no other column
+      const bool in = t + TPR * v < groups;
+#pragma unroll
+      for (int j = 0; j < GE; ++j) {
+        x[v][j] = in ? (x[v][j] - mean) * rstd : 0.f;
+        const float dy = d[v][j];
+        dg[v][j] = fmaf(dy, x[v][j], dg[v][j]);
+        db[v][j] += dy;
+        d[v][j] = dy * ga[v][j];
+        c[0] += d[v][j];
+        c[1] = fmaf(d[v][j], x[v][j], c[1]);
+      }
+    }
+    ln_row_sum<TPR>(c, red);
+    const float c1 = c[0] * inv, c2 = c[1] * inv;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int g = t + TPR * v;
+      if (g < groups) {
+        float o[GE];
+#pragma unroll
+        for (int j = 0; j < GE; ++j) o[j] = rstd * (d[v][j] - c1 - x[v][j] * c2);
+        if (a.d_sum) {
+          float r[GE];
+          ln_load<ACT, GE>(a.d_sum, at + size_t(g) * GE, r);
+#pragma unroll
+          for (int j = 0; j < GE; ++j) o[j] += r[j];
+        }
+        ln_store<ACT, GE>(a.dx, at + size_t(g) * GE, o);
+      }
+    }
+  }
+  if (!a.part) return;
+  float* out = a.part + size_t(blockIdx.x) * 2 * a.width;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if constexpr (RPW == 1) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int g = t + TPR * v;
+        if (g < groups)
+#pragma unroll
+          for (int j = 0; j < GE; ++j) out[size_t(k) * a.width + size_t(g) * GE + j] = k ? db[v][j] : dg[v][j];
+      }
+    } else {
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < GE; ++j) cols[sub][(t + TPR * v) * GE + j] = k ? db[v][j] : dg[v][j];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.width; c += 256) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < RPW; ++w) s += cols[w][c];
+        out[size_t(k) * a.width + c] = s;
+      }
+    }
+  }
+}
+
+// Column sums of the P partial rows, in order: 64 columns per workgroup, 16
+// waves with a contiguous range of the rows each, their sums added in order.
+__global__ __launch_bounds__(1024) void ln_colsum_kernel(const float* part, float* dgamma, float* dbeta, int P,
+                                                         int width) {
+  __shared__ float sm[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane, n = 2 * width;
+  const int per = (P + 15) / 16, p1 = min(P, (wave + 1) * per);
+  float s = 0.f;
+  if (c < n) {
+#pragma unroll 8
+    for (int p = wave * per; p < p1; ++p) s += part[size_t(p) * n + c];
+  }
+  sm[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < n) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += sm[w][lane];
+    if (c < width) dgamma[c] = s;
+    else dbeta[c - width] = s;
+  }
+}
+
+namespace {
+
+bool ln_aligned(const void* p, size_t b) { return reinterpret_cast<uintptr_t>(p) % b == 0; }
+
+// Threads per row and groups per thread for a row of `groups` groups.
+struct LnShape {
+  int tpr, nv;
+};
+LnShape ln_shape(int ge, int groups) {
+  if (ge == 8) {
+    if (groups <= 64) return {64, 1};
+    if (groups <= 128) return {64, 2};
+    if (groups <= 256) return {64, 4};
+    if (groups <= 512) return {256, 2};
+    if (groups <= 1024) return {256, 4};
+    return {512, 4};
+  }
+  if (ge == 2) {
+    if (groups <= 128) return {64, 2};
+    if (groups <= 512) return {64, 8};
+    if (groups <= 2048) return {256, 8};
+    return {512, 16};
+  }
+  if (groups <= 256) return {64, 4};
+  if (groups <= 1024) return {64, 16};
+  if (groups <= 4096) return {256, 16};
+  return {1024, 16};
+}
+
+int ln_group(int width, bool v16, bool pair) { return width % 8 == 0 && v16 ? 8 : width % 2 == 0 && pair ? 2 : 1; }
+
+template <int ACT, int GE, int TPR, int NV>
+hipError_t fwd_go(const LnFwdArgs& a, hipStream_t s) {
+  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;
+  const int blocks = (a.rows + RPW - 1) / RPW;
+  hipLaunchKernelGGL((ln_fwd_kernel<ACT, GE, TPR, NV>), dim3(unsigned(blocks < 2048 ? blocks : 2048)),
+                     dim3(TPR > 256 ? TPR : 256), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int ACT, int DACT, int GE, int TPR, int NV>
+hipError_t bwd_go(const LnBwdArgs& a, int blocks, hipStream_t s) {
+  hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV>), dim3(unsigned(blocks)), dim3(TPR > 256 ? TPR : 256), 0, s,
+                     a);
+  return hipGetLastError();
+}
+
+#define LN_SHAPES(GO)                          \
+  if (ge == 8) {                               \
+    if (sh.tpr == 512) return GO(8, 512, 4);   \
+    if (sh.tpr == 256 && sh.nv == 4) return GO(8, 256, 4); \
+    if (sh.tpr == 256) return GO(8, 256, 2);   \
+    if (sh.nv == 4) return GO(8, 64, 4);       \
+    if (sh.nv == 2) return GO(8, 64, 2);       \
+    return GO(8, 64, 1);                       \
+  }                                            \
+  if (ge == 2) {                               \
+    if (sh.tpr == 512) return GO(2, 512, 16);  \
+    if (sh.tpr == 256) return GO(2, 256, 8);   \
+    if (sh.nv == 8) return GO(2, 64, 8);       \
+    return GO(2, 64, 2);                       \
+  }                                            \
+  if (sh.tpr == 1024) return GO(1, 1024, 16);  \
+  if (sh.tpr == 256) return GO(1, 256, 16);    \
+  if (sh.nv == 16) return GO(1, 64, 16);       \
+  return GO(1, 64, 4);
+
+template <int ACT>
+hipError_t fwd_act(const LnFwdArgs& a, int ge, hipStream_t s) {
+  const LnShape sh = ln_shape(ge, a.width / ge);
+#define LN_GO(G, T, V) fwd_go<ACT, G, T, V>(a, s)
+  LN_SHAPES(LN_GO)
+#undef LN_GO
+}
+
+template <int ACT, int DACT>
+hipError_t bwd_act(const LnBwdArgs& a, int ge, hipStream_t s) {
+  const LnShape sh = ln_shape(ge, a.width / ge);
+  const int blocks = ln_bwd_blocks(a.rows, a.width);
+#define LN_GO(G, T, V) bwd_go<ACT, DACT, G, T, V>(a, blocks, s)
+  LN_SHAPES(LN_GO)
+#undef LN_GO
+}
+
+}  // namespace
+
+// Workgroups of the backward, one partial row each: enough to fill the GPU,
+// no more than there are groups of 4 rows.
+int ln_bwd_blocks(int rows, int width) {
+  const int need = (rows + 3) / 4;
+  return need < 512 ? need : 512;
+}
+
+size_t ln_bwd_workspace(int rows, int width) { return size_t(ln_bwd_blocks(rows, width)) * 2 * width * 4; }
+
+hipError_t launch_ln_fwd(const LnFwdArgs& a, int act, hipStream_t s) {
+  if (a.rows == 0) return hipSuccess;
+  const size_t pair = act == ACT_BF16 ? 4 : 8;
+  auto all = [&](size_t b, size_t f) {
+    return ln_aligned(a.x, b) && ln_aligned(a.res, b) && ln_aligned(a.sum, b) && ln_aligned(a.y, b) &&
+           ln_aligned(a.gamma, f) && ln_aligned(a.beta, f);
+  };
+  const int ge = ln_group(a.width, all(16, 16), all(pair, 8));
+  return act == ACT_BF16 ? fwd_act<ACT_BF16>(a, ge, s) : fwd_act<ACT_F32>(a, ge, s);
+}
+
+hipError_t launch_ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, int act, int dact, hipStream_t s) {
+  const size_t pair = act == ACT_BF16 ? 4 : 8, dpair = dact == ACT_BF16 ? 4 : 8;
+  auto all = [&](size_t b, size_t d, size_t f) {
+    return ln_aligned(a.s, b) && ln_aligned(a.d_sum, b) && ln_aligned(a.dx, b) && ln_aligned(a.dy, d) &&
+           ln_aligned(a.gamma, f);
+  };
+  const int ge = ln_group(a.width, all(16, 16, 16), all(pair, dpair, 8));
+  if (a.rows > 0) {
+    const hipError_t e = act == ACT_BF16
+                             ? (dact == ACT_BF16 ? bwd_act<ACT_BF16, ACT_BF16>(a, ge, s) : bwd_act<ACT_BF16, ACT_F32>(a, ge, s))
+                             : bwd_act<ACT_F32, ACT_F32>(a, ge, s);
+    if (e != hipSuccess) return e;
+  }
+  if (!dgamma) return hipSuccess;
+  hipLaunchKernelGGL(ln_colsum_kernel, dim3(unsigned((2 * a.width + 63) / 64)), dim3(1024), 0, s, a.part, dgamma, dbeta,
+                     ln_bwd_blocks(a.rows, a.width), a.width);
+  return hipGetLastError();
+}
+
+}  // namespace bmoe

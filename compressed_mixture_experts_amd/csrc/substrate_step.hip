@@ -1,0 +1,97 @@
+// Step of a latent substrate and its ternary codes (include/bmoe_update.h):
+//     W' = fl32((1 - decay) W - step O),  scale = mean |W'|,
+//     code = sign(W') where 2 |W'| > scale.
+// The codes need the mean over all of W', so there are two passes, both bound
+// by memory: the first reads W and O, writes W' and one fp64 partial sum of
+// |W'| per workgroup; the second adds the partial sums (every workgroup the
+// same ones in the same order), reads W' again and writes 2 bits per weight.
+// fp64 keeps the codes independent of how the sum was split: a weight's code
+// could only differ if an fp32 number lay within about 1e-13 of the threshold
+// relative to it.
+#include "common.hpp"
+
+namespace bmoe {
+
+constexpr int SS_BLOCKS = 1024;  // most workgroups of the first pass
+
+__device__ __forceinline__ double ss_wave_sum(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  return v;
+}
+
+// The sum over a workgroup of 256, valid in every thread.
+__device__ __forceinline__ double ss_block_sum(double v, double* red) {
+  v = ss_wave_sum(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return ((red[0] + red[1]) + red[2]) + red[3];
+}
+
+template <bool UPD>
+__global__ __launch_bounds__(256) void sub_update_kernel(SubStepArgs a) {
+#pragma clang fp contract(off)
+  __shared__ double red[4];
+  const size_t quads = a.n / 4;
+  double s = 0.0;
+  for (size_t q = size_t(blockIdx.x) * 256 + threadIdx.x; q < quads; q += size_t(gridDim.x) * 256) {
+    float4 w = reinterpret_cast<const float4*>(a.w)[q];
+    if constexpr (UPD) {
+      const uint2 o = reinterpret_cast<const uint2*>(a.o)[q];
+      // two products and a difference in fp64, one rounding to fp32
+      w.x = float(a.keep * double(w.x) - a.step * double(bf16lo(o.x)));
+      w.y = float(a.keep * double(w.y) - a.step * double(bf16hi(o.x)));
+      w.z = float(a.keep * double(w.z) - a.step * double(bf16lo(o.y)));
+      w.w = float(a.keep * double(w.w) - a.step * double(bf16hi(o.y)));
+      reinterpret_cast<float4*>(a.w_out)[q] = w;
+    }
+    s += (fabs(double(w.x)) + fabs(double(w.y))) + (fabs(double(w.z)) + fabs(double(w.w)));
+  }
+  s = ss_block_sum(s, red);
+  if (threadIdx.x == 0) a.part[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(256) void sub_codes_kernel(SubStepArgs a, const float* w, int blocks) {
+  __shared__ double red[4];
+  double s = 0.0;
+  for (int p = threadIdx.x; p < blocks; p += 256) s += a.part[p];
+  const double mean = ss_block_sum(s, red) / double(a.n);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && a.scale) *a.scale = float(mean);
+  const size_t words = a.n / 16;
+  for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < words; i += size_t(gridDim.x) * 256) {
+    uint32_t code = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = reinterpret_cast<const float4*>(w)[4 * i + k];
+      const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 4 * k + j, bit = 16 * (c & 1) + (c >> 1);
+        // false for a NaN weight and for a NaN or infinite mean
+        if (2.0 * fabs(double(e[j])) > mean) code |= (e[j] < 0.f ? 0x101u : 0x1u) << bit;
+      }
+    }
+    a.packed[i] = code;
+  }
+}
+
+static int ss_blocks(size_t n) {
+  const size_t b = (n / 4 + 255) / 256;
+  return int(b < SS_BLOCKS ? b : SS_BLOCKS);
+}
+
+size_t sub_step_workspace(size_t n) { return size_t(ss_blocks(n)) * 8; }
+
+hipError_t launch_sub_step(const SubStepArgs& a, hipStream_t s) {
+  const int blocks = ss_blocks(a.n);
+  if (a.o) hipLaunchKernelGGL(sub_update_kernel<true>, dim3(unsigned(blocks)), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(sub_update_kernel<false>, dim3(unsigned(blocks)), dim3(256), 0, s, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const size_t cb = (a.n / 16 + 255) / 256;
+  hipLaunchKernelGGL(sub_codes_kernel, dim3(unsigned(cb < 1024 ? cb : 1024)), dim3(256), 0, s, a, a.o ? a.w_out : a.w,
+                     blocks);
+  return hipGetLastError();
+}
+
+}  // namespace bmoe

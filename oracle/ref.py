@@ -547,3 +547,67 @@ def substrate_weight_grad(U: np.ndarray, dZ: np.ndarray, alpha: float = 1.0) -> 
     (no clipping of the latent weights' gradient): the pages name the
     estimator and nothing more."""
     return alpha * (np.asarray(dZ, dtype=np.float64).T @ np.asarray(U, dtype=np.float64))
+
+
+# --------------------------------------------------------------------------- training step around the layer
+def layer_norm(s: np.ndarray, gamma=None, beta=None, eps: float = 1e-5):
+    """Row norm (include/bmoe_norm.h) of s [rows][width] in fp64: returns
+    (y, mean, rstd)."""
+    s = np.asarray(s, dtype=np.float64)
+    mean = s.mean(axis=1)
+    c = s - mean[:, None]
+    rstd = 1.0 / np.sqrt((c * c).mean(axis=1) + eps)
+    y = c * rstd[:, None]
+    if gamma is not None:
+        y = y * np.asarray(gamma, dtype=np.float64)
+    if beta is not None:
+        y = y + np.asarray(beta, dtype=np.float64)
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None):
+    """Gradients of sum(dy * y) (+ sum(d_sum * s)) in s, gamma and beta, fp64,
+    at the given mean and rstd."""
+    dy, s = np.asarray(dy, dtype=np.float64), np.asarray(s, dtype=np.float64)
+    mean, rstd = np.asarray(mean, dtype=np.float64)[:, None], np.asarray(rstd, dtype=np.float64)[:, None]
+    xhat = (s - mean) * rstd
+    v = dy if gamma is None else dy * np.asarray(gamma, dtype=np.float64)
+    dx = rstd * (v - v.mean(axis=1, keepdims=True) - xhat * (v * xhat).mean(axis=1, keepdims=True))
+    if d_sum is not None:
+        dx = dx + np.asarray(d_sum, dtype=np.float64)
+    return dx, (dy * xhat).sum(axis=0), dy.sum(axis=0)
+
+
+NS_COEFFS, NS_STEPS = (3.4445, -4.7750, 2.0315), 5
+
+
+def orthogonalize(grad, momentum=None, mu: float = 0.95, nesterov: bool = True):
+    """Momentum step and Newton-Schulz steps (include/bmoe_update.h) in fp64:
+    returns (o, momentum')."""
+    u = np.asarray(grad, dtype=np.float64)
+    m1 = None
+    if momentum is not None:
+        m1 = mu * np.asarray(momentum, dtype=np.float64) + u
+        u = u + mu * m1 if nesterov else m1
+    norm = np.linalg.norm(u)
+    x = u / norm if norm > 0 else u
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.T
+    a, b, c = NS_COEFFS
+    for _ in range(NS_STEPS):
+        g = x @ x.T
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return (x.T if tall else x), m1
+
+
+def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0):
+    """Latent substrate step and mean-magnitude ternary codes
+    (include/bmoe_update.h): returns (w' fp32, codes int8, scale fp64)."""
+    w = np.asarray(w, dtype=np.float32)
+    if o is not None:
+        w = ((1.0 - decay) * w.astype(np.float64) - step * np.asarray(o, dtype=np.float64)).astype(np.float32)
+    mag = np.abs(w.astype(np.float64))
+    scale = mag.sum() / mag.size
+    codes = np.where(2.0 * mag > scale, np.sign(w), 0.0).astype(np.int8)
+    return w, codes, scale

@@ -1,0 +1,283 @@
+"""Orthogonalised updates and the substrate step (include/bmoe_update.h) on the
+GPU against the fp64 oracle, and a whole training step of a normalised layer.
+
+Bars for the orthogonalised update, relative Frobenius norm.  A rounding to
+fp16 is off by at most 2^-11, 2^-12 in the mean square.  The map of one step
+stretches a change of a settled singular value by at most 4 and what lies
+outside the gradient's row space by a = 3.44.  About ten roundings (A, P, T, Q,
+X of the five steps) act on settled values: sqrt(10) * 4 * 2^-12 = 3.1e-3 for a
+gradient whose row space is full; the rounding of X_3 to one term grows
+a^2 = 11.8-fold outside a smaller row space and ||X_3|| / ||X_5|| is at most
+1.2 / 0.68: 11.8 * 1.8 * 2^-11 = 1.0e-2 more.  bf16 adds 2^-8 at most.  Bars:
+7e-3 (full rank), 1.7e-2 (any).
+"""
+import ctypes
+
+import numpy as np
+import pytest
+
+import compressed_mixture_experts_amd as bm
+from compressed_mixture_experts_amd import workloads as wl
+from oracle import ref
+from gpu_helpers import log, to_dev, to_f64
+
+pytestmark = pytest.mark.gpu
+FULL, ANY = 7e-3, 1.7e-2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    bm.lib()
+    yield
+
+
+def matrix(kind, rows, cols, seed):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    k = min(rows, cols)
+    if kind == "normal":
+        return n(rows, cols)
+    if kind == "rows":  # a sum over routed rows of unequal size
+        return (n(rows, 2 * k) * torch.exp(n(2 * k))) @ n(2 * k, cols) * 1e-3
+    if kind == "low":
+        return n(rows, max(1, k // 8)) @ n(max(1, k // 8), cols)
+    if kind == "one":
+        return n(rows, 1) @ n(1, cols)
+    if kind == "outliers":
+        m = n(rows, cols)
+        m[:, ::97] *= 50.0
+        return m
+    raise ValueError(kind)
+
+
+def rel(a, b):
+    return np.linalg.norm(a - b) / np.linalg.norm(b)
+
+
+ORTHO = [
+    # rows, cols: one element, one row and column, ragged, square, wide and tall, several tiles
+    (1, 1), (1, 300), (300, 1), (2, 3), (16, 16), (17, 129), (64, 64), (128, 128), (129, 127), (100, 260), (260, 100),
+    (256, 256), (255, 513), (512, 512), (384, 640), (640, 384), (300, 777), (1000, 250), (1024, 1024), (512, 2048),
+]
+
+
+@pytest.mark.parametrize("rows,cols", ORTHO)
+def test_orthogonalize_matches_oracle(rows, cols):
+    log(f"orthogonalize {rows} x {cols}")
+    for kind in ("rows", "normal"):
+        g = matrix(kind, rows, cols, rows * 7 + cols)
+        o, m = bm.orthogonalize(g.cuda())
+        assert m is None and o.shape == (rows, cols)
+        want, _ = ref.orthogonalize(g.double().numpy())
+        e = rel(to_f64(o), want)
+        log(f"  {kind}: {e:.2e}")
+        assert e <= FULL, (kind, e)
+
+
+@pytest.mark.parametrize("kind", ["low", "one", "outliers"])
+@pytest.mark.parametrize("rows,cols", [(256, 256), (300, 777), (1000, 250)])
+def test_orthogonalize_hard_spectra(rows, cols, kind):
+    g = matrix(kind, rows, cols, 21)
+    want, _ = ref.orthogonalize(g.double().numpy())
+    e = rel(to_f64(bm.orthogonalize(g.cuda())[0]), want)
+    log(f"orthogonalize {kind} {rows} x {cols}: {e:.2e}")
+    assert e <= (FULL if kind == "outliers" else ANY), e
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("nesterov", [False, True])
+@pytest.mark.parametrize("rows,cols", [(200, 328), (129, 67)])
+def test_orthogonalize_momentum(rows, cols, nesterov, dtype):
+    import torch
+    g = matrix("rows", rows, cols, 31)
+    if dtype == "bf16":
+        g = g.bfloat16()
+    m = matrix("normal", rows, cols, 32) * 0.1
+    gd, md = g.cuda(), m.cuda()
+    o, m1 = bm.orthogonalize(gd, md, mu=0.9, nesterov=nesterov)
+    want, wm = ref.orthogonalize(to_f64(g), to_f64(m), mu=float(np.float32(0.9)), nesterov=nesterov)
+    # one fused multiply-add
+    assert (np.abs(to_f64(m1) - wm) <= 2.0 ** -24 * np.abs(wm)).all() and rel(to_f64(o), want) <= FULL
+    # the momentum in place
+    o2, m2 = bm.orthogonalize(gd, md, mu=0.9, nesterov=nesterov, momentum_out=md)
+    assert m2 is md and (md == m1).all() and (o2 == o).all()
+
+
+def test_orthogonalize_scale_zero_and_non_finite():
+    import torch
+    g = matrix("rows", 192, 320, 41).cuda()
+    o = bm.orthogonalize(g)[0]
+    # a power of two changes only the norm, exactly; far ends of fp32 included
+    for k in (40, -60, 100):
+        assert (bm.orthogonalize(g * 2.0 ** k)[0] == o).all(), k
+    assert (bm.orthogonalize(torch.zeros_like(g))[0] == 0).all()
+    for bad in (float("nan"), float("inf")):
+        h = g.clone()
+        h[5, 7] = bad
+        assert torch.isnan(bm.orthogonalize(h)[0]).all()
+    # an error in an earlier call does not stay in anything later calls read
+    assert (bm.orthogonalize(g)[0] == o).all()
+
+
+def test_orthogonalize_singular_values():
+    import torch
+    o = bm.orthogonalize(matrix("normal", 384, 1200, 43).cuda())[0]
+    sv = torch.linalg.svdvals(o.double().cpu())
+    assert sv.max() < 1.21 and sv.min() > 0.66, (sv.min(), sv.max())
+
+
+def test_orthogonalize_tall_is_transposed_wide():
+    """Both orientations run the same products on the same padded matrices;
+    only the order of the norm's fp64 sum differs."""
+    g = matrix("rows", 333, 150, 44).cuda()
+    a, b = bm.orthogonalize(g)[0], bm.orthogonalize(g.T.contiguous())[0]
+    assert rel(to_f64(a), to_f64(b.T)) <= 2.0 ** -8
+
+
+def test_orthogonalize_unaligned_and_rows_behind():
+    import torch
+    g = matrix("rows", 70, 136, 45).cuda()
+    o = bm.orthogonalize(g)[0]
+    buf = torch.empty(g.numel() + 8, device="cuda")
+    v = buf[3:3 + g.numel()].view(g.shape)
+    v.copy_(g)
+    out = torch.full((72, 136), 5.0, dtype=torch.bfloat16, device="cuda")
+    off = torch.full((g.numel() + 8,), 5.0, dtype=torch.bfloat16, device="cuda")
+    bm.orthogonalize(v, out=off[1:1 + g.numel()].view(g.shape))
+    bm.orthogonalize(g, out=out[:70])
+    assert (out[70:] == 5.0).all() and (out[:70] == o).all()
+    assert (off[0] == 5.0) and (off[1 + g.numel():] == 5.0).all()
+    assert rel(to_f64(off[1:1 + g.numel()].view(g.shape)), to_f64(o)) <= 2.0 ** -8
+
+
+def test_orthogonalize_streams_and_graph():
+    """Two streams at once and two captured graphs, replayed in turn with eager
+    calls between, all equal to the eager result."""
+    import torch
+    gs = [matrix("rows", 256, 384, 51).cuda(), matrix("rows", 384, 256, 52).cuda()]
+    ms = [torch.randn_like(g) * 0.01 for g in gs]
+    want = [bm.orthogonalize(g, m) for g, m in zip(gs, ms)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(5):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k].append(bm.orthogonalize(gs[k], ms[k]))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all((o == want[k][0]).all() and (m == want[k][1]).all() for o, m in got[k])
+    graphs, outs, ins = [], [], [g.clone() for g in gs]
+    for k in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(bm.orthogonalize(ins[k], ms[k]))
+        graphs.append(graph)
+    for rep in range(3):
+        for k in range(2):
+            ins[k].copy_(gs[k] * (1 + 0.25 * rep) + rep * ms[k])
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        for k in range(2):
+            eager = bm.orthogonalize(ins[k], ms[k])
+            assert (outs[k][0] == eager[0]).all() and (outs[k][1] == eager[1]).all(), (rep, k)
+
+
+# ------------------------------------------------------------------ substrate step
+STEP = [(1, 16), (3, 16), (5, 48), (64, 64), (100, 1040), (512, 512), (1000, 2064), (2048, 1024), (16384, 16)]
+
+
+@pytest.mark.parametrize("rows,cols", STEP)
+@pytest.mark.parametrize("update", [False, True])
+def test_substrate_step_is_exact(rows, cols, update):
+    """W' is one rounding of an fp64 value, the codes a comparison of fp64 values:
+    both equal the oracle's bit for bit; scale is one rounding of a sum whose
+    order differs (fp64: below 2^-40 of it)."""
+    import torch
+    r = np.random.default_rng(rows + cols)
+    w = r.standard_normal((rows, cols)).astype(np.float32)
+    o = torch.from_numpy(r.standard_normal((rows, cols)).astype(np.float32)).bfloat16()
+    w1, packed, scale = bm.substrate_step(torch.from_numpy(w).cuda(), o.cuda() if update else None, step=0.03, decay=0.001)
+    ww, codes, ws = ref.substrate_step(w, to_f64(o) if update else None, step=0.03, decay=0.001)
+    assert (w1.cpu().numpy() == ww).all()
+    assert (packed.cpu().numpy().view(np.uint32) == bm.pack_ternary(codes)).all()
+    assert abs(float(scale) - ws) <= (2.0 ** -24 + 2.0 ** -40) * ws
+
+
+def test_substrate_step_ties_zero_and_non_finite():
+    import torch
+    tie = torch.tensor([[3.0] * 4 + [-3.0] * 4 + [1.0] * 4 + [-1.0] * 4])
+    _, packed, scale = bm.substrate_step(tie.cuda())
+    codes = np.array([[1] * 4 + [-1] * 4 + [0] * 8], np.int8)
+    assert float(scale) == 2.0 and (packed.cpu().numpy().view(np.uint32) == bm.pack_ternary(codes)).all()
+    _, packed, scale = bm.substrate_step(torch.zeros(4, 32, device="cuda"))
+    assert (packed == 0).all() and float(scale) == 0.0
+    for bad in (float("nan"), float("inf")):
+        w = torch.randn(8, 64, device="cuda")
+        w[2, 5] = bad
+        _, packed, scale = bm.substrate_step(w)
+        assert (packed == 0).all() and not np.isfinite(float(scale))
+
+
+def test_substrate_step_in_place_and_graph():
+    import torch
+    g = torch.Generator().manual_seed(61)
+    w0 = torch.randn(320, 256, generator=g).cuda()
+    o = torch.randn(320, 256, generator=g).bfloat16().cuda()
+    want = bm.substrate_step(w0, o, step=0.1, decay=0.01)
+    w, packed = w0.clone(), torch.empty(320, 16, dtype=torch.int32, device="cuda")
+    got = bm.substrate_step(w, o, step=0.1, decay=0.01, w_out=w, packed=packed)
+    assert got[0] is w and got[1] is packed and all((a == b).all() for a, b in zip(got, want))
+    w.copy_(w0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = bm.substrate_step(w, o, step=0.1, decay=0.01, w_out=w, packed=packed)
+    eager = w0
+    for k in range(4):
+        graph.replay()
+        torch.cuda.synchronize()
+        eager, p, s = bm.substrate_step(eager, o, step=0.1, decay=0.01)
+        assert (out[0] == eager).all() and (packed == p).all() and (out[2] == s).all(), k
+
+
+# ------------------------------------------------------------------ a training step
+@pytest.mark.parametrize("d_ff", [0, 256])
+def test_training_step_of_a_normalised_layer(d_ff):
+    """x -> s = x + residual -> norm -> layer -> gradients -> norm's backward ->
+    orthogonalised update of every substrate -> new codes in the layer's own
+    w_base -> next forward, each link against the oracle at the GPU's inputs."""
+    import torch
+    cfg = wl.small_config(d_model=128, d_ff=d_ff, n_experts=6, top_k=2, tokens=90, act="bf16", seed_index=700 + d_ff)
+    inp = wl.generate(cfg)
+    layer = bm.Layer.from_inputs(inp, device="cuda")
+    x = to_dev(inp.x, "bf16")
+    g = torch.Generator().manual_seed(71)
+    res = torch.randn(x.shape, generator=g).bfloat16().cuda()
+    gamma, beta = (1 + 0.1 * torch.randn(128, generator=g)).cuda(), (0.1 * torch.randn(128, generator=g)).cuda()
+    dy = torch.randn(x.shape, generator=g).bfloat16().cuda()
+    n, s, mean, rstd = bm.layer_norm_forward(x, gamma, beta, residual=res)
+    y, state = layer.forward_train(n)
+    grads = layer.backward(n, dy, state)
+    ds, dgamma, dbeta = bm.layer_norm_backward(grads["x"], s, gamma, mean, rstd, d_sum=dy)
+    wx, wg, wb = ref.layer_norm_backward(to_f64(grads["x"]), to_f64(s), to_f64(gamma), to_f64(mean), to_f64(rstd), to_f64(dy))
+    # bf16's half step per element and fp32 sums
+    assert rel(to_f64(ds), wx) <= 2.0 ** -8 and rel(to_f64(dgamma), wg) <= 1e-5 and rel(to_f64(dbeta), wb) <= 1e-5
+    codes = []
+    for m, latent in enumerate(inp.w_base):
+        w = torch.from_numpy(latent.astype(np.float32)).cuda() + 0.1 * torch.randn(latent.shape, generator=g).cuda()
+        mom = torch.zeros_like(w)
+        o, _ = bm.orthogonalize(grads["w_base"][m], mom, momentum_out=mom)
+        assert rel(to_f64(o), ref.orthogonalize(to_f64(grads["w_base"][m]), np.zeros(latent.shape))[0]) <= ANY
+        w0 = w.cpu().numpy()
+        bm.substrate_step(w, o, step=0.5, decay=0.01, w_out=w, packed=layer.w_base[m])
+        ww, cc, _ = ref.substrate_step(w0, to_f64(o), step=0.5, decay=0.01)
+        assert (w.cpu().numpy() == ww).all()
+        codes.append(cc)
+    assert any((c != b).any() for c, b in zip(codes, inp.w_base))
+    inp.w_base = codes
+    want = bm.Layer.from_inputs(inp, device="cuda").forward(n)
+    assert (layer.forward(n) == want).all()
