@@ -26,9 +26,11 @@
 // Layouts: every product is D[m][n] = sum_k A[m][k] B[n][k], both operands
 // with k contiguous.  A = X X^T reads X as XS [S][L]; X' = P X, taken as
 // X'^T = X^T P (P symmetric), reads X as XL [L][S].  A product's epilogue
-// writes its tile both ways.  S and L are padded to multiples of 128 with
-// zeros, which stay zero.
+// writes its tile both ways.  S and L are padded with zeros to whole tiles,
+// which stay zero.
 #include "common.hpp"
+
+#include <type_traits>
 
 namespace bmoe {
 
@@ -39,11 +41,7 @@ typedef __attribute__((address_space(3))) void ns_lds_t;
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr int NS_SUMS = 512;        // partial sums of squares
-constexpr int NS_T = 128;           // output tile
 constexpr int NS_K = 64;            // contraction step
-constexpr int NS_TILE = NS_T * NS_K;
-constexpr int NS_ST = NS_T + 4;     // row stride of the staged output tile (halves)
-constexpr int NS_LDS = 2 * 2 * NS_TILE * 2;
 
 // ------------------------------------------------------------------ momentum
 template <bool BF>
@@ -187,7 +185,7 @@ struct NsGemm {
   const _Float16* a;        // [M][K]
   const _Float16* a2;       // second term of the left operand, or null
   const _Float16* b;        // [N][K]
-  int32_t M, N, K;          // multiples of NS_T, NS_T and NS_K
+  int32_t M, N, K;          // multiples of the tile's sides and NS_K
   float alpha;              // D = alpha sum (+ beta C + diag on the diagonal)
   // NS_SYM: d [N][N]; c [N][N] or null
   const _Float16* c;
@@ -200,22 +198,34 @@ struct NsGemm {
   int32_t rows, cols;       // of out
 };
 
-// One workgroup of four waves per 128 x 128 tile of D, each wave 64 x 64 (4 x 4
-// MFMA blocks of 16 x 16 x 32).  Both operand tiles of a 64-deep step come
-// straight into LDS (16 bytes per lane), the next step's while this one's
-// products run, two buffers.  Chunk ch (16 bytes) of row r sits at ch ^ (r % 8)
-// of its row.
-template <int MODE>
-__global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p) {
-  extern __shared__ __attribute__((aligned(16))) _Float16 sm[];  // [2][A tile | B tile]
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// One workgroup per TM x TN tile of D, NW = WM x WN waves of one TM / WM x TN / WN
+// part each (MFMA blocks of 16 x 16 x 32).  Both operand tiles of a 64-deep step
+// come straight into LDS (16 bytes per lane), NBUF steps in a ring, so that
+// NBUF - 1 steps are on their way while one is used.  Chunk ch (16 bytes) of row
+// r sits at ch ^ (r % 8) of its row.
+//
+// A step is two 32-deep halves with a set of fragments in registers each: the
+// reads of the next half are issued among the products of the current one, and
+// the barrier that frees a ring place stands between the halves, where every
+// wave has products of its own to do on both sides.
+template <int MODE, int TM, int TN, int WM, int WN, int NBUF>
+__global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
+  constexpr int NW = WM * WN, NT = 64 * NW;
+  constexpr int PM = TM / WM, PN = TN / WN, IM = PM / 16, IN = PN / 16;
+  constexpr int STAGE = (TM + TN) * NS_K;        // halves of a ring place
+  constexpr int LPW = (TM + TN) / 8 / NW;        // loads per wave and step
+  constexpr int ST = TN + 4;                     // row stride of the staged tile (halves)
+  static_assert((TM + TN) / 8 % NW == 0 && PM % 16 == 0 && PN % 16 == 0, "whole loads and blocks per wave");
+  extern __shared__ __attribute__((aligned(16))) _Float16 sm[];  // [NBUF][TM rows of A | TN rows of B][64]
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int wm = wave & 1, wn = wave >> 1;
+  const int wm = wave % WM, wn = wave / WM;
   int tm, tn;
   {
     int t = xcd_remap(blockIdx.x, gridDim.x);
-    const int nt = p.N / NS_T;
+    const int nt = p.N / TN;
     if constexpr (MODE == NS_SYM) {
+      static_assert(MODE != NS_SYM || TM == TN, "mirrored tiles are square");
       tm = 0;
       while (t >= nt - tm) {
         t -= nt - tm;
@@ -227,81 +237,137 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p) {
       tn = t % nt;
     }
   }
-  const int m0 = tm * NS_T, n0 = tn * NS_T;
+  const int m0 = tm * TM, n0 = tn * TN;
   const int K = p.K, nk1 = K / NS_K, nk = p.a2 ? 2 * nk1 : nk1;
-  // loads of a step: 32 of 8 rows each, 8 per wave; waves 0 and 1 A, 2 and 3 B
-  const int lrow = 64 * (wave & 1) + (lane >> 3), lch = 8 * ((lane & 7) ^ (lane >> 3));
-  const bool isb = wave >= 2;
-  const size_t lbase = size_t((isb ? n0 : m0) + lrow) * K + lch;
+  // a load fills 8 rows of 64; this lane's place in it
+  const int loff = (lane >> 3) * K + 8 * ((lane & 7) ^ (lane >> 3));
+  // step kt (past the last one: the last one again, never read) into ring place `buf`
   auto load = [&](int kt, int buf) {
+    kt = min(kt, nk - 1);
     const bool second = kt >= nk1;
-    const _Float16* src = (isb ? p.b : second ? p.a2 : p.a) + lbase + (second ? kt - nk1 : kt) * NS_K;
-    _Float16* dst = sm + buf * 2 * NS_TILE + (isb ? NS_TILE : 0) + 64 * (wave & 1) * NS_K;
+    const _Float16* pa = (second ? p.a2 : p.a) + size_t(m0) * K + (second ? kt - nk1 : kt) * NS_K;
+    const _Float16* pb = p.b + size_t(n0) * K + (second ? kt - nk1 : kt) * NS_K;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + size_t(8 * j) * K), (ns_lds_t*)(dst + 8 * j * NS_K), 16, 0, 0);
-  };
-  f32x4_t acc[4][4];  // [n block][m block]
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  load(0, 0);
-  __syncthreads();
-  for (int kt = 0; kt < nk; ++kt) {
-    const int buf = kt & 1;
-    if (kt + 1 < nk) load(kt + 1, buf ^ 1);
-    const _Float16* A = sm + buf * 2 * NS_TILE + (64 * wm + l16) * NS_K;
-    const _Float16* B = sm + buf * 2 * NS_TILE + NS_TILE + (64 * wn + l16) * NS_K;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int ch = 8 * ((4 * s + g) ^ (l16 & 7));
-      f16x8_t fa[4], fb[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        fa[i] = *reinterpret_cast<const f16x8_t*>(A + 16 * i * NS_K + ch);
-        fb[i] = *reinterpret_cast<const f16x8_t*>(B + 16 * i * NS_K + ch);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[i], fa[j], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < LPW; ++j) {
+      const int q = wave * LPW + j;  // 8-row group
+      const _Float16* src = q < TM / 8 ? pa + size_t(8 * q) * K : pb + size_t(8 * (q - TM / 8)) * K;
+      __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + loff), (ns_lds_t*)(sm + buf * STAGE + 8 * q * NS_K), 16, 0, 0);
     }
-    __syncthreads();  // waits for this wave's loads, then for every wave
+  };
+  f32x4_t acc[IN][IM];
+#pragma unroll
+  for (int i = 0; i < IN; ++i)
+#pragma unroll
+    for (int j = 0; j < IM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  f16x8_t fa[2][IM], fb[2][IN];
+  auto read = [&](int buf, int h, f16x8_t (&a)[IM], f16x8_t (&b)[IN]) {
+    const int ch = 8 * ((4 * h + g) ^ (l16 & 7));
+    const _Float16* A = sm + buf * STAGE + (PM * wm + l16) * NS_K + ch;
+    const _Float16* B = sm + buf * STAGE + (TM + PN * wn + l16) * NS_K + ch;
+#pragma unroll
+    for (int j = 0; j < IM; ++j) a[j] = *reinterpret_cast<const f16x8_t*>(A + 16 * j * NS_K);
+#pragma unroll
+    for (int i = 0; i < IN; ++i) b[i] = *reinterpret_cast<const f16x8_t*>(B + 16 * i * NS_K);
+  };
+  auto mul = [&](const f16x8_t (&a)[IM], const f16x8_t (&b)[IN]) {
+#pragma unroll
+    for (int i = 0; i < IN; ++i)
+#pragma unroll
+      for (int j = 0; j < IM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[i], a[j], acc[i][j], 0, 0, 0);
+  };
+  // order of a region: `loads` global loads, then the reads, each behind one
+  // product, then the other products; nothing crosses the region's end
+  auto spread = [&](auto loads) {
+    constexpr int NL = decltype(loads)::value;
+#pragma unroll
+    for (int m = 0; m < NL; ++m) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    }
+#pragma unroll
+    for (int m = 0; m < IM + IN; ++m) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, IM * IN, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // this wave's reads are done and its loads of all but the newest `left` steps
+  // have arrived; then the same of every wave
+  auto arrive = [&]() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * LPW) : "memory");
+  };
+#pragma unroll
+  for (int b = 0; b < NBUF - 1; ++b) load(b, b);
+  arrive();
+  load(NBUF - 1, NBUF - 1);
+  read(0, 0, fa[0], fb[0]);
+  int buf = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+    const int next = buf + 1 == NBUF ? 0 : buf + 1;
+    read(buf, 1, fa[1], fb[1]);
+    mul(fa[0], fb[0]);
+    spread(std::integral_constant<int, 0>{});
+    arrive();
+    load(kt + NBUF, buf);
+    read(next, 0, fa[0], fb[0]);
+    mul(fa[1], fb[1]);
+    spread(std::integral_constant<int, LPW>{});
+    buf = next;
   }
-  // acc[i][j][r] = D[m0 + 64 wm + 16 j + l16][n0 + 64 wn + 16 i + 4 g + r]
-  _Float16* st = sm;  // [NS_T][NS_ST]
-  const int rows_m = 64 * wm + l16, cols_n = 64 * wn + 4 * g;
+  // loads past the last step may still be writing to the ring
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // acc[i][j][r] = D[m0 + PM wm + 16 j + l16][n0 + PN wn + 16 i + 4 g + r]
+  _Float16* st = sm;  // [TM][ST]
+  const int rows_m = PM * wm + l16, cols_n = PN * wn + 4 * g;
   auto staged = [&](auto&& f) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < IM; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<f16x4_t*>(st + (rows_m + 16 * j) * NS_ST + cols_n + 16 * i) = f(i, j);
+      for (int i = 0; i < IN; ++i)
+        *reinterpret_cast<f16x4_t*>(st + (rows_m + 16 * j) * ST + cols_n + 16 * i) = f(i, j);
     __syncthreads();
   };
-  // the staged tile to dst (row stride ld) as it is
-  auto direct = [&](_Float16* dst, size_t ld) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int r = 16 * q + (tid >> 4), c = 8 * (tid & 15);
-      const uint2 u = *reinterpret_cast<const uint2*>(st + r * NS_ST + c);
-      const uint2 v = *reinterpret_cast<const uint2*>(st + r * NS_ST + c + 4);
-      *reinterpret_cast<uint4*>(dst + size_t(r) * ld + c) = make_uint4(u.x, u.y, v.x, v.y);
-    }
+  constexpr int PIECES = TM * TN / 8 / NT;  // 16-byte pieces of the tile per thread
+  auto row8 = [&](int r, int c) {
+    const uint2 u = *reinterpret_cast<const uint2*>(st + r * ST + c);
+    const uint2 v = *reinterpret_cast<const uint2*>(st + r * ST + c + 4);
+    return make_uint4(u.x, u.y, v.x, v.y);
   };
   // column c of the staged tile, rows r .. r + 7
   auto column8 = [&](int c, int r) {
     f16x8_t v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = st[(r + e) * NS_ST + c];
-    return v;
+    for (int e = 0; e < 8; ++e) v[e] = st[(r + e) * ST + c];
+    return __builtin_bit_cast(uint4, v);
+  };
+  // piece q of this thread: (row, first column), and (column, first row) of the
+  // transposed tile, 128 contiguous bytes per 8 lanes
+  auto piece = [&](int q, int& r, int& c) {
+    const int k = tid + NT * q;
+    r = k / (TN / 8);
+    c = 8 * (k % (TN / 8));
+  };
+  auto tpiece = [&](int q, int& c, int& r) {
+    const int k = tid + NT * q;
+    c = (k >> 3) % TN;
+    r = 8 * ((k & 7) + 8 * ((k >> 3) / TN));
+  };
+  auto direct = [&](_Float16* dst, size_t ld) {
+#pragma unroll 4
+    for (int q = 0; q < PIECES; ++q) {
+      int r, c;
+      piece(q, r, c);
+      *reinterpret_cast<uint4*>(dst + size_t(r) * ld + c) = row8(r, c);
+    }
   };
   auto transposed = [&](_Float16* dst, size_t ld) {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int c = 32 * (q >> 1) + (tid >> 3), r = 8 * (tid & 7) + 64 * (q & 1);
-      *reinterpret_cast<f16x8_t*>(dst + size_t(c) * ld + r) = column8(c, r);
+#pragma unroll 4
+    for (int q = 0; q < PIECES; ++q) {
+      int r, c;
+      tpiece(q, c, r);
+      *reinterpret_cast<uint4*>(dst + size_t(c) * ld + r) = column8(c, r);
     }
   };
   if constexpr (MODE == NS_SYM) {
@@ -349,27 +415,24 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p) {
       return __builtin_bit_cast(f16x4_t, o);
     });
     const bool tall = p.rows > p.cols;
-    const size_t ld = p.cols;
     const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
+#pragma unroll 4
+    for (int q = 0; q < PIECES; ++q) {
       int r, c;  // of out
-      f16x8_t v;
+      uint4 u;
       if (tall) {
-        const int lr = 16 * q + (tid >> 4), lc = 8 * (tid & 15);
-        r = m0 + lr;
-        c = n0 + lc;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = st[lr * NS_ST + lc + e];
+        piece(q, r, c);
+        u = row8(r, c);
+        r += m0;
+        c += n0;
       } else {
-        const int lc = 32 * (q >> 1) + (tid >> 3), lr = 8 * (tid & 7) + 64 * (q & 1);
-        r = n0 + lc;
-        c = m0 + lr;
-        v = column8(lc, lr);
+        tpiece(q, r, c);
+        u = column8(r, c);
+        r += n0;
+        c += m0;
       }
       if (r >= p.rows || c >= p.cols) continue;
-      uint16_t* dst = p.out + size_t(r) * ld + c;
-      const uint4 u = __builtin_bit_cast(uint4, v);
+      uint16_t* dst = p.out + size_t(r) * p.cols + c;
       if (vec) {
         *reinterpret_cast<uint4*>(dst) = u;
       } else {
@@ -385,6 +448,12 @@ __global__ __launch_bounds__(256, 2) void ns_gemm_kernel(NsGemm p) {
 // ------------------------------------------------------------------ host
 namespace {
 
+// Padded side: whole tiles of the size its products use.
+int ns_pad(int n) {
+  const int q = n <= 512 ? 64 : n <= 1536 ? 128 : 256;
+  return (n + q - 1) / q * q;
+}
+
 struct NsPlan {
   size_t part, xs, xh[2], xl[2], A, T, P, Q, total;
   int S, L, Sp, Lp;
@@ -394,8 +463,8 @@ NsPlan ns_plan(int rows, int cols) {
   NsPlan q{};
   q.S = rows < cols ? rows : cols;
   q.L = rows < cols ? cols : rows;
-  q.Sp = (q.S + NS_T - 1) / NS_T * NS_T;
-  q.Lp = (q.L + NS_T - 1) / NS_T * NS_T;
+  q.Sp = ns_pad(q.S);
+  q.Lp = ns_pad(q.L);
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -417,12 +486,30 @@ NsPlan ns_plan(int rows, int cols) {
   return q;
 }
 
+template <int MODE, int T, int WM, int WN, int NBUF>
+hipError_t ns_tile(const NsGemm& p, hipStream_t s) {
+  const int nt = p.N / T;
+  const int tiles = MODE == NS_SYM ? nt * (nt + 1) / 2 : (p.M / T) * nt;
+  constexpr size_t ring = size_t(NBUF) * 2 * T * NS_K * 2, stage = size_t(T) * (T + 4) * 2;
+  constexpr size_t lds = ring > stage ? ring : stage;
+  const auto kernel = ns_gemm_kernel<MODE, T, T, WM, WN, NBUF>;
+  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles)), dim3(64 * WM * WN), lds, s, p);
+  return hipGetLastError();
+}
+
+// Tile of a product by its number of tiles.
 template <int MODE>
 hipError_t ns_go(const NsGemm& p, hipStream_t s) {
-  const int nt = p.N / NS_T;
-  const int tiles = MODE == NS_SYM ? nt * (nt + 1) / 2 : (p.M / NS_T) * nt;
-  hipLaunchKernelGGL(ns_gemm_kernel<MODE>, dim3(unsigned(tiles)), dim3(256), NS_LDS, s, p);
-  return hipGetLastError();
+  auto tiles = [&](int t) {
+    if (p.M % t || p.N % t) return 0;
+    return MODE == NS_SYM ? (p.N / t) * (p.N / t + 1) / 2 : (p.M / t) * (p.N / t);
+  };
+  if constexpr (MODE != NS_SYM)
+    if (tiles(256) >= 192) return ns_tile<MODE, 256, 2, 4, 2>(p, s);
+  if (tiles(128) >= 100) return ns_tile<MODE, 128, 2, 2, 4>(p, s);
+  return ns_tile<MODE, 64, 2, 2, 4>(p, s);
 }
 
 }  // namespace
