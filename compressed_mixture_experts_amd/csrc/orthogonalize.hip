@@ -26,8 +26,8 @@
 // Layouts: every product is D[m][n] = sum_k A[m][k] B[n][k], both operands
 // with k contiguous.  A = X X^T reads X as XS [S][L]; X' = P X, taken as
 // X'^T = X^T P (P symmetric), reads X as XL [L][S].  A product's epilogue
-// writes its tile both ways.  S and L are padded with zeros to whole tiles,
-// which stay zero.
+// writes its tile both ways.  S and L are padded to
+// multiples of 64 with zeros, which stay zero.
 #include "common.hpp"
 
 #include <type_traits>
@@ -185,7 +185,7 @@ struct NsGemm {
   const _Float16* a;        // [M][K]
   const _Float16* a2;       // second term of the left operand, or null
   const _Float16* b;        // [N][K]
-  int32_t M, N, K;          // multiples of the tile's sides and NS_K
+  int32_t M, N, K;          // multiples of NS_K
   float alpha;              // D = alpha sum (+ beta C + diag on the diagonal)
   // NS_SYM: d [N][N]; c [N][N] or null
   const _Float16* c;
@@ -218,13 +218,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   static_assert((TM + TN) / 8 % NW == 0 && PM % 16 == 0 && PN % 16 == 0, "whole loads and blocks per wave");
   extern __shared__ __attribute__((aligned(16))) _Float16 sm[];  // [NBUF][TM rows of A | TN rows of B][64]
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, g = lane >> 4;
+  const int l16 = lane & 15, g = lane >> 4;  // row of a block, 16-byte chunk of its depth
   const int wm = wave % WM, wn = wave / WM;
   int tm, tn;
   {
     int t = xcd_remap(blockIdx.x, gridDim.x);
-    const int nt = p.N / TN;
+    const int nt = (p.N + TN - 1) / TN;
     if constexpr (MODE == NS_SYM) {
+      // tiles on and above the diagonal, row by row
       static_assert(MODE != NS_SYM || TM == TN, "mirrored tiles are square");
       tm = 0;
       while (t >= nt - tm) {
@@ -245,12 +246,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   auto load = [&](int kt, int buf) {
     kt = min(kt, nk - 1);
     const bool second = kt >= nk1;
-    const _Float16* pa = (second ? p.a2 : p.a) + size_t(m0) * K + (second ? kt - nk1 : kt) * NS_K;
-    const _Float16* pb = p.b + size_t(n0) * K + (second ? kt - nk1 : kt) * NS_K;
+    const _Float16* pa = (second ? p.a2 : p.a) + (second ? kt - nk1 : kt) * NS_K;
+    const _Float16* pb = p.b + (second ? kt - nk1 : kt) * NS_K;
 #pragma unroll
     for (int j = 0; j < LPW; ++j) {
-      const int q = wave * LPW + j;  // 8-row group
-      const _Float16* src = q < TM / 8 ? pa + size_t(8 * q) * K : pb + size_t(8 * (q - TM / 8)) * K;
+      // 8-row group q; groups past the matrix (M and N are multiples of 8) read
+      // its last one and are not stored
+      const int q = wave * LPW + j;
+      const _Float16* src = q < TM / 8 ? pa + size_t(min(m0 + 8 * q, p.M - 8)) * K
+                                       : pb + size_t(min(n0 + 8 * q - TM, p.N - 8)) * K;
       __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + loff), (ns_lds_t*)(sm + buf * STAGE + 8 * q * NS_K), 16, 0, 0);
     }
   };
@@ -320,16 +324,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
 
   // acc[i][j][r] = D[m0 + PM wm + 16 j + l16][n0 + PN wn + 16 i + 4 g + r]
   _Float16* st = sm;  // [TM][ST]
-  const int rows_m = PM * wm + l16, cols_n = PN * wn + 4 * g;
+  // f(four sums of consecutive columns, row, first column) to the staged tile
   auto staged = [&](auto&& f) {
 #pragma unroll
     for (int j = 0; j < IM; ++j)
 #pragma unroll
-      for (int i = 0; i < IN; ++i)
-        *reinterpret_cast<f16x4_t*>(st + (rows_m + 16 * j) * ST + cols_n + 16 * i) = f(i, j);
+      for (int i = 0; i < IN; ++i) {
+        const int m = PM * wm + 16 * j + l16, n = PN * wn + 16 * i + 4 * g;
+        *reinterpret_cast<f16x4_t*>(st + m * ST + n) = f(acc[i][j], m, n);
+      }
     __syncthreads();
   };
-  constexpr int PIECES = TM * TN / 8 / NT;  // 16-byte pieces of the tile per thread
   auto row8 = [&](int r, int c) {
     const uint2 u = *reinterpret_cast<const uint2*>(st + r * ST + c);
     const uint2 v = *reinterpret_cast<const uint2*>(st + r * ST + c + 4);
@@ -342,42 +347,43 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     for (int e = 0; e < 8; ++e) v[e] = st[(r + e) * ST + c];
     return __builtin_bit_cast(uint4, v);
   };
-  // piece q of this thread: (row, first column), and (column, first row) of the
-  // transposed tile, 128 contiguous bytes per 8 lanes
-  auto piece = [&](int q, int& r, int& c) {
-    const int k = tid + NT * q;
-    r = k / (TN / 8);
-    c = 8 * (k % (TN / 8));
+  // f(row, first column) for every 16-byte piece of the tile inside M x N, and
+  // f(column, first row) for those of the transposed tile, RL of them (up to
+  // 192 contiguous bytes) per group of lanes
+  constexpr int PIECES = TM * TN / 8, RL = TM % 64 == 0 ? 8 : TM / 8;
+  auto pieces = [&](auto&& f) {
+#pragma unroll 4
+    for (int q = 0; q < (PIECES + NT - 1) / NT; ++q) {
+      const int k = tid + NT * q;
+      if (PIECES % NT != 0 && k >= PIECES) break;
+      const int r = k / (TN / 8), c = 8 * (k % (TN / 8));
+      if (m0 + r < p.M && n0 + c < p.N) f(r, c);
+    }
   };
-  auto tpiece = [&](int q, int& c, int& r) {
-    const int k = tid + NT * q;
-    c = (k >> 3) % TN;
-    r = 8 * ((k & 7) + 8 * ((k >> 3) / TN));
+  auto tpieces = [&](auto&& f) {
+#pragma unroll 4
+    for (int q = 0; q < (PIECES + NT - 1) / NT; ++q) {
+      const int k = tid + NT * q;
+      if (PIECES % NT != 0 && k >= PIECES) break;
+      const int c = k / RL % TN, r = 8 * (k % RL + RL * (k / RL / TN));
+      if (m0 + r < p.M && n0 + c < p.N) f(c, r);
+    }
   };
   auto direct = [&](_Float16* dst, size_t ld) {
-#pragma unroll 4
-    for (int q = 0; q < PIECES; ++q) {
-      int r, c;
-      piece(q, r, c);
-      *reinterpret_cast<uint4*>(dst + size_t(r) * ld + c) = row8(r, c);
-    }
+    pieces([&](int r, int c) { *reinterpret_cast<uint4*>(dst + size_t(r) * ld + c) = row8(r, c); });
   };
   auto transposed = [&](_Float16* dst, size_t ld) {
-#pragma unroll 4
-    for (int q = 0; q < PIECES; ++q) {
-      int r, c;
-      tpiece(q, c, r);
-      *reinterpret_cast<uint4*>(dst + size_t(c) * ld + r) = column8(c, r);
-    }
+    tpieces([&](int c, int r) { *reinterpret_cast<uint4*>(dst + size_t(c) * ld + r) = column8(c, r); });
   };
   if constexpr (MODE == NS_SYM) {
-    staged([&](int i, int j) {
-      const int m = m0 + rows_m + 16 * j, n = n0 + cols_n + 16 * i;
+    staged([&](f32x4_t a, int m, int n) {
+      m += m0;
+      n += n0;
       f16x4_t cv = {0, 0, 0, 0}, o;
-      if (p.c) cv = *reinterpret_cast<const f16x4_t*>(p.c + size_t(m) * p.N + n);
+      if (p.c && m < p.M && n < p.N) cv = *reinterpret_cast<const f16x4_t*>(p.c + size_t(m) * p.N + n);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float v = fmaf(p.alpha, acc[i][j][r], p.beta * float(cv[r]));
+        float v = fmaf(p.alpha, a[r], p.beta * float(cv[r]));
         if (m == n + r) v += p.diag;
         o[r] = _Float16(v);
       }
@@ -386,21 +392,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     direct(p.d + size_t(m0) * p.N + n0, p.N);
     if (tm != tn) transposed(p.d + size_t(n0) * p.N + m0, p.N);
   } else if constexpr (MODE == NS_PROD) {
-    staged([&](int i, int j) {
+    staged([&](f32x4_t a, int, int) {
       f16x4_t o;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = _Float16(p.alpha * acc[i][j][r]);
+      for (int r = 0; r < 4; ++r) o[r] = _Float16(p.alpha * a[r]);
       return o;
     });
     direct(p.d + size_t(m0) * p.N + n0, p.N);
     transposed(p.dt + size_t(n0) * p.M + m0, p.M);
     if (p.lo) {
       __syncthreads();
-      staged([&](int i, int j) {
+      staged([&](f32x4_t a, int, int) {
         f16x4_t o;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const float v = p.alpha * acc[i][j][r];
+          const float v = p.alpha * a[r];
           o[r] = _Float16(v - float(_Float16(v)));
         }
         return o;
@@ -408,30 +414,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
       direct(p.lo + size_t(m0) * p.N + n0, p.N);
     }
   } else {
-    staged([&](int i, int j) {
+    staged([&](f32x4_t a, int, int) {
       uint2 o;
-      o.x = pack_bf16x2(p.alpha * acc[i][j][0], p.alpha * acc[i][j][1]);
-      o.y = pack_bf16x2(p.alpha * acc[i][j][2], p.alpha * acc[i][j][3]);
+      o.x = pack_bf16x2(p.alpha * a[0], p.alpha * a[1]);
+      o.y = pack_bf16x2(p.alpha * a[2], p.alpha * a[3]);
       return __builtin_bit_cast(f16x4_t, o);
     });
-    const bool tall = p.rows > p.cols;
     const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
-#pragma unroll 4
-    for (int q = 0; q < PIECES; ++q) {
-      int r, c;  // of out
-      uint4 u;
-      if (tall) {
-        piece(q, r, c);
-        u = row8(r, c);
-        r += m0;
-        c += n0;
-      } else {
-        tpiece(q, r, c);
-        u = column8(r, c);
-        r += n0;
-        c += m0;
-      }
-      if (r >= p.rows || c >= p.cols) continue;
+    // eight columns of out from row r, column c on
+    auto put = [&](int r, int c, uint4 u) {
+      if (r >= p.rows || c >= p.cols) return;
       uint16_t* dst = p.out + size_t(r) * p.cols + c;
       if (vec) {
         *reinterpret_cast<uint4*>(dst) = u;
@@ -441,18 +433,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
         for (int e = 0; e < 8; ++e)
           if (c + e < p.cols) dst[e] = uint16_t(w[e >> 1] >> (16 * (e & 1)));
       }
-    }
+    };
+    if (p.rows > p.cols) pieces([&](int r, int c) { put(m0 + r, n0 + c, row8(r, c)); });
+    else tpieces([&](int c, int r) { put(n0 + c, m0 + r, column8(c, r)); });
   }
 }
 
 // ------------------------------------------------------------------ host
 namespace {
 
-// Padded side: whole tiles of the size its products use.
-int ns_pad(int n) {
-  const int q = n <= 512 ? 64 : n <= 1536 ? 128 : 256;
-  return (n + q - 1) / q * q;
-}
+// Padded side: whole contraction steps.
+int ns_pad(int n) { return (n + NS_K - 1) / NS_K * NS_K; }
 
 struct NsPlan {
   size_t part, xs, xh[2], xl[2], A, T, P, Q, total;
@@ -486,30 +477,52 @@ NsPlan ns_plan(int rows, int cols) {
   return q;
 }
 
+// Tiles of side t in a product's result.
+template <int MODE>
+int ns_tiles(const NsGemm& p, int t) {
+  const int nm = (p.M + t - 1) / t, nn = (p.N + t - 1) / t;
+  return MODE == NS_SYM ? nn * (nn + 1) / 2 : nm * nn;
+}
+
 template <int MODE, int T, int WM, int WN, int NBUF>
 hipError_t ns_tile(const NsGemm& p, hipStream_t s) {
-  const int nt = p.N / T;
-  const int tiles = MODE == NS_SYM ? nt * (nt + 1) / 2 : (p.M / T) * nt;
   constexpr size_t ring = size_t(NBUF) * 2 * T * NS_K * 2, stage = size_t(T) * (T + 4) * 2;
   constexpr size_t lds = ring > stage ? ring : stage;
   const auto kernel = ns_gemm_kernel<MODE, T, T, WM, WN, NBUF>;
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles)), dim3(64 * WM * WN), lds, s, p);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(ns_tiles<MODE>(p, T))), dim3(64 * WM * WN), lds, s, p);
   return hipGetLastError();
 }
 
-// Tile of a product by its number of tiles.
+// Time of a product in tiles of side t, per step of 64, in microseconds: a lone
+// tile's step takes `one` (latency and the CU's own limits), all tiles together
+// 256 t bytes each from L2 into LDS at 16 TB/s and 128 t^2 operations at 1.15
+// PFLOP/s (rates of whole products of 2048 x 8192 on this GPU).
+template <int MODE>
+double ns_cost(const NsGemm& p, int t, double one) {
+  const double n = ns_tiles<MODE>(p, t), a = n * t * 256 / 16e6, b = n * t * t * 128 / 1.15e9;
+  return a > b ? (a > one ? a : one) : (b > one ? b : one);
+}
+
+// Picks the tile with the least of those times.  Measured per product, symmetric
+// ones of side 512 / 1024 / 2048 with K = the side: tiles of 32 4.1 / 9.4 / 36
+// us, 64 5.5 / 7.2 / 22-24, 96 8.3 / 10.6 / 18.5, 128 11 / 14.4 / 22.5; general
+// ones of 512 x 512, 4096 x 1024, 8192 x 2048: 32 4.0 / 32 / 290, 64 4.7 / 19 /
+// 153, 128 8.6 / 15.9 / 86, 256 19.6 / 31 / 67.
 template <int MODE>
 hipError_t ns_go(const NsGemm& p, hipStream_t s) {
-  auto tiles = [&](int t) {
-    if (p.M % t || p.N % t) return 0;
-    return MODE == NS_SYM ? (p.N / t) * (p.N / t + 1) / 2 : (p.M / t) * (p.N / t);
-  };
-  if constexpr (MODE != NS_SYM)
-    if (tiles(256) >= 192) return ns_tile<MODE, 256, 2, 4, 2>(p, s);
-  if (tiles(128) >= 100) return ns_tile<MODE, 128, 2, 2, 4>(p, s);
-  return ns_tile<MODE, 64, 2, 2, 4>(p, s);
+  const double c32 = ns_cost<MODE>(p, 32, 0.14), c64 = ns_cost<MODE>(p, 64, 0.205), c128 = ns_cost<MODE>(p, 128, 0.41);
+  if (c32 < c64) return ns_tile<MODE, 32, 2, 2, 4>(p, s);
+  if constexpr (MODE == NS_SYM) {
+    const double c96 = ns_cost<MODE>(p, 96, 0.32);
+    if (c64 < c96) return ns_tile<MODE, 64, 2, 2, 4>(p, s);
+    if (c96 < c128) return ns_tile<MODE, 96, 2, 2, 4>(p, s);
+  } else {
+    if (c64 < c128) return ns_tile<MODE, 64, 2, 2, 4>(p, s);
+    if (ns_cost<MODE>(p, 256, 1.2) <= c128) return ns_tile<MODE, 256, 2, 4, 2>(p, s);
+  }
+  return ns_tile<MODE, 128, 2, 2, 3>(p, s);
 }
 
 }  // namespace
