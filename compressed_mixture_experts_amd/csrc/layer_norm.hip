@@ -61,8 +61,17 @@ __device__ __forceinline__ void ln_load(const void* p, size_t i, float* v) {
 
 template <int ACT, int GE>
 __device__ __forceinline__ void ln_store(void* p, size_t i, const float* v) {
-  if constexpr (GE == 8) {
-    store8<ACT>(p, i, v);
+  // results go past L2, which the rows to come need (streamed stores: 122 ->
+  // 119 us at 32768 x 2048 bf16, 12.9 -> 11.7 us at 8192 x 1024; streamed loads
+  // lose where the producer left its rows in the last-level cache: 15.7 us)
+  typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+  if constexpr (GE == 8 && ACT == ACT_BF16) {
+    const u32x4_t u = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    __builtin_nontemporal_store(u, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i));
+  } else if constexpr (GE == 8) {
+    f32x4_t* q = reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + i);
+    __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, q);
+    __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, q + 1);
   } else if constexpr (GE == 2 && ACT == ACT_BF16) {
     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + i) = pack_bf16x2(v[0], v[1]);
   } else if constexpr (GE == 2) {
@@ -83,8 +92,16 @@ __device__ __forceinline__ void ln_round(float* v) {
   }
 }
 
+// Waves per SIMD that the kernels' registers leave room for: the row itself, and
+// per column gamma and beta (forward) or gamma and two sums (backward).  A grid of
+// exactly the workgroups that run at a time loses no partial last round: 32768 x
+// 2048 forward 111 us with 3 per CU (as many as fit), 146 with 4, 122 with 8 and
+// 125 with one per 4 rows.
+constexpr int ln_fwd_waves(int ge, int nv) { return ge * nv >= 32 ? 3 : ge * nv >= 16 ? (ge == 8 ? 5 : 4) : 8; }
+constexpr int ln_threads(int tpr) { return tpr > 256 ? tpr : 256; }
+
 template <int ACT, int GE, int TPR, int NV>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(LnFwdArgs a) {
+__global__ __launch_bounds__(ln_threads(TPR), TPR > 512 ? 4 : ln_fwd_waves(GE, NV)) void ln_fwd_kernel(LnFwdArgs a) {
   constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;  // rows per workgroup
   __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
@@ -168,7 +185,7 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_fwd_kernel(LnFwdArgs
 // rows of its workgroup; at the end the workgroup adds its waves' sums in
 // order (through LDS) and writes one partial row [dgamma | dbeta].
 template <int ACT, int DACT, int GE, int TPR, int NV>
-__global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_kernel(LnBwdArgs a) {
+__global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
   constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;
   __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
   __shared__ float cols[RPW > 1 ? RPW : 1][RPW > 1 ? TPR * NV * GE : 1];
@@ -265,25 +282,33 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_kernel(LnBwdArgs
   }
 }
 
-// Column sums of the P partial rows, in order: 64 columns per workgroup, 16
-// waves with a contiguous range of the rows each, their sums added in order.
+// Column sums of the P partial rows: 16 columns per workgroup, 64 groups of
+// lanes that take the rows p, p + 64, ... each, their sums added in order (8 rows
+// per thread at 512 partial rows, all loads in flight at once).
 __global__ __launch_bounds__(1024) void ln_colsum_kernel(const float* part, float* dgamma, float* dbeta, int P,
                                                          int width) {
-  __shared__ float sm[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane, n = 2 * width;
-  const int per = (P + 15) / 16, p1 = min(P, (wave + 1) * per);
+  __shared__ float sm[64][17];
+  const int col = threadIdx.x & 15, grp = threadIdx.x >> 4;
+  const int c = blockIdx.x * 16 + col, n = 2 * width;
   float s = 0.f;
   if (c < n) {
 #pragma unroll 8
-    for (int p = wave * per; p < p1; ++p) s += part[size_t(p) * n + c];
+    for (int p = grp; p < P; p += 64) s += part[size_t(p) * n + c];
   }
-  sm[wave][lane] = s;
+  sm[grp][col] = s;
   __syncthreads();
-  if (wave == 0 && c < n) {
+  if (threadIdx.x < 128) {  // eight sums of eight groups, then those
+    const int k = threadIdx.x >> 4;
     s = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) s += sm[w][lane];
+    for (int w = 0; w < 8; ++w) s += sm[8 * k + w][col];
+    sm[8 * k][col] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < 16 && c < n) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sm[8 * w][col];
     if (c < width) dgamma[c] = s;
     else dbeta[c - width] = s;
   }
@@ -303,14 +328,14 @@ LnShape ln_shape(int ge, int groups) {
     if (groups <= 128) return {64, 2};
     if (groups <= 256) return {64, 4};
     if (groups <= 512) return {256, 2};
-    if (groups <= 1024) return {256, 4};
-    return {512, 4};
+    if (groups <= 1024) return {512, 2};
+    return {1024, 2};
   }
   if (ge == 2) {
     if (groups <= 128) return {64, 2};
     if (groups <= 512) return {64, 8};
     if (groups <= 2048) return {256, 8};
-    return {512, 16};
+    return {1024, 8};
   }
   if (groups <= 256) return {64, 4};
   if (groups <= 1024) return {64, 16};
@@ -320,33 +345,35 @@ LnShape ln_shape(int ge, int groups) {
 
 int ln_group(int width, bool v16, bool pair) { return width % 8 == 0 && v16 ? 8 : width % 2 == 0 && pair ? 2 : 1; }
 
+constexpr int LN_CUS = 256;  // of a whole MI355X
+
 template <int ACT, int GE, int TPR, int NV>
 hipError_t fwd_go(const LnFwdArgs& a, hipStream_t s) {
-  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;
+  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR, waves = TPR > 512 ? 4 : ln_fwd_waves(GE, NV);
+  constexpr int most = LN_CUS * (waves * 256 / ln_threads(TPR));
   const int blocks = (a.rows + RPW - 1) / RPW;
-  hipLaunchKernelGGL((ln_fwd_kernel<ACT, GE, TPR, NV>), dim3(unsigned(blocks < 2048 ? blocks : 2048)),
-                     dim3(TPR > 256 ? TPR : 256), 0, s, a);
+  hipLaunchKernelGGL((ln_fwd_kernel<ACT, GE, TPR, NV>), dim3(unsigned(blocks < most ? blocks : most)),
+                     dim3(ln_threads(TPR)), 0, s, a);
   return hipGetLastError();
 }
 
 template <int ACT, int DACT, int GE, int TPR, int NV>
 hipError_t bwd_go(const LnBwdArgs& a, int blocks, hipStream_t s) {
-  hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV>), dim3(unsigned(blocks)), dim3(TPR > 256 ? TPR : 256), 0, s,
-                     a);
+  hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV>), dim3(unsigned(blocks)), dim3(ln_threads(TPR)), 0, s, a);
   return hipGetLastError();
 }
 
 #define LN_SHAPES(GO)                          \
   if (ge == 8) {                               \
-    if (sh.tpr == 512) return GO(8, 512, 4);   \
-    if (sh.tpr == 256 && sh.nv == 4) return GO(8, 256, 4); \
+    if (sh.tpr == 1024) return GO(8, 1024, 2); \
+    if (sh.tpr == 512) return GO(8, 512, 2);   \
     if (sh.tpr == 256) return GO(8, 256, 2);   \
     if (sh.nv == 4) return GO(8, 64, 4);       \
     if (sh.nv == 2) return GO(8, 64, 2);       \
     return GO(8, 64, 1);                       \
   }                                            \
   if (ge == 2) {                               \
-    if (sh.tpr == 512) return GO(2, 512, 16);  \
+    if (sh.tpr == 1024) return GO(2, 1024, 8); \
     if (sh.tpr == 256) return GO(2, 256, 8);   \
     if (sh.nv == 8) return GO(2, 64, 8);       \
     return GO(2, 64, 2);                       \
@@ -375,8 +402,10 @@ hipError_t bwd_act(const LnBwdArgs& a, int ge, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups of the backward, one partial row each: enough to fill the GPU,
-// no more than there are groups of 4 rows.
+// Workgroups of the backward, one partial row each: what runs at a time (two
+// per CU with the sums of a whole row of 2048 in registers; 32768 x 2048 136 us
+// with 512, 163 with 768, 143 with 1024), no more than there are groups of 4
+// rows.
 int ln_bwd_blocks(int rows, int width) {
   const int need = (rows + 3) / 4;
   return need < 512 ? need : 512;
@@ -409,7 +438,7 @@ hipError_t launch_ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, int ac
     if (e != hipSuccess) return e;
   }
   if (!dgamma) return hipSuccess;
-  hipLaunchKernelGGL(ln_colsum_kernel, dim3(unsigned((2 * a.width + 63) / 64)), dim3(1024), 0, s, a.part, dgamma, dbeta,
+  hipLaunchKernelGGL(ln_colsum_kernel, dim3(unsigned((2 * a.width + 15) / 16)), dim3(1024), 0, s, a.part, dgamma, dbeta,
                      ln_bwd_blocks(a.rows, a.width), a.width);
   return hipGetLastError();
 }

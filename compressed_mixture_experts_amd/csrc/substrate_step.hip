@@ -53,25 +53,45 @@ __global__ __launch_bounds__(256) void sub_update_kernel(SubStepArgs a) {
 
 __global__ __launch_bounds__(256) void sub_codes_kernel(SubStepArgs a, const float* w, int blocks) {
   __shared__ double red[4];
+  // a wave takes 1024 weights at a time, four loads of 1 KiB; four lanes hold the
+  // 16 columns of a word between them, and lane l keeps the word of load l % 4
+  const int lane = threadIdx.x & 63;
+  const size_t words = a.n / 16, step = size_t(gridDim.x) * 256;
+  size_t w0 = size_t(blockIdx.x) * 256 + (threadIdx.x & ~63u);
+  float4 v[4];
+  auto load = [&]() {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const size_t quad = 4 * w0 + 64 * k + lane;
+      v[k] = quad < 4 * words ? reinterpret_cast<const float4*>(w)[quad] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  load();  // on their way while the partial sums are added
   double s = 0.0;
   for (int p = threadIdx.x; p < blocks; p += 256) s += a.part[p];
   const double mean = ss_block_sum(s, red) / double(a.n);
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.scale) *a.scale = float(mean);
-  const size_t words = a.n / 16;
-  for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < words; i += size_t(gridDim.x) * 256) {
-    uint32_t code = 0;
+  while (w0 < words) {
+    uint32_t keep = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float4 v = reinterpret_cast<const float4*>(w)[4 * i + k];
-      const float e[4] = {v.x, v.y, v.z, v.w};
+      const float e[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      uint32_t code = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int c = 4 * k + j, bit = 16 * (c & 1) + (c >> 1);
+        // column c = 4 (lane % 4) + j: bit 16 (c % 2) + c / 2, the sign 8 above;
         // false for a NaN weight and for a NaN or infinite mean
-        if (2.0 * fabs(double(e[j])) > mean) code |= (e[j] < 0.f ? 0x101u : 0x1u) << bit;
+        if (2.0 * fabs(double(e[j])) > mean) code |= (e[j] < 0.f ? 0x101u : 0x1u) << (16 * (j & 1) + (j >> 1));
       }
+      code <<= 2 * (lane & 3);
+      code |= __shfl_xor(code, 1);
+      code |= __shfl_xor(code, 2);
+      if ((lane & 3) == k) keep = code;
     }
-    a.packed[i] = code;
+    const size_t word = w0 + 16 * (lane & 3) + (lane >> 2);
+    if (word < words) a.packed[word] = keep;
+    w0 += step;
+    load();
   }
 }
 
@@ -89,7 +109,7 @@ hipError_t launch_sub_step(const SubStepArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const size_t cb = (a.n / 16 + 255) / 256;
-  hipLaunchKernelGGL(sub_codes_kernel, dim3(unsigned(cb < 1024 ? cb : 1024)), dim3(256), 0, s, a, a.o ? a.w_out : a.w,
+  hipLaunchKernelGGL(sub_codes_kernel, dim3(unsigned(cb < 2048 ? cb : 2048)), dim3(256), 0, s, a, a.o ? a.w_out : a.w,
                      blocks);
   return hipGetLastError();
 }
