@@ -12,7 +12,7 @@
 // have, and a step multiplies what is small by a = 3.44: noise of X_0 grows
 // 485-fold, that of X_2 41-fold.  A rounding of A, T, P or Q only bends P,
 // which multiplies X from the left and adds no direction to its rows.  So X_0
-// and X_2, where it matters most, are kept as hi + lo (two fp16 terms, 22
+// and X_2, where it matters most, are kept as hi + lo (two fp16 terms, 17
 // bits) in the products P X, and the first two steps are taken together,
 //     A_1 = P_0 A_0 P_0 = P_0 T,   Q = P_1 P_0,   X_2 = Q X_0,
 // (everything in A is a polynomial of A_0: the factors commute and stay
@@ -30,6 +30,8 @@
 // multiples of 64 with zeros, which stay zero.
 #include "common.hpp"
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 namespace bmoe {
@@ -42,6 +44,15 @@ typedef __attribute__((address_space(3))) void ns_lds_t;
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr int NS_SUMS = 512;        // partial sums of squares
 constexpr int NS_K = 64;            // contraction step
+
+// The second term of v = hi + lo with 5 significant bits: hi has 11 and lo starts
+// one below: 17 bits, whose noise stays below that of X_3, and products of numbers whose last bits are
+// zero take less of the power that bounds the large products' clock (785 -> 770
+// us at 2048 x 8192; 764 with lo = 0).
+__device__ __forceinline__ _Float16 ns_lo(float v, _Float16 hi) {
+  const uint16_t b = __builtin_bit_cast(uint16_t, _Float16(v - float(hi)));
+  return __builtin_bit_cast(_Float16, uint16_t((b + 0x20u) & 0xFFC0u));
+}
 
 // ------------------------------------------------------------------ momentum
 template <bool BF>
@@ -145,7 +156,7 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
         v = float(double(a.m ? ns_u(g, a.m_out[at], a.mu, a.nesterov) : g) * scale);
       }
       hi[j] = _Float16(v);
-      lo[j] = _Float16(v - float(hi[j]));
+      lo[j] = ns_lo(v, hi[j]);
     }
     *reinterpret_cast<f16x4_t*>(&th[lr][lc]) = hi;
     *reinterpret_cast<f16x4_t*>(&tl[lr][lc]) = lo;
@@ -188,6 +199,7 @@ struct NsGemm {
   int32_t M, N, K;          // multiples of NS_K
   float alpha;              // D = alpha sum (+ beta C + diag on the diagonal)
   // NS_SYM: d [N][N]; c [N][N] or null
+  int32_t band;             // tile rows of a band of tiles
   const _Float16* c;
   float beta, diag;
   _Float16* d;              // NS_SYM; NS_PROD: D's hi [M][N]
@@ -208,7 +220,7 @@ struct NsGemm {
 // reads of the next half are issued among the products of the current one, and
 // the barrier that frees a ring place stands between the halves, where every
 // wave has products of its own to do on both sides.
-template <int MODE, int TM, int TN, int WM, int WN, int NBUF>
+template <int MODE, int TM, int TN, int WM, int WN, int NBUF, bool EARLY>
 __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   constexpr int NW = WM * WN, NT = 64 * NW;
   constexpr int PM = TM / WM, PN = TN / WN, IM = PM / 16, IN = PN / 16;
@@ -225,14 +237,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     int t = xcd_remap(blockIdx.x, gridDim.x);
     const int nt = (p.N + TN - 1) / TN;
     if constexpr (MODE == NS_SYM) {
-      // tiles on and above the diagonal, row by row
+      // tiles on and above the diagonal, by bands of p.band tile rows, column by
+      // column within a band: the tiles an XCD runs at a time form a block that
+      // needs few row blocks of the operand in its L2
       static_assert(MODE != NS_SYM || TM == TN, "mirrored tiles are square");
-      tm = 0;
-      while (t >= nt - tm) {
-        t -= nt - tm;
-        ++tm;
+      const int h = p.band;
+      int r0 = 0;
+      for (;; r0 += h) {
+        const int hh = min(h, nt - r0), band = hh * (nt - r0) - hh * (hh - 1) / 2;
+        if (t < band) break;
+        t -= band;
       }
-      tn = tm + t;
+      tn = r0;
+      for (int n = 1; t >= n; n = min(h, tn - r0 + 1)) {
+        t -= n;
+        ++tn;
+      }
+      tm = r0 + t;
     } else {
       tm = t / nt;
       tn = t % nt;
@@ -240,23 +261,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   }
   const int m0 = tm * TM, n0 = tn * TN;
   const int K = p.K, nk1 = K / NS_K, nk = p.a2 ? 2 * nk1 : nk1;
-  // a load fills 8 rows of 64; this lane's place in it
-  const int loff = (lane >> 3) * K + 8 * ((lane & 7) ^ (lane >> 3));
-  // step kt (past the last one: the last one again, never read) into ring place `buf`
+  // a load fills 8 rows of 64; a wave's loads are all of A or all of B.  Byte
+  // offsets of this lane's pieces in it; 8-row groups past the matrix (M and N
+  // are multiples of 8) read its last one and are not stored
+  static_assert(TM / 8 % LPW == 0, "no wave loads both operands");
+  const bool isb = wave * LPW >= TM / 8;
+  uint32_t off[LPW];
+#pragma unroll
+  for (int j = 0; j < LPW; ++j) {
+    const int q = wave * LPW + j;
+    const int row = (isb ? min(n0 + 8 * q - TM, p.N - 8) : min(m0 + 8 * q, p.M - 8)) + (lane >> 3);
+    off[j] = 2u * (uint32_t(row) * uint32_t(K) + 8u * ((lane & 7) ^ (lane >> 3)));
+  }
+  // this wave's loads of step kt (past the last one: the last one again, never
+  // read) into ring place `buf`
   auto load = [&](int kt, int buf) {
     kt = min(kt, nk - 1);
-    const bool second = kt >= nk1;
-    const _Float16* pa = (second ? p.a2 : p.a) + (second ? kt - nk1 : kt) * NS_K;
-    const _Float16* pb = p.b + (second ? kt - nk1 : kt) * NS_K;
+    const char* src = reinterpret_cast<const char*>(isb ? p.b : kt >= nk1 ? p.a2 : p.a) +
+                      size_t(kt >= nk1 ? kt - nk1 : kt) * (2 * NS_K);
+    _Float16* dst = sm + buf * STAGE + wave * LPW * 8 * NS_K;
 #pragma unroll
-    for (int j = 0; j < LPW; ++j) {
-      // 8-row group q; groups past the matrix (M and N are multiples of 8) read
-      // its last one and are not stored
-      const int q = wave * LPW + j;
-      const _Float16* src = q < TM / 8 ? pa + size_t(min(m0 + 8 * q, p.M - 8)) * K
-                                       : pb + size_t(min(n0 + 8 * q - TM, p.N - 8)) * K;
-      __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + loff), (ns_lds_t*)(sm + buf * STAGE + 8 * q * NS_K), 16, 0, 0);
-    }
+    for (int j = 0; j < LPW; ++j)
+      __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + off[j]), (ns_lds_t*)(dst + 8 * j * NS_K), 16, 0, 0);
   };
   f32x4_t acc[IN][IM];
 #pragma unroll
@@ -279,19 +305,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
 #pragma unroll
       for (int j = 0; j < IM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b[i], a[j], acc[i][j], 0, 0, 0);
   };
-  // order of a region: `loads` global loads, then the reads, each behind one
-  // product, then the other products; nothing crosses the region's end
+  // order of a region with NL loads: a read behind each of the first products, the
+  // loads evenly among the others; nothing crosses the region's end
   auto spread = [&](auto loads) {
-    constexpr int NL = decltype(loads)::value;
-#pragma unroll
-    for (int m = 0; m < NL; ++m) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-    }
+    constexpr int NL = decltype(loads)::value, REST = IM * IN - IM - IN;
+    constexpr int GAP = NL > 0 && REST / NL > 0 ? REST / NL : 1;
 #pragma unroll
     for (int m = 0; m < IM + IN; ++m) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+#pragma unroll
+    for (int m = 0; m < NL; ++m) {
+      __builtin_amdgcn_sched_group_barrier(0x008, GAP, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
     __builtin_amdgcn_sched_group_barrier(0x008, IM * IN, 0);
     __builtin_amdgcn_sched_barrier(0);
@@ -313,8 +340,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     mul(fa[0], fb[0]);
     spread(std::integral_constant<int, 0>{});
     arrive();
-    load(kt + NBUF, buf);
+    // the loads among the products behind the reads: a burst of them before the
+    // reads holds its wave up (tile 256: 131 -> 123 us for X = Q X_0 at 2048 x
+    // 8192); with few products to a step (EARLY) they go first, to arrive sooner
+    if constexpr (EARLY) load(kt + NBUF, buf);
     read(next, 0, fa[0], fb[0]);
+    if constexpr (!EARLY) load(kt + NBUF, buf);
     mul(fa[1], fb[1]);
     spread(std::integral_constant<int, LPW>{});
     buf = next;
@@ -407,7 +438,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float v = p.alpha * a[r];
-          o[r] = _Float16(v - float(_Float16(v)));
+          o[r] = ns_lo(v, _Float16(v));
         }
         return o;
       });
@@ -485,13 +516,16 @@ int ns_tiles(const NsGemm& p, int t) {
 }
 
 template <int MODE, int T, int WM, int WN, int NBUF>
-hipError_t ns_tile(const NsGemm& p, hipStream_t s) {
+hipError_t ns_tile(NsGemm p, hipStream_t s) {
   constexpr size_t ring = size_t(NBUF) * 2 * T * NS_K * 2, stage = size_t(T) * (T + 4) * 2;
   constexpr size_t lds = ring > stage ? ring : stage;
-  const auto kernel = ns_gemm_kernel<MODE, T, T, WM, WN, NBUF>;
+  const auto kernel = ns_gemm_kernel<MODE, T, T, WM, WN, NBUF, T <= 64>;
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3(unsigned(ns_tiles<MODE>(p, T))), dim3(64 * WM * WN), lds, s, p);
+  const int tiles = ns_tiles<MODE>(p, T);
+  // as high as the block of tiles of one of the eight XCDs is wide
+  if (MODE == NS_SYM) p.band = std::max(1, int(std::lround(std::sqrt(tiles / 8.0))));
+  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles)), dim3(64 * WM * WN), lds, s, p);
   return hipGetLastError();
 }
 
@@ -506,10 +540,10 @@ double ns_cost(const NsGemm& p, int t, double one) {
 }
 
 // Picks the tile with the least of those times.  Measured per product, symmetric
-// ones of side 512 / 1024 / 2048 with K = the side: tiles of 32 4.1 / 9.4 / 36
-// us, 64 5.5 / 7.2 / 22-24, 96 8.3 / 10.6 / 18.5, 128 11 / 14.4 / 22.5; general
-// ones of 512 x 512, 4096 x 1024, 8192 x 2048: 32 4.0 / 32 / 290, 64 4.7 / 19 /
-// 153, 128 8.6 / 15.9 / 86, 256 19.6 / 31 / 67.
+// ones of side 512 / 1024 / 2048 with K = the side: tiles of 32 4.1 / 8.8 / 36
+// us, 64 5.6 / 7.2 / 23.6, 96 8.9 / 10.2 / 18.2, 128 11 / 12.0 / 20.4; general
+// ones of 512 x 512, 4096 x 1024, 8192 x 2048: 32 3.7 / 30 / 289, 64 4.5 / 18.4 /
+// 152, 128 8 / 14.0 / 83, 256 18.2 / 27.3 / 66.
 template <int MODE>
 hipError_t ns_go(const NsGemm& p, hipStream_t s) {
   const double c32 = ns_cost<MODE>(p, 32, 0.14), c64 = ns_cost<MODE>(p, 64, 0.205), c128 = ns_cost<MODE>(p, 128, 0.41);
@@ -522,7 +556,7 @@ hipError_t ns_go(const NsGemm& p, hipStream_t s) {
     if (c64 < c128) return ns_tile<MODE, 64, 2, 2, 4>(p, s);
     if (ns_cost<MODE>(p, 256, 1.2) <= c128) return ns_tile<MODE, 256, 2, 4, 2>(p, s);
   }
-  return ns_tile<MODE, 128, 2, 2, 3>(p, s);
+  return ns_tile<MODE, 128, 2, 4, 3>(p, s);
 }
 
 }  // namespace
