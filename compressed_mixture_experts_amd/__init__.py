@@ -416,6 +416,20 @@ class Layer:
                                          int(state.numel()), ctypes.byref(g), _ptr(ws), nw, _stream_handle()))
         return out
 
+    def step_substrate(self, m: int, w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None):
+        """substrate_step of latent substrate m ([d_out][d_in] fp32) with the
+        codes written into this layer; weights prepared before are prepared
+        again.  Returns (W', scale)."""
+        if not 0 <= m < len(self.w_base):
+            raise ValueError(f"the layer has no substrate {m}")
+        d_out, d_in = 1 << int(self.phi[m].shape[1]), 1 << int(self.theta[m].shape[1])
+        if tuple(w.shape) != (d_out, d_in):
+            raise ValueError(f"w has shape {tuple(w.shape)}, substrate {m} is {(d_out, d_in)}")
+        w, _, scale = substrate_step(w, o, step, decay, w_out=w_out, packed=self.w_base[m])
+        if self._prep is not None:
+            self.prepare()
+        return w, scale
+
     def kernel_names(self) -> List[str]:
         """Names of the kernel launches of one forward, in order."""
         n = ctypes.c_int32(0)
@@ -681,8 +695,8 @@ def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None,
     """Latent substrate step W' = (1 - decay) W - step O (W [rows][cols] fp32, O
     bf16; W' = W without O) and its ternary codes at threshold mean |W'| / 2.
     Returns (W', packed [rows][cols / 16] int32 in pack_ternary's format,
-    scale: 0-d fp32 tensor mean |W'|).  w_out may be w itself; packed may be a
-    layer's w_base tensor (call Layer.prepare again afterwards where used)."""
+    scale: 0-d fp32 tensor mean |W'|).  w_out may be w itself (Layer.step_substrate
+    writes the codes into a layer)."""
     torch = _torch()
     dev = w.device
     rows, cols = w.shape

@@ -55,41 +55,35 @@ __device__ __forceinline__ _Float16 ns_lo(float v, _Float16 hi) {
 }
 
 // ------------------------------------------------------------------ momentum
-template <bool BF>
-__device__ __forceinline__ float ns_grad(const void* g, size_t i) {
-  return load1<BF ? ACT_BF16 : ACT_F32>(g, i);
-}
-
 // U's element from the gradient and the momentum M' (as stored).
 __device__ __forceinline__ float ns_u(float g, float m1, float mu, int nesterov) {
   return nesterov ? fmaf(mu, m1, g) : m1;
 }
 
+// W consecutive elements from i on (W = 4: 16-byte, or for bf16 8-byte, loads).
+template <bool BF, int W>
+__device__ __forceinline__ void ns_load_grad(const void* g, size_t i, float (&v)[W]) {
+  if constexpr (W == 1) {
+    v[0] = load1<BF ? ACT_BF16 : ACT_F32>(g, i);
+  } else if constexpr (BF) {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(g) + i);
+    v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
+  } else {
+    const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(g) + i);
+    v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+  }
+}
+
 // M' = mu M + G and the sum of U^2 (fp64 partial sums, one per workgroup).
-template <bool BF, bool V4>
+template <bool BF, int W>
 __global__ __launch_bounds__(256) void ns_momentum_kernel(OrthoArgs a, double* part) {
   __shared__ double red[4];
-  constexpr int W = V4 ? 4 : 1;
-  const size_t n = size_t(a.rows) * a.cols / W;
+  const size_t n = size_t(a.rows) * a.cols;
   double s = 0.0;
-  for (size_t q = size_t(blockIdx.x) * 256 + threadIdx.x; q < n; q += size_t(gridDim.x) * 256) {
+  for (size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * W; i < n; i += size_t(gridDim.x) * 256 * W) {
     float g[W], m[W];
-    if constexpr (V4) {
-      if constexpr (BF) {
-        const uint2 u = reinterpret_cast<const uint2*>(a.grad)[q];
-        g[0] = bf16lo(u.x); g[1] = bf16hi(u.x); g[2] = bf16lo(u.y); g[3] = bf16hi(u.y);
-      } else {
-        const float4 u = reinterpret_cast<const float4*>(a.grad)[q];
-        g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w;
-      }
-      if (a.m) {
-        const float4 u = reinterpret_cast<const float4*>(a.m)[q];
-        m[0] = u.x; m[1] = u.y; m[2] = u.z; m[3] = u.w;
-      }
-    } else {
-      g[0] = ns_grad<BF>(a.grad, q);
-      if (a.m) m[0] = a.m[q];
-    }
+    ns_load_grad<BF, W>(a.grad, i, g);
+    if (a.m) ns_load_grad<false, W>(a.m, i, m);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       float u = g[j];
@@ -100,8 +94,8 @@ __global__ __launch_bounds__(256) void ns_momentum_kernel(OrthoArgs a, double* p
       s = fma(double(u), double(u), s);
     }
     if (a.m) {
-      if constexpr (V4) reinterpret_cast<float4*>(a.m_out)[q] = make_float4(m[0], m[1], m[2], m[3]);
-      else a.m_out[q] = m[0];
+      if constexpr (W == 4) *reinterpret_cast<float4*>(a.m_out + i) = make_float4(m[0], m[1], m[2], m[3]);
+      else a.m_out[i] = m[0];
     }
   }
 #pragma unroll
@@ -123,11 +117,39 @@ struct NsCast {
   int32_t Sp, Lp;
 };
 
-template <bool BF>
+template <bool BF, int W>
 __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
   __shared__ double red[4];
   __shared__ _Float16 th[64][68], tl[64][68];
   const int tid = threadIdx.x;
+  const bool tall = a.rows > a.cols;
+  const int cp = tall ? c.Sp : c.Lp;  // padded columns
+  const int tc = cp / 64;
+  const int r0 = int(blockIdx.x / tc) * 64, c0 = int(blockIdx.x % tc) * 64;
+  const int lc = 4 * (tid & 15);
+  // four rows of four elements per thread, on their way while the norm is added up
+  float g[4][4], m[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 16 * i + (tid >> 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) g[i][j] = m[i][j] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; j += W) {
+      const size_t at = size_t(r) * a.cols + c0 + lc + j;
+      if (r < a.rows && c0 + lc + j < a.cols) {
+        float v[W];
+        ns_load_grad<BF, W>(a.grad, at, v);
+#pragma unroll
+        for (int e = 0; e < W; ++e) g[i][j + e] = v[e];
+        if (a.m) {
+          ns_load_grad<false, W>(a.m_out, at, v);
+#pragma unroll
+          for (int e = 0; e < W; ++e) m[i][j + e] = v[e];
+        }
+      }
+    }
+  }
   double s = 0.0;
   for (int p = tid; p < c.parts; p += 256) s += c.part[p];
 #pragma unroll
@@ -137,30 +159,19 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
   const double norm = sqrt(((red[0] + red[1]) + red[2]) + red[3]);
   // NaN for a norm that is NaN or infinite, so that all of the result is NaN
   const double scale = norm > 0.0 ? (norm < __builtin_inf() ? 16384.0 / norm : __builtin_nan("")) : (norm == 0.0 ? 0.0 : norm);
-  const bool tall = a.rows > a.cols;
-  const int cp = tall ? c.Sp : c.Lp;  // padded columns
-  const int tc = cp / 64;
-  const int r0 = int(blockIdx.x / tc) * 64, c0 = int(blockIdx.x % tc) * 64;
-  const int lc = 4 * (tid & 15);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int lr = 16 * i + (tid >> 4), r = r0 + lr;
+    const int lr = 16 * i + (tid >> 4);
     f16x4_t hi, lo;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int col = c0 + lc + j;
-      float v = 0.f;
-      if (r < a.rows && col < a.cols) {
-        const size_t at = size_t(r) * a.cols + col;
-        const float g = ns_grad<BF>(a.grad, at);
-        v = float(double(a.m ? ns_u(g, a.m_out[at], a.mu, a.nesterov) : g) * scale);
-      }
+      const float v = float(double(a.m ? ns_u(g[i][j], m[i][j], a.mu, a.nesterov) : g[i][j]) * scale);
       hi[j] = _Float16(v);
       lo[j] = ns_lo(v, hi[j]);
     }
     *reinterpret_cast<f16x4_t*>(&th[lr][lc]) = hi;
     *reinterpret_cast<f16x4_t*>(&tl[lr][lc]) = lo;
-    const size_t at = size_t(r) * cp + c0 + lc;
+    const size_t at = size_t(r0 + lr) * cp + c0 + lc;
     if (tall) {
       *reinterpret_cast<f16x4_t*>(c.xh + at) = hi;
       *reinterpret_cast<f16x4_t*>(c.xl + at) = lo;
@@ -570,26 +581,25 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   double* part = reinterpret_cast<double*>(ws + q.part);
   const size_t n = size_t(a.rows) * a.cols;
   auto al = [](const void* p, size_t b) { return reinterpret_cast<uintptr_t>(p) % b == 0; };
-  const bool v4 = n % 4 == 0 && al(a.grad, a.grad_bf16 ? 8 : 16) && al(a.m, 16) && al(a.m_out, 16);
-  const size_t work = (v4 ? n / 4 : n);
-  const size_t nb = (work + 255) / 256;
+  // four elements at a time where whole rows are aligned to it
+  const bool v4 = a.cols % 4 == 0 && al(a.grad, a.grad_bf16 ? 8 : 16) && al(a.m, 16) && al(a.m_out, 16);
+  const size_t nb = ((v4 ? n / 4 : n) + 255) / 256;
   const int blocks = int(nb < NS_SUMS ? nb : NS_SUMS);
-#define NS_MOM(BF, V) hipLaunchKernelGGL((ns_momentum_kernel<BF, V>), dim3(unsigned(blocks)), dim3(256), 0, s, a, part)
-  if (a.grad_bf16) {
-    if (v4) NS_MOM(true, true);
-    else NS_MOM(true, false);
-  } else {
-    if (v4) NS_MOM(false, true);
-    else NS_MOM(false, false);
-  }
-#undef NS_MOM
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   const NsCast c{part, blocks, at(q.xs), at(q.xh[0]), at(q.xl[0]), q.Sp, q.Lp};
   const unsigned tiles = unsigned((q.Sp / 64) * (q.Lp / 64));
-  if (a.grad_bf16) hipLaunchKernelGGL(ns_cast_kernel<true>, dim3(tiles), dim3(256), 0, s, a, c);
-  else hipLaunchKernelGGL(ns_cast_kernel<false>, dim3(tiles), dim3(256), 0, s, a, c);
-  e = hipGetLastError();
+  hipError_t e = hipSuccess;
+  auto head = [&](auto bf, auto w) {
+    hipLaunchKernelGGL((ns_momentum_kernel<decltype(bf)::value, decltype(w)::value>), dim3(unsigned(blocks)), dim3(256), 0,
+                       s, a, part);
+    e = hipGetLastError();
+    if (e != hipSuccess) return;
+    hipLaunchKernelGGL((ns_cast_kernel<decltype(bf)::value, decltype(w)::value>), dim3(tiles), dim3(256), 0, s, a, c);
+    e = hipGetLastError();
+  };
+  using four = std::integral_constant<int, 4>;
+  using single = std::integral_constant<int, 1>;
+  if (a.grad_bf16) v4 ? head(std::true_type{}, four{}) : head(std::true_type{}, single{});
+  else v4 ? head(std::false_type{}, four{}) : head(std::false_type{}, single{});
   if (e != hipSuccess) return e;
 
   constexpr float up13 = 8192.f, dn13 = 1.f / 8192.f;

@@ -11,8 +11,6 @@ a^2 = 11.8-fold outside a smaller row space and ||X_3|| / ||X_5|| is at most
 1.2 / 0.68: 11.8 * 1.8 * 2^-11 = 1.0e-2 more.  bf16 adds 2^-8 at most.  Bars:
 7e-3 (full rank), 1.7e-2 (any).
 """
-import ctypes
-
 import numpy as np
 import pytest
 
@@ -273,7 +271,7 @@ def test_training_step_of_a_normalised_layer(d_ff):
         o, _ = bm.orthogonalize(grads["w_base"][m], mom, momentum_out=mom)
         assert rel(to_f64(o), ref.orthogonalize(to_f64(grads["w_base"][m]), np.zeros(latent.shape))[0]) <= ANY
         w0 = w.cpu().numpy()
-        bm.substrate_step(w, o, step=0.5, decay=0.01, w_out=w, packed=layer.w_base[m])
+        layer.step_substrate(m, w, o, step=0.5, decay=0.01, w_out=w)
         ww, cc, _ = ref.substrate_step(w0, to_f64(o), step=0.5, decay=0.01)
         assert (w.cpu().numpy() == ww).all()
         codes.append(cc)
@@ -281,3 +279,23 @@ def test_training_step_of_a_normalised_layer(d_ff):
     inp.w_base = codes
     want = bm.Layer.from_inputs(inp, device="cuda").forward(n)
     assert (layer.forward(n) == want).all()
+
+
+def test_step_substrate_prepares_again():
+    """A prepared layer forwards with the new codes, not with those it was
+    prepared from; misfit substrates are refused."""
+    import torch
+    inp = wl.generate(wl.small_config(d_model=256, d_ff=0, n_experts=4, top_k=2, tokens=50, act="bf16", seed_index=720))
+    layer = bm.Layer.from_inputs(inp, device="cuda").prepare()
+    x = to_dev(inp.x, "bf16")
+    before = layer.forward(x).clone()
+    w = torch.randn(256, 256, generator=torch.Generator().manual_seed(72)).cuda()
+    layer.step_substrate(0, w)
+    inp.w_base = [ref.substrate_step(w.cpu().numpy())[1]]
+    want = bm.Layer.from_inputs(inp, device="cuda").prepare().forward(x)
+    got = layer.forward(x)
+    assert (got == want).all() and (got != before).any()
+    with pytest.raises(ValueError):
+        layer.step_substrate(1, w)
+    with pytest.raises(ValueError):
+        layer.step_substrate(0, w[:128])
