@@ -44,6 +44,8 @@ typedef __attribute__((address_space(3))) void ns_lds_t;
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr int NS_SUMS = 512;        // partial sums of squares
 constexpr int NS_K = 64;            // contraction step
+constexpr int NS_SPLIT = 16;        // most workgroups that share a tile
+constexpr int NS_SHARED = 512;      // most workgroups of a product that shares tiles
 
 // The second term of v = hi + lo with 5 significant bits: hi has 11 and lo starts
 // one below: 17 bits, whose noise stays below that of X_3, and products of numbers whose last bits are
@@ -114,6 +116,7 @@ struct NsCast {
   _Float16* xs;             // [Sp][Lp]
   _Float16* xh;             // [Lp][Sp]
   _Float16* xl;             // [Lp][Sp]
+  int32_t* ticket;          // [NS_SHARED / 2], cleared
   int32_t Sp, Lp;
 };
 
@@ -122,6 +125,8 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
   __shared__ double red[4];
   __shared__ _Float16 th[64][68], tl[64][68];
   const int tid = threadIdx.x;
+  if (blockIdx.x == 0) c.ticket[tid] = 0;
+  static_assert(NS_SHARED / 2 == 256, "one ticket per thread");
   const bool tall = a.rows > a.cols;
   const int cp = tall ? c.Sp : c.Lp;  // padded columns
   const int tc = cp / 64;
@@ -211,6 +216,9 @@ struct NsGemm {
   float alpha;              // D = alpha sum (+ beta C + diag on the diagonal)
   // NS_SYM: d [N][N]; c [N][N] or null
   int32_t band;             // tile rows of a band of tiles
+  int32_t split;            // workgroups that share a tile's depth
+  float* part;              // [tiles][split][tile] their sums when split > 1
+  int32_t* ticket;          // [tiles] zero before and after the product
   const _Float16* c;
   float beta, diag;
   _Float16* d;              // NS_SYM; NS_PROD: D's hi [M][N]
@@ -243,11 +251,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;  // row of a block, 16-byte chunk of its depth
   const int wm = wave % WM, wn = wave / WM;
-  int tm, tn;
+  int tm, tn, tile = 0, share = 0;
   {
     int t = xcd_remap(blockIdx.x, gridDim.x);
     const int nt = (p.N + TN - 1) / TN;
     if constexpr (MODE == NS_SYM) {
+      share = t % p.split;
+      t /= p.split;
+      tile = t;
       // tiles on and above the diagonal, by bands of p.band tile rows, column by
       // column within a band: the tiles an XCD runs at a time form a block that
       // needs few row blocks of the operand in its L2
@@ -271,7 +282,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     }
   }
   const int m0 = tm * TM, n0 = tn * TN;
-  const int K = p.K, nk1 = K / NS_K, nk = p.a2 ? 2 * nk1 : nk1;
+  const int K = p.K, nk1 = K / NS_K;
+  // this workgroup's steps: k0 .. k0 + nk - 1
+  int k0 = 0, nk = MODE != NS_SYM && p.a2 ? 2 * nk1 : nk1;
+  if constexpr (MODE == NS_SYM) {
+    const int per = (nk1 + p.split - 1) / p.split;
+    k0 = share * per;
+    nk = min(per, nk1 - k0);
+  }
   // a load fills 8 rows of 64; a wave's loads are all of A or all of B.  Byte
   // offsets of this lane's pieces in it; 8-row groups past the matrix (M and N
   // are multiples of 8) read its last one and are not stored
@@ -287,7 +305,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   // this wave's loads of step kt (past the last one: the last one again, never
   // read) into ring place `buf`
   auto load = [&](int kt, int buf) {
-    kt = min(kt, nk - 1);
+    kt = k0 + min(kt, nk - 1);
     const char* src = reinterpret_cast<const char*>(isb ? p.b : kt >= nk1 ? p.a2 : p.a) +
                       size_t(kt >= nk1 ? kt - nk1 : kt) * (2 * NS_K);
     _Float16* dst = sm + buf * STAGE + wave * LPW * 8 * NS_K;
@@ -363,6 +381,62 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   }
   // loads past the last step may still be writing to the ring
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  if constexpr (MODE == NS_SYM) {
+    if (p.split > 1) {
+      // the sums go to memory; the workgroup that comes last to a tile adds all of
+      // them in the order of the depth and goes on alone.  Nobody waits.  The
+      // XCDs' L2s do not see each other's writes, so the sums are stored past them
+      // and read past them (agent scope); a fence that writes the whole L2 back
+      // instead cost 54 us a product.
+      constexpr int PAIRS = IM * IN * 2;
+      typedef float f32x2_t __attribute__((ext_vector_type(2)));
+      unsigned long long* own =
+          reinterpret_cast<unsigned long long*>(p.part) + (size_t(tile) * p.split + share) * PAIRS * NT + tid;
+#pragma unroll
+      for (int i = 0; i < IN; ++i)
+#pragma unroll
+        for (int j = 0; j < IM; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const f32x2_t v = {acc[i][j][2 * h], acc[i][j][2 * h + 1]};
+            __hip_atomic_store(own + ((i * IM + j) * 2 + h) * NT, __builtin_bit_cast(unsigned long long, v),
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // they are there before the ticket says so
+      __syncthreads();
+      int* last = reinterpret_cast<int*>(sm);
+      if (tid == 0) {
+        *last = __hip_atomic_fetch_add(p.ticket + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.split - 1;
+        if (*last) p.ticket[tile] = 0;
+      }
+      __syncthreads();
+      if (!*last) return;
+      const unsigned long long* all =
+          reinterpret_cast<const unsigned long long*>(p.part) + size_t(tile) * p.split * PAIRS * NT + tid;
+      constexpr int G = 32 / PAIRS > 0 ? 32 / PAIRS : 1;  // shares read at a time
+      for (int q0 = 0; q0 < p.split; q0 += G) {
+        unsigned long long v[G][PAIRS];
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+          if (q0 + q < p.split)
+#pragma unroll
+            for (int k = 0; k < PAIRS; ++k)
+              v[q][k] = __hip_atomic_load(all + (size_t(q0 + q) * PAIRS + k) * NT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+          if (q0 + q < p.split)
+#pragma unroll
+            for (int k = 0; k < PAIRS; ++k) {
+              const f32x2_t w = __builtin_bit_cast(f32x2_t, v[q][k]);
+              f32x4_t& a = acc[k / 2 / IM][k / 2 % IM];
+              a[2 * (k % 2)] = q0 + q == 0 ? w.x : a[2 * (k % 2)] + w.x;
+              a[2 * (k % 2) + 1] = q0 + q == 0 ? w.y : a[2 * (k % 2) + 1] + w.y;
+            }
+      }
+      __syncthreads();  // *last is read before the tile is staged over it
+    }
+  }
 
   // acc[i][j][r] = D[m0 + PM wm + 16 j + l16][n0 + PN wn + 16 i + 4 g + r]
   _Float16* st = sm;  // [TM][ST]
@@ -487,8 +561,64 @@ namespace {
 // Padded side: whole contraction steps.
 int ns_pad(int n) { return (n + NS_K - 1) / NS_K * NS_K; }
 
+// Tiles of side t in a product's result.
+template <int MODE>
+int ns_tiles(const NsGemm& p, int t) {
+  const int nm = (p.M + t - 1) / t, nn = (p.N + t - 1) / t;
+  return MODE == NS_SYM ? nn * (nn + 1) / 2 : nm * nn;
+}
+
+// Time of a product in tiles of side t, `split` workgroups to a tile, in
+// microseconds: a lone tile's step of 64 takes `one` (latency and the CU's own
+// limits), all together 256 t bytes a step and workgroup from L2 into LDS at 16
+// TB/s (12 where shares read different parts of the depth) and 128 t^2 operations at 1.15 PFLOP/s (rates of whole products of 2048 x
+// 8192 on this GPU); adding a tile's shares up takes 1.4 us and more with its area
+// and their number (a symmetric product of side 64 and K = 8192 in tiles of 32:
+// 16.8 us whole, 7.6 in four shares, 5.8 in sixteen; of 512 and 8192 in tiles of
+// 64: 24.6, 11.9 in four, 11.5 in six, 16.5 in eight).
+template <int MODE>
+double ns_time(const NsGemm& p, int t, double one, int split) {
+  const int steps = p.K / NS_K * (p.a2 ? 2 : 1), n = ns_tiles<MODE>(p, t) * split;
+  const double step = std::max({one, double(n) * t * 256 / (split > 1 ? 12e6 : 16e6), double(n) * t * t * 128 / 1.15e9});
+  return (steps + split - 1) / split * step + (split > 1 ? 1.4 + t / 64.0 * t / 64.0 * (0.8 + 0.4 * split) : 0.0);
+}
+
+struct NsTile {
+  int side, split;
+};
+
+// Steps of a lone tile of 32, 64, 96, 128 and 256: 0.14, 0.205, 0.32, 0.41 and 1.2
+// us.  Measured per product, symmetric ones of side 512 / 1024 / 2048 with K = the
+// side: tiles of 32 4.1 / 8.8 / 36 us, 64 5.6 / 7.2 / 23.6, 96 8.9 / 10.2 / 18.2,
+// 128 11 / 12.0 / 20.4; general ones of 512 x 512, 4096 x 1024, 8192 x 2048: 32
+// 3.7 / 30 / 289, 64 4.5 / 18.4 / 152, 128 8 / 14.0 / 83, 256 18.2 / 27.3 / 66.
+template <int MODE>
+NsTile ns_pick(const NsGemm& p) {
+  NsTile best{0, 1};
+  double least = 0;
+  auto look = [&](int side, double one) {
+    // as many workgroups as run at a time: two per CU up to tiles of 64
+    const int most = (side <= 64 ? NS_SHARED : NS_SHARED / 2) / std::max(1, ns_tiles<MODE>(p, side)), steps = p.K / NS_K;
+    for (int split = 1; split == 1 || (MODE == NS_SYM && split <= std::min(most, NS_SPLIT)); ++split) {
+      // whole shares only
+      if (split > 1 && (split - 1) * ((steps + split - 1) / split) >= steps) continue;
+      const double time = ns_time<MODE>(p, side, one, split);
+      if (!best.side || time < least) {
+        best = NsTile{side, split};
+        least = time;
+      }
+    }
+  };
+  look(32, 0.14);
+  look(64, 0.205);
+  if (MODE == NS_SYM) look(96, 0.32);
+  look(128, 0.41);
+  if (MODE != NS_SYM) look(256, 1.2);
+  return best;
+}
+
 struct NsPlan {
-  size_t part, xs, xh[2], xl[2], A, T, P, Q, total;
+  size_t part, xs, xh[2], xl[2], A, T, P, Q, shares, ticket, total;
   int S, L, Sp, Lp;
 };
 
@@ -515,59 +645,46 @@ NsPlan ns_plan(int rows, int cols) {
   q.T = take(s);
   q.P = take(s);
   q.Q = take(s);
+  size_t shares = 0;
+  for (int depth : {q.Lp, q.Sp}) {
+    NsGemm g{};
+    g.M = g.N = q.Sp;
+    g.K = depth;
+    const NsTile t = ns_pick<NS_SYM>(g);
+    if (t.split > 1) shares = std::max(shares, size_t(ns_tiles<NS_SYM>(g, t.side)) * t.split * t.side * t.side * 4);
+  }
+  q.shares = take(shares);
+  q.ticket = take(NS_SHARED / 2 * 4);
   q.total = o;
   return q;
 }
 
-// Tiles of side t in a product's result.
-template <int MODE>
-int ns_tiles(const NsGemm& p, int t) {
-  const int nm = (p.M + t - 1) / t, nn = (p.N + t - 1) / t;
-  return MODE == NS_SYM ? nn * (nn + 1) / 2 : nm * nn;
-}
-
 template <int MODE, int T, int WM, int WN, int NBUF>
-hipError_t ns_tile(NsGemm p, hipStream_t s) {
+hipError_t ns_tile(NsGemm p, int split, hipStream_t s) {
   constexpr size_t ring = size_t(NBUF) * 2 * T * NS_K * 2, stage = size_t(T) * (T + 4) * 2;
   constexpr size_t lds = ring > stage ? ring : stage;
   const auto kernel = ns_gemm_kernel<MODE, T, T, WM, WN, NBUF, T <= 64>;
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
   if (e != hipSuccess) return e;
   const int tiles = ns_tiles<MODE>(p, T);
+  p.split = split;
   // as high as the block of tiles of one of the eight XCDs is wide
   if (MODE == NS_SYM) p.band = std::max(1, int(std::lround(std::sqrt(tiles / 8.0))));
-  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles)), dim3(64 * WM * WN), lds, s, p);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * split)), dim3(64 * WM * WN), lds, s, p);
   return hipGetLastError();
 }
 
-// Time of a product in tiles of side t, per step of 64, in microseconds: a lone
-// tile's step takes `one` (latency and the CU's own limits), all tiles together
-// 256 t bytes each from L2 into LDS at 16 TB/s and 128 t^2 operations at 1.15
-// PFLOP/s (rates of whole products of 2048 x 8192 on this GPU).
-template <int MODE>
-double ns_cost(const NsGemm& p, int t, double one) {
-  const double n = ns_tiles<MODE>(p, t), a = n * t * 256 / 16e6, b = n * t * t * 128 / 1.15e9;
-  return a > b ? (a > one ? a : one) : (b > one ? b : one);
-}
-
-// Picks the tile with the least of those times.  Measured per product, symmetric
-// ones of side 512 / 1024 / 2048 with K = the side: tiles of 32 4.1 / 8.8 / 36
-// us, 64 5.6 / 7.2 / 23.6, 96 8.9 / 10.2 / 18.2, 128 11 / 12.0 / 20.4; general
-// ones of 512 x 512, 4096 x 1024, 8192 x 2048: 32 3.7 / 30 / 289, 64 4.5 / 18.4 /
-// 152, 128 8 / 14.0 / 83, 256 18.2 / 27.3 / 66.
 template <int MODE>
 hipError_t ns_go(const NsGemm& p, hipStream_t s) {
-  const double c32 = ns_cost<MODE>(p, 32, 0.14), c64 = ns_cost<MODE>(p, 64, 0.205), c128 = ns_cost<MODE>(p, 128, 0.41);
-  if (c32 < c64) return ns_tile<MODE, 32, 2, 2, 4>(p, s);
+  const NsTile t = ns_pick<MODE>(p);
+  if (t.side == 32) return ns_tile<MODE, 32, 2, 2, 4>(p, t.split, s);
+  if (t.side == 64) return ns_tile<MODE, 64, 2, 2, 4>(p, t.split, s);
   if constexpr (MODE == NS_SYM) {
-    const double c96 = ns_cost<MODE>(p, 96, 0.32);
-    if (c64 < c96) return ns_tile<MODE, 64, 2, 2, 4>(p, s);
-    if (c96 < c128) return ns_tile<MODE, 96, 2, 2, 4>(p, s);
+    if (t.side == 96) return ns_tile<MODE, 96, 2, 2, 4>(p, t.split, s);
   } else {
-    if (c64 < c128) return ns_tile<MODE, 64, 2, 2, 4>(p, s);
-    if (ns_cost<MODE>(p, 256, 1.2) <= c128) return ns_tile<MODE, 256, 2, 4, 2>(p, s);
+    if (t.side == 256) return ns_tile<MODE, 256, 2, 4, 2>(p, t.split, s);
   }
-  return ns_tile<MODE, 128, 2, 4, 3>(p, s);
+  return ns_tile<MODE, 128, 2, 4, 3>(p, t.split, s);
 }
 
 }  // namespace
@@ -585,7 +702,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   const bool v4 = a.cols % 4 == 0 && al(a.grad, a.grad_bf16 ? 8 : 16) && al(a.m, 16) && al(a.m_out, 16);
   const size_t nb = ((v4 ? n / 4 : n) + 255) / 256;
   const int blocks = int(nb < NS_SUMS ? nb : NS_SUMS);
-  const NsCast c{part, blocks, at(q.xs), at(q.xh[0]), at(q.xl[0]), q.Sp, q.Lp};
+  const NsCast c{part, blocks, at(q.xs), at(q.xh[0]), at(q.xl[0]), reinterpret_cast<int32_t*>(ws + q.ticket), q.Sp, q.Lp};
   const unsigned tiles = unsigned((q.Sp / 64) * (q.Lp / 64));
   hipError_t e = hipSuccess;
   auto head = [&](auto bf, auto w) {
@@ -606,6 +723,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   _Float16 *A = at(q.A), *T = at(q.T), *P = at(q.P), *Q = at(q.Q);
   NsGemm sym{};
   sym.M = sym.N = q.Sp;
+  sym.part = reinterpret_cast<float*>(ws + q.shares);
+  sym.ticket = reinterpret_cast<int32_t*>(ws + q.ticket);
   // A (2^13) = XS XS^T, factors 2^14 each
   auto gram = [&]() {
     NsGemm g = sym;
