@@ -620,6 +620,7 @@ NsTile ns_pick(const NsGemm& p) {
 struct NsPlan {
   size_t part, xs, xh[2], xl[2], A, T, P, Q, shares, ticket, total;
   int S, L, Sp, Lp;
+  NsTile gram, square;      // tiles of X X^T and of the products of side S
 };
 
 NsPlan ns_plan(int rows, int cols) {
@@ -646,13 +647,16 @@ NsPlan ns_plan(int rows, int cols) {
   q.P = take(s);
   q.Q = take(s);
   size_t shares = 0;
-  for (int depth : {q.Lp, q.Sp}) {
+  auto pick = [&](int depth) {
     NsGemm g{};
     g.M = g.N = q.Sp;
     g.K = depth;
     const NsTile t = ns_pick<NS_SYM>(g);
     if (t.split > 1) shares = std::max(shares, size_t(ns_tiles<NS_SYM>(g, t.side)) * t.split * t.side * t.side * 4);
-  }
+    return t;
+  };
+  q.gram = pick(q.Lp);
+  q.square = pick(q.Sp);
   q.shares = take(shares);
   q.ticket = take(NS_SHARED / 2 * 4);
   q.total = o;
@@ -675,8 +679,7 @@ hipError_t ns_tile(NsGemm p, int split, hipStream_t s) {
 }
 
 template <int MODE>
-hipError_t ns_go(const NsGemm& p, hipStream_t s) {
-  const NsTile t = ns_pick<MODE>(p);
+hipError_t ns_go(const NsGemm& p, NsTile t, hipStream_t s) {
   if (t.side == 32) return ns_tile<MODE, 32, 2, 2, 4>(p, t.split, s);
   if (t.side == 64) return ns_tile<MODE, 64, 2, 2, 4>(p, t.split, s);
   if constexpr (MODE == NS_SYM) {
@@ -732,7 +735,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     g.K = q.Lp;
     g.alpha = 1.f / 32768.f;
     g.d = A;
-    return ns_go<NS_SYM>(g, s);
+    return ns_go<NS_SYM>(g, q.gram, s);
   };
   // d (2^13) = a I + b A + c A A of the matrix in src (2^13)
   auto poly = [&](const _Float16* src, _Float16* d) {
@@ -743,7 +746,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     g.beta = NS_B;
     g.diag = NS_A * up13;
     g.d = d;
-    return ns_go<NS_SYM>(g, s);
+    return ns_go<NS_SYM>(g, q.square, s);
   };
   // d = x y of commuting symmetric matrices, times alpha
   auto mul = [&](const _Float16* x, const _Float16* y, float alpha, _Float16* d) {
@@ -753,7 +756,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     g.K = q.Sp;
     g.alpha = alpha;
     g.d = d;
-    return ns_go<NS_SYM>(g, s);
+    return ns_go<NS_SYM>(g, q.square, s);
   };
   // X (from buffer k, hi + lo when two) times f (2^logf) into the other buffer
   NsGemm prod{};
@@ -768,40 +771,46 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     g.d = at(q.xh[k ^ 1]);
     g.lo = keep_lo ? at(q.xl[k ^ 1]) : nullptr;
     g.dt = at(q.xs);
-    return ns_go<NS_PROD>(g, s);
+    return ns_go<NS_PROD>(g, ns_pick<NS_PROD>(g), s);
   };
 #define NS_DO(call)                     \
   do {                                  \
     e = (call);                         \
     if (e != hipSuccess) return e;      \
   } while (0)
-  // steps 0 and 1: P_0, T = P_0 A_0, A_1 = P_0 T, P_1, Q = P_1 P_0 (2^11), X_2 = Q X_0
+  int k = 0;  // buffer that holds X
+  auto next = [&](bool two, const _Float16* f, float alpha, bool keep_lo) {
+    const hipError_t r = step(k, two, f, alpha, keep_lo);
+    k ^= 1;
+    return r;
+  };
+  // steps 0 and 1 together: P_0, T = P_0 A_0, A_1 = P_0 T, P_1, Q = P_1 P_0 (2^11),
+  // X_2 = Q X_0 (one by one they took 74 us in place of 77 at 512 x 512, a launch
+  // less, but 179 in place of 170 at 1024 x 2048 and 1939 of 1936 at 4096 x 4096)
   NS_DO(gram());
   NS_DO(poly(A, P));
   NS_DO(mul(P, A, dn13, T));
   NS_DO(mul(P, T, dn13, A));
   NS_DO(poly(A, T));
   NS_DO(mul(T, P, 1.f / 32768.f, Q));
-  NS_DO(step(0, true, Q, 1.f / 2048.f, true));
-  // step 2
-  NS_DO(gram());
-  NS_DO(poly(A, P));
-  NS_DO(step(1, true, P, dn13, false));
-  // step 3
-  NS_DO(gram());
-  NS_DO(poly(A, P));
-  NS_DO(step(0, false, P, dn13, false));
+  NS_DO(next(true, Q, 1.f / 2048.f, true));
+  // step 2 from two terms, step 3 from one
+  for (bool two : {true, false}) {
+    NS_DO(gram());
+    NS_DO(poly(A, P));
+    NS_DO(next(two, P, dn13, false));
+  }
   // step 4: X_5 (unscaled) in bf16
   NS_DO(gram());
   NS_DO(poly(A, P));
   NsGemm g = prod;
-  g.a = at(q.xh[1]);
+  g.a = at(q.xh[k]);
   g.b = P;
   g.alpha = dn13 / 16384.f;
   g.out = a.out;
   g.rows = a.rows;
   g.cols = a.cols;
-  NS_DO(ns_go<NS_LAST>(g, s));
+  NS_DO(ns_go<NS_LAST>(g, ns_pick<NS_LAST>(g), s));
 #undef NS_DO
   return hipSuccess;
 }
