@@ -20,14 +20,21 @@
 // X in one fp16 term throughout, a gradient of rank S / 8 came out 2e-2 off,
 // with this 3e-3; full-rank ones 1e-3.
 //
-// Symmetric results (A, T A, P, Q) compute only the tiles on and above the
+// A, P, T and Q round most where they are largest, on the diagonal, and there all
+// alike when X's rows are equally long: 48 x 16384 normal entries came out 5e-3
+// off.  So each keeps the ratio of its true diagonal to the stored one (fp32) and
+// what it is multiplied into is multiplied by that ratio's row or column as well:
+// exact for the diagonal's part, within fp16's rounding for the others' (now
+// 1.7e-3, bf16's own).
+//
+// Symmetric results (A, T, P, Q) compute only the tiles on and above the
 // diagonal and write each also mirrored.
 //
 // Layouts: every product is D[m][n] = sum_k A[m][k] B[n][k], both operands
 // with k contiguous.  A = X X^T reads X as XS [S][L]; X' = P X, taken as
 // X'^T = X^T P (P symmetric), reads X as XL [L][S].  A product's epilogue
-// writes its tile both ways.  S and L are padded to
-// multiples of 64 with zeros, which stay zero.
+// writes its tile both ways.  S and L are padded to multiples of 64 with zeros,
+// which stay zero.
 #include "common.hpp"
 
 #include <algorithm>
@@ -48,9 +55,9 @@ constexpr int NS_SPLIT = 16;        // most workgroups that share a tile
 constexpr int NS_SHARED = 512;      // most workgroups of a product that shares tiles
 
 // The second term of v = hi + lo with 5 significant bits: hi has 11 and lo starts
-// one below: 17 bits, whose noise stays below that of X_3, and products of numbers whose last bits are
-// zero take less of the power that bounds the large products' clock (785 -> 770
-// us at 2048 x 8192; 764 with lo = 0).
+// one below, so the pair has 17, whose noise stays below that of X_3.  Products
+// of numbers whose last bits are zero take less of the power that bounds the
+// large products' clock (785 -> 770 us at 2048 x 8192; 764 with lo = 0).
 __device__ __forceinline__ _Float16 ns_lo(float v, _Float16 hi) {
   const uint16_t b = __builtin_bit_cast(uint16_t, _Float16(v - float(hi)));
   return __builtin_bit_cast(_Float16, uint16_t((b + 0x20u) & 0xFFC0u));
@@ -214,6 +221,9 @@ struct NsGemm {
   const _Float16* b;        // [N][K]
   int32_t M, N, K;          // multiples of NS_K
   float alpha;              // D = alpha sum (+ beta C + diag on the diagonal)
+  const float* ra;          // [N] true over stored diagonal of a (NS_SYM; and of c) and
+  const float* rb;          // of b, or null
+  float* rd;                // NS_SYM: the same of d, written
   // NS_SYM: d [N][N]; c [N][N] or null
   int32_t band;             // tile rows of a band of tiles
   int32_t split;            // workgroups that share a tile's depth
@@ -313,6 +323,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     for (int j = 0; j < LPW; ++j)
       __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + off[j]), (ns_lds_t*)(dst + 8 * j * NS_K), 16, 0, 0);
   };
+  // the ratios of this lane's rows and columns (1 past the matrix), read behind
+  // the first steps' loads: ahead of them or in the epilogue their latency shows
+  float ram[IM], rbm[IM];
+  f32x4_t ran[IN], rbn[IN];
+  auto ratios = [&](const float* r, float (&rm)[IM], f32x4_t (&rn)[IN]) {
+#pragma unroll
+    for (int j = 0; j < IM; ++j) {
+      const int m = m0 + PM * wm + 16 * j + l16;
+      rm[j] = MODE == NS_SYM && r && m < p.M ? r[m] : 1.f;
+    }
+#pragma unroll
+    for (int i = 0; i < IN; ++i) {
+      const int n = n0 + PN * wn + 16 * i + 4 * g;
+      rn[i] = f32x4_t{1.f, 1.f, 1.f, 1.f};
+      if (r && n < p.N) rn[i] = *reinterpret_cast<const f32x4_t*>(r + n);
+    }
+  };
   f32x4_t acc[IN][IM];
 #pragma unroll
   for (int i = 0; i < IN; ++i)
@@ -361,6 +388,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   for (int b = 0; b < NBUF - 1; ++b) load(b, b);
   arrive();
   load(NBUF - 1, NBUF - 1);
+  if constexpr (MODE == NS_SYM) ratios(p.ra, ram, ran);
+  ratios(p.rb, rbm, rbn);
   read(0, 0, fa[0], fb[0]);
   int buf = 0;
   for (int kt = 0; kt < nk; ++kt) {
@@ -440,14 +469,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
 
   // acc[i][j][r] = D[m0 + PM wm + 16 j + l16][n0 + PN wn + 16 i + 4 g + r]
   _Float16* st = sm;  // [TM][ST]
-  // f(four sums of consecutive columns, row, first column) to the staged tile
+  // f(four sums of consecutive columns, row, first column, blocks) to the staged tile
   auto staged = [&](auto&& f) {
 #pragma unroll
     for (int j = 0; j < IM; ++j)
 #pragma unroll
       for (int i = 0; i < IN; ++i) {
         const int m = PM * wm + 16 * j + l16, n = PN * wn + 16 * i + 4 * g;
-        *reinterpret_cast<f16x4_t*>(st + m * ST + n) = f(acc[i][j], m, n);
+        *reinterpret_cast<f16x4_t*>(st + m * ST + n) = f(acc[i][j], m, n, i, j);
       }
     __syncthreads();
   };
@@ -492,48 +521,65 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     tpieces([&](int c, int r) { *reinterpret_cast<uint4*>(dst + size_t(c) * ld + r) = column8(c, r); });
   };
   if constexpr (MODE == NS_SYM) {
-    staged([&](f32x4_t a, int m, int n) {
+    float dv[IM], ds[IM];  // this lane's elements of the diagonal, true and stored
+#pragma unroll
+    for (int j = 0; j < IM; ++j) dv[j] = ds[j] = 1.f;
+    staged([&](f32x4_t a, int m, int n, int i, int j) {
       m += m0;
       n += n0;
       f16x4_t cv = {0, 0, 0, 0}, o;
       if (p.c && m < p.M && n < p.N) cv = *reinterpret_cast<const f16x4_t*>(p.c + size_t(m) * p.N + n);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        float v = fmaf(p.alpha, a[r], p.beta * float(cv[r]));
-        if (m == n + r) v += p.diag;
+        const float sa = 0.5f * (ram[j] + ran[i][r]), sb = 0.5f * (rbm[j] + rbn[i][r]);
+        float v = sa * fmaf(p.alpha * sb, a[r], p.beta * float(cv[r]));
+        const bool on = m == n + r;
+        v += on ? p.diag : 0.f;
         o[r] = _Float16(v);
+        dv[j] = on ? v : dv[j];
+        ds[j] = on ? float(o[r]) : ds[j];
       }
       return o;
     });
     direct(p.d + size_t(m0) * p.N + n0, p.N);
     if (tm != tn) transposed(p.d + size_t(n0) * p.N + m0, p.N);
+    // the ratios, 1 where the stored value is subnormal and its rounding coarse; at
+    // the end, where no barrier waits for the stores
+    if (tm == tn) {
+#pragma unroll
+      for (int j = 0; j < IM; ++j) {
+        const int ml = PM * wm + 16 * j + l16, nl = ml - PN * wn;  // its column in this wave's part
+        if (nl >= 0 && nl < PN && (nl >> 2 & 3) == g && m0 + ml < p.M)
+          p.rd[m0 + ml] = fabsf(ds[j]) >= 6.1035156e-5f ? dv[j] / ds[j] : 1.f;
+      }
+    }
   } else if constexpr (MODE == NS_PROD) {
-    staged([&](f32x4_t a, int, int) {
+    staged([&](f32x4_t a, int, int, int i, int) {
+      a *= p.alpha * rbn[i];
       f16x4_t o;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) o[r] = _Float16(p.alpha * a[r]);
+      for (int r = 0; r < 4; ++r) o[r] = _Float16(a[r]);
       return o;
     });
     direct(p.d + size_t(m0) * p.N + n0, p.N);
     transposed(p.dt + size_t(n0) * p.M + m0, p.M);
     if (p.lo) {
       __syncthreads();
-      staged([&](f32x4_t a, int, int) {
+      staged([&](f32x4_t a, int, int, int i, int) {
+        a *= p.alpha * rbn[i];
         f16x4_t o;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float v = p.alpha * a[r];
-          o[r] = ns_lo(v, _Float16(v));
-        }
+        for (int r = 0; r < 4; ++r) o[r] = ns_lo(a[r], _Float16(a[r]));
         return o;
       });
       direct(p.lo + size_t(m0) * p.N + n0, p.N);
     }
   } else {
-    staged([&](f32x4_t a, int, int) {
+    staged([&](f32x4_t a, int, int, int i, int) {
+      a *= p.alpha * rbn[i];
       uint2 o;
-      o.x = pack_bf16x2(p.alpha * a[0], p.alpha * a[1]);
-      o.y = pack_bf16x2(p.alpha * a[2], p.alpha * a[3]);
+      o.x = pack_bf16x2(a[0], a[1]);
+      o.y = pack_bf16x2(a[2], a[3]);
       return __builtin_bit_cast(f16x4_t, o);
     });
     const bool vec = p.cols % 8 == 0 && reinterpret_cast<uintptr_t>(p.out) % 16 == 0;
@@ -618,7 +664,7 @@ NsTile ns_pick(const NsGemm& p) {
 }
 
 struct NsPlan {
-  size_t part, xs, xh[2], xl[2], A, T, P, Q, shares, ticket, total;
+  size_t part, xs, xh[2], xl[2], m[4], r[4], shares, ticket, total;
   int S, L, Sp, Lp;
   NsTile gram, square;      // tiles of X X^T and of the products of side S
 };
@@ -642,10 +688,10 @@ NsPlan ns_plan(int rows, int cols) {
     q.xh[k] = take(x);
     q.xl[k] = take(x);
   }
-  q.A = take(s);
-  q.T = take(s);
-  q.P = take(s);
-  q.Q = take(s);
+  for (int k = 0; k < 4; ++k) {
+    q.m[k] = take(s);
+    q.r[k] = take(size_t(q.Sp) * 4);
+  }
   size_t shares = 0;
   auto pick = [&](int depth) {
     NsGemm g{};
@@ -723,7 +769,13 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
 
   constexpr float up13 = 8192.f, dn13 = 1.f / 8192.f;
-  _Float16 *A = at(q.A), *T = at(q.T), *P = at(q.P), *Q = at(q.Q);
+  // a symmetric matrix and the ratios of its true diagonal to the stored one
+  struct Sym {
+    _Float16* m;
+    float* r;
+  };
+  auto matrix = [&](int k) { return Sym{at(q.m[k]), reinterpret_cast<float*>(ws + q.r[k])}; };
+  const Sym A = matrix(0), T = matrix(1), P = matrix(2), Q = matrix(3);
   NsGemm sym{};
   sym.M = sym.N = q.Sp;
   sym.part = reinterpret_cast<float*>(ws + q.shares);
@@ -734,42 +786,51 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     g.a = g.b = at(q.xs);
     g.K = q.Lp;
     g.alpha = 1.f / 32768.f;
-    g.d = A;
+    g.d = A.m;
+    g.rd = A.r;
     return ns_go<NS_SYM>(g, q.gram, s);
   };
-  // d (2^13) = a I + b A + c A A of the matrix in src (2^13)
-  auto poly = [&](const _Float16* src, _Float16* d) {
+  // d (2^13) = a I + b x + c x x (x 2^13)
+  auto poly = [&](Sym x, Sym d) {
     NsGemm g = sym;
-    g.a = g.b = g.c = src;
+    g.a = g.b = g.c = x.m;
+    g.ra = g.rb = x.r;
     g.K = q.Sp;
     g.alpha = NS_C * dn13;
     g.beta = NS_B;
     g.diag = NS_A * up13;
-    g.d = d;
+    g.d = d.m;
+    g.rd = d.r;
     return ns_go<NS_SYM>(g, q.square, s);
   };
   // d = x y of commuting symmetric matrices, times alpha
-  auto mul = [&](const _Float16* x, const _Float16* y, float alpha, _Float16* d) {
+  auto mul = [&](Sym x, Sym y, float alpha, Sym d) {
     NsGemm g = sym;
-    g.a = x;
-    g.b = y;
+    g.a = x.m;
+    g.b = y.m;
+    g.ra = x.r;
+    g.rb = y.r;
     g.K = q.Sp;
     g.alpha = alpha;
-    g.d = d;
+    g.d = d.m;
+    g.rd = d.r;
     return ns_go<NS_SYM>(g, q.square, s);
   };
-  // X (from buffer k, hi + lo when two) times f (2^logf) into the other buffer
+  // X (in buffer k; hi + lo when two) times f into the other buffer
   NsGemm prod{};
   prod.M = q.Lp;
   prod.N = prod.K = q.Sp;
-  auto step = [&](int k, bool two, const _Float16* f, float alpha, bool keep_lo) {
+  int k = 0;
+  auto next = [&](bool two, Sym f, float alpha, bool keep_lo) {
     NsGemm g = prod;
     g.a = at(q.xh[k]);
     g.a2 = two ? at(q.xl[k]) : nullptr;
-    g.b = f;
+    g.b = f.m;
+    g.rb = f.r;
     g.alpha = alpha;
-    g.d = at(q.xh[k ^ 1]);
-    g.lo = keep_lo ? at(q.xl[k ^ 1]) : nullptr;
+    k ^= 1;
+    g.d = at(q.xh[k]);
+    g.lo = keep_lo ? at(q.xl[k]) : nullptr;
     g.dt = at(q.xs);
     return ns_go<NS_PROD>(g, ns_pick<NS_PROD>(g), s);
   };
@@ -778,12 +839,6 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     e = (call);                         \
     if (e != hipSuccess) return e;      \
   } while (0)
-  int k = 0;  // buffer that holds X
-  auto next = [&](bool two, const _Float16* f, float alpha, bool keep_lo) {
-    const hipError_t r = step(k, two, f, alpha, keep_lo);
-    k ^= 1;
-    return r;
-  };
   // steps 0 and 1 together: P_0, T = P_0 A_0, A_1 = P_0 T, P_1, Q = P_1 P_0 (2^11),
   // X_2 = Q X_0 (one by one they took 74 us in place of 77 at 512 x 512, a launch
   // less, but 179 in place of 170 at 1024 x 2048 and 1939 of 1936 at 4096 x 4096)
@@ -805,7 +860,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   NS_DO(poly(A, P));
   NsGemm g = prod;
   g.a = at(q.xh[k]);
-  g.b = P;
+  g.b = P.m;
+  g.rb = P.r;
   g.alpha = dn13 / 16384.f;
   g.out = a.out;
   g.rows = a.rows;

@@ -75,6 +75,39 @@ def test_orthogonalize_matches_oracle(rows, cols):
         assert e <= FULL, (kind, e)
 
 
+def exact_on_gpu(u):
+    """ref.orthogonalize without momentum, the same formula in fp64 on the GPU
+    (CPU products of these sizes take seconds)."""
+    import torch
+    x = u.double()
+    x = x / x.norm()
+    tall = x.shape[0] > x.shape[1]
+    x = x.T.contiguous() if tall else x
+    a, b, c = ref.NS_COEFFS
+    for _ in range(ref.NS_STEPS):
+        g = x @ x.T.contiguous()
+        x = a * x + (b * g + c * (g @ g)) @ x
+    return x.T if tall else x
+
+
+# every tile size and shared depths: tiles of 32 whole and shared, 64 whole and
+# shared, 96, 128, 256, cut tiles of each
+LARGE = [(40, 2500), (2500, 40), (63, 8191), (200, 1025), (500, 6000), (6000, 500), (1000, 1024), (1100, 1300), (1900, 2000),
+         (2200, 5000), (5000, 2200), (16384, 48), (1, 16384)]
+
+
+@pytest.mark.parametrize("rows,cols", LARGE)
+def test_orthogonalize_large(rows, cols):
+    g = matrix("normal", rows, cols, rows + cols).cuda()
+    o = bm.orthogonalize(g)[0]
+    want = exact_on_gpu(g)
+    e = ((o.double() - want).norm() / want.norm()).item()
+    log(f"orthogonalize {rows} x {cols}: {e:.2e}")
+    assert e <= FULL, e
+    for _ in range(3):  # shares are added in order whoever comes last
+        assert (bm.orthogonalize(g)[0] == o).all()
+
+
 @pytest.mark.parametrize("kind", ["low", "one", "outliers"])
 @pytest.mark.parametrize("rows,cols", [(256, 256), (300, 777), (1000, 250)])
 def test_orthogonalize_hard_spectra(rows, cols, kind):
@@ -155,7 +188,7 @@ def test_orthogonalize_streams_and_graph():
     """Two streams at once and two captured graphs, replayed in turn with eager
     calls between, all equal to the eager result."""
     import torch
-    gs = [matrix("rows", 256, 384, 51).cuda(), matrix("rows", 384, 256, 52).cuda()]
+    gs = [matrix("rows", 100, 4096, 51).cuda(), matrix("rows", 384, 256, 52).cuda()]
     ms = [torch.randn_like(g) * 0.01 for g in gs]
     want = [bm.orthogonalize(g, m) for g, m in zip(gs, ms)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
