@@ -21,6 +21,7 @@
 #include "bmoe_train.h"
 #include "bmoe_update.h"
 #include "common.hpp"
+#include "step_ops.hpp"
 
 using namespace bmoe;
 

@@ -11,7 +11,7 @@
 //
 // GE = 8 (16-byte vectors) needs a width that is a multiple of 8 and 16-byte
 // aligned arrays; GE = 2 an even width; else GE = 1.
-#include "common.hpp"
+#include "step_ops.hpp"
 
 namespace bmoe {
 

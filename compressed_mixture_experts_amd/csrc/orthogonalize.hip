@@ -35,7 +35,7 @@
 // X'^T = X^T P (P symmetric), reads X as XL [L][S].  A product's epilogue
 // writes its tile both ways.  S and L are padded to multiples of 64 with zeros,
 // which stay zero.
-#include "common.hpp"
+#include "step_ops.hpp"
 
 #include <algorithm>
 #include <cmath>

@@ -8,7 +8,7 @@
 // fp64 keeps the codes independent of how the sum was split: a weight's code
 // could only differ if an fp32 number lay within about 1e-13 of the threshold
 // relative to it.
-#include "common.hpp"
+#include "step_ops.hpp"
 
 namespace bmoe {
 
