@@ -565,158 +565,162 @@ def _operand(name: str, t, shape, dtypes, device):
     return t
 
 
-def _raw_stream(device) -> int:
-    """Handle of `device`'s current stream, without a torch Stream object (0.1
-    instead of 2.7 us of a call whose kernel takes 3)."""
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
-
-
 def _on_device(fn):
-    """Run fn(tensor, ...) with the first tensor's GPU as the current
-    device, so that the launches go to that device's current stream."""
-    name = next(iter(inspect.signature(fn).parameters))
+    """Run fn(tensor, ...) with the first tensor's GPU as the current device, its
+    current stream's handle as `_stream` (read without a torch Stream object: 0.1
+    instead of 2.7 us of a call whose kernel takes 3)."""
+    sig = inspect.signature(fn)
+    public = sig.replace(parameters=[q for q in sig.parameters.values() if q.name != "_stream"])
+    name = next(iter(public.parameters))
 
     @functools.wraps(fn)
     def run(*args, **kw):
         torch = _torch()
-        first = args[0] if args else kw[name]
-        if not first.is_cuda:
-            raise ValueError(f"{fn.__name__} needs GPU tensors, got one on {first.device}")
+        first = args[0] if args else kw.get(name)
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            public.bind(*args, **kw)      # a missing argument is Python's own TypeError
+            what = f"{name} on {first.device}" if isinstance(first, torch.Tensor) else f"{name} = {first!r}"
+            raise ValueError(f"{fn.__name__} needs GPU tensors, got {what}")
         if first.dim() != 2:
             raise ValueError(f"{fn.__name__} expects a 2-D tensor, got {tuple(first.shape)}")
-        if first.device.index == torch.cuda.current_device():
-            return fn(*args, **kw)
-        with torch.cuda.device(first.device):
-            return fn(*args, **kw)
+        index = first.device.index
+        if index == torch.cuda.current_device():
+            return fn(*args, **kw, _stream=torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(index):
+            return fn(*args, **kw, _stream=torch._C._cuda_getCurrentRawStream(index))
+    run.__signature__ = public
     return run
 
 
-def _scratch(nbytes: int, device):
-    torch = _torch()
-    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name: str, a: int, b: int) -> int:
+    """What the library's size query `name` says for (a, b): sizes alone decide."""
+    n = ctypes.c_size_t(0)
+    _check(getattr(lib(), name)(a, b, ctypes.byref(n)))
+    return int(n.value)
 
 
 @_on_device
 def layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, stats: bool = True, y=None,
-                       sum_out=None):
+                       sum_out=None, *, _stream=None):
     """Row norm of s = x (+ residual): y = (s - mean) rstd gamma + beta.
     x, residual [rows][width] fp32 or bf16; gamma, beta [width] fp32 or None
     (ones, zeros).  Returns (y, s, mean, rstd): s is x itself without a
     residual, mean and rstd ([rows] fp32) are None with stats=False."""
     torch = _torch()
-    dev, kinds, f32 = x.device, (torch.float32, torch.bfloat16), (torch.float32,)
-    rows, width = x.shape
-    _operand("x", x, x.shape, kinds, dev)
-    for name, t in (("gamma", gamma), ("beta", beta)):
-        if t is not None:
-            _operand(name, t, (width,), f32, dev)
-    same = (x.dtype,)
+    dev, kind, shape = x.device, x.dtype, x.shape
+    rows, width = shape
+    _operand("x", x, shape, (torch.float32, torch.bfloat16), dev)
+    if gamma is not None:
+        _operand("gamma", gamma, (width,), (torch.float32,), dev)
+    if beta is not None:
+        _operand("beta", beta, (width,), (torch.float32,), dev)
     if residual is None:
         if sum_out is not None:
             raise ValueError("sum_out needs a residual")
     else:
-        _operand("residual", residual, x.shape, same, dev)
-        sum_out = torch.empty_like(x) if sum_out is None else _operand("sum_out", sum_out, x.shape, same, dev)
-    y = torch.empty_like(x) if y is None else _operand("y", y, x.shape, same, dev)
+        _operand("residual", residual, shape, (kind,), dev)
+        sum_out = torch.empty_like(x) if sum_out is None else _operand("sum_out", sum_out, shape, (kind,), dev)
+    y = torch.empty_like(x) if y is None else _operand("y", y, shape, (kind,), dev)
     mean = rstd = None
     if stats:
         mean, rstd = torch.empty(rows, dtype=torch.float32, device=dev), torch.empty(rows, dtype=torch.float32, device=dev)
-    _check(lib().bmoe_layer_norm_forward(rows, width, BF16 if x.dtype == torch.bfloat16 else F32, _ptr(x), _ptr(residual),
-                                         _ptr(gamma), _ptr(beta), float(eps), _ptr(sum_out), _ptr(y), _ptr(mean),
-                                         _ptr(rstd), _raw_stream(dev)))
+    _check(lib().bmoe_layer_norm_forward(
+        rows, width, BF16 if kind is torch.bfloat16 else F32, x.data_ptr(), None if residual is None else residual.data_ptr(),
+        None if gamma is None else gamma.data_ptr(), None if beta is None else beta.data_ptr(), eps,
+        None if residual is None else sum_out.data_ptr(), y.data_ptr(), mean.data_ptr() if stats else None,
+        rstd.data_ptr() if stats else None, _stream))
     return y, x if residual is None else sum_out, mean, rstd
 
 
 @_on_device
-def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None, weight_grads: bool = True, dx=None):
+def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None, weight_grads: bool = True, dx=None, *, _stream=None):
     """Backward of layer_norm_forward at its s, mean and rstd: dy [rows][width]
     fp32 or of s's dtype, d_sum [rows][width] like s or None (gradient that
     reaches s past the norm, added into dx).  Returns (dx like s, dgamma,
     dbeta [width] fp32; None with weight_grads=False)."""
     torch = _torch()
-    dev, f32 = dy.device, (torch.float32,)
-    rows, width = dy.shape
-    _operand("s", s, dy.shape, (torch.float32, torch.bfloat16), dev)
-    _operand("dy", dy, dy.shape, (torch.float32, s.dtype), dev)
+    dev, kind, shape, f32 = dy.device, s.dtype, dy.shape, (torch.float32,)
+    rows, width = shape
+    _operand("s", s, shape, (torch.float32, torch.bfloat16), dev)
+    _operand("dy", dy, shape, (torch.float32, kind), dev)
     if gamma is not None:
         _operand("gamma", gamma, (width,), f32, dev)
     _operand("mean", mean, (rows,), f32, dev)
     _operand("rstd", rstd, (rows,), f32, dev)
     if d_sum is not None:
-        _operand("d_sum", d_sum, dy.shape, (s.dtype,), dev)
-    dx = torch.empty_like(s) if dx is None else _operand("dx", dx, dy.shape, (s.dtype,), dev)
+        _operand("d_sum", d_sum, shape, (kind,), dev)
+    dx = torch.empty_like(s) if dx is None else _operand("dx", dx, shape, (kind,), dev)
     dgamma = dbeta = ws = None
     nbytes = 0
     if weight_grads:
-        dgamma, dbeta = (torch.empty(width, dtype=torch.float32, device=dev) for _ in range(2))
-        nb = ctypes.c_size_t(0)
-        _check(lib().bmoe_layer_norm_backward_workspace(rows, width, ctypes.byref(nb)))
-        nbytes = int(nb.value)
-        ws = _scratch(nbytes, dev)
-    _check(lib().bmoe_layer_norm_backward(rows, width, BF16 if s.dtype == torch.bfloat16 else F32,
-                                          BF16 if dy.dtype == torch.bfloat16 else F32, _ptr(dy), _ptr(s), _ptr(gamma),
-                                          _ptr(mean), _ptr(rstd), _ptr(d_sum), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
-                                          _ptr(ws), nbytes, _raw_stream(dev)))
+        dgamma, dbeta = torch.empty(width, dtype=torch.float32, device=dev), torch.empty(width, dtype=torch.float32, device=dev)
+        nbytes = _workspace_bytes("bmoe_layer_norm_backward_workspace", rows, width)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check(lib().bmoe_layer_norm_backward(
+        rows, width, BF16 if kind is torch.bfloat16 else F32, BF16 if dy.dtype is torch.bfloat16 else F32, dy.data_ptr(),
+        s.data_ptr(), None if gamma is None else gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        None if d_sum is None else d_sum.data_ptr(), dx.data_ptr(), dgamma.data_ptr() if weight_grads else None,
+        dbeta.data_ptr() if weight_grads else None, ws.data_ptr() if weight_grads else None, nbytes, _stream))
     return dx, dgamma, dbeta
 
 
 @_on_device
-def orthogonalize(grad, momentum=None, mu: float = 0.95, nesterov: bool = True, momentum_out=None, out=None):
+def orthogonalize(grad, momentum=None, mu: float = 0.95, nesterov: bool = True, momentum_out=None, out=None, *,
+                  _stream=None):
     """Orthogonalised update of a matrix gradient [rows][cols] (fp32 or bf16):
     momentum step M' = mu M + G (fp32, when momentum is given) and five
     Newton-Schulz steps on G + mu M' (or M', or G).  Returns (out bf16
     [rows][cols], M' or None); momentum_out may be momentum itself."""
     torch = _torch()
-    dev, f32 = grad.device, (torch.float32,)
-    rows, cols = grad.shape
-    _operand("grad", grad, grad.shape, (torch.float32, torch.bfloat16), dev)
+    dev, shape, f32 = grad.device, grad.shape, (torch.float32,)
+    rows, cols = shape
+    _operand("grad", grad, shape, (torch.float32, torch.bfloat16), dev)
     if momentum is None:
         if momentum_out is not None:
             raise ValueError("momentum_out needs a momentum")
     else:
-        _operand("momentum", momentum, grad.shape, f32, dev)
+        _operand("momentum", momentum, shape, f32, dev)
         momentum_out = (torch.empty_like(momentum) if momentum_out is None else
-                        _operand("momentum_out", momentum_out, grad.shape, f32, dev))
+                        _operand("momentum_out", momentum_out, shape, f32, dev))
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
     else:
-        _operand("out", out, grad.shape, (torch.bfloat16,), dev)
-    nb = ctypes.c_size_t(0)
-    _check(lib().bmoe_orthogonalize_workspace(rows, cols, ctypes.byref(nb)))
-    ws = _scratch(int(nb.value), dev)
-    _check(lib().bmoe_orthogonalize(rows, cols, BF16 if grad.dtype == torch.bfloat16 else F32, _ptr(grad),
-                                    _ptr(momentum), _ptr(momentum_out), float(mu), 1 if nesterov else 0, _ptr(out),
-                                    _ptr(ws), int(nb.value), _raw_stream(dev)))
+        _operand("out", out, shape, (torch.bfloat16,), dev)
+    nbytes = _workspace_bytes("bmoe_orthogonalize_workspace", rows, cols)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check(lib().bmoe_orthogonalize(rows, cols, BF16 if grad.dtype is torch.bfloat16 else F32, grad.data_ptr(),
+                                    _ptr(momentum), _ptr(momentum_out), float(mu), 1 if nesterov else 0, out.data_ptr(),
+                                    ws.data_ptr(), nbytes, _stream))
     return out, momentum_out
 
 
 @_on_device
-def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None, packed=None):
+def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None, packed=None, *, _stream=None):
     """Latent substrate step W' = (1 - decay) W - step O (W [rows][cols] fp32, O
     bf16; W' = W without O) and its ternary codes at threshold mean |W'| / 2.
     Returns (W', packed [rows][cols / 16] int32 in pack_ternary's format,
     scale: 0-d fp32 tensor mean |W'|).  w_out may be w itself (Layer.step_substrate
     writes the codes into a layer)."""
     torch = _torch()
-    dev = w.device
-    rows, cols = w.shape
-    _operand("w", w, w.shape, (torch.float32,), dev)
+    dev, shape = w.device, w.shape
+    rows, cols = shape
+    _operand("w", w, shape, (torch.float32,), dev)
     if o is None:
         if w_out is not None:
             raise ValueError("w_out needs an update o")
     else:
-        _operand("o", o, w.shape, (torch.bfloat16,), dev)
-        w_out = torch.empty_like(w) if w_out is None else _operand("w_out", w_out, w.shape, (torch.float32,), dev)
+        _operand("o", o, shape, (torch.bfloat16,), dev)
+        w_out = torch.empty_like(w) if w_out is None else _operand("w_out", w_out, shape, (torch.float32,), dev)
+    nbytes = _workspace_bytes("bmoe_substrate_step_workspace", rows, cols)
     if packed is None:
         packed = torch.empty((rows, cols // 16), dtype=torch.int32, device=dev)
     else:
         _operand("packed", packed, (rows, cols // 16), (torch.int32,), dev)
     scale = torch.empty((), dtype=torch.float32, device=dev)
-    nb = ctypes.c_size_t(0)
-    _check(lib().bmoe_substrate_step_workspace(rows, cols, ctypes.byref(nb)))
-    ws = _scratch(int(nb.value), dev)
-    _check(lib().bmoe_substrate_step(rows, cols, _ptr(w), _ptr(o), float(step), float(decay), _ptr(w_out), _ptr(packed),
-                                     _ptr(scale), _ptr(ws), int(nb.value), _raw_stream(dev)))
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check(lib().bmoe_substrate_step(rows, cols, w.data_ptr(), _ptr(o), float(step), float(decay), _ptr(w_out),
+                                     packed.data_ptr(), scale.data_ptr(), ws.data_ptr(), nbytes, _stream))
     return w if o is None else w_out, packed, scale
 
 
