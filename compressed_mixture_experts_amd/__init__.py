@@ -419,7 +419,8 @@ class Layer:
     def step_substrate(self, m: int, w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None):
         """substrate_step of latent substrate m ([d_out][d_in] fp32) with the
         codes written into this layer; weights prepared before are prepared
-        again.  Returns (W', scale)."""
+        again in the same buffer, which graphs captured from this layer read.
+        Returns (W', scale)."""
         if not 0 <= m < len(self.w_base):
             raise ValueError(f"the layer has no substrate {m}")
         d_out, d_in = 1 << int(self.phi[m].shape[1]), 1 << int(self.theta[m].shape[1])
@@ -427,7 +428,9 @@ class Layer:
             raise ValueError(f"w has shape {tuple(w.shape)}, substrate {m} is {(d_out, d_in)}")
         w, _, scale = substrate_step(w, o, step, decay, w_out=w_out, packed=self.w_base[m])
         if self._prep is not None:
-            self.prepare()
+            with _torch().cuda.device(w.device):
+                _check(lib().bmoe_prepare(ctypes.byref(self.struct), self.struct.prepared, self.struct.prepared_bytes,
+                                          _stream_handle()))
         return w, scale
 
     def kernel_names(self) -> List[str]:

@@ -332,3 +332,37 @@ def test_step_substrate_prepares_again():
         layer.step_substrate(1, w)
     with pytest.raises(ValueError):
         layer.step_substrate(0, w[:128])
+
+
+@pytest.mark.parametrize("d_ff", [0, 512])
+def test_step_substrate_under_captured_forward(d_ff):
+    """A forward captured before a substrate step replays with the step's codes:
+    the prepared weights stay where the graph reads them, and a step captured
+    itself prepares again at every replay."""
+    import torch
+    inp = wl.generate(wl.small_config(d_model=256, d_ff=d_ff, n_experts=4, top_k=2, tokens=50, act="bf16", seed_index=721))
+    layer = bm.Layer.from_inputs(inp, device="cuda").prepare()
+    kept = layer.struct.prepared
+    x = to_dev(inp.x, "bf16")
+    y = torch.empty_like(x)
+    layer.forward(x, y)
+    torch.cuda.synchronize()
+    fwd, upd = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(fwd):
+        layer.forward(x, y)
+    rows, cols = (d_ff, 256) if d_ff else (256, 256)
+    src = torch.zeros(rows, cols, device="cuda")
+    with torch.cuda.graph(upd):
+        layer.step_substrate(0, src)
+    assert layer.struct.prepared == kept
+    for k in range(3):
+        step = torch.randn(rows, cols, generator=torch.Generator().manual_seed(80 + k)).cuda()
+        if k == 1:
+            layer.step_substrate(0, step)         # eager, between replays
+        else:
+            src.copy_(step)
+            upd.replay()
+        fwd.replay()
+        inp.w_base = [ref.substrate_step(step.cpu().numpy())[1]] + list(inp.w_base[1:])
+        want = bm.Layer.from_inputs(inp, device="cuda").prepare().forward(x)
+        assert (y == want).all(), k
