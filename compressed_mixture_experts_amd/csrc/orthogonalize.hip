@@ -266,8 +266,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     int t = xcd_remap(blockIdx.x, gridDim.x);
     const int nt = (p.N + TN - 1) / TN;
     if constexpr (MODE == NS_SYM) {
-      share = t % p.split;
-      t /= p.split;
+      // an XCD's workgroups take the same share of many tiles: its L2 then holds few
+      // columns of the operand (118 -> 114 us a call at 256 x 8192, 357 -> 350 at
+      // 1024 x 8192 against all shares of few tiles)
+      const int all = int(gridDim.x) / p.split;
+      share = t / all;
+      t -= share * all;
       tile = t;
       // tiles on and above the diagonal, by bands of p.band tile rows, column by
       // column within a band: the tiles an XCD runs at a time form a block that
@@ -617,15 +621,17 @@ int ns_tiles(const NsGemm& p, int t) {
 // Time of a product in tiles of side t, `split` workgroups to a tile, in
 // microseconds: a lone tile's step of 64 takes `one` (latency and the CU's own
 // limits), all together 256 t bytes a step and workgroup from L2 into LDS at 16
-// TB/s (12 where shares read different parts of the depth) and 128 t^2 operations at 1.15 PFLOP/s (rates of whole products of 2048 x
-// 8192 on this GPU); adding a tile's shares up takes 1.4 us and more with its area
-// and their number (a symmetric product of side 64 and K = 8192 in tiles of 32:
-// 16.8 us whole, 7.6 in four shares, 5.8 in sixteen; of 512 and 8192 in tiles of
-// 64: 24.6, 11.9 in four, 11.5 in six, 16.5 in eight).
+// TB/s (13 where shares read different parts of the depth: 768 x 8192 took 261 us
+// a call with the tiles that 12 picks, 250 with 13 or more; 512 x 4096 138 with 14,
+// 136 with 13) and 128 t^2 operations at 1.15 PFLOP/s (rates of whole products of
+// 2048 x 8192 on this GPU); adding a tile's shares up takes 1.4 us and more with
+// its area and their number (a symmetric product of side 64 and K = 8192 in tiles
+// of 32: 16.8 us whole, 7.6 in four shares, 5.8 in sixteen; of 512 and 8192 in
+// tiles of 64: 24.6, 11.9 in four, 11.5 in six, 16.5 in eight).
 template <int MODE>
 double ns_time(const NsGemm& p, int t, double one, int split) {
   const int steps = p.K / NS_K * (p.a2 ? 2 : 1), n = ns_tiles<MODE>(p, t) * split;
-  const double step = std::max({one, double(n) * t * 256 / (split > 1 ? 12e6 : 16e6), double(n) * t * t * 128 / 1.15e9});
+  const double step = std::max({one, double(n) * t * 256 / (split > 1 ? 13e6 : 16e6), double(n) * t * t * 128 / 1.15e9});
   return (steps + split - 1) / split * step + (split > 1 ? 1.4 + t / 64.0 * t / 64.0 * (0.8 + 0.4 * split) : 0.0);
 }
 
