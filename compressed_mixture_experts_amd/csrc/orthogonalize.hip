@@ -11,14 +11,18 @@
 // Roundings.  A rounding of X adds noise in directions the gradient may not
 // have, and a step multiplies what is small by a = 3.44: noise of X_0 grows
 // 485-fold, that of X_2 41-fold.  A rounding of A, T, P or Q only bends P,
-// which multiplies X from the left and adds no direction to its rows.  So X_0
-// and X_2, where it matters most, are kept as hi + lo (two fp16 terms, 17
-// bits) in the products P X, and the first two steps are taken together,
-//     A_1 = P_0 A_0 P_0 = P_0 T,   Q = P_1 P_0,   X_2 = Q X_0,
+// which multiplies X from the left and adds no direction to its rows.  So up to
+// X_2, where it matters most, X is kept as hi + lo in the products P X: hi fp16 and
+// lo e4m3 (16 bits together, noise below X_3's own), whose products with P's e4m3
+// copy run at twice fp16's rate.  With X in one fp16 term throughout, a gradient
+// of rank S / 8 came out 2e-2 off, with this 3e-3; full-rank ones 1e-3.  lo in fp16
+// brings rank one from 6.5e-3 to 5e-3 and nothing else, and costs more (755 and 731
+// us at 2048 x 8192, 428 and 412 at 1300 x 6000).
+//
+// Long matrices take the first two steps together,
+//     A_1 = P_0 A_0 P_0 = P_0 T,   Q = P_1 P_0,   X_2 = Q X_0
 // (everything in A is a polynomial of A_0: the factors commute and stay
-// symmetric), which saves X_1's rounding and its two products with L.  With
-// X in one fp16 term throughout, a gradient of rank S / 8 came out 2e-2 off,
-// with this 3e-3; full-rank ones 1e-3.
+// symmetric), which saves X_1's rounding and its two products with L.
 //
 // A, P, T and Q round most where they are largest, on the diagonal, and there all
 // alike when X's rows are equally long: 48 x 16384 normal entries came out 5e-3
@@ -45,6 +49,8 @@ namespace bmoe {
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef const __attribute__((address_space(1))) void ns_glob_t;
 typedef __attribute__((address_space(3))) void ns_lds_t;
 
@@ -54,13 +60,26 @@ constexpr int NS_K = 64;            // contraction step
 constexpr int NS_SPLIT = 16;        // most workgroups that share a tile
 constexpr int NS_SHARED = 512;      // most workgroups of a product that shares tiles
 
-// The second term of v = hi + lo with 5 significant bits: hi has 11 and lo starts
-// one below, so the pair has 17, whose noise stays below that of X_3.  Products
-// of numbers whose last bits are zero take less of the power that bounds the
-// large products' clock (785 -> 770 us at 2048 x 8192; 764 with lo = 0).
-__device__ __forceinline__ _Float16 ns_lo(float v, _Float16 hi) {
-  const uint16_t b = __builtin_bit_cast(uint16_t, _Float16(v - float(hi)));
-  return __builtin_bit_cast(_Float16, uint16_t((b + 0x20u) & 0xFFC0u));
+// The second terms of four v = hi + lo: (v - hi) 2^5 as four e4m3 bytes.  hi is off
+// by at most 8 (X's entries stay below 2^15), so nothing saturates, and e4m3's last
+// subnormal place, 2^-9, is 2^-14 of X's: 2^-16 off at most, or 2^-4 of lo.
+constexpr float NS_LO = 32.f;
+__device__ __forceinline__ uint32_t ns_lo4(f32x4_t v, f16x4_t hi) {
+  int u = __builtin_amdgcn_cvt_pk_fp8_f32((v[0] - float(hi[0])) * NS_LO, (v[1] - float(hi[1])) * NS_LO, 0, false);
+  u = __builtin_amdgcn_cvt_pk_fp8_f32((v[2] - float(hi[2])) * NS_LO, (v[3] - float(hi[3])) * NS_LO, u, true);
+  return uint32_t(u);
+}
+// Eight fp16 values times f as e4m3 bytes.
+__device__ __forceinline__ uint2 ns_fp8x8(uint4 h, float f) {
+  const f16x8_t v = __builtin_bit_cast(f16x8_t, h);
+  uint32_t u[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(float(v[4 * k]) * f, float(v[4 * k + 1]) * f, 0, false);
+    w = __builtin_amdgcn_cvt_pk_fp8_f32(float(v[4 * k + 2]) * f, float(v[4 * k + 3]) * f, w, true);
+    u[k] = uint32_t(w);
+  }
+  return make_uint2(u[0], u[1]);
 }
 
 // ------------------------------------------------------------------ momentum
@@ -122,7 +141,9 @@ struct NsCast {
   int32_t parts;
   _Float16* xs;             // [Sp][Lp]
   _Float16* xh;             // [Lp][Sp]
-  _Float16* xl;             // [Lp][Sp]
+  uint8_t* xl;              // [Lp] rows of 2 Sp bytes, Sp of them second terms
+  uint8_t* zero[3];         // rows of 2 Sp bytes to clear from Sp up to a multiple of 128: Lp of
+                            // xl and of the other X's second terms, Sp of the factor's e4m3 copy
   int32_t* ticket;          // [NS_SHARED / 2], cleared
   int32_t Sp, Lp;
 };
@@ -130,7 +151,8 @@ struct NsCast {
 template <bool BF, int W>
 __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
   __shared__ double red[4];
-  __shared__ _Float16 th[64][68], tl[64][68];
+  __shared__ _Float16 th[64][68];
+  __shared__ uint32_t tl[64][17];
   const int tid = threadIdx.x;
   if (blockIdx.x == 0) c.ticket[tid] = 0;
   static_assert(NS_SHARED / 2 == 256, "one ticket per thread");
@@ -174,19 +196,20 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int lr = 16 * i + (tid >> 4);
-    f16x4_t hi, lo;
+    f32x4_t v;
+    f16x4_t hi;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float v = float(double(a.m ? ns_u(g[i][j], m[i][j], a.mu, a.nesterov) : g[i][j]) * scale);
-      hi[j] = _Float16(v);
-      lo[j] = ns_lo(v, hi[j]);
+      v[j] = float(double(a.m ? ns_u(g[i][j], m[i][j], a.mu, a.nesterov) : g[i][j]) * scale);
+      hi[j] = _Float16(v[j]);
     }
+    const uint32_t lo = ns_lo4(v, hi);
     *reinterpret_cast<f16x4_t*>(&th[lr][lc]) = hi;
-    *reinterpret_cast<f16x4_t*>(&tl[lr][lc]) = lo;
+    tl[lr][tid & 15] = lo;
     const size_t at = size_t(r0 + lr) * cp + c0 + lc;
     if (tall) {
       *reinterpret_cast<f16x4_t*>(c.xh + at) = hi;
-      *reinterpret_cast<f16x4_t*>(c.xl + at) = lo;
+      *reinterpret_cast<uint32_t*>(c.xl + 2 * at - (c0 + lc)) = lo;
     } else {
       *reinterpret_cast<f16x4_t*>(c.xs + at) = hi;
     }
@@ -196,19 +219,28 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int tcx = 16 * i + (tid >> 4);  // column of the tile, row of the transposed one
-    f16x4_t hi, lo;
+    f16x4_t hi;
+    uint32_t lo = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       hi[j] = th[lc + j][tcx];
-      lo[j] = tl[lc + j][tcx];
+      lo |= (tl[lc + j][tcx >> 2] >> (8 * (tcx & 3)) & 0xFFu) << (8 * j);
     }
     const size_t at = size_t(c0 + tcx) * rp + r0 + lc;
     if (tall) {
       *reinterpret_cast<f16x4_t*>(c.xs + at) = hi;
     } else {
       *reinterpret_cast<f16x4_t*>(c.xh + at) = hi;
-      *reinterpret_cast<f16x4_t*>(c.xl + at) = lo;
+      *reinterpret_cast<uint32_t*>(c.xl + 2 * at - (r0 + lc)) = lo;
     }
+  }
+  const int l0 = tall ? r0 : c0, s0 = tall ? c0 : r0;
+  if (c.Sp % 128 != 0 && s0 + 64 == c.Sp) {
+    const int l = l0 + (tid >> 2);
+    const size_t at = size_t(l) * 2 * c.Sp + c.Sp + 16 * (tid & 3);
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (k < 2 || l < c.Sp) *reinterpret_cast<uint4*>(c.zero[k] + at) = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -217,22 +249,29 @@ enum NsMode { NS_SYM = 0, NS_PROD = 1, NS_LAST = 2 };
 
 struct NsGemm {
   const _Float16* a;        // [M][K]
-  const _Float16* a2;       // second term of the left operand, or null
   const _Float16* b;        // [N][K]
+  const uint8_t* a8;        // NS_PROD: [M] rows of 2 K bytes, K of them the second term of a and 0
+                            // up to a multiple of 128 (the offsets of a then hold here too); or null
+  const uint8_t* b8;        // [N] such rows, b as e4m3
+  int32_t exp8;             // sum of a b scales 2^exp8 times that of a8 b8
   int32_t M, N, K;          // multiples of NS_K
+  int32_t grid, tiles;      // workgroups; NS_SYM: tiles, else tiles of a row of tiles
+  uint32_t by_tiles;        // floor(2^32 / tiles) + 1 (0 for 1): t / tiles = t by_tiles / 2^32
   float alpha;              // D = alpha sum (+ beta C + diag on the diagonal)
   const float* ra;          // [N] true over stored diagonal of a (NS_SYM; and of c) and
   const float* rb;          // of b, or null
   float* rd;                // NS_SYM: the same of d, written
   // NS_SYM: d [N][N]; c [N][N] or null
-  int32_t band;             // tile rows of a band of tiles
-  int32_t split;            // workgroups that share a tile's depth
+  int32_t band;             // tile rows of a band of tiles: 2^band
+  int32_t split, per;       // workgroups that share a tile's depth, steps of each
   float* part;              // [tiles][split][tile] their sums when split > 1
   int32_t* ticket;          // [tiles] zero before and after the product
   const _Float16* c;
   float beta, diag;
   _Float16* d;              // NS_SYM; NS_PROD: D's hi [M][N]
-  _Float16* lo;             // NS_PROD: D's lo [M][N], or null
+  uint8_t* d8;              // NS_SYM: D times f8 as e4m3 (a later product's b8), or null
+  float f8;
+  uint8_t* lo;              // NS_PROD: D's second term (a later product's a8), or null
   _Float16* dt;             // NS_PROD: D's hi transposed [N][M]
   // NS_LAST: bf16, D cut to rows x cols and transposed back when wide
   uint16_t* out;
@@ -263,47 +302,63 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   const int wm = wave % WM, wn = wave / WM;
   int tm, tn, tile = 0, share = 0;
   {
-    int t = xcd_remap(blockIdx.x, gridDim.x);
-    const int nt = (p.N + TN - 1) / TN;
+    // one read of all that the loads' addresses need, and no division: what happens
+    // before the first loads is on every product's path (82.4 -> 78.9 us a
+    // call at 512 x 512, 219.8 -> 212 at 1024 x 4096)
+    asm volatile("" ::"s"(p.a), "s"(p.b), "s"(p.M), "s"(p.N), "s"(p.K), "s"(p.grid), "s"(p.tiles), "s"(p.by_tiles),
+                 "s"(p.band), "s"(p.split), "s"(p.per));
+    int t = xcd_remap(blockIdx.x, p.grid);
+    // t / p.tiles: right below 2^32 / p.tiles (at most 512 tiles to a row, at most
+    // NS_SHARED workgroups that share tiles)
+    auto quotient = [&]() { return p.by_tiles ? int(__umulhi(uint32_t(t), p.by_tiles)) : t; };
     if constexpr (MODE == NS_SYM) {
       // an XCD's workgroups take the same share of many tiles: its L2 then holds few
       // columns of the operand (118 -> 114 us a call at 256 x 8192, 357 -> 350 at
       // 1024 x 8192 against all shares of few tiles)
-      const int all = int(gridDim.x) / p.split;
-      share = t / all;
-      t -= share * all;
+      if (p.split > 1) {
+        share = quotient();
+        t -= share * p.tiles;
+      }
       tile = t;
-      // tiles on and above the diagonal, by bands of p.band tile rows, column by
+      // tiles on and above the diagonal, by bands of 2^p.band tile rows, column by
       // column within a band: the tiles an XCD runs at a time form a block that
       // needs few row blocks of the operand in its L2
       static_assert(MODE != NS_SYM || TM == TN, "mirrored tiles are square");
-      const int h = p.band;
+      const int nt = (p.N + TN - 1) / TN, h = 1 << p.band;
       int r0 = 0;
       for (;; r0 += h) {
         const int hh = min(h, nt - r0), band = hh * (nt - r0) - hh * (hh - 1) / 2;
         if (t < band) break;
         t -= band;
       }
-      tn = r0;
-      for (int n = 1; t >= n; n = min(h, tn - r0 + 1)) {
-        t -= n;
-        ++tn;
+      // columns of 1, 2, .. h - 1 tiles, then of h
+      int c = 0;
+      const int few = h * (h - 1) / 2;
+      if (t >= few) {
+        t -= few;
+        c = h - 1 + (t >> p.band);
+        t &= h - 1;
+      } else {
+        while (t > c) t -= ++c;
       }
+      tn = r0 + c;
       tm = r0 + t;
     } else {
-      tm = t / nt;
-      tn = t % nt;
+      tm = quotient();
+      tn = t - tm * p.tiles;
     }
   }
   const int m0 = tm * TM, n0 = tn * TN;
   const int K = p.K, nk1 = K / NS_K;
   // this workgroup's steps: k0 .. k0 + nk - 1
-  int k0 = 0, nk = MODE != NS_SYM && p.a2 ? 2 * nk1 : nk1;
+  int k0 = 0, nk = nk1;
   if constexpr (MODE == NS_SYM) {
-    const int per = (nk1 + p.split - 1) / p.split;
-    k0 = share * per;
-    nk = min(per, nk1 - k0);
+    k0 = share * p.per;
+    nk = min(p.per, nk1 - k0);
   }
+  const int nkh = nk;  // steps in fp16, then those of the second term: 128 deep
+  const bool two = MODE == NS_PROD && p.a8;
+  if (two) nk += (nk1 + 1) / 2;
   // a load fills 8 rows of 64; a wave's loads are all of A or all of B.  Byte
   // offsets of this lane's pieces in it; 8-row groups past the matrix (M and N
   // are multiples of 8) read its last one and are not stored
@@ -316,16 +371,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     const int row = (isb ? min(n0 + 8 * q - TM, p.N - 8) : min(m0 + 8 * q, p.M - 8)) + (lane >> 3);
     off[j] = 2u * (uint32_t(row) * uint32_t(K) + 8u * ((lane & 7) ^ (lane >> 3)));
   }
-  // this wave's loads of step kt (past the last one: the last one again, never
-  // read) into ring place `buf`
-  auto load = [&](int kt, int buf) {
-    kt = k0 + min(kt, nk - 1);
-    const char* src = reinterpret_cast<const char*>(isb ? p.b : kt >= nk1 ? p.a2 : p.a) +
-                      size_t(kt >= nk1 ? kt - nk1 : kt) * (2 * NS_K);
+  // pieces j0 .. j1 - 1 of this wave's loads of step kt (past the last one: the last
+  // one again, never read) into ring place `buf`
+  auto load = [&](int kt, int buf, int j0 = 0, int j1 = 64) {
+    kt = min(kt, nk - 1);
+    const bool second = MODE == NS_PROD && kt >= nkh;
+    const char* src = second ? reinterpret_cast<const char*>(isb ? p.b8 : p.a8) : reinterpret_cast<const char*>(isb ? p.b : p.a);
+    src += size_t(second ? kt - nkh : k0 + kt) * (2 * NS_K);
     _Float16* dst = sm + buf * STAGE + wave * LPW * 8 * NS_K;
 #pragma unroll
     for (int j = 0; j < LPW; ++j)
-      __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + off[j]), (ns_lds_t*)(dst + 8 * j * NS_K), 16, 0, 0);
+      if (j >= j0 && j < j1)
+        __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + off[j]), (ns_lds_t*)(dst + 8 * j * NS_K), 16, 0, 0);
   };
   // the ratios of this lane's rows and columns (1 past the matrix), read behind
   // the first steps' loads: ahead of them or in the epilogue their latency shows
@@ -369,7 +426,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   // loads evenly among the others; nothing crosses the region's end
   auto spread = [&](auto loads) {
     constexpr int NL = decltype(loads)::value, REST = IM * IN - IM - IN;
-    constexpr int GAP = NL > 0 && REST / NL > 0 ? REST / NL : 1;
+    constexpr int GAP = NL > 0 && REST / std::max(NL, 1) > 0 ? REST / std::max(NL, 1) : 1;
 #pragma unroll
     for (int m = 0; m < IM + IN; ++m) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -394,9 +451,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   load(NBUF - 1, NBUF - 1);
   if constexpr (MODE == NS_SYM) ratios(p.ra, ram, ran);
   ratios(p.rb, rbm, rbn);
+  if constexpr (MODE == NS_SYM)
+    asm volatile("" ::"s"(p.d), "s"(p.c), "s"(p.d8), "s"(p.f8), "s"(p.rd), "s"(p.alpha), "s"(p.beta), "s"(p.diag));
   read(0, 0, fa[0], fb[0]);
   int buf = 0;
-  for (int kt = 0; kt < nk; ++kt) {
+  for (int kt = 0; kt < nkh; ++kt) {
     const int next = buf + 1 == NBUF ? 0 : buf + 1;
     read(buf, 1, fa[1], fb[1]);
     mul(fa[0], fb[0]);
@@ -411,6 +470,54 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     mul(fa[1], fb[1]);
     spread(std::integral_constant<int, LPW>{});
     buf = next;
+  }
+  if constexpr (MODE == NS_PROD) {
+    // the second term's steps: 128 bytes of a row are 128 deep, and lane group g takes
+    // the chunks g and 4 + g of both operands.  The fragments are as large as both
+    // halves' above, so there is one set: the lower blocks' rows are read among the
+    // upper ones' products and the other way round, each column block's as soon as
+    // its last product is issued.
+    if (two) {
+      constexpr int H = IM / 2, R = IM - H;
+      i32x8_t ea[IM], eb[IN];
+      auto read8 = [&](int buf, int row) {
+        const _Float16* q = sm + buf * STAGE + (row + l16) * NS_K;
+        const int ch = 8 * (g ^ (l16 & 7));
+        const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(q + ch), hi = *reinterpret_cast<const i32x4_t*>(q + (ch ^ 32));
+        return i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      };
+      auto mul8 = [&](int i, int j) {
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(eb[i], ea[j], acc[i][j], 0, 0, 0, 127 + p.exp8, 0, 127);
+      };
+#pragma unroll
+      for (int i = 0; i < IN; ++i) eb[i] = read8(buf, TM + PN * wn + 16 * i);
+#pragma unroll
+      for (int j = 0; j < H; ++j) ea[j] = read8(buf, PM * wm + 16 * j);
+      for (int kt = nkh; kt < nk; ++kt) {
+        const int next = buf + 1 == NBUF ? 0 : buf + 1;
+#pragma unroll
+        for (int i = 0; i < IN; ++i) {
+#pragma unroll
+          for (int j = H + i * R / IN; j < H + (i + 1) * R / IN; ++j) ea[j] = read8(buf, PM * wm + 16 * j);
+#pragma unroll
+          for (int j = 0; j < H; ++j) mul8(i, j);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        arrive();
+        if constexpr (EARLY) load(kt + NBUF, buf);
+#pragma unroll
+        for (int i = 0; i < IN; ++i) {
+#pragma unroll
+          for (int j = H; j < IM; ++j) mul8(i, j);
+          eb[i] = read8(next, TM + PN * wn + 16 * i);
+#pragma unroll
+          for (int j = i * H / IN; j < (i + 1) * H / IN; ++j) ea[j] = read8(next, PM * wm + 16 * j);
+          if constexpr (!EARLY) load(kt + NBUF, buf, i * LPW / IN, (i + 1) * LPW / IN);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        buf = next;
+      }
+    }
   }
   // loads past the last step may still be writing to the ring
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -545,8 +652,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
       }
       return o;
     });
-    direct(p.d + size_t(m0) * p.N + n0, p.N);
-    if (tm != tn) transposed(p.d + size_t(n0) * p.N + m0, p.N);
+    // eight values to d, and to its e4m3 copy
+    auto put = [&](int row, int col, uint4 u) {
+      *reinterpret_cast<uint4*>(p.d + size_t(row) * p.N + col) = u;
+      if (p.d8) *reinterpret_cast<uint2*>(p.d8 + 2 * size_t(row) * p.N + col) = ns_fp8x8(u, p.f8);
+    };
+    pieces([&](int r, int c) { put(m0 + r, n0 + c, row8(r, c)); });
+    if (tm != tn) tpieces([&](int c, int r) { put(n0 + c, m0 + r, column8(c, r)); });
     // the ratios, 1 where the stored value is subnormal and its rounding coarse; at
     // the end, where no barrier waits for the stores
     if (tm == tn) {
@@ -568,15 +680,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     direct(p.d + size_t(m0) * p.N + n0, p.N);
     transposed(p.dt + size_t(n0) * p.M + m0, p.M);
     if (p.lo) {
+      constexpr int SW = TN / 4 + 1;  // row stride of the staged bytes (words)
+      uint32_t* s8 = reinterpret_cast<uint32_t*>(sm);
       __syncthreads();
-      staged([&](f32x4_t a, int, int, int i, int) {
-        a *= p.alpha * rbn[i];
-        f16x4_t o;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[r] = ns_lo(a[r], _Float16(a[r]));
-        return o;
+      for (int j = 0; j < IM; ++j)
+#pragma unroll
+        for (int i = 0; i < IN; ++i) {
+          const f32x4_t v = acc[i][j] * (p.alpha * rbn[i]);
+          f16x4_t hi;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) hi[r] = _Float16(v[r]);
+          s8[(PM * wm + 16 * j + l16) * SW + (PN * wn + 16 * i) / 4 + g] = ns_lo4(v, hi);
+        }
+      __syncthreads();
+      pieces([&](int r, int c) {
+        const uint32_t* q = s8 + r * SW + c / 4;
+        *reinterpret_cast<uint2*>(p.lo + 2 * size_t(m0 + r) * p.N + n0 + c) = make_uint2(q[0], q[1]);
       });
-      direct(p.lo + size_t(m0) * p.N + n0, p.N);
     }
   } else {
     staged([&](f32x4_t a, int, int, int i, int) {
@@ -630,7 +751,7 @@ int ns_tiles(const NsGemm& p, int t) {
 // tiles of 64: 24.6, 11.9 in four, 11.5 in six, 16.5 in eight).
 template <int MODE>
 double ns_time(const NsGemm& p, int t, double one, int split) {
-  const int steps = p.K / NS_K * (p.a2 ? 2 : 1), n = ns_tiles<MODE>(p, t) * split;
+  const int nk = p.K / NS_K, steps = p.a8 ? nk + (nk + 1) / 2 : nk, n = ns_tiles<MODE>(p, t) * split;
   const double step = std::max({one, double(n) * t * 256 / (split > 1 ? 13e6 : 16e6), double(n) * t * t * 128 / 1.15e9});
   return (steps + split - 1) / split * step + (split > 1 ? 1.4 + t / 64.0 * t / 64.0 * (0.8 + 0.4 * split) : 0.0);
 }
@@ -670,7 +791,7 @@ NsTile ns_pick(const NsGemm& p) {
 }
 
 struct NsPlan {
-  size_t part, xs, xh[2], xl[2], m[4], r[4], shares, ticket, total;
+  size_t part, xs, xh[2], xl[2], m[4], r[4], m8, shares, ticket, total;
   int S, L, Sp, Lp;
   NsTile gram, square;      // tiles of X X^T and of the products of side S
 };
@@ -698,6 +819,7 @@ NsPlan ns_plan(int rows, int cols) {
     q.m[k] = take(s);
     q.r[k] = take(size_t(q.Sp) * 4);
   }
+  q.m8 = take(s);
   size_t shares = 0;
   auto pick = [&](int depth) {
     NsGemm g{};
@@ -723,9 +845,13 @@ hipError_t ns_tile(NsGemm p, int split, hipStream_t s) {
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
   if (e != hipSuccess) return e;
   const int tiles = ns_tiles<MODE>(p, T);
+  p.grid = tiles * split;
+  p.tiles = MODE == NS_SYM ? tiles : (p.N + T - 1) / T;
+  p.by_tiles = p.tiles > 1 ? uint32_t((uint64_t(1) << 32) / uint32_t(p.tiles)) + 1 : 0;
   p.split = split;
-  // as high as the block of tiles of one of the eight XCDs is wide
-  if (MODE == NS_SYM) p.band = std::max(1, int(std::lround(std::sqrt(tiles / 8.0))));
+  p.per = (p.K / NS_K + split - 1) / split;
+  // about as high as the block of tiles of one of the eight XCDs is wide
+  p.band = std::max(0, int(std::lround(std::log2(tiles / 8.0) / 2)));
   hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * split)), dim3(64 * WM * WN), lds, s, p);
   return hipGetLastError();
 }
@@ -757,7 +883,10 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   const bool v4 = a.cols % 4 == 0 && al(a.grad, a.grad_bf16 ? 8 : 16) && al(a.m, 16) && al(a.m_out, 16);
   const size_t nb = ((v4 ? n / 4 : n) + 255) / 256;
   const int blocks = int(nb < NS_SUMS ? nb : NS_SUMS);
-  const NsCast c{part, blocks, at(q.xs), at(q.xh[0]), at(q.xl[0]), reinterpret_cast<int32_t*>(ws + q.ticket), q.Sp, q.Lp};
+  auto bytes = [&](size_t off) { return reinterpret_cast<uint8_t*>(ws + off); };
+  int32_t* ticket = reinterpret_cast<int32_t*>(ws + q.ticket);
+  const NsCast c{part, blocks, at(q.xs), at(q.xh[0]), bytes(q.xl[0]), {bytes(q.xl[0]), bytes(q.xl[1]), bytes(q.m8)},
+                 ticket, q.Sp, q.Lp};
   const unsigned tiles = unsigned((q.Sp / 64) * (q.Lp / 64));
   hipError_t e = hipSuccess;
   auto head = [&](auto bf, auto w) {
@@ -775,17 +904,21 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
 
   constexpr float up13 = 8192.f, dn13 = 1.f / 8192.f;
-  // a symmetric matrix and the ratios of its true diagonal to the stored one
+  // a symmetric matrix and the ratios of its true diagonal to the stored one; with
+  // an exponent it is the factor of a two-term X, whose second term takes it as
+  // e4m3 times 2^-e8 (P at most 3.45 times 2^13 and Q at most 11.9 times 2^11: 221
+  // and 381 of e4m3's 448)
   struct Sym {
     _Float16* m;
     float* r;
+    int e8 = 0;
   };
-  auto matrix = [&](int k) { return Sym{at(q.m[k]), reinterpret_cast<float*>(ws + q.r[k])}; };
-  const Sym A = matrix(0), T = matrix(1), P = matrix(2), Q = matrix(3);
+  auto matrix = [&](int k, int e8 = 0) { return Sym{at(q.m[k]), reinterpret_cast<float*>(ws + q.r[k]), e8}; };
+  const Sym A = matrix(0), T = matrix(1), P = matrix(2), P2 = matrix(2, 7), Q = matrix(3, 6);
   NsGemm sym{};
   sym.M = sym.N = q.Sp;
   sym.part = reinterpret_cast<float*>(ws + q.shares);
-  sym.ticket = reinterpret_cast<int32_t*>(ws + q.ticket);
+  sym.ticket = ticket;
   // A (2^13) = XS XS^T, factors 2^14 each
   auto gram = [&]() {
     NsGemm g = sym;
@@ -807,6 +940,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     g.diag = NS_A * up13;
     g.d = d.m;
     g.rd = d.r;
+    g.d8 = d.e8 ? bytes(q.m8) : nullptr;
+    g.f8 = std::ldexp(1.f, -d.e8);
     return ns_go<NS_SYM>(g, q.square, s);
   };
   // d = x y of commuting symmetric matrices, times alpha
@@ -820,23 +955,29 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     g.alpha = alpha;
     g.d = d.m;
     g.rd = d.r;
+    g.d8 = d.e8 ? bytes(q.m8) : nullptr;
+    g.f8 = std::ldexp(1.f, -d.e8);
     return ns_go<NS_SYM>(g, q.square, s);
   };
-  // X (in buffer k; hi + lo when two) times f into the other buffer
+  // X (in buffer k; hi + lo where f has an e4m3 copy) times f into the other buffer
   NsGemm prod{};
   prod.M = q.Lp;
   prod.N = prod.K = q.Sp;
   int k = 0;
-  auto next = [&](bool two, Sym f, float alpha, bool keep_lo) {
+  auto next = [&](Sym f, float alpha, bool keep_lo) {
     NsGemm g = prod;
     g.a = at(q.xh[k]);
-    g.a2 = two ? at(q.xl[k]) : nullptr;
     g.b = f.m;
+    if (f.e8) {
+      g.a8 = bytes(q.xl[k]);
+      g.b8 = bytes(q.m8);
+      g.exp8 = f.e8 - 5;  // NS_LO = 2^5
+    }
     g.rb = f.r;
     g.alpha = alpha;
     k ^= 1;
     g.d = at(q.xh[k]);
-    g.lo = keep_lo ? at(q.xl[k]) : nullptr;
+    g.lo = keep_lo ? bytes(q.xl[k]) : nullptr;
     g.dt = at(q.xs);
     return ns_go<NS_PROD>(g, ns_pick<NS_PROD>(g), s);
   };
@@ -845,21 +986,32 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     e = (call);                         \
     if (e != hipSuccess) return e;      \
   } while (0)
-  // steps 0 and 1 together: P_0, T = P_0 A_0, A_1 = P_0 T, P_1, Q = P_1 P_0 (2^11),
-  // X_2 = Q X_0 (one by one they took 74 us in place of 77 at 512 x 512, a launch
-  // less, but 179 in place of 170 at 1024 x 2048 and 1939 of 1936 at 4096 x 4096)
-  NS_DO(gram());
-  NS_DO(poly(A, P));
-  NS_DO(mul(P, A, dn13, T));
-  NS_DO(mul(P, T, dn13, A));
-  NS_DO(poly(A, T));
-  NS_DO(mul(T, P, 1.f / 32768.f, Q));
-  NS_DO(next(true, Q, 1.f / 2048.f, true));
-  // step 2 from two terms, step 3 from one
-  for (bool two : {true, false}) {
+  if (4 * q.L <= 5 * q.S) {
+    // steps 0 and 1 one by one, from two terms: a product less than together (us a
+    // call, one by one and together: 76 and 79 at 512 x 512, 133 and 137 at 1024 x
+    // 1024, 348 and 352 at 2048 x 2048; both 152 at 1024 x 1280; 176 and 171 at 1024 x
+    // 2048, 223 and 212 at 1024 x 4096)
+    for (int i = 0; i < 2; ++i) {
+      NS_DO(gram());
+      NS_DO(poly(A, P2));
+      NS_DO(next(P2, dn13, true));
+    }
+  } else {
+    // together: P_0, T = P_0 A_0, A_1 = P_0 T, P_1, Q = P_1 P_0 (2^11), X_2 = Q X_0,
+    // three products of side S for two with L
     NS_DO(gram());
     NS_DO(poly(A, P));
-    NS_DO(next(two, P, dn13, false));
+    NS_DO(mul(P, A, dn13, T));
+    NS_DO(mul(P, T, dn13, A));
+    NS_DO(poly(A, T));
+    NS_DO(mul(T, P, 1.f / 32768.f, Q));
+    NS_DO(next(Q, 1.f / 2048.f, true));
+  }
+  // step 2 from two terms, step 3 from one
+  for (const Sym& f : {P2, P}) {
+    NS_DO(gram());
+    NS_DO(poly(A, f));
+    NS_DO(next(f, dn13, false));
   }
   // step 4: X_5 (unscaled) in bf16
   NS_DO(gram());

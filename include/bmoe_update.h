@@ -35,12 +35,12 @@ extern "C" {
  * than about 1e-3 of ||U||_F, its singular vectors stay.  O = X.
  *
  * Precision.  Products run on the matrix cores in fp16 with fp32 sums, every
- * factor scaled by a power of two to the middle of fp16's range; X is kept as a
- * sum of two fp16 terms where a rounding of it would grow most, and the
+ * factor scaled by a power of two to the middle of fp16's range; X is kept as
+ * fp16 and an 8-bit second term where a rounding of it would grow most, and the
  * symmetric factors' diagonals are corrected in fp32.  Measured
  * ||O - O_exact|| / ||O_exact|| before O's rounding to bf16 (1.7e-3 by itself):
  * below 1e-3 for gradients of full rank whose singular values fall off like
- * 1 / k or slower, 3e-3 at rank min(rows, cols) / 8, 5e-3 at rank one.  M' is
+ * 1 / k or slower, 3e-3 at rank min(rows, cols) / 8, 7e-3 at rank one.  M' is
  * fp32.  A NaN or an infinity in U makes all of O NaN.
  *
  * rows, cols in [1, 16384].
