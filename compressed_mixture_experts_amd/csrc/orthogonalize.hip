@@ -278,8 +278,8 @@ struct NsGemm {
   int32_t rows, cols;       // of out
 };
 
-// One workgroup per TM x TN tile of D, NW = WM x WN waves of one TM / WM x TN / WN
-// part each (MFMA blocks of 16 x 16 x 32).  Both operand tiles of a 64-deep step
+// One workgroup per TM x TN tile of D, KG groups of NW = WM x WN waves of one TM /
+// WM x TN / WN part each (MFMA blocks of 16 x 16 x 32).  Both operand tiles of a 64-deep step
 // come straight into LDS (16 bytes per lane), NBUF steps in a ring, so that
 // NBUF - 1 steps are on their way while one is used.  Chunk ch (16 bytes) of row
 // r sits at ch ^ (r % 8) of its row.
@@ -288,16 +288,24 @@ struct NsGemm {
 // reads of the next half are issued among the products of the current one, and
 // the barrier that frees a ring place stands between the halves, where every
 // wave has products of its own to do on both sides.
-template <int MODE, int TM, int TN, int WM, int WN, int NBUF, bool EARLY>
-__global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
-  constexpr int NW = WM * WN, NT = 64 * NW;
+//
+// With KG = 2 a step is 128 deep and a second group of as many waves takes its
+// second half, in sums of its own that the first group's end up added to: two
+// waves per SIMD where a tile leaves registers for four waves only, at the same
+// LDS traffic (tiles of 96, X X^T of 2048 x 8192: 54 -> 50 us; tiles of 32 and 64
+// gain nothing).
+template <int MODE, int TM, int TN, int WM, int WN, int KG, int NBUF, bool EARLY>
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p) {
+  constexpr int NW = WM * WN, NT = 64 * NW * KG;
+  static_assert(KG == 1 || (KG == 2 && MODE == NS_SYM), "the second term's steps are one group's");
   constexpr int PM = TM / WM, PN = TN / WN, IM = PM / 16, IN = PN / 16;
   constexpr int STAGE = (TM + TN) * NS_K;        // halves of a ring place
   constexpr int LPW = (TM + TN) / 8 / NW;        // loads per wave and step
   constexpr int ST = TN + 4;                     // row stride of the staged tile (halves)
   static_assert((TM + TN) / 8 % NW == 0 && PM % 16 == 0 && PN % 16 == 0, "whole loads and blocks per wave");
-  extern __shared__ __attribute__((aligned(16))) _Float16 sm[];  // [NBUF][TM rows of A | TN rows of B][64]
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  extern __shared__ __attribute__((aligned(16))) _Float16 sm[];  // [NBUF][KG][TM rows of A | TN rows of B][64]
+  const int tid = threadIdx.x, lane = tid & 63, any = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = KG > 1 ? any / NW : 0, wave = KG > 1 ? any % NW : any;
   const int l16 = lane & 15, g = lane >> 4;  // row of a block, 16-byte chunk of its depth
   const int wm = wave % WM, wn = wave / WM;
   int tm, tn, tile = 0, share = 0;
@@ -356,7 +364,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     k0 = share * p.per;
     nk = min(p.per, nk1 - k0);
   }
-  const int nkh = nk;  // steps in fp16, then those of the second term: 128 deep
+  const int nkh = KG > 1 ? nk / KG : nk;  // whole steps in fp16, then those of the second term: 128 deep
   const bool two = MODE == NS_PROD && p.a8;
   if (two) nk += (nk1 + 1) / 2;
   // a load fills 8 rows of 64; a wave's loads are all of A or all of B.  Byte
@@ -374,11 +382,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   // pieces j0 .. j1 - 1 of this wave's loads of step kt (past the last one: the last
   // one again, never read) into ring place `buf`
   auto load = [&](int kt, int buf, int j0 = 0, int j1 = 64) {
-    kt = min(kt, nk - 1);
+    kt = min(KG > 1 ? kt * KG + kg : kt, nk - 1);
     const bool second = MODE == NS_PROD && kt >= nkh;
     const char* src = second ? reinterpret_cast<const char*>(isb ? p.b8 : p.a8) : reinterpret_cast<const char*>(isb ? p.b : p.a);
     src += size_t(second ? kt - nkh : k0 + kt) * (2 * NS_K);
-    _Float16* dst = sm + buf * STAGE + wave * LPW * 8 * NS_K;
+    _Float16* dst = sm + (buf * KG + kg) * STAGE + wave * LPW * 8 * NS_K;
 #pragma unroll
     for (int j = 0; j < LPW; ++j)
       if (j >= j0 && j < j1)
@@ -409,8 +417,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   f16x8_t fa[2][IM], fb[2][IN];
   auto read = [&](int buf, int h, f16x8_t (&a)[IM], f16x8_t (&b)[IN]) {
     const int ch = 8 * ((4 * h + g) ^ (l16 & 7));
-    const _Float16* A = sm + buf * STAGE + (PM * wm + l16) * NS_K + ch;
-    const _Float16* B = sm + buf * STAGE + (TM + PN * wn + l16) * NS_K + ch;
+    const _Float16* A = sm + (buf * KG + kg) * STAGE + (PM * wm + l16) * NS_K + ch;
+    const _Float16* B = sm + (buf * KG + kg) * STAGE + (TM + PN * wn + l16) * NS_K + ch;
 #pragma unroll
     for (int j = 0; j < IM; ++j) a[j] = *reinterpret_cast<const f16x8_t*>(A + 16 * j * NS_K);
 #pragma unroll
@@ -471,6 +479,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     spread(std::integral_constant<int, LPW>{});
     buf = next;
   }
+  if (KG > 1 && nkh * KG + kg < nk) {  // an odd depth's last piece is the first group's
+    read(buf, 1, fa[1], fb[1]);
+    mul(fa[0], fb[0]);
+    mul(fa[1], fb[1]);
+  }
   if constexpr (MODE == NS_PROD) {
     // the second term's steps: 128 bytes of a row are 128 deep, and lane group g takes
     // the chunks g and 4 + g of both operands.  The fragments are as large as both
@@ -521,6 +534,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   }
   // loads past the last step may still be writing to the ring
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  const bool first = KG == 1 || kg == 0;  // whose sums are the tile's
+  if constexpr (KG > 1) {
+    f32x4_t* q = reinterpret_cast<f32x4_t*>(sm) + wave * 64 + lane;
+    if (!first) {
+#pragma unroll
+      for (int i = 0; i < IN; ++i)
+#pragma unroll
+        for (int j = 0; j < IM; ++j) q[(i * IM + j) * 64 * NW] = acc[i][j];
+    }
+    __syncthreads();
+    if (first) {
+#pragma unroll
+      for (int i = 0; i < IN; ++i)
+#pragma unroll
+        for (int j = 0; j < IM; ++j) acc[i][j] += q[(i * IM + j) * 64 * NW];
+    }
+    __syncthreads();
+  }
 
   if constexpr (MODE == NS_SYM) {
     if (p.split > 1) {
@@ -529,20 +560,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
       // XCDs' L2s do not see each other's writes, so the sums are stored past them
       // and read past them (agent scope); a fence that writes the whole L2 back
       // instead cost 54 us a product.
-      constexpr int PAIRS = IM * IN * 2;
+      constexpr int PAIRS = IM * IN * 2, NS = 64 * NW;  // pairs of sums, threads that hold them
       typedef float f32x2_t __attribute__((ext_vector_type(2)));
       unsigned long long* own =
-          reinterpret_cast<unsigned long long*>(p.part) + (size_t(tile) * p.split + share) * PAIRS * NT + tid;
+          reinterpret_cast<unsigned long long*>(p.part) + (size_t(tile) * p.split + share) * PAIRS * NS + tid;
+      if (first) {
 #pragma unroll
-      for (int i = 0; i < IN; ++i)
+        for (int i = 0; i < IN; ++i)
 #pragma unroll
-        for (int j = 0; j < IM; ++j)
+          for (int j = 0; j < IM; ++j)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const f32x2_t v = {acc[i][j][2 * h], acc[i][j][2 * h + 1]};
-            __hip_atomic_store(own + ((i * IM + j) * 2 + h) * NT, __builtin_bit_cast(unsigned long long, v),
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          }
+            for (int h = 0; h < 2; ++h) {
+              const f32x2_t v = {acc[i][j][2 * h], acc[i][j][2 * h + 1]};
+              __hip_atomic_store(own + ((i * IM + j) * 2 + h) * NS, __builtin_bit_cast(unsigned long long, v),
+                                 __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+      }
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // they are there before the ticket says so
       __syncthreads();
       int* last = reinterpret_cast<int*>(sm);
@@ -553,16 +586,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
       __syncthreads();
       if (!*last) return;
       const unsigned long long* all =
-          reinterpret_cast<const unsigned long long*>(p.part) + size_t(tile) * p.split * PAIRS * NT + tid;
+          reinterpret_cast<const unsigned long long*>(p.part) + size_t(tile) * p.split * PAIRS * NS + tid;
       constexpr int G = 32 / PAIRS > 0 ? 32 / PAIRS : 1;  // shares read at a time
-      for (int q0 = 0; q0 < p.split; q0 += G) {
+      for (int q0 = 0; first && q0 < p.split; q0 += G) {
         unsigned long long v[G][PAIRS];
 #pragma unroll
         for (int q = 0; q < G; ++q)
           if (q0 + q < p.split)
 #pragma unroll
             for (int k = 0; k < PAIRS; ++k)
-              v[q][k] = __hip_atomic_load(all + (size_t(q0 + q) * PAIRS + k) * NT, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+              v[q][k] = __hip_atomic_load(all + (size_t(q0 + q) * PAIRS + k) * NS, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
         for (int q = 0; q < G; ++q)
           if (q0 + q < p.split)
@@ -582,13 +615,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
   _Float16* st = sm;  // [TM][ST]
   // f(four sums of consecutive columns, row, first column, blocks) to the staged tile
   auto staged = [&](auto&& f) {
+    if (first) {
 #pragma unroll
-    for (int j = 0; j < IM; ++j)
+      for (int j = 0; j < IM; ++j)
 #pragma unroll
-      for (int i = 0; i < IN; ++i) {
-        const int m = PM * wm + 16 * j + l16, n = PN * wn + 16 * i + 4 * g;
-        *reinterpret_cast<f16x4_t*>(st + m * ST + n) = f(acc[i][j], m, n, i, j);
-      }
+        for (int i = 0; i < IN; ++i) {
+          const int m = PM * wm + 16 * j + l16, n = PN * wn + 16 * i + 4 * g;
+          *reinterpret_cast<f16x4_t*>(st + m * ST + n) = f(acc[i][j], m, n, i, j);
+        }
+    }
     __syncthreads();
   };
   auto row8 = [&](int r, int c) {
@@ -661,7 +696,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void ns_gemm_kernel(NsGemm p) {
     if (tm != tn) tpieces([&](int c, int r) { put(n0 + c, m0 + r, column8(c, r)); });
     // the ratios, 1 where the stored value is subnormal and its rounding coarse; at
     // the end, where no barrier waits for the stores
-    if (tm == tn) {
+    if (tm == tn && first) {
 #pragma unroll
       for (int j = 0; j < IM; ++j) {
         const int ml = PM * wm + 16 * j + l16, nl = ml - PN * wn;  // its column in this wave's part
@@ -837,11 +872,11 @@ NsPlan ns_plan(int rows, int cols) {
   return q;
 }
 
-template <int MODE, int T, int WM, int WN, int NBUF>
+template <int MODE, int T, int WM, int WN, int KG, int NBUF>
 hipError_t ns_tile(NsGemm p, int split, hipStream_t s) {
-  constexpr size_t ring = size_t(NBUF) * 2 * T * NS_K * 2, stage = size_t(T) * (T + 4) * 2;
+  constexpr size_t ring = size_t(NBUF) * KG * 2 * T * NS_K * 2, stage = size_t(T) * (T + 4) * 2;
   constexpr size_t lds = ring > stage ? ring : stage;
-  const auto kernel = ns_gemm_kernel<MODE, T, T, WM, WN, NBUF, T <= 64>;
+  const auto kernel = ns_gemm_kernel<MODE, T, T, WM, WN, KG, NBUF, T <= 64>;
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
   if (e != hipSuccess) return e;
   const int tiles = ns_tiles<MODE>(p, T);
@@ -852,20 +887,20 @@ hipError_t ns_tile(NsGemm p, int split, hipStream_t s) {
   p.per = (p.K / NS_K + split - 1) / split;
   // about as high as the block of tiles of one of the eight XCDs is wide
   p.band = std::max(0, int(std::lround(std::log2(tiles / 8.0) / 2)));
-  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * split)), dim3(64 * WM * WN), lds, s, p);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * split)), dim3(64 * WM * WN * KG), lds, s, p);
   return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t ns_go(const NsGemm& p, NsTile t, hipStream_t s) {
-  if (t.side == 32) return ns_tile<MODE, 32, 2, 2, 4>(p, t.split, s);
-  if (t.side == 64) return ns_tile<MODE, 64, 2, 2, 4>(p, t.split, s);
+  if (t.side == 32) return ns_tile<MODE, 32, 2, 2, 1, 4>(p, t.split, s);
+  if (t.side == 64) return ns_tile<MODE, 64, 2, 2, 1, 4>(p, t.split, s);
   if constexpr (MODE == NS_SYM) {
-    if (t.side == 96) return ns_tile<MODE, 96, 2, 2, 4>(p, t.split, s);
+    if (t.side == 96) return ns_tile<MODE, 96, 2, 2, 2, 3>(p, t.split, s);
   } else {
-    if (t.side == 256) return ns_tile<MODE, 256, 2, 4, 2>(p, t.split, s);
+    if (t.side == 256) return ns_tile<MODE, 256, 2, 4, 1, 2>(p, t.split, s);
   }
-  return ns_tile<MODE, 128, 2, 4, 3>(p, t.split, s);
+  return ns_tile<MODE, 128, 2, 4, 1, 3>(p, t.split, s);
 }
 
 }  // namespace
