@@ -93,7 +93,11 @@ def exact_on_gpu(u):
 # every tile size and shared depths: tiles of 32 whole and shared, 64 whole and
 # shared, 96, 128, 256, cut tiles of each
 LARGE = [(40, 2500), (2500, 40), (63, 8191), (200, 1025), (500, 6000), (6000, 500), (1000, 1024), (1100, 1300), (1900, 2000),
-         (2200, 5000), (5000, 2200), (16384, 48), (1, 16384)]
+         (2200, 5000), (5000, 2200), (16384, 48), (1, 16384),
+         # sides of an odd number of 64: a half step at the end of the second terms' depth
+         # and, in tiles of 96, one group's last piece, whole and in shares
+         (1590, 1600), (1600, 1590), (890, 8190), (1210, 8190), (8190, 1200), (2235, 2240), (1344, 1340), (700, 704),
+         (320, 8190), (330, 1340), (830, 3390)]
 
 
 @pytest.mark.parametrize("rows,cols", LARGE)
