@@ -112,6 +112,15 @@ def test_orthogonalize_large(rows, cols):
         assert (bm.orthogonalize(g)[0] == o).all()
 
 
+def test_orthogonalize_largest():
+    """The largest matrix the library takes."""
+    import torch
+    g = torch.randn(16384, 16384, generator=torch.Generator("cuda").manual_seed(5), device="cuda")
+    o = bm.orthogonalize(g)[0]
+    want = exact_on_gpu(g)
+    assert ((o.double() - want).norm() / want.norm()).item() <= FULL
+
+
 @pytest.mark.parametrize("kind", ["low", "one", "outliers"])
 @pytest.mark.parametrize("rows,cols", [(256, 256), (300, 777), (1000, 250)])
 def test_orthogonalize_hard_spectra(rows, cols, kind):
