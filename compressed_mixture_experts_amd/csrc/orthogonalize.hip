@@ -471,7 +471,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
     arrive();
     // the loads among the products behind the reads: a burst of them before the
     // reads holds its wave up (tile 256: 131 -> 123 us for X = Q X_0 at 2048 x
-    // 8192); with few products to a step (EARLY) they go first, to arrive sooner
+    // 8192 with an fp16 second term); with few products to a step (EARLY) they go
+    // first, to arrive sooner
     if constexpr (EARLY) load(kt + NBUF, buf);
     read(next, 0, fa[0], fb[0]);
     if constexpr (!EARLY) load(kt + NBUF, buf);
@@ -800,6 +801,9 @@ struct NsTile {
 // side: tiles of 32 4.1 / 8.8 / 36 us, 64 5.6 / 7.2 / 23.6, 96 8.9 / 10.2 / 18.2,
 // 128 11 / 12.0 / 20.4; general ones of 512 x 512, 4096 x 1024, 8192 x 2048: 32
 // 3.7 / 30 / 289, 64 4.5 / 18.4 / 152, 128 8 / 14.0 / 83, 256 18.2 / 27.3 / 66.
+// (96 has got faster since with its second group of waves; a smaller step for it
+// would only take it where 64, two workgroups to a CU, is better: 0.27 makes 255 of
+// 240 us a call at 1536 x 1536, 0.24 235 of 185 at 1408 x 1408.)
 template <int MODE>
 NsTile ns_pick(const NsGemm& p) {
   NsTile best{0, 1};
