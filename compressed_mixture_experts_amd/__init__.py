@@ -557,42 +557,45 @@ def substrate_input_grad(dz, wt_packed, d_in: int, alpha: float = 1.0):
 def _operand(name: str, t, shape, dtypes, device):
     """Check one tensor of a training-step operator: dense, on `device`, of the
     given shape and one of the dtypes."""
+    if t.device == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}, expected a GPU tensor on {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _on_device(fn):
-    """Run fn(tensor, ...) with the first tensor's GPU as the current device, its
-    current stream's handle as `_stream` (read without a torch Stream object: 0.1
-    instead of 2.7 us of a call whose kernel takes 3)."""
+    """Run fn(matrix, ...) with the first argument's GPU as the current device."""
     sig = inspect.signature(fn)
-    public = sig.replace(parameters=[q for q in sig.parameters.values() if q.name != "_stream"])
-    name = next(iter(public.parameters))
+    name = next(iter(sig.parameters))
 
     @functools.wraps(fn)
     def run(*args, **kw):
         torch = _torch()
         first = args[0] if args else kw.get(name)
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            public.bind(*args, **kw)      # a missing argument is Python's own TypeError
-            what = f"{name} on {first.device}" if isinstance(first, torch.Tensor) else f"{name} = {first!r}"
-            raise ValueError(f"{fn.__name__} needs GPU tensors, got {what}")
-        if first.dim() != 2:
+        if isinstance(first, torch.Tensor):
+            index = first.get_device()
+            if index >= 0 and first.dim() == 2:
+                if index == torch._C._cuda_getDevice():
+                    return fn(*args, **kw)
+                with torch.cuda.device(index):
+                    return fn(*args, **kw)
+        sig.bind(*args, **kw)      # a missing argument is Python's own TypeError
+        if isinstance(first, torch.Tensor) and first.is_cuda:
             raise ValueError(f"{fn.__name__} expects a 2-D tensor, got {tuple(first.shape)}")
-        index = first.device.index
-        if index == torch.cuda.current_device():
-            return fn(*args, **kw, _stream=torch._C._cuda_getCurrentRawStream(index))
-        with torch.cuda.device(index):
-            return fn(*args, **kw, _stream=torch._C._cuda_getCurrentRawStream(index))
-    run.__signature__ = public
+        what = f"{name} on {first.device}" if isinstance(first, torch.Tensor) else f"{name} = {first!r}"
+        raise ValueError(f"{fn.__name__} needs GPU tensors, got {what}")
     return run
+
+
+def _raw_stream(t) -> int:
+    """Handle of the current stream of t's GPU, without a torch Stream object (0.1
+    instead of 2.7 us of a call whose kernel takes 3)."""
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
 @functools.lru_cache(maxsize=4096)
@@ -605,7 +608,7 @@ def _workspace_bytes(name: str, a: int, b: int) -> int:
 
 @_on_device
 def layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, residual=None, stats: bool = True, y=None,
-                       sum_out=None, *, _stream=None):
+                       sum_out=None):
     """Row norm of s = x (+ residual): y = (s - mean) rstd gamma + beta.
     x, residual [rows][width] fp32 or bf16; gamma, beta [width] fp32 or None
     (ones, zeros).  Returns (y, s, mean, rstd): s is x itself without a
@@ -632,12 +635,12 @@ def layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, residual=Non
         rows, width, BF16 if kind is torch.bfloat16 else F32, x.data_ptr(), None if residual is None else residual.data_ptr(),
         None if gamma is None else gamma.data_ptr(), None if beta is None else beta.data_ptr(), eps,
         None if residual is None else sum_out.data_ptr(), y.data_ptr(), mean.data_ptr() if stats else None,
-        rstd.data_ptr() if stats else None, _stream))
+        rstd.data_ptr() if stats else None, _raw_stream(x)))
     return y, x if residual is None else sum_out, mean, rstd
 
 
 @_on_device
-def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None, weight_grads: bool = True, dx=None, *, _stream=None):
+def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None, weight_grads: bool = True, dx=None):
     """Backward of layer_norm_forward at its s, mean and rstd: dy [rows][width]
     fp32 or of s's dtype, d_sum [rows][width] like s or None (gradient that
     reaches s past the norm, added into dx).  Returns (dx like s, dgamma,
@@ -664,13 +667,12 @@ def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None, weight_grads: bool
         rows, width, BF16 if kind is torch.bfloat16 else F32, BF16 if dy.dtype is torch.bfloat16 else F32, dy.data_ptr(),
         s.data_ptr(), None if gamma is None else gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
         None if d_sum is None else d_sum.data_ptr(), dx.data_ptr(), dgamma.data_ptr() if weight_grads else None,
-        dbeta.data_ptr() if weight_grads else None, ws.data_ptr() if weight_grads else None, nbytes, _stream))
+        dbeta.data_ptr() if weight_grads else None, ws.data_ptr() if weight_grads else None, nbytes, _raw_stream(dy)))
     return dx, dgamma, dbeta
 
 
 @_on_device
-def orthogonalize(grad, momentum=None, mu: float = 0.95, nesterov: bool = True, momentum_out=None, out=None, *,
-                  _stream=None):
+def orthogonalize(grad, momentum=None, mu: float = 0.95, nesterov: bool = True, momentum_out=None, out=None):
     """Orthogonalised update of a matrix gradient [rows][cols] (fp32 or bf16):
     momentum step M' = mu M + G (fp32, when momentum is given) and five
     Newton-Schulz steps on G + mu M' (or M', or G).  Returns (out bf16
@@ -694,12 +696,12 @@ def orthogonalize(grad, momentum=None, mu: float = 0.95, nesterov: bool = True, 
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check(lib().bmoe_orthogonalize(rows, cols, BF16 if grad.dtype is torch.bfloat16 else F32, grad.data_ptr(),
                                     _ptr(momentum), _ptr(momentum_out), float(mu), 1 if nesterov else 0, out.data_ptr(),
-                                    ws.data_ptr(), nbytes, _stream))
+                                    ws.data_ptr(), nbytes, _raw_stream(grad)))
     return out, momentum_out
 
 
 @_on_device
-def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None, packed=None, *, _stream=None):
+def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None, packed=None):
     """Latent substrate step W' = (1 - decay) W - step O (W [rows][cols] fp32, O
     bf16; W' = W without O) and its ternary codes at threshold mean |W'| / 2.
     Returns (W', packed [rows][cols / 16] int32 in pack_ternary's format,
@@ -723,7 +725,7 @@ def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None,
     scale = torch.empty((), dtype=torch.float32, device=dev)
     ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check(lib().bmoe_substrate_step(rows, cols, w.data_ptr(), _ptr(o), float(step), float(decay), _ptr(w_out),
-                                     packed.data_ptr(), scale.data_ptr(), ws.data_ptr(), nbytes, _stream))
+                                     packed.data_ptr(), scale.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(w)))
     return w if o is None else w_out, packed, scale
 
 
