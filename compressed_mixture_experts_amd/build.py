@@ -45,6 +45,10 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I", os.path.join(ROOT, "include"),
 ]
+# of single sources: the first 13 argument registers of the orthogonalised update's
+# kernels arrive in registers, where 17 short launches in a chain would each wait
+# for a read of theirs
+FLAGS_OF = {"orthogonalize.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=13"]}
 # host-only sanitizers: each flag goes to the host compilation alone
 HOST_SANITIZE = ["-Xarch_host", "-fsanitize=address,undefined", "-Xarch_host", "-fno-sanitize-recover=undefined",
                  "-Xarch_host", "-fno-omit-frame-pointer"]
@@ -52,7 +56,7 @@ HOST_SANITIZE = ["-Xarch_host", "-fsanitize=address,undefined", "-Xarch_host", "
 
 def _compile(job) -> str:
     src, obj, extra = job
-    cmd = [HIPCC, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *FLAGS, *FLAGS_OF.get(src, []), *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True, timeout=900)
     if r.returncode != 0:
         raise RuntimeError(f"hipcc failed for {src}:\n{r.stderr}")

@@ -104,26 +104,26 @@ __device__ __forceinline__ void ns_load_grad(const void* g, size_t i, float (&v)
 
 // M' = mu M + G and the sum of U^2 (fp64 partial sums, one per workgroup).
 template <bool BF, int W>
-__global__ __launch_bounds__(256) void ns_momentum_kernel(OrthoArgs a, double* part) {
+__global__ __launch_bounds__(256) void ns_momentum_kernel(const void* grad, const float* mom, float* m_out, double* part,
+                                                           size_t n, float mu, int nesterov) {
   __shared__ double red[4];
-  const size_t n = size_t(a.rows) * a.cols;
   double s = 0.0;
   for (size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * W; i < n; i += size_t(gridDim.x) * 256 * W) {
     float g[W], m[W];
-    ns_load_grad<BF, W>(a.grad, i, g);
-    if (a.m) ns_load_grad<false, W>(a.m, i, m);
+    ns_load_grad<BF, W>(grad, i, g);
+    if (mom) ns_load_grad<false, W>(mom, i, m);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
       float u = g[j];
-      if (a.m) {
-        m[j] = fmaf(a.mu, m[j], g[j]);
-        u = ns_u(g[j], m[j], a.mu, a.nesterov);
+      if (mom) {
+        m[j] = fmaf(mu, m[j], g[j]);
+        u = ns_u(g[j], m[j], mu, nesterov);
       }
       s = fma(double(u), double(u), s);
     }
-    if (a.m) {
-      if constexpr (W == 4) *reinterpret_cast<float4*>(a.m_out + i) = make_float4(m[0], m[1], m[2], m[3]);
-      else a.m_out[i] = m[0];
+    if (mom) {
+      if constexpr (W == 4) *reinterpret_cast<float4*>(m_out + i) = make_float4(m[0], m[1], m[2], m[3]);
+      else m_out[i] = m[0];
     }
   }
 #pragma unroll
@@ -137,27 +137,25 @@ __global__ __launch_bounds__(256) void ns_momentum_kernel(OrthoArgs a, double* p
 // matrix, written in the caller's orientation from registers and transposed
 // through LDS.
 struct NsCast {
-  const double* part;       // NS_SUMS-bounded partial sums of U^2
-  int32_t parts;
   _Float16* xs;             // [Sp][Lp]
   _Float16* xh;             // [Lp][Sp]
   uint8_t* xl;              // [Lp] rows of 2 Sp bytes, Sp of them second terms
   uint8_t* zero[3];         // rows of 2 Sp bytes to clear from Sp up to a multiple of 128: Lp of
                             // xl and of the other X's second terms, Sp of the factor's e4m3 copy
   int32_t* ticket;          // [NS_SHARED / 2], cleared
-  int32_t Sp, Lp;
 };
 
 template <bool BF, int W>
-__global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
+__global__ __launch_bounds__(256) void ns_cast_kernel(const void* grad, const float* mom, const double* part, int parts,
+                                                       int rows, int cols, int Sp, int Lp, float mu, int nesterov, NsCast c) {
   __shared__ double red[4];
   __shared__ _Float16 th[64][68];
   __shared__ uint32_t tl[64][17];
   const int tid = threadIdx.x;
   if (blockIdx.x == 0) c.ticket[tid] = 0;
   static_assert(NS_SHARED / 2 == 256, "one ticket per thread");
-  const bool tall = a.rows > a.cols;
-  const int cp = tall ? c.Sp : c.Lp;  // padded columns
+  const bool tall = rows > cols;
+  const int cp = tall ? Sp : Lp;  // padded columns
   const int tc = cp / 64;
   const int r0 = int(blockIdx.x / tc) * 64, c0 = int(blockIdx.x % tc) * 64;
   const int lc = 4 * (tid & 15);
@@ -170,14 +168,14 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
     for (int j = 0; j < 4; ++j) g[i][j] = m[i][j] = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; j += W) {
-      const size_t at = size_t(r) * a.cols + c0 + lc + j;
-      if (r < a.rows && c0 + lc + j < a.cols) {
+      const size_t at = size_t(r) * cols + c0 + lc + j;
+      if (r < rows && c0 + lc + j < cols) {
         float v[W];
-        ns_load_grad<BF, W>(a.grad, at, v);
+        ns_load_grad<BF, W>(grad, at, v);
 #pragma unroll
         for (int e = 0; e < W; ++e) g[i][j + e] = v[e];
-        if (a.m) {
-          ns_load_grad<false, W>(a.m_out, at, v);
+        if (mom) {
+          ns_load_grad<false, W>(mom, at, v);
 #pragma unroll
           for (int e = 0; e < W; ++e) m[i][j + e] = v[e];
         }
@@ -185,7 +183,7 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
     }
   }
   double s = 0.0;
-  for (int p = tid; p < c.parts; p += 256) s += c.part[p];
+  for (int p = tid; p < parts; p += 256) s += part[p];
 #pragma unroll
   for (int k = 1; k < 64; k <<= 1) s += __shfl_xor(s, k);
   if ((tid & 63) == 0) red[tid >> 6] = s;
@@ -200,7 +198,7 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
     f16x4_t hi;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[j] = float(double(a.m ? ns_u(g[i][j], m[i][j], a.mu, a.nesterov) : g[i][j]) * scale);
+      v[j] = float(double(mom ? ns_u(g[i][j], m[i][j], mu, nesterov) : g[i][j]) * scale);
       hi[j] = _Float16(v[j]);
     }
     const uint32_t lo = ns_lo4(v, hi);
@@ -215,7 +213,7 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
     }
   }
   __syncthreads();
-  const int rp = tall ? c.Lp : c.Sp;  // padded rows
+  const int rp = tall ? Lp : Sp;  // padded rows
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int tcx = 16 * i + (tid >> 4);  // column of the tile, row of the transposed one
@@ -235,12 +233,12 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(OrthoArgs a, NsCast c) {
     }
   }
   const int l0 = tall ? r0 : c0, s0 = tall ? c0 : r0;
-  if (c.Sp % 128 != 0 && s0 + 64 == c.Sp) {
+  if (Sp % 128 != 0 && s0 + 64 == Sp) {
     const int l = l0 + (tid >> 2);
-    const size_t at = size_t(l) * 2 * c.Sp + c.Sp + 16 * (tid & 3);
+    const size_t at = size_t(l) * 2 * Sp + Sp + 16 * (tid & 3);
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      if (k < 2 || l < c.Sp) *reinterpret_cast<uint4*>(c.zero[k] + at) = make_uint4(0, 0, 0, 0);
+      if (k < 2 || l < Sp) *reinterpret_cast<uint4*>(c.zero[k] + at) = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -295,7 +293,9 @@ struct NsGemm {
 // LDS traffic (tiles of 96, X X^T of 2048 x 8192: 54 -> 50 us; tiles of 32 and 64
 // gain nothing).
 template <int MODE, int TM, int TN, int WM, int WN, int KG, int NBUF, bool EARLY>
-__global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p) {
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(
+    const _Float16* left, const _Float16* right, int M, int N, int K, int grid, int tiles, uint32_t by_tiles, int log_band,
+    int split, int per, NsGemm p) {
   constexpr int NW = WM * WN, NT = 64 * NW * KG;
   static_assert(KG == 1 || (KG == 2 && MODE == NS_SYM), "the second term's steps are one group's");
   constexpr int PM = TM / WM, PN = TN / WN, IM = PM / 16, IN = PN / 16;
@@ -310,29 +310,27 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
   const int wm = wave % WM, wn = wave / WM;
   int tm, tn, tile = 0, share = 0;
   {
-    // one read of all that the loads' addresses need, and no division: what happens
-    // before the first loads is on every product's path (82.4 -> 78.9 us a
-    // call at 512 x 512, 219.8 -> 212 at 1024 x 4096)
-    asm volatile("" ::"s"(p.a), "s"(p.b), "s"(p.M), "s"(p.N), "s"(p.K), "s"(p.grid), "s"(p.tiles), "s"(p.by_tiles),
-                 "s"(p.band), "s"(p.split), "s"(p.per));
-    int t = xcd_remap(blockIdx.x, p.grid);
-    // t / p.tiles: right below 2^32 / p.tiles (at most 512 tiles to a row, at most
+    // no division here: what happens before the first loads is on every product's
+    // path (with two of them and arguments read where they are used 82.4 in place of
+    // 78.9 us a call at 512 x 512, 219.8 of 212 at 1024 x 4096)
+    int t = xcd_remap(blockIdx.x, grid);
+    // t / tiles: right below 2^32 / tiles (at most 512 tiles to a row, at most
     // NS_SHARED workgroups that share tiles)
-    auto quotient = [&]() { return p.by_tiles ? int(__umulhi(uint32_t(t), p.by_tiles)) : t; };
+    auto quotient = [&]() { return by_tiles ? int(__umulhi(uint32_t(t), by_tiles)) : t; };
     if constexpr (MODE == NS_SYM) {
       // an XCD's workgroups take the same share of many tiles: its L2 then holds few
       // columns of the operand (118 -> 114 us a call at 256 x 8192, 357 -> 350 at
       // 1024 x 8192 against all shares of few tiles)
-      if (p.split > 1) {
+      if (split > 1) {
         share = quotient();
-        t -= share * p.tiles;
+        t -= share * tiles;
       }
       tile = t;
-      // tiles on and above the diagonal, by bands of 2^p.band tile rows, column by
+      // tiles on and above the diagonal, by bands of 2^log_band tile rows, column by
       // column within a band: the tiles an XCD runs at a time form a block that
       // needs few row blocks of the operand in its L2
       static_assert(MODE != NS_SYM || TM == TN, "mirrored tiles are square");
-      const int nt = (p.N + TN - 1) / TN, h = 1 << p.band;
+      const int nt = (N + TN - 1) / TN, h = 1 << log_band;
       int r0 = 0;
       for (;; r0 += h) {
         const int hh = min(h, nt - r0), band = hh * (nt - r0) - hh * (hh - 1) / 2;
@@ -344,7 +342,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       const int few = h * (h - 1) / 2;
       if (t >= few) {
         t -= few;
-        c = h - 1 + (t >> p.band);
+        c = h - 1 + (t >> log_band);
         t &= h - 1;
       } else {
         while (t > c) t -= ++c;
@@ -353,16 +351,16 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       tm = r0 + t;
     } else {
       tm = quotient();
-      tn = t - tm * p.tiles;
+      tn = t - tm * tiles;
     }
   }
   const int m0 = tm * TM, n0 = tn * TN;
-  const int K = p.K, nk1 = K / NS_K;
+  const int nk1 = K / NS_K;
   // this workgroup's steps: k0 .. k0 + nk - 1
   int k0 = 0, nk = nk1;
   if constexpr (MODE == NS_SYM) {
-    k0 = share * p.per;
-    nk = min(p.per, nk1 - k0);
+    k0 = share * per;
+    nk = min(per, nk1 - k0);
   }
   const int nkh = KG > 1 ? nk / KG : nk;  // whole steps in fp16, then those of the second term: 128 deep
   const bool two = MODE == NS_PROD && p.a8;
@@ -372,25 +370,33 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
   // are multiples of 8) read its last one and are not stored
   static_assert(TM / 8 % LPW == 0, "no wave loads both operands");
   const bool isb = wave * LPW >= TM / 8;
+  // where the fragments take all registers (tiles of 256) the first row's part, the
+  // same for the whole wave, stays in scalar ones (706 -> 699 us a call at 2048 x
+  // 8192); elsewhere the additions at every load cost more (197 -> 199 at 1024 x 4096)
+  constexpr bool SCALAR = TM == 256;
+  const uint32_t lane_off = 2u * (__umul24(lane >> 3, K) + 8u * ((lane & 7) ^ (lane >> 3)));
   uint32_t off[LPW];
 #pragma unroll
   for (int j = 0; j < LPW; ++j) {
     const int q = wave * LPW + j;
-    const int row = (isb ? min(n0 + 8 * q - TM, p.N - 8) : min(m0 + 8 * q, p.M - 8)) + (lane >> 3);
-    off[j] = 2u * (uint32_t(row) * uint32_t(K) + 8u * ((lane & 7) ^ (lane >> 3)));
+    off[j] = 2u * uint32_t(isb ? min(n0 + 8 * q - TM, N - 8) : min(m0 + 8 * q, M - 8)) * uint32_t(K);
+    if (!SCALAR) off[j] += lane_off;
   }
+  const char* base = reinterpret_cast<const char*>(isb ? right : left);
+  const char* base8 = reinterpret_cast<const char*>(isb ? p.b8 : p.a8);
   // pieces j0 .. j1 - 1 of this wave's loads of step kt (past the last one: the last
-  // one again, never read) into ring place `buf`
-  auto load = [&](int kt, int buf, int j0 = 0, int j1 = 64) {
+  // one again, never read) into ring place `buf`; the first step of all waits for no
+  // argument but the preloaded ones
+  auto load = [&](int kt, int buf, int j0 = 0, int j1 = 64, bool head = false) {
     kt = min(KG > 1 ? kt * KG + kg : kt, nk - 1);
-    const bool second = MODE == NS_PROD && kt >= nkh;
-    const char* src = second ? reinterpret_cast<const char*>(isb ? p.b8 : p.a8) : reinterpret_cast<const char*>(isb ? p.b : p.a);
+    const bool second = MODE == NS_PROD && !head && kt >= nkh;
+    const char* src = second ? base8 : base;
     src += size_t(second ? kt - nkh : k0 + kt) * (2 * NS_K);
     _Float16* dst = sm + (buf * KG + kg) * STAGE + wave * LPW * 8 * NS_K;
 #pragma unroll
     for (int j = 0; j < LPW; ++j)
       if (j >= j0 && j < j1)
-        __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + off[j]), (ns_lds_t*)(dst + 8 * j * NS_K), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds((ns_glob_t*)(src + off[j] + (SCALAR ? lane_off : 0u)), (ns_lds_t*)(dst + 8 * j * NS_K), 16, 0, 0);
   };
   // the ratios of this lane's rows and columns (1 past the matrix), read behind
   // the first steps' loads: ahead of them or in the epilogue their latency shows
@@ -400,13 +406,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
 #pragma unroll
     for (int j = 0; j < IM; ++j) {
       const int m = m0 + PM * wm + 16 * j + l16;
-      rm[j] = MODE == NS_SYM && r && m < p.M ? r[m] : 1.f;
+      rm[j] = MODE == NS_SYM && r && m < M ? r[m] : 1.f;
     }
 #pragma unroll
     for (int i = 0; i < IN; ++i) {
       const int n = n0 + PN * wn + 16 * i + 4 * g;
       rn[i] = f32x4_t{1.f, 1.f, 1.f, 1.f};
-      if (r && n < p.N) rn[i] = *reinterpret_cast<const f32x4_t*>(r + n);
+      if (r && n < N) rn[i] = *reinterpret_cast<const f32x4_t*>(r + n);
     }
   };
   f32x4_t acc[IN][IM];
@@ -454,7 +460,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * LPW) : "memory");
   };
 #pragma unroll
-  for (int b = 0; b < NBUF - 1; ++b) load(b, b);
+  for (int b = 0; b < NBUF - 1; ++b) load(b, b, 0, 64, b == 0);
   arrive();
   load(NBUF - 1, NBUF - 1);
   if constexpr (MODE == NS_SYM) ratios(p.ra, ram, ran);
@@ -555,7 +561,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
   }
 
   if constexpr (MODE == NS_SYM) {
-    if (p.split > 1) {
+    if (split > 1) {
       // the sums go to memory; the workgroup that comes last to a tile adds all of
       // them in the order of the depth and goes on alone.  Nobody waits.  The
       // XCDs' L2s do not see each other's writes, so the sums are stored past them
@@ -564,7 +570,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       constexpr int PAIRS = IM * IN * 2, NS = 64 * NW;  // pairs of sums, threads that hold them
       typedef float f32x2_t __attribute__((ext_vector_type(2)));
       unsigned long long* own =
-          reinterpret_cast<unsigned long long*>(p.part) + (size_t(tile) * p.split + share) * PAIRS * NS + tid;
+          reinterpret_cast<unsigned long long*>(p.part) + (size_t(tile) * split + share) * PAIRS * NS + tid;
       if (first) {
 #pragma unroll
         for (int i = 0; i < IN; ++i)
@@ -581,25 +587,25 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       __syncthreads();
       int* last = reinterpret_cast<int*>(sm);
       if (tid == 0) {
-        *last = __hip_atomic_fetch_add(p.ticket + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == p.split - 1;
+        *last = __hip_atomic_fetch_add(p.ticket + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == split - 1;
         if (*last) p.ticket[tile] = 0;
       }
       __syncthreads();
       if (!*last) return;
       const unsigned long long* all =
-          reinterpret_cast<const unsigned long long*>(p.part) + size_t(tile) * p.split * PAIRS * NS + tid;
+          reinterpret_cast<const unsigned long long*>(p.part) + size_t(tile) * split * PAIRS * NS + tid;
       constexpr int G = 32 / PAIRS > 0 ? 32 / PAIRS : 1;  // shares read at a time
-      for (int q0 = 0; first && q0 < p.split; q0 += G) {
+      for (int q0 = 0; first && q0 < split; q0 += G) {
         unsigned long long v[G][PAIRS];
 #pragma unroll
         for (int q = 0; q < G; ++q)
-          if (q0 + q < p.split)
+          if (q0 + q < split)
 #pragma unroll
             for (int k = 0; k < PAIRS; ++k)
               v[q][k] = __hip_atomic_load(all + (size_t(q0 + q) * PAIRS + k) * NS, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
         for (int q = 0; q < G; ++q)
-          if (q0 + q < p.split)
+          if (q0 + q < split)
 #pragma unroll
             for (int k = 0; k < PAIRS; ++k) {
               const f32x2_t w = __builtin_bit_cast(f32x2_t, v[q][k]);
@@ -649,7 +655,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       const int k = tid + NT * q;
       if (PIECES % NT != 0 && k >= PIECES) break;
       const int r = k / (TN / 8), c = 8 * (k % (TN / 8));
-      if (m0 + r < p.M && n0 + c < p.N) f(r, c);
+      if (m0 + r < M && n0 + c < N) f(r, c);
     }
   };
   auto tpieces = [&](auto&& f) {
@@ -658,7 +664,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       const int k = tid + NT * q;
       if (PIECES % NT != 0 && k >= PIECES) break;
       const int c = k / RL % TN, r = 8 * (k % RL + RL * (k / RL / TN));
-      if (m0 + r < p.M && n0 + c < p.N) f(c, r);
+      if (m0 + r < M && n0 + c < N) f(c, r);
     }
   };
   auto direct = [&](_Float16* dst, size_t ld) {
@@ -675,7 +681,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       m += m0;
       n += n0;
       f16x4_t cv = {0, 0, 0, 0}, o;
-      if (p.c && m < p.M && n < p.N) cv = *reinterpret_cast<const f16x4_t*>(p.c + size_t(m) * p.N + n);
+      if (p.c && m < M && n < N) cv = *reinterpret_cast<const f16x4_t*>(p.c + size_t(m) * N + n);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float sa = 0.5f * (ram[j] + ran[i][r]), sb = 0.5f * (rbm[j] + rbn[i][r]);
@@ -690,8 +696,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
     });
     // eight values to d, and to its e4m3 copy
     auto put = [&](int row, int col, uint4 u) {
-      *reinterpret_cast<uint4*>(p.d + size_t(row) * p.N + col) = u;
-      if (p.d8) *reinterpret_cast<uint2*>(p.d8 + 2 * size_t(row) * p.N + col) = ns_fp8x8(u, p.f8);
+      *reinterpret_cast<uint4*>(p.d + size_t(row) * N + col) = u;
+      if (p.d8) *reinterpret_cast<uint2*>(p.d8 + 2 * size_t(row) * N + col) = ns_fp8x8(u, p.f8);
     };
     pieces([&](int r, int c) { put(m0 + r, n0 + c, row8(r, c)); });
     if (tm != tn) tpieces([&](int c, int r) { put(n0 + c, m0 + r, column8(c, r)); });
@@ -701,7 +707,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
 #pragma unroll
       for (int j = 0; j < IM; ++j) {
         const int ml = PM * wm + 16 * j + l16, nl = ml - PN * wn;  // its column in this wave's part
-        if (nl >= 0 && nl < PN && (nl >> 2 & 3) == g && m0 + ml < p.M)
+        if (nl >= 0 && nl < PN && (nl >> 2 & 3) == g && m0 + ml < M)
           p.rd[m0 + ml] = fabsf(ds[j]) >= 6.1035156e-5f ? dv[j] / ds[j] : 1.f;
       }
     }
@@ -713,8 +719,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       for (int r = 0; r < 4; ++r) o[r] = _Float16(a[r]);
       return o;
     });
-    direct(p.d + size_t(m0) * p.N + n0, p.N);
-    transposed(p.dt + size_t(n0) * p.M + m0, p.M);
+    direct(p.d + size_t(m0) * N + n0, N);
+    transposed(p.dt + size_t(n0) * M + m0, M);
     if (p.lo) {
       constexpr int SW = TN / 4 + 1;  // row stride of the staged bytes (words)
       uint32_t* s8 = reinterpret_cast<uint32_t*>(sm);
@@ -732,7 +738,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(NsGemm p)
       __syncthreads();
       pieces([&](int r, int c) {
         const uint32_t* q = s8 + r * SW + c / 4;
-        *reinterpret_cast<uint2*>(p.lo + 2 * size_t(m0 + r) * p.N + n0 + c) = make_uint2(q[0], q[1]);
+        *reinterpret_cast<uint2*>(p.lo + 2 * size_t(m0 + r) * N + n0 + c) = make_uint2(q[0], q[1]);
       });
     }
   } else {
@@ -891,7 +897,8 @@ hipError_t ns_tile(NsGemm p, int split, hipStream_t s) {
   p.per = (p.K / NS_K + split - 1) / split;
   // about as high as the block of tiles of one of the eight XCDs is wide
   p.band = std::max(0, int(std::lround(std::log2(tiles / 8.0) / 2)));
-  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * split)), dim3(64 * WM * WN * KG), lds, s, p);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(tiles * split)), dim3(64 * WM * WN * KG), lds, s, p.a, p.b, p.M, p.N, p.K, p.grid, p.tiles,
+                     p.by_tiles, p.band, p.split, p.per, p);
   return hipGetLastError();
 }
 
@@ -924,16 +931,16 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   const int blocks = int(nb < NS_SUMS ? nb : NS_SUMS);
   auto bytes = [&](size_t off) { return reinterpret_cast<uint8_t*>(ws + off); };
   int32_t* ticket = reinterpret_cast<int32_t*>(ws + q.ticket);
-  const NsCast c{part, blocks, at(q.xs), at(q.xh[0]), bytes(q.xl[0]), {bytes(q.xl[0]), bytes(q.xl[1]), bytes(q.m8)},
-                 ticket, q.Sp, q.Lp};
+  const NsCast c{at(q.xs), at(q.xh[0]), bytes(q.xl[0]), {bytes(q.xl[0]), bytes(q.xl[1]), bytes(q.m8)}, ticket};
   const unsigned tiles = unsigned((q.Sp / 64) * (q.Lp / 64));
   hipError_t e = hipSuccess;
   auto head = [&](auto bf, auto w) {
     hipLaunchKernelGGL((ns_momentum_kernel<decltype(bf)::value, decltype(w)::value>), dim3(unsigned(blocks)), dim3(256), 0,
-                       s, a, part);
+                       s, a.grad, a.m, a.m_out, part, n, a.mu, a.nesterov);
     e = hipGetLastError();
     if (e != hipSuccess) return;
-    hipLaunchKernelGGL((ns_cast_kernel<decltype(bf)::value, decltype(w)::value>), dim3(tiles), dim3(256), 0, s, a, c);
+    hipLaunchKernelGGL((ns_cast_kernel<decltype(bf)::value, decltype(w)::value>), dim3(tiles), dim3(256), 0, s, a.grad,
+                       a.m ? a.m_out : nullptr, part, blocks, a.rows, a.cols, q.Sp, q.Lp, a.mu, a.nesterov, c);
     e = hipGetLastError();
   };
   using four = std::integral_constant<int, 4>;
