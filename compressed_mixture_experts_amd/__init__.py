@@ -662,12 +662,13 @@ def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None, weight_grads: bool
     if weight_grads:
         dgamma, dbeta = torch.empty(width, dtype=torch.float32, device=dev), torch.empty(width, dtype=torch.float32, device=dev)
         nbytes = _workspace_bytes("bmoe_layer_norm_backward_workspace", rows, width)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check(lib().bmoe_layer_norm_backward(
         rows, width, BF16 if kind is torch.bfloat16 else F32, BF16 if dy.dtype is torch.bfloat16 else F32, dy.data_ptr(),
         s.data_ptr(), None if gamma is None else gamma.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
         None if d_sum is None else d_sum.data_ptr(), dx.data_ptr(), dgamma.data_ptr() if weight_grads else None,
-        dbeta.data_ptr() if weight_grads else None, ws.data_ptr() if weight_grads else None, nbytes, _raw_stream(dy)))
+        dbeta.data_ptr() if weight_grads else None, None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dy)))
     return dx, dgamma, dbeta
 
 

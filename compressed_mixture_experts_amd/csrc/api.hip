@@ -1612,9 +1612,8 @@ bmoe_status bmoe_layer_norm_backward(int32_t rows, int32_t width, int32_t dtype,
   if (overlaps_any(rws, {rdy, rs, rg, rm, rr, rd})) return fail(BMOE_ERR_ALIAS, "the workspace overlaps an input");
   st = check_device();
   if (st != BMOE_OK) return st;
-  const LnBwdArgs a{dy, s, gamma, mean, rstd, d_sum, dx, dgamma ? static_cast<float*>(workspace) : nullptr, rows, width};
-  BMOE_HIP(launch_ln_bwd(a, dgamma, dbeta, dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32,
-                         dy_dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, stream));
+  const LnBwdArgs a{dy, s, gamma, mean, rstd, d_sum, dx, dgamma, dbeta, static_cast<float*>(workspace), rows, width, 0};
+  BMOE_HIP(launch_ln_bwd(a, dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, dy_dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, stream));
   return ok();
 }
 

@@ -183,14 +183,56 @@ __global__ __launch_bounds__(ln_threads(TPR), TPR > 512 ? 4 : ln_fwd_waves(GE, N
   }
 }
 
-// Backward.  Each thread keeps its columns' sums of dy xhat and dy over the
-// rows of its workgroup; at the end the workgroup adds its waves' sums in
-// order (through LDS) and writes one partial row [dgamma | dbeta].
-template <int ACT, int DACT, int GE, int TPR, int NV>
+// dgamma and dbeta of 16 columns over all rows, by one workgroup of NT threads:
+// NT / 16 groups of lanes that take the rows g, g + NT / 16, ... each, their sums
+// added in order.  8 columns read more lines twice (512 x 4096 fp32 15.9 us in
+// place of 11.4, 333 x 1000 4.2 of 4.5).
+constexpr int LN_COLS = 16;
+template <int ACT, int DACT, int NT>
+__device__ __forceinline__ void ln_columns(const LnBwdArgs& a, int block) {
+  constexpr int G = NT / LN_COLS;
+  __shared__ float2 sm[G][LN_COLS + 1];
+  const int col = threadIdx.x % LN_COLS, grp = threadIdx.x / LN_COLS, c = block * LN_COLS + col;
+  float dg = 0.f, db = 0.f;
+  if (c < a.width) {
+#pragma unroll 8
+    for (int r = grp; r < a.rows; r += G) {
+      const size_t at = size_t(r) * a.width + c;
+      const float dy = load1<DACT>(a.dy, at);
+      dg = fmaf(dy, (load1<ACT>(a.s, at) - a.mean[r]) * a.rstd[r], dg);
+      db += dy;
+    }
+  }
+  sm[grp][col] = make_float2(dg, db);
+  __syncthreads();
+  if (grp == 0 && c < a.width) {
+    dg = db = 0.f;
+#pragma unroll
+    for (int w = 0; w < G; ++w) {
+      dg += sm[w][col].x;
+      db += sm[w][col].y;
+    }
+    a.dgamma[c] = dg;
+    a.dbeta[c] = db;
+  }
+}
+
+// Backward.  With SUMS each thread keeps its columns' sums of dy xhat and dy over
+// the rows of its workgroup; at the end the workgroup adds its waves' sums in
+// order (through LDS) and writes one partial row [dgamma | dbeta].  Without, the
+// workgroups behind a.row_blocks, if any, take the columns' sums from the inputs
+// again.
+template <int ACT, int DACT, int GE, int TPR, int NV, bool SUMS>
 __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
   constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;
+  if constexpr (!SUMS) {
+    if (int(blockIdx.x) >= a.row_blocks) {
+      ln_columns<ACT, DACT, ln_threads(TPR)>(a, int(blockIdx.x) - a.row_blocks);
+      return;
+    }
+  }
   __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
-  __shared__ float cols[RPW > 1 ? RPW : 1][RPW > 1 ? TPR * NV * GE : 1];
+  __shared__ float cols[SUMS && RPW > 1 ? RPW : 1][SUMS && RPW > 1 ? TPR * NV * GE : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int groups = a.width / GE;
   const float inv = 1.0f / float(a.width);
@@ -205,7 +247,7 @@ __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
     }
     if (g < groups && a.gamma) ln_load<ACT_F32, GE>(a.gamma, size_t(g) * GE, ga[v]);
   }
-  for (int row = blockIdx.x * RPW + sub; row < a.rows; row += gridDim.x * RPW) {
+  for (int row = blockIdx.x * RPW + sub; row < a.rows; row += a.row_blocks * RPW) {
     const size_t at = size_t(row) * a.width;
     float x[NV][GE], d[NV][GE];
 #pragma unroll
@@ -229,8 +271,10 @@ __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
       for (int j = 0; j < GE; ++j) {
         x[v][j] = in ? (x[v][j] - mean) * rstd : 0.f;
         const float dy = d[v][j];
-        dg[v][j] = fmaf(dy, x[v][j], dg[v][j]);
-        db[v][j] += dy;
+        if constexpr (SUMS) {
+          dg[v][j] = fmaf(dy, x[v][j], dg[v][j]);
+          db[v][j] += dy;
+        }
         d[v][j] = dy * ga[v][j];
         c[0] += d[v][j];
         c[1] = fmaf(d[v][j], x[v][j], c[1]);
@@ -255,30 +299,31 @@ __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
       }
     }
   }
-  if (!a.part) return;
-  float* out = a.part + size_t(blockIdx.x) * 2 * a.width;
+  if constexpr (SUMS) {
+    float* out = a.part + size_t(blockIdx.x) * 2 * a.width;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if constexpr (RPW == 1) {
+    for (int k = 0; k < 2; ++k) {
+      if constexpr (RPW == 1) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int g = t + TPR * v;
-        if (g < groups)
+        for (int v = 0; v < NV; ++v) {
+          const int g = t + TPR * v;
+          if (g < groups)
 #pragma unroll
-          for (int j = 0; j < GE; ++j) out[size_t(k) * a.width + size_t(g) * GE + j] = k ? db[v][j] : dg[v][j];
-      }
-    } else {
-      __syncthreads();
+            for (int j = 0; j < GE; ++j) out[size_t(k) * a.width + size_t(g) * GE + j] = k ? db[v][j] : dg[v][j];
+        }
+      } else {
+        __syncthreads();
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int j = 0; j < GE; ++j) cols[sub][(t + TPR * v) * GE + j] = k ? db[v][j] : dg[v][j];
-      __syncthreads();
-      for (int c = threadIdx.x; c < a.width; c += 256) {
-        float s = 0.f;
+          for (int j = 0; j < GE; ++j) cols[sub][(t + TPR * v) * GE + j] = k ? db[v][j] : dg[v][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.width; c += 256) {
+          float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < RPW; ++w) s += cols[w][c];
-        out[size_t(k) * a.width + c] = s;
+          for (int w = 0; w < RPW; ++w) s += cols[w][c];
+          out[size_t(k) * a.width + c] = s;
+        }
       }
     }
   }
@@ -360,8 +405,25 @@ hipError_t fwd_go(const LnFwdArgs& a, hipStream_t s) {
 }
 
 template <int ACT, int DACT, int GE, int TPR, int NV>
-hipError_t bwd_go(const LnBwdArgs& a, int blocks, hipStream_t s) {
-  hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV>), dim3(unsigned(blocks)), dim3(ln_threads(TPR)), 0, s, a);
+hipError_t bwd_go(LnBwdArgs a, hipStream_t s) {
+  const dim3 threads(ln_threads(TPR));
+  if (a.part) {
+    hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV, true>), dim3(unsigned(a.row_blocks)), threads, 0, s, a);
+    return hipGetLastError();
+  }
+  int columns = a.dgamma ? (a.width + LN_COLS - 1) / LN_COLS : 0;
+  if (columns && (a.dx == a.s || a.dx == a.dy)) {  // in place: the columns first
+    const int rows = a.row_blocks;
+    a.row_blocks = 0;
+    hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV, false>), dim3(unsigned(columns)), threads, 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    a.row_blocks = rows;
+    columns = 0;
+  }
+  const int grid = a.row_blocks + columns;
+  if (grid == 0) return hipSuccess;
+  hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV, false>), dim3(unsigned(grid)), threads, 0, s, a);
   return hipGetLastError();
 }
 
@@ -396,24 +458,29 @@ hipError_t fwd_act(const LnFwdArgs& a, int ge, hipStream_t s) {
 template <int ACT, int DACT>
 hipError_t bwd_act(const LnBwdArgs& a, int ge, hipStream_t s) {
   const LnShape sh = ln_shape(ge, a.width / ge);
-  const int blocks = ln_bwd_blocks(a.rows, a.width);
-#define LN_GO(G, T, V) bwd_go<ACT, DACT, G, T, V>(a, blocks, s)
+#define LN_GO(G, T, V) bwd_go<ACT, DACT, G, T, V>(a, s)
   LN_SHAPES(LN_GO)
 #undef LN_GO
 }
 
 }  // namespace
 
-// Workgroups of the backward, one partial row each: what runs at a time (two
-// per CU with the sums of a whole row of 2048 in registers; 32768 x 2048 136 us
-// with 512, 163 with 768, 143 with 1024), no more than there are groups of 4
-// rows.
-int ln_bwd_blocks(int rows, int width) {
+// Rows' workgroups of the backward: what runs at a time (two per CU with the sums
+// of a whole row of 2048 in registers; 32768 x 2048 136 us with 512, 163 with 768,
+// 143 with 1024), no more than there are groups of 4 rows.
+static int ln_bwd_blocks(int rows) {
   const int need = (rows + 3) / 4;
   return need < 512 ? need : 512;
 }
 
-size_t ln_bwd_workspace(int rows, int width) { return size_t(ln_bwd_blocks(rows, width)) * 2 * width * 4; }
+// Whether one launch takes the columns' sums too, from inputs read twice, in place
+// of partial rows and a second launch.  Long columns and inputs beyond the L2s lose
+// (us on the GPU, one launch and two, fp32: 333 x 1000 4.5 and 6.3, 1024 x 512 6.9
+// and 6.8, 512 x 4096 11.4 and 14.8, 1024 x 2048 10.7 and 13.2; 1024 x 4096 19.1 and
+// 17.7, 2048 x 512 12.4 and 8.1; the host needs 9.5 and 12.5 a call).
+static bool ln_bwd_once(int rows, int width) { return rows <= 1024 && size_t(rows) * width <= size_t(1) << 21; }
+
+size_t ln_bwd_workspace(int rows, int width) { return ln_bwd_once(rows, width) ? 0 : size_t(ln_bwd_blocks(rows)) * 2 * width * 4; }
 
 hipError_t launch_ln_fwd(const LnFwdArgs& a, int act, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
@@ -426,22 +493,21 @@ hipError_t launch_ln_fwd(const LnFwdArgs& a, int act, hipStream_t s) {
   return act == ACT_BF16 ? fwd_act<ACT_BF16>(a, ge, s) : fwd_act<ACT_F32>(a, ge, s);
 }
 
-hipError_t launch_ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, int act, int dact, hipStream_t s) {
+hipError_t launch_ln_bwd(LnBwdArgs a, int act, int dact, hipStream_t s) {
   const size_t pair = act == ACT_BF16 ? 4 : 8, dpair = dact == ACT_BF16 ? 4 : 8;
   auto all = [&](size_t b, size_t d, size_t f) {
     return ln_aligned(a.s, b) && ln_aligned(a.d_sum, b) && ln_aligned(a.dx, b) && ln_aligned(a.dy, d) &&
            ln_aligned(a.gamma, f);
   };
   const int ge = ln_group(a.width, all(16, 16, 16), all(pair, dpair, 8));
-  if (a.rows > 0) {
-    const hipError_t e = act == ACT_BF16
-                             ? (dact == ACT_BF16 ? bwd_act<ACT_BF16, ACT_BF16>(a, ge, s) : bwd_act<ACT_BF16, ACT_F32>(a, ge, s))
-                             : bwd_act<ACT_F32, ACT_F32>(a, ge, s);
-    if (e != hipSuccess) return e;
-  }
-  if (!dgamma) return hipSuccess;
-  hipLaunchKernelGGL(ln_colsum_kernel, dim3(unsigned((2 * a.width + 15) / 16)), dim3(1024), 0, s, a.part, dgamma, dbeta,
-                     ln_bwd_blocks(a.rows, a.width), a.width);
+  a.row_blocks = ln_bwd_blocks(a.rows);
+  if (!a.dgamma || ln_bwd_once(a.rows, a.width)) a.part = nullptr;
+  const hipError_t e = act == ACT_BF16
+                           ? (dact == ACT_BF16 ? bwd_act<ACT_BF16, ACT_BF16>(a, ge, s) : bwd_act<ACT_BF16, ACT_F32>(a, ge, s))
+                           : bwd_act<ACT_F32, ACT_F32>(a, ge, s);
+  if (e != hipSuccess || !a.part) return e;
+  hipLaunchKernelGGL(ln_colsum_kernel, dim3(unsigned((2 * a.width + 15) / 16)), dim3(1024), 0, s, a.part, a.dgamma,
+                     a.dbeta, a.row_blocks, a.width);
   return hipGetLastError();
 }
 

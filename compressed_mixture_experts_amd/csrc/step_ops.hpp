@@ -27,13 +27,15 @@ struct LnBwdArgs {
   const float* rstd;        // [rows]
   const void* d_sum;        // [rows][width] or null
   void* dx;                 // [rows][width]
-  float* part;              // [ln_bwd_blocks][2][width] or null
+  float* dgamma;            // [width] or null
+  float* dbeta;             // [width] when dgamma is set
+  float* part;              // the workspace
   int32_t rows, width;
+  int32_t row_blocks;       // the launcher's
 };
-int ln_bwd_blocks(int rows, int width);
 size_t ln_bwd_workspace(int rows, int width);
 hipError_t launch_ln_fwd(const LnFwdArgs& a, int act, hipStream_t s);
-hipError_t launch_ln_bwd(const LnBwdArgs& a, float* dgamma, float* dbeta, int act, int dact, hipStream_t s);
+hipError_t launch_ln_bwd(LnBwdArgs a, int act, int dact, hipStream_t s);
 
 // Latent substrate step and ternary codes (substrate_step.hip).
 struct SubStepArgs {

@@ -52,7 +52,7 @@ bmoe_status bmoe_layer_norm_forward(int32_t rows, int32_t width, int32_t dtype, 
                                     float* rstd, hipStream_t stream);
 
 /* Device workspace bytes of bmoe_layer_norm_backward (per-workgroup partial
- * sums of the weights' gradients). */
+ * sums of the weights' gradients; 0 for few rows, whose gradients need none). */
 bmoe_status bmoe_layer_norm_backward_workspace(int32_t rows, int32_t width, size_t* bytes);
 
 /* Backward at the forward's s, mean and rstd.  With xhat = (s - mean) rstd and
@@ -73,9 +73,10 @@ bmoe_status bmoe_layer_norm_backward_workspace(int32_t rows, int32_t width, size
  *   dgamma, dbeta  [width] fp32, written (zero for rows = 0): both or neither
  *             NULL.
  *   workspace at least bmoe_layer_norm_backward_workspace bytes, 16-byte
- *             aligned, contents undefined after; may be NULL when dgamma is.
- * Column sums are fp32: each workgroup's rows in order, the workgroups' sums
- * in order.  Errors as above, and BMOE_ERR_WORKSPACE. */
+ *             aligned, contents undefined after; may be NULL when dgamma is, or when
+ *             that is 0.
+ * Column sums are fp32, added in an order that the sizes and the alignment
+ * alone decide.  Errors as above, and BMOE_ERR_WORKSPACE. */
 bmoe_status bmoe_layer_norm_backward(int32_t rows, int32_t width, int32_t dtype, int32_t dy_dtype, const void* dy,
                                      const void* s, const float* gamma, const float* mean, const float* rstd,
                                      const void* d_sum, void* dx, float* dgamma, float* dbeta, void* workspace,

@@ -24,7 +24,7 @@ def ptr(k):
 
 FWD = dict(rows=8, width=64, dtype=0, x=ptr(0), residual=ptr(1), gamma=ptr(2), beta=ptr(3), eps=1e-5, sum=ptr(4),
            y=ptr(5), mean=ptr(6), rstd=ptr(7), stream=None)
-BWD = dict(rows=8, width=64, dtype=0, dy_dtype=0, dy=ptr(0), s=ptr(1), gamma=ptr(2), mean=ptr(3), rstd=ptr(4),
+BWD = dict(rows=2000, width=64, dtype=0, dy_dtype=0, dy=ptr(0), s=ptr(1), gamma=ptr(2), mean=ptr(3), rstd=ptr(4),
            d_sum=ptr(5), dx=ptr(6), dgamma=ptr(7), dbeta=ptr(8), ws=ptr(9), ws_bytes=BIG, stream=None)
 ORTHO = dict(rows=40, cols=72, dtype=0, grad=ptr(0), momentum=ptr(1), momentum_out=ptr(2), mu=0.9, nesterov=1, out=ptr(3),
              ws=ptr(4), ws_bytes=BIG, stream=None)
@@ -105,7 +105,13 @@ def test_workspace_sizes(name, shape):
     n = ctypes.c_size_t(77)
     assert getattr(bm.lib(), name)(*shape, ctypes.byref(n)) == SHAPE and n.value == 77
     assert getattr(bm.lib(), name)(64, 64, None) == NULL
-    assert getattr(bm.lib(), name)(64, 64, ctypes.byref(n)) == 0 and 0 < n.value < 64 * MB
+    assert getattr(bm.lib(), name)(2000, 64, ctypes.byref(n)) == 0 and 0 < n.value < 64 * MB
+
+
+def test_norm_gradients_of_few_rows_need_no_workspace():
+    n = ctypes.c_size_t(77)
+    for rows, width, none in ((0, 64, True), (1024, 2048, True), (1025, 8, False), (1024, 2049, False)):
+        assert bm.lib().bmoe_layer_norm_backward_workspace(rows, width, ctypes.byref(n)) == 0 and (n.value == 0) == none
 
 
 def test_nothing_to_do():

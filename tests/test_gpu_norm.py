@@ -79,10 +79,14 @@ def check_backward(c, got, s, dy, gamma, mean, rstd, d_sum):
     assert (np.abs(to_f64(dx) - wx) <= tol + b * (np.abs(wx) + tol)).all(), "dx"
     if dg is not None:
         # depth of a column's sum: a wave's rows, the workgroup's waves, the
-        # partial rows of one wave of the second kernel, its 16 waves
+        # partial rows of one group of the second kernel (64 groups), their sums; or,
+        # at up to 1024 rows, a 16th of the rows and 16 sums (a 64th and 64 in a
+        # workgroup of 1024)
         rows = dy64.shape[0]
         blocks = max(1, min(512, -(-rows // 4)))
         depth = -(-rows // blocks) + 4 + -(-blocks // 16) + 16
+        if rows <= 1024:
+            depth = max(depth, -(-rows // 16) + 64)
         assert (np.abs(to_f64(dg) - wg) <= (depth + 4) * U * (np.abs(dy64) * xh).sum(axis=0)).all(), "dgamma"
         assert (np.abs(to_f64(db) - wb) <= (depth + 1) * U * np.abs(dy64).sum(axis=0)).all(), "dbeta"
 
@@ -93,6 +97,8 @@ CASES = [
     (1, 2048), (6, 2056), (5, 4096), (3, 4104), (4, 8192), (2, 16384), (2, 8200),
     (17, 77), (8, 255), (5, 257), (6, 777), (3, 1023), (4, 1025), (2, 4095), (2, 4097), (2, 16383),
     (13, 254), (5, 258), (3, 1022), (3, 1026), (2, 4094), (2, 4098), (2, 16382), (2500, 96), (2301, 33),
+    # one launch and two for the columns' sums: at 1024 rows, at 2^21 elements
+    (1024, 100), (1025, 100), (1024, 2048), (1000, 2100), (511, 4104), (512, 4098), (128, 16384), (700, 33),
 ]
 
 
@@ -162,6 +168,22 @@ def test_norm_in_place():
         t = {"s": want[1].clone(), "d_sum": d["ds"].clone(), "dy": dy.clone()}
         dx, g, b = bm.layer_norm_backward(t["dy"], t["s"], d["gamma"], want[2], want[3], d_sum=t["d_sum"], dx=t[name])
         assert (dx == wdx).all() and (g == wg).all() and (b == wb).all(), name
+
+
+@pytest.mark.parametrize("rows,width,kind", [(1024, 2048, "bf16"), (1000, 777, "f32"), (1024, 64, "f32"), (1100, 2048, "bf16")])
+def test_norm_gradient_in_place(rows, width, kind):
+    """The columns' sums are those of the inputs, whichever of them dx overwrites."""
+    c = draw(rows, width, kind, rows)
+    d = {k: v.cuda() for k, v in c.items() if k != "dt"}
+    _, s, mean, rstd = bm.layer_norm_forward(d["x"], d["gamma"], d["beta"])
+    dy = d["dy"].to(c["dt"])
+    want = bm.layer_norm_backward(dy, s, d["gamma"], mean, rstd)
+    check_backward(c, want, s, dy, d["gamma"], mean, rstd, None)
+    for name in ("s", "dy"):
+        for _ in range(4):
+            t = {"s": s.clone(), "dy": dy.clone()}
+            got = bm.layer_norm_backward(t["dy"], t["s"], d["gamma"], mean, rstd, dx=t[name])
+            assert all((a == b).all() for a, b in zip(got, want)), name
 
 
 @pytest.mark.parametrize("width", [64, 777, 4096])
