@@ -724,9 +724,9 @@ def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None,
     else:
         _operand("packed", packed, (rows, cols // 16), (torch.int32,), dev)
     scale = torch.empty((), dtype=torch.float32, device=dev)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
     _check(lib().bmoe_substrate_step(rows, cols, w.data_ptr(), _ptr(o), float(step), float(decay), _ptr(w_out),
-                                     packed.data_ptr(), scale.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(w)))
+                                     packed.data_ptr(), scale.data_ptr(), _ptr(ws), nbytes, _raw_stream(w)))
     return w if o is None else w_out, packed, scale
 
 

@@ -1670,13 +1670,13 @@ bmoe_status bmoe_substrate_step(int32_t rows, int32_t cols, const float* w, cons
   if (st != BMOE_OK) return st;
   if (!std::isfinite(step) || !std::isfinite(decay))
     return fail(BMOE_ERR_SHAPE, "step=%g and decay=%g must be finite", step, decay);
-  if (!w || !packed || !workspace) return fail(BMOE_ERR_NULL, "w / packed / workspace is NULL");
+  const size_t n = size_t(rows) * cols, need = sub_step_workspace(n);
+  if (!w || !packed || (need > 0 && !workspace)) return fail(BMOE_ERR_NULL, "w / packed / workspace is NULL");
   if (!o != !w_out) return fail(BMOE_ERR_NULL, "o and w_out go together");
   if (!aligned(w, 16) || !aligned(o, 16) || !aligned(w_out, 16) || !aligned(packed, 16))
     return fail(BMOE_ERR_ALIGN, "w, o, w_out and packed must be 16-byte aligned");
-  if (!aligned(scale, 4) || !aligned(workspace, 16))
+  if (!aligned(scale, 4) || (need > 0 && !aligned(workspace, 16)))
     return fail(BMOE_ERR_ALIGN, "scale must be 4-byte aligned, the workspace 16-byte aligned");
-  const size_t n = size_t(rows) * cols, need = sub_step_workspace(n);
   if (workspace_bytes < need)
     return fail(BMOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
   const Range rw{w, n * 4}, ro{o, n * 2}, rwo{w_out, n * 4}, rp{packed, n / 4}, rs{scale, 4}, rws{workspace, need};

@@ -78,7 +78,8 @@ bmoe_status bmoe_orthogonalize(int32_t rows, int32_t cols, int32_t grad_dtype, c
  *   scale    1 fp32, written, or NULL: the w_scale under which the codes
  *            stand for W'.
  *   workspace at least bmoe_substrate_step_workspace bytes, 16-byte aligned,
- *            contents undefined after.
+ *            contents undefined after; may be NULL when that is 0 (few
+ *             weights).
  * rows >= 1, cols a positive multiple of 16, rows * cols below 2^31; step and
  * decay finite.  A layer's prepared buffer (bmoe_prepare) is stale after its
  * w_base changed.  Errors: BMOE_ERR_SHAPE, BMOE_ERR_NULL, BMOE_ERR_ALIGN,

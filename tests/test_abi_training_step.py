@@ -28,7 +28,7 @@ BWD = dict(rows=2000, width=64, dtype=0, dy_dtype=0, dy=ptr(0), s=ptr(1), gamma=
            d_sum=ptr(5), dx=ptr(6), dgamma=ptr(7), dbeta=ptr(8), ws=ptr(9), ws_bytes=BIG, stream=None)
 ORTHO = dict(rows=40, cols=72, dtype=0, grad=ptr(0), momentum=ptr(1), momentum_out=ptr(2), mu=0.9, nesterov=1, out=ptr(3),
              ws=ptr(4), ws_bytes=BIG, stream=None)
-STEP = dict(rows=40, cols=64, w=ptr(0), o=ptr(1), step=0.1, decay=0.0, w_out=ptr(2), packed=ptr(3), scale=ptr(4),
+STEP = dict(rows=2000, cols=64, w=ptr(0), o=ptr(1), step=0.1, decay=0.0, w_out=ptr(2), packed=ptr(3), scale=ptr(4),
             ws=ptr(5), ws_bytes=BIG, stream=None)
 CALLS = {"bmoe_layer_norm_forward": FWD, "bmoe_layer_norm_backward": BWD, "bmoe_orthogonalize": ORTHO,
          "bmoe_substrate_step": STEP}
@@ -108,8 +108,10 @@ def test_workspace_sizes(name, shape):
     assert getattr(bm.lib(), name)(2000, 64, ctypes.byref(n)) == 0 and 0 < n.value < 64 * MB
 
 
-def test_norm_gradients_of_few_rows_need_no_workspace():
+def test_few_rows_and_weights_need_no_workspace():
     n = ctypes.c_size_t(77)
+    for rows, cols, none in ((1, 16, True), (256, 64, True), (257, 64, False)):
+        assert bm.lib().bmoe_substrate_step_workspace(rows, cols, ctypes.byref(n)) == 0 and (n.value == 0) == none
     for rows, width, none in ((0, 64, True), (1024, 2048, True), (1025, 8, False), (1024, 2049, False)):
         assert bm.lib().bmoe_layer_norm_backward_workspace(rows, width, ctypes.byref(n)) == 0 and (n.value == 0) == none
 

@@ -232,7 +232,7 @@ def test_orthogonalize_streams_and_graph():
 
 
 # ------------------------------------------------------------------ substrate step
-STEP = [(1, 16), (3, 16), (5, 48), (64, 64), (100, 1040), (512, 512), (1000, 2064), (2048, 1024), (16384, 16)]
+STEP = [(1, 16), (3, 16), (5, 48), (64, 64), (256, 64), (257, 64), (1024, 64), (1025, 64), (100, 1040), (512, 512), (1000, 2064), (2048, 1024), (16384, 16)]
 
 
 @pytest.mark.parametrize("rows,cols", STEP)
@@ -260,20 +260,21 @@ def test_substrate_step_ties_zero_and_non_finite():
     assert float(scale) == 2.0 and (packed.cpu().numpy().view(np.uint32) == bm.pack_ternary(codes)).all()
     _, packed, scale = bm.substrate_step(torch.zeros(4, 32, device="cuda"))
     assert (packed == 0).all() and float(scale) == 0.0
-    for bad in (float("nan"), float("inf")):
-        w = torch.randn(8, 64, device="cuda")
+    for bad, rows in ((float("nan"), 8), (float("inf"), 8), (float("nan"), 1100), (float("inf"), 1100)):
+        w = torch.randn(rows, 64, device="cuda")
         w[2, 5] = bad
         _, packed, scale = bm.substrate_step(w)
         assert (packed == 0).all() and not np.isfinite(float(scale))
 
 
-def test_substrate_step_in_place_and_graph():
+@pytest.mark.parametrize("rows", [320, 64, 30])
+def test_substrate_step_in_place_and_graph(rows):
     import torch
     g = torch.Generator().manual_seed(61)
-    w0 = torch.randn(320, 256, generator=g).cuda()
-    o = torch.randn(320, 256, generator=g).bfloat16().cuda()
+    w0 = torch.randn(rows, 256, generator=g).cuda()
+    o = torch.randn(rows, 256, generator=g).bfloat16().cuda()
     want = bm.substrate_step(w0, o, step=0.1, decay=0.01)
-    w, packed = w0.clone(), torch.empty(320, 16, dtype=torch.int32, device="cuda")
+    w, packed = w0.clone(), torch.empty(rows, 16, dtype=torch.int32, device="cuda")
     got = bm.substrate_step(w, o, step=0.1, decay=0.01, w_out=w, packed=packed)
     assert got[0] is w and got[1] is packed and all((a == b).all() for a, b in zip(got, want))
     w.copy_(w0)
