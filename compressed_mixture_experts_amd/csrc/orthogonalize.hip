@@ -781,57 +781,62 @@ int ns_tiles(const NsGemm& p, int t) {
   return MODE == NS_SYM ? nn * (nn + 1) / 2 : nm * nn;
 }
 
-// Time of a product in tiles of side t, `split` workgroups to a tile, in
-// microseconds: a lone tile's step of 64 takes `one` (latency and the CU's own
-// limits), all together 256 t bytes a step and workgroup from L2 into LDS at 16
-// TB/s (13 where shares read different parts of the depth: 768 x 8192 took 261 us
-// a call with the tiles that 12 picks, 250 with 13 or more; 512 x 4096 138 with 14,
-// 136 with 13) and 128 t^2 operations at 1.15 PFLOP/s (rates of whole products of
-// 2048 x 8192 on this GPU); adding a tile's shares up takes 1.4 us and more with
-// its area and their number (a symmetric product of side 64 and K = 8192 in tiles
-// of 32: 16.8 us whole, 7.6 in four shares, 5.8 in sixteen; of 512 and 8192 in
-// tiles of 64: 24.6, 11.9 in four, 11.5 in six, 16.5 in eight).
-template <int MODE>
-double ns_time(const NsGemm& p, int t, double one, int split) {
-  const int nk = p.K / NS_K, steps = p.a8 ? nk + (nk + 1) / 2 : nk, n = ns_tiles<MODE>(p, t) * split;
-  const double step = std::max({one, double(n) * t * 256 / (split > 1 ? 13e6 : 16e6), double(n) * t * t * 128 / 1.15e9});
-  return (steps + split - 1) / split * step + (split > 1 ? 1.4 + t / 64.0 * t / 64.0 * (0.8 + 0.4 * split) : 0.0);
-}
+// A tile side: microseconds of a step of 64 by a lone workgroup of a CU (latency
+// and the CU's own limits), and by each of two that share one (0: one fills it).
+struct NsSide {
+  int side;
+  double one, two;
+};
 
 struct NsTile {
   int side, split;
 };
 
-// Steps of a lone tile of 32, 64, 96, 128 and 256: 0.14, 0.205, 0.32, 0.41 and 1.2
-// us.  Measured per product, symmetric ones of side 512 / 1024 / 2048 with K = the
-// side: tiles of 32 4.1 / 8.8 / 36 us, 64 5.6 / 7.2 / 23.6, 96 8.9 / 10.2 / 18.2,
-// 128 11 / 12.0 / 20.4; general ones of 512 x 512, 4096 x 1024, 8192 x 2048: 32
-// 3.7 / 30 / 289, 64 4.5 / 18.4 / 152, 128 8 / 14.0 / 83, 256 18.2 / 27.3 / 66.
-// (96 has got faster since with its second group of waves; a smaller step for it
-// would only take it where 64, two workgroups to a CU, is better: 0.27 makes 255 of
-// 240 us a call at 1536 x 1536, 0.24 235 of 185 at 1408 x 1408.)
+// Time of a product in tiles of a side, `split` workgroups to a tile, in
+// microseconds.  A step takes what the CU does, or all workgroups together: 256 t
+// bytes each from L2 into LDS at 23 TB/s (19 where the operand is beyond the L2s, 16
+// where shares read different parts of the depth and in general products) and 128
+// t^2 operations at 1.15 PFLOP/s.  Two workgroups of a CU take longer where the
+// operand is beyond the L2s, and where some CUs get a third.  Adding a tile's shares
+// up takes 1.4 us and more with its area and their number.  The constants are fitted
+// to whole calls with every side and split forced, 23 sizes from 192 x 8192 to 1800
+// x 8192 and 20 square ones from 320 to 2560.
+template <int MODE>
+double ns_time(const NsGemm& p, NsSide s, int split) {
+  const int t = s.side, nk = p.K / NS_K, steps = p.a8 ? nk + (nk + 1) / 2 : nk, n = ns_tiles<MODE>(p, t) * split;
+  const int cus = NS_SHARED / 2;
+  const bool far = 2.0 * p.N * p.K >= 8 << 20;
+  double cu = s.one;
+  if (MODE == NS_SYM && s.two == 0) cu = s.one * ((n + cus - 1) / cus);
+  else if (MODE == NS_SYM && n > cus) cu = s.two * (far ? 1.28 : 1.0) * (n > 2 * cus ? 1.25 : 1.0);
+  const double rate = MODE == NS_SYM && split == 1 ? (far ? 19e6 : 23e6) : 16e6;
+  const double step = std::max({cu, double(n) * t * 256 / rate, double(n) * t * t * 128 / 1.15e9});
+  const double join = 1.4 + (t > 64 ? 1.9 * t * t / 4096 : t > 32 ? 1.0 : 0.42) * (0.8 + 0.4 * split);
+  return (steps + split - 1) / split * step + (split > 1 ? join : 0.0);
+}
+
 template <int MODE>
 NsTile ns_pick(const NsGemm& p) {
   NsTile best{0, 1};
   double least = 0;
-  auto look = [&](int side, double one) {
+  auto look = [&](NsSide s) {
     // as many workgroups as run at a time: two per CU up to tiles of 64
-    const int most = (side <= 64 ? NS_SHARED : NS_SHARED / 2) / std::max(1, ns_tiles<MODE>(p, side)), steps = p.K / NS_K;
+    const int most = (s.two > 0 ? NS_SHARED : NS_SHARED / 2) / std::max(1, ns_tiles<MODE>(p, s.side)), steps = p.K / NS_K;
     for (int split = 1; split == 1 || (MODE == NS_SYM && split <= std::min(most, NS_SPLIT)); ++split) {
       // whole shares only
       if (split > 1 && (split - 1) * ((steps + split - 1) / split) >= steps) continue;
-      const double time = ns_time<MODE>(p, side, one, split);
+      const double time = ns_time<MODE>(p, s, split);
       if (!best.side || time < least) {
-        best = NsTile{side, split};
+        best = NsTile{s.side, split};
         least = time;
       }
     }
   };
-  look(32, 0.14);
-  look(64, 0.205);
-  if (MODE == NS_SYM) look(96, 0.32);
-  look(128, 0.41);
-  if (MODE != NS_SYM) look(256, 1.2);
+  look({32, 0.14, 0.17});
+  look({64, 0.205, 0.29});
+  if (MODE == NS_SYM) look({96, 0.32, 0});
+  look({128, 0.41, 0});
+  if (MODE != NS_SYM) look({256, 1.2, 0});
   return best;
 }
 
