@@ -794,25 +794,33 @@ struct NsTile {
 
 // Time of a product in tiles of a side, `split` workgroups to a tile, in
 // microseconds.  A step takes what the CU does, or all workgroups together: 256 t
-// bytes each from L2 into LDS at 23 TB/s (19 where the operand is beyond the L2s, 16
-// where shares read different parts of the depth and in general products) and 128
-// t^2 operations at 1.15 PFLOP/s.  Two workgroups of a CU take longer where the
-// operand is beyond the L2s, and where some CUs get a third.  Adding a tile's shares
-// up takes 1.4 us and more with its area and their number.  The constants are fitted
-// to whole calls with every side and split forced, 23 sizes from 192 x 8192 to 1800
-// x 8192 and 20 square ones from 320 to 2560.
+// bytes each from L2 into LDS and 128 t^2 operations at 1.15 PFLOP/s.  Symmetric
+// products get 23 TB/s from L2 (19 where the operand is beyond the L2s, 16 where
+// shares read different parts of the depth), two workgroups of a CU take longer where
+// the operand is beyond the L2s and where some CUs get a third, and adding a tile's
+// shares up takes 1.4 us and more with its area and their number.  General ones get
+// 20 TB/s in small tiles and 14 in large ones, whole rounds of workgroups, and the
+// epilogue of a large tile counts.  The constants are fitted to whole calls with
+// every side and split forced: X X^T of 23 sizes from 192 x 8192 to 1800 x 8192, the
+// products of side 320 to 2560, those with X of 35 sizes from 64 x 2000 to 2048 x 8192.
 template <int MODE>
 double ns_time(const NsGemm& p, NsSide s, int split) {
   const int t = s.side, nk = p.K / NS_K, steps = p.a8 ? nk + (nk + 1) / 2 : nk, n = ns_tiles<MODE>(p, t) * split;
   const int cus = NS_SHARED / 2;
-  const bool far = 2.0 * p.N * p.K >= 8 << 20;
-  double cu = s.one;
-  if (MODE == NS_SYM && s.two == 0) cu = s.one * ((n + cus - 1) / cus);
-  else if (MODE == NS_SYM && n > cus) cu = s.two * (far ? 1.28 : 1.0) * (n > 2 * cus ? 1.25 : 1.0);
-  const double rate = MODE == NS_SYM && split == 1 ? (far ? 19e6 : 23e6) : 16e6;
+  double cu = s.one, rate, once = 0.0;
+  if (s.two == 0) cu = s.one * ((n + cus - 1) / cus);
+  if constexpr (MODE == NS_SYM) {
+    const bool far = 2.0 * p.N * p.K >= 8 << 20;
+    if (s.two > 0 && n > cus) cu = s.two * (far ? 1.28 : 1.0) * (n > 2 * cus ? 1.25 : 1.0);
+    rate = split > 1 ? 16e6 : far ? 19e6 : 23e6;
+    if (split > 1) once = 1.4 + (t > 64 ? 1.9 * t * t / 4096 : t > 32 ? 1.0 : 0.42) * (0.8 + 0.4 * split);
+  } else {
+    if (s.two > 0 && n > cus) cu = s.two * ((n + 2 * cus - 1) / (2 * cus));
+    rate = t > 64 ? 14e6 : 20e6;
+    once = t > 128 ? 3.4 : t > 64 ? 1.4 : t > 32 ? 0.5 : 0.0;
+  }
   const double step = std::max({cu, double(n) * t * 256 / rate, double(n) * t * t * 128 / 1.15e9});
-  const double join = 1.4 + (t > 64 ? 1.9 * t * t / 4096 : t > 32 ? 1.0 : 0.42) * (0.8 + 0.4 * split);
-  return (steps + split - 1) / split * step + (split > 1 ? join : 0.0);
+  return (steps + split - 1) / split * step + once;
 }
 
 template <int MODE>

@@ -98,7 +98,7 @@ LARGE = [(40, 2500), (2500, 40), (63, 8191), (200, 1025), (500, 6000), (6000, 50
          # and, in tiles of 96, one group's last piece, whole and in shares
          (1590, 1600), (1600, 1590), (890, 8190), (1210, 8190), (8190, 1200), (2235, 2240), (1344, 1340), (700, 704),
          (320, 8190), (330, 1340), (830, 3390), (1980, 1970), (1150, 8100), (1470, 8100), (1470, 3000), (3130, 3136),
-         (440, 8100), (1200, 16384)]
+         (440, 8100), (1200, 16384), (2170, 2176), (60, 8100), (950, 16384), (2900, 2944), (190, 8100)]
 
 
 @pytest.mark.parametrize("rows,cols", LARGE)
