@@ -2,15 +2,11 @@
 //
 // Both passes are bound by HBM: a few operations per element read once and
 // written once.  A row is held in registers between its loads and its stores:
-// TPR threads (one wave up to 2048 columns with 16-byte loads, else a whole
-// workgroup) hold NV groups of GE consecutive elements each, group v of thread
-// t being group t + TPR v of the row, so every load is contiguous over the
-// wave.  One wave per row needs no LDS and no barrier.  Workgroups loop over
-// rows, which keeps gamma, beta and the backward's column sums of the
-// thread's columns in registers.
-//
-// GE = 8 (16-byte vectors) needs a width that is a multiple of 8 and 16-byte
-// aligned arrays; GE = 2 an even width; else GE = 1.
+// TPR threads (one wave up to 2048 columns in groups of 8, else a whole workgroup)
+// hold NV groups of consecutive elements each, group v of thread t being group t +
+// TPR v of the row, so every load is contiguous over the wave.  One wave per row
+// needs no LDS and no barrier.  Workgroups loop over rows, which keeps gamma, beta
+// and the backward's column sums of the thread's columns in registers.
 #include "step_ops.hpp"
 
 namespace bmoe {
@@ -42,55 +38,99 @@ __device__ __forceinline__ void ln_row_sum(float (&v)[N], float2* red) {
   }
 }
 
-template <int ACT, int GE>
-__device__ __forceinline__ void ln_load(const void* p, size_t i, float* v) {
-  if constexpr (GE == 8) {
+// How a row is cut into groups of consecutive elements: 8 at 16-byte alignment in a
+// width that they divide (LN_WHOLE), 8 at any alignment with the last group's
+// elements one by one (LN_ANY), 2 (LN_PAIR) or 1 (LN_SINGLE).
+enum LnCut { LN_WHOLE, LN_ANY, LN_PAIR, LN_SINGLE };
+constexpr int ln_elems(int cut) { return cut <= LN_ANY ? 8 : cut == LN_PAIR ? 2 : 1; }
+
+// The group from element i on, n elements (or more) before the row's end.
+template <int ACT, int CUT>
+__device__ __forceinline__ void ln_load(const void* p, size_t i, int n, float* v) {
+  typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+  typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+  if constexpr (CUT == LN_WHOLE) {
     load8<ACT>(p, i, v);
-  } else if constexpr (GE == 2 && ACT == ACT_BF16) {
+  } else if constexpr (CUT == LN_PAIR && ACT == ACT_BF16) {
     const uint32_t u = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i);
     v[0] = bf16lo(u);
     v[1] = bf16hi(u);
-  } else if constexpr (GE == 2) {
+  } else if constexpr (CUT == LN_PAIR) {
     const float2 u = *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
     v[0] = u.x;
     v[1] = u.y;
-  } else {
+  } else if constexpr (CUT == LN_SINGLE) {
     v[0] = load1<ACT>(p, i);
+  } else if (n < 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? load1<ACT>(p, i + j) : 0.f;
+  } else if constexpr (ACT == ACT_BF16) {
+    const u32x4_any_t u = *reinterpret_cast<const u32x4_any_t*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = bf16lo(u[k]);
+      v[2 * k + 1] = bf16hi(u[k]);
+    }
+  } else {
+    const f32x4_any_t* q = reinterpret_cast<const f32x4_any_t*>(static_cast<const float*>(p) + i);
+    const f32x4_any_t lo = q[0], hi = q[1];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = lo[k];
+      v[4 + k] = hi[k];
+    }
   }
 }
 
-template <int ACT, int GE>
-__device__ __forceinline__ void ln_store(void* p, size_t i, const float* v) {
+template <int ACT, int CUT>
+__device__ __forceinline__ void ln_store(void* p, size_t i, int n, const float* v) {
   // results go past L2, which the rows to come need (streamed stores: 122 ->
   // 119 us at 32768 x 2048 bf16, 12.9 -> 11.7 us at 8192 x 1024; streamed loads
   // lose where the producer left its rows in the last-level cache: 15.7 us).  With a
   // pass behind that reads y, streamed and plain stores: 161 and 165 us at 32768 x
-  // 2048, 19.3 and 18.1 at 8192 x 1024
+  // 2048, 19.3 and 18.1 at 8192 x 1024.  Groups that share lines are stored plainly.
   typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-  if constexpr (GE == 8 && ACT == ACT_BF16) {
-    const u32x4_t u = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-    __builtin_nontemporal_store(u, reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i));
-  } else if constexpr (GE == 8) {
-    f32x4_t* q = reinterpret_cast<f32x4_t*>(static_cast<float*>(p) + i);
-    __builtin_nontemporal_store(f32x4_t{v[0], v[1], v[2], v[3]}, q);
-    __builtin_nontemporal_store(f32x4_t{v[4], v[5], v[6], v[7]}, q + 1);
-  } else if constexpr (GE == 2 && ACT == ACT_BF16) {
+  typedef uint32_t u32x4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+  typedef float f32x4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+  if constexpr (CUT == LN_PAIR && ACT == ACT_BF16) {
     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p) + i) = pack_bf16x2(v[0], v[1]);
-  } else if constexpr (GE == 2) {
+  } else if constexpr (CUT == LN_PAIR) {
     *reinterpret_cast<float2*>(static_cast<float*>(p) + i) = make_float2(v[0], v[1]);
-  } else if constexpr (ACT == ACT_BF16) {
+  } else if constexpr (CUT == LN_SINGLE && ACT == ACT_BF16) {
     static_cast<uint16_t*>(p)[i] = uint16_t(pack_bf16x2(v[0], v[0]));
-  } else {
+  } else if constexpr (CUT == LN_SINGLE) {
     static_cast<float*>(p)[i] = v[0];
+  } else if (CUT == LN_ANY && n < 8) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j) {
+      if (j >= n) continue;
+      if constexpr (ACT == ACT_BF16) static_cast<uint16_t*>(p)[i + j] = uint16_t(pack_bf16x2(v[j], v[j]));
+      else static_cast<float*>(p)[i + j] = v[j];
+    }
+  } else if constexpr (ACT == ACT_BF16) {
+    const u32x4_t u = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    uint16_t* q = static_cast<uint16_t*>(p) + i;
+    if constexpr (CUT == LN_WHOLE) __builtin_nontemporal_store(u, reinterpret_cast<u32x4_t*>(q));
+    else *reinterpret_cast<u32x4_any_t*>(q) = u;
+  } else {
+    const f32x4_t lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
+    float* q = static_cast<float*>(p) + i;
+    if constexpr (CUT == LN_WHOLE) {
+      __builtin_nontemporal_store(lo, reinterpret_cast<f32x4_t*>(q));
+      __builtin_nontemporal_store(hi, reinterpret_cast<f32x4_t*>(q) + 1);
+    } else {
+      reinterpret_cast<f32x4_any_t*>(q)[0] = lo;
+      reinterpret_cast<f32x4_any_t*>(q)[1] = hi;
+    }
   }
 }
 
 // The values as the activation dtype stores them.
-template <int ACT, int GE>
+template <int ACT, int E>
 __device__ __forceinline__ void ln_round(float* v) {
   if constexpr (ACT == ACT_BF16) {
 #pragma unroll
-    for (int j = 0; j < GE; ++j) v[j] = float(__bf16(v[j]));
+    for (int j = 0; j < E; ++j) v[j] = float(__bf16(v[j]));
   }
 }
 
@@ -99,69 +139,69 @@ __device__ __forceinline__ void ln_round(float* v) {
 // exactly the workgroups that run at a time loses no partial last round: 32768 x
 // 2048 forward 111 us with 3 per CU (as many as fit), 146 with 4, 122 with 8 and
 // 125 with one per 4 rows.
-constexpr int ln_fwd_waves(int ge, int nv) { return ge * nv >= 32 ? 3 : ge * nv >= 16 ? (ge == 8 ? 5 : 4) : 8; }
+constexpr int ln_fwd_waves(int e, int nv) { return e * nv >= 32 ? 3 : e * nv >= 16 ? (e == 8 ? 5 : 4) : 8; }
 constexpr int ln_threads(int tpr) { return tpr > 256 ? tpr : 256; }
 
-template <int ACT, int GE, int TPR, int NV>
-__global__ __launch_bounds__(ln_threads(TPR), TPR > 512 ? 4 : ln_fwd_waves(GE, NV)) void ln_fwd_kernel(LnFwdArgs a) {
-  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;  // rows per workgroup
+template <int ACT, int CUT, int TPR, int NV>
+__global__ __launch_bounds__(ln_threads(TPR), TPR > 512 ? 4 : ln_fwd_waves(ln_elems(CUT), NV)) void ln_fwd_kernel(LnFwdArgs a) {
+  constexpr int E = ln_elems(CUT), RPW = TPR > 256 ? 1 : 256 / TPR;  // rows per workgroup
   __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const int groups = a.width / GE;
+  const int groups = (a.width + E - 1) / E;
   const float inv = 1.0f / float(a.width);
-  float ga[NV][GE], be[NV][GE];
+  float ga[NV][E], be[NV][E];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int g = t + TPR * v;
 #pragma unroll
-    for (int j = 0; j < GE; ++j) {
+    for (int j = 0; j < E; ++j) {
       ga[v][j] = 1.f;
       be[v][j] = 0.f;
     }
-    if (g < groups && a.gamma) ln_load<ACT_F32, GE>(a.gamma, size_t(g) * GE, ga[v]);
-    if (g < groups && a.beta) ln_load<ACT_F32, GE>(a.beta, size_t(g) * GE, be[v]);
+    if (g < groups && a.gamma) ln_load<ACT_F32, CUT>(a.gamma, size_t(g) * E, a.width - E * g, ga[v]);
+    if (g < groups && a.beta) ln_load<ACT_F32, CUT>(a.beta, size_t(g) * E, a.width - E * g, be[v]);
   }
   for (int row = blockIdx.x * RPW + sub; row < a.rows; row += gridDim.x * RPW) {
     const size_t at = size_t(row) * a.width;
-    float x[NV][GE];
+    float x[NV][E];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int g = t + TPR * v;
 #pragma unroll
-      for (int j = 0; j < GE; ++j) x[v][j] = 0.f;
-      if (g < groups) ln_load<ACT, GE>(a.x, at + size_t(g) * GE, x[v]);
+      for (int j = 0; j < E; ++j) x[v][j] = 0.f;
+      if (g < groups) ln_load<ACT, CUT>(a.x, at + size_t(g) * E, a.width - E * g, x[v]);
     }
     if (a.res) {
-      float r[NV][GE];
+      float r[NV][E];
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int g = t + TPR * v;
 #pragma unroll
-        for (int j = 0; j < GE; ++j) r[v][j] = 0.f;
-        if (g < groups) ln_load<ACT, GE>(a.res, at + size_t(g) * GE, r[v]);
+        for (int j = 0; j < E; ++j) r[v][j] = 0.f;
+        if (g < groups) ln_load<ACT, CUT>(a.res, at + size_t(g) * E, a.width - E * g, r[v]);
       }
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int g = t + TPR * v;
 #pragma unroll
-        for (int j = 0; j < GE; ++j) x[v][j] += r[v][j];
-        ln_round<ACT, GE>(x[v]);
-        if (g < groups) ln_store<ACT, GE>(a.sum, at + size_t(g) * GE, x[v]);
+        for (int j = 0; j < E; ++j) x[v][j] += r[v][j];
+        ln_round<ACT, E>(x[v]);
+        if (g < groups) ln_store<ACT, CUT>(a.sum, at + size_t(g) * E, a.width - E * g, x[v]);
       }
     }
     float s[1] = {0.f}, q[1] = {0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int j = 0; j < GE; ++j) s[0] += x[v][j];
+      for (int j = 0; j < E; ++j) s[0] += x[v][j];
     ln_row_sum<TPR>(s, red);
     const float mean = s[0] * inv;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       if (t + TPR * v < groups) {
 #pragma unroll
-        for (int j = 0; j < GE; ++j) {
-          const float c = x[v][j] - mean;
+        for (int j = 0; j < E; ++j) {
+          const float c = (CUT != LN_ANY || E * (t + TPR * v) + j < a.width) ? x[v][j] - mean : 0.f;
           q[0] = fmaf(c, c, q[0]);
         }
       }
@@ -171,10 +211,10 @@ __global__ __launch_bounds__(ln_threads(TPR), TPR > 512 ? 4 : ln_fwd_waves(GE, N
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int g = t + TPR * v;
-      float y[GE];
+      float y[E];
 #pragma unroll
-      for (int j = 0; j < GE; ++j) y[j] = fmaf((x[v][j] - mean) * rstd, ga[v][j], be[v][j]);
-      if (g < groups) ln_store<ACT, GE>(a.y, at + size_t(g) * GE, y);
+      for (int j = 0; j < E; ++j) y[j] = fmaf((x[v][j] - mean) * rstd, ga[v][j], be[v][j]);
+      if (g < groups) ln_store<ACT, CUT>(a.y, at + size_t(g) * E, a.width - E * g, y);
     }
     if (t == 0 && a.mean) {
       a.mean[row] = mean;
@@ -222,9 +262,9 @@ __device__ __forceinline__ void ln_columns(const LnBwdArgs& a, int block) {
 // order (through LDS) and writes one partial row [dgamma | dbeta].  Without, the
 // workgroups behind a.row_blocks, if any, take the columns' sums from the inputs
 // again.
-template <int ACT, int DACT, int GE, int TPR, int NV, bool SUMS>
+template <int ACT, int DACT, int CUT, int TPR, int NV, bool SUMS>
 __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
-  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR;
+  constexpr int E = ln_elems(CUT), RPW = TPR > 256 ? 1 : 256 / TPR;
   if constexpr (!SUMS) {
     if (int(blockIdx.x) >= a.row_blocks) {
       ln_columns<ACT, DACT, ln_threads(TPR)>(a, int(blockIdx.x) - a.row_blocks);
@@ -232,44 +272,44 @@ __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
     }
   }
   __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
-  __shared__ float cols[SUMS && RPW > 1 ? RPW : 1][SUMS && RPW > 1 ? TPR * NV * GE : 1];
+  __shared__ float cols[SUMS && RPW > 1 ? RPW : 1][SUMS && RPW > 1 ? TPR * NV * E : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-  const int groups = a.width / GE;
+  const int groups = (a.width + E - 1) / E;
   const float inv = 1.0f / float(a.width);
-  float ga[NV][GE], dg[NV][GE], db[NV][GE];
+  float ga[NV][E], dg[NV][E], db[NV][E];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
     const int g = t + TPR * v;
 #pragma unroll
-    for (int j = 0; j < GE; ++j) {
+    for (int j = 0; j < E; ++j) {
       ga[v][j] = 1.f;
       dg[v][j] = db[v][j] = 0.f;
     }
-    if (g < groups && a.gamma) ln_load<ACT_F32, GE>(a.gamma, size_t(g) * GE, ga[v]);
+    if (g < groups && a.gamma) ln_load<ACT_F32, CUT>(a.gamma, size_t(g) * E, a.width - E * g, ga[v]);
   }
   for (int row = blockIdx.x * RPW + sub; row < a.rows; row += a.row_blocks * RPW) {
     const size_t at = size_t(row) * a.width;
-    float x[NV][GE], d[NV][GE];
+    float x[NV][E], d[NV][E];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int g = t + TPR * v;
 #pragma unroll
-      for (int j = 0; j < GE; ++j) x[v][j] = d[v][j] = 0.f;
+      for (int j = 0; j < E; ++j) x[v][j] = d[v][j] = 0.f;
       if (g < groups) {
-        ln_load<ACT, GE>(a.s, at + size_t(g) * GE, x[v]);
-        ln_load<DACT, GE>(a.dy, at + size_t(g) * GE, d[v]);
+        ln_load<ACT, CUT>(a.s, at + size_t(g) * E, a.width - E * g, x[v]);
+        ln_load<DACT, CUT>(a.dy, at + size_t(g) * E, a.width - E * g, d[v]);
       }
     }
     const float mean = a.mean[row], rstd = a.rstd[row];
     float c[2] = {0.f, 0.f};  // sums of v and v xhat
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      // groups past the row: dy is zero there and xhat is made zero, so that
+      // past the row dy is zero and xhat is made zero, so that
       // an infinite rstd or mean reaches no other column
-      const bool in = t + TPR * v < groups;
+      const int in = a.width - E * (t + TPR * v);
 #pragma unroll
-      for (int j = 0; j < GE; ++j) {
-        x[v][j] = in ? (x[v][j] - mean) * rstd : 0.f;
+      for (int j = 0; j < E; ++j) {
+        x[v][j] = (CUT == LN_ANY ? j < in : in > 0) ? (x[v][j] - mean) * rstd : 0.f;
         const float dy = d[v][j];
         if constexpr (SUMS) {
           dg[v][j] = fmaf(dy, x[v][j], dg[v][j]);
@@ -286,16 +326,16 @@ __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
     for (int v = 0; v < NV; ++v) {
       const int g = t + TPR * v;
       if (g < groups) {
-        float o[GE];
+        float o[E];
 #pragma unroll
-        for (int j = 0; j < GE; ++j) o[j] = rstd * (d[v][j] - c1 - x[v][j] * c2);
+        for (int j = 0; j < E; ++j) o[j] = rstd * (d[v][j] - c1 - x[v][j] * c2);
         if (a.d_sum) {
-          float r[GE];
-          ln_load<ACT, GE>(a.d_sum, at + size_t(g) * GE, r);
+          float r[E];
+          ln_load<ACT, CUT>(a.d_sum, at + size_t(g) * E, a.width - E * g, r);
 #pragma unroll
-          for (int j = 0; j < GE; ++j) o[j] += r[j];
+          for (int j = 0; j < E; ++j) o[j] += r[j];
         }
-        ln_store<ACT, GE>(a.dx, at + size_t(g) * GE, o);
+        ln_store<ACT, CUT>(a.dx, at + size_t(g) * E, a.width - E * g, o);
       }
     }
   }
@@ -309,14 +349,15 @@ __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
           const int g = t + TPR * v;
           if (g < groups)
 #pragma unroll
-            for (int j = 0; j < GE; ++j) out[size_t(k) * a.width + size_t(g) * GE + j] = k ? db[v][j] : dg[v][j];
+            for (int j = 0; j < E; ++j)
+              if (CUT != LN_ANY || E * g + j < a.width) out[size_t(k) * a.width + size_t(g) * E + j] = k ? db[v][j] : dg[v][j];
         }
       } else {
         __syncthreads();
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
-          for (int j = 0; j < GE; ++j) cols[sub][(t + TPR * v) * GE + j] = k ? db[v][j] : dg[v][j];
+          for (int j = 0; j < E; ++j) cols[sub][(t + TPR * v) * E + j] = k ? db[v][j] : dg[v][j];
         __syncthreads();
         for (int c = threadIdx.x; c < a.width; c += 256) {
           float s = 0.f;
@@ -369,8 +410,8 @@ bool ln_aligned(const void* p, size_t b) { return reinterpret_cast<uintptr_t>(p)
 struct LnShape {
   int tpr, nv;
 };
-LnShape ln_shape(int ge, int groups) {
-  if (ge == 8) {
+LnShape ln_shape(int cut, int groups) {
+  if (cut <= LN_ANY) {
     if (groups <= 64) return {64, 1};
     if (groups <= 128) return {64, 2};
     if (groups <= 256) return {64, 4};
@@ -378,44 +419,51 @@ LnShape ln_shape(int ge, int groups) {
     if (groups <= 1024) return {512, 2};
     return {1024, 2};
   }
-  if (ge == 2) {
+  if (cut == LN_PAIR) {
     if (groups <= 128) return {64, 2};
     if (groups <= 512) return {64, 8};
     if (groups <= 2048) return {256, 8};
     return {1024, 8};
   }
-  if (groups <= 256) return {64, 4};
-  if (groups <= 1024) return {64, 16};
-  if (groups <= 4096) return {256, 16};
-  return {1024, 16};
+  return groups <= 256 ? LnShape{64, 4} : LnShape{64, 16};  // 512 at most
 }
 
-int ln_group(int width, bool v16, bool pair) { return width % 8 == 0 && v16 ? 8 : width % 2 == 0 && pair ? 2 : 1; }
+// whole, pair: what alignment and width allow.  Wide rows of any alignment take 16
+// bytes at a time (forward and gradient in us, so and by pairs or singles: 8220 x 1443
+// bf16 25 and 41, 55 and 81; 16384 x 2047 bf16 71 and 121, 172 and 264; 5000 x 4099
+// fp32 72 and 100, 77 and 168), narrow ones lose by the last group's single accesses
+// (20000 x 255 bf16 19 and 49, 15 and 35), as do fp32's pairs in the forward (4096 x
+// 2046 26 and 22) and above 4096 in the gradient (3000 x 8190 118 and 110).
+int ln_cut(int width, bool whole, bool pair, bool keep_pairs) {
+  if (whole) return LN_WHOLE;
+  if (pair && (width <= 512 || keep_pairs)) return LN_PAIR;
+  return width > 512 ? LN_ANY : pair ? LN_PAIR : LN_SINGLE;
+}
 
 constexpr int LN_CUS = 256;  // of a whole MI355X
 
-template <int ACT, int GE, int TPR, int NV>
+template <int ACT, int CUT, int TPR, int NV>
 hipError_t fwd_go(const LnFwdArgs& a, hipStream_t s) {
-  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR, waves = TPR > 512 ? 4 : ln_fwd_waves(GE, NV);
+  constexpr int RPW = TPR > 256 ? 1 : 256 / TPR, waves = TPR > 512 ? 4 : ln_fwd_waves(ln_elems(CUT), NV);
   constexpr int most = LN_CUS * (waves * 256 / ln_threads(TPR));
   const int blocks = (a.rows + RPW - 1) / RPW;
-  hipLaunchKernelGGL((ln_fwd_kernel<ACT, GE, TPR, NV>), dim3(unsigned(blocks < most ? blocks : most)),
+  hipLaunchKernelGGL((ln_fwd_kernel<ACT, CUT, TPR, NV>), dim3(unsigned(blocks < most ? blocks : most)),
                      dim3(ln_threads(TPR)), 0, s, a);
   return hipGetLastError();
 }
 
-template <int ACT, int DACT, int GE, int TPR, int NV>
+template <int ACT, int DACT, int CUT, int TPR, int NV>
 hipError_t bwd_go(LnBwdArgs a, hipStream_t s) {
   const dim3 threads(ln_threads(TPR));
   if (a.part) {
-    hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV, true>), dim3(unsigned(a.row_blocks)), threads, 0, s, a);
+    hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, CUT, TPR, NV, true>), dim3(unsigned(a.row_blocks)), threads, 0, s, a);
     return hipGetLastError();
   }
   int columns = a.dgamma ? (a.width + LN_COLS - 1) / LN_COLS : 0;
   if (columns && (a.dx == a.s || a.dx == a.dy)) {  // in place: the columns first
     const int rows = a.row_blocks;
     a.row_blocks = 0;
-    hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV, false>), dim3(unsigned(columns)), threads, 0, s, a);
+    hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, CUT, TPR, NV, false>), dim3(unsigned(columns)), threads, 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     a.row_blocks = rows;
@@ -423,42 +471,40 @@ hipError_t bwd_go(LnBwdArgs a, hipStream_t s) {
   }
   const int grid = a.row_blocks + columns;
   if (grid == 0) return hipSuccess;
-  hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, GE, TPR, NV, false>), dim3(unsigned(grid)), threads, 0, s, a);
+  hipLaunchKernelGGL((ln_bwd_kernel<ACT, DACT, CUT, TPR, NV, false>), dim3(unsigned(grid)), threads, 0, s, a);
   return hipGetLastError();
 }
 
-#define LN_SHAPES(GO)                          \
-  if (ge == 8) {                               \
-    if (sh.tpr == 1024) return GO(8, 1024, 2); \
-    if (sh.tpr == 512) return GO(8, 512, 2);   \
-    if (sh.tpr == 256) return GO(8, 256, 2);   \
-    if (sh.nv == 4) return GO(8, 64, 4);       \
-    if (sh.nv == 2) return GO(8, 64, 2);       \
-    return GO(8, 64, 1);                       \
-  }                                            \
-  if (ge == 2) {                               \
-    if (sh.tpr == 1024) return GO(2, 1024, 8); \
-    if (sh.tpr == 256) return GO(2, 256, 8);   \
-    if (sh.nv == 8) return GO(2, 64, 8);       \
-    return GO(2, 64, 2);                       \
-  }                                            \
-  if (sh.tpr == 1024) return GO(1, 1024, 16);  \
-  if (sh.tpr == 256) return GO(1, 256, 16);    \
-  if (sh.nv == 16) return GO(1, 64, 16);       \
-  return GO(1, 64, 4);
+#define LN_SHAPES_8(GO, CUT)                 \
+  if (sh.tpr == 1024) return GO(CUT, 1024, 2); \
+  if (sh.tpr == 512) return GO(CUT, 512, 2);   \
+  if (sh.tpr == 256) return GO(CUT, 256, 2);   \
+  if (sh.nv == 4) return GO(CUT, 64, 4);       \
+  if (sh.nv == 2) return GO(CUT, 64, 2);       \
+  return GO(CUT, 64, 1);
+
+#define LN_SHAPES(GO)                                                       \
+  const int e = ln_elems(cut);                                              \
+  const LnShape sh = ln_shape(cut, (a.width + e - 1) / e);                  \
+  if (cut == LN_WHOLE) { LN_SHAPES_8(GO, LN_WHOLE) }                        \
+  if (cut == LN_ANY) { LN_SHAPES_8(GO, LN_ANY) }                            \
+  if (cut == LN_PAIR) {                                                     \
+    if (sh.tpr == 1024) return GO(LN_PAIR, 1024, 8);                        \
+    if (sh.tpr == 256) return GO(LN_PAIR, 256, 8);                          \
+    return sh.nv == 8 ? GO(LN_PAIR, 64, 8) : GO(LN_PAIR, 64, 2);            \
+  }                                                                         \
+  return sh.nv == 16 ? GO(LN_SINGLE, 64, 16) : GO(LN_SINGLE, 64, 4);
 
 template <int ACT>
-hipError_t fwd_act(const LnFwdArgs& a, int ge, hipStream_t s) {
-  const LnShape sh = ln_shape(ge, a.width / ge);
-#define LN_GO(G, T, V) fwd_go<ACT, G, T, V>(a, s)
+hipError_t fwd_act(const LnFwdArgs& a, int cut, hipStream_t s) {
+#define LN_GO(C, T, V) fwd_go<ACT, C, T, V>(a, s)
   LN_SHAPES(LN_GO)
 #undef LN_GO
 }
 
 template <int ACT, int DACT>
-hipError_t bwd_act(const LnBwdArgs& a, int ge, hipStream_t s) {
-  const LnShape sh = ln_shape(ge, a.width / ge);
-#define LN_GO(G, T, V) bwd_go<ACT, DACT, G, T, V>(a, s)
+hipError_t bwd_act(const LnBwdArgs& a, int cut, hipStream_t s) {
+#define LN_GO(C, T, V) bwd_go<ACT, DACT, C, T, V>(a, s)
   LN_SHAPES(LN_GO)
 #undef LN_GO
 }
@@ -484,27 +530,27 @@ size_t ln_bwd_workspace(int rows, int width) { return ln_bwd_once(rows, width) ?
 
 hipError_t launch_ln_fwd(const LnFwdArgs& a, int act, hipStream_t s) {
   if (a.rows == 0) return hipSuccess;
-  const size_t pair = act == ACT_BF16 ? 4 : 8;
+  const size_t two = act == ACT_BF16 ? 4 : 8;
   auto all = [&](size_t b, size_t f) {
     return ln_aligned(a.x, b) && ln_aligned(a.res, b) && ln_aligned(a.sum, b) && ln_aligned(a.y, b) &&
            ln_aligned(a.gamma, f) && ln_aligned(a.beta, f);
   };
-  const int ge = ln_group(a.width, all(16, 16), all(pair, 8));
-  return act == ACT_BF16 ? fwd_act<ACT_BF16>(a, ge, s) : fwd_act<ACT_F32>(a, ge, s);
+  const int cut = ln_cut(a.width, a.width % 8 == 0 && all(16, 16), a.width % 2 == 0 && all(two, 8), act == ACT_F32);
+  return act == ACT_BF16 ? fwd_act<ACT_BF16>(a, cut, s) : fwd_act<ACT_F32>(a, cut, s);
 }
 
 hipError_t launch_ln_bwd(LnBwdArgs a, int act, int dact, hipStream_t s) {
-  const size_t pair = act == ACT_BF16 ? 4 : 8, dpair = dact == ACT_BF16 ? 4 : 8;
+  const size_t two = act == ACT_BF16 ? 4 : 8, dtwo = dact == ACT_BF16 ? 4 : 8;
   auto all = [&](size_t b, size_t d, size_t f) {
     return ln_aligned(a.s, b) && ln_aligned(a.d_sum, b) && ln_aligned(a.dx, b) && ln_aligned(a.dy, d) &&
            ln_aligned(a.gamma, f);
   };
-  const int ge = ln_group(a.width, all(16, 16, 16), all(pair, dpair, 8));
+  const int cut = ln_cut(a.width, a.width % 8 == 0 && all(16, 16, 16), a.width % 2 == 0 && all(two, dtwo, 8), a.width > 4096);
   a.row_blocks = ln_bwd_blocks(a.rows);
   if (!a.dgamma || ln_bwd_once(a.rows, a.width)) a.part = nullptr;
   const hipError_t e = act == ACT_BF16
-                           ? (dact == ACT_BF16 ? bwd_act<ACT_BF16, ACT_BF16>(a, ge, s) : bwd_act<ACT_BF16, ACT_F32>(a, ge, s))
-                           : bwd_act<ACT_F32, ACT_F32>(a, ge, s);
+                           ? (dact == ACT_BF16 ? bwd_act<ACT_BF16, ACT_BF16>(a, cut, s) : bwd_act<ACT_BF16, ACT_F32>(a, cut, s))
+                           : bwd_act<ACT_F32, ACT_F32>(a, cut, s);
   if (e != hipSuccess || !a.part) return e;
   hipLaunchKernelGGL(ln_colsum_kernel, dim3(unsigned((2 * a.width + 15) / 16)), dim3(1024), 0, s, a.part, a.dgamma,
                      a.dbeta, a.row_blocks, a.width);

@@ -17,7 +17,7 @@
  *
  * Widths 1 .. 16384, rows 0 .. 2^24; arrays are row-major and
  * dense, aligned to their element size (16-byte alignment and a width that is
- * a multiple of 8 take the 16-byte loads).  Memory rules as in bmoe.h: every
+ * a multiple of 8 are fastest).  Memory rules as in bmoe.h: every
  * pointer is caller-owned device memory, nothing is allocated or
  * synchronised, all work is enqueued on `stream`, results do not depend on
  * scheduling, and all errors but BMOE_ERR_HIP are found before anything is

@@ -170,7 +170,8 @@ def test_norm_in_place():
         assert (dx == wdx).all() and (g == wg).all() and (b == wb).all(), name
 
 
-@pytest.mark.parametrize("rows,width,kind", [(1024, 2048, "bf16"), (1000, 777, "f32"), (1024, 64, "f32"), (1100, 2048, "bf16")])
+@pytest.mark.parametrize("rows,width,kind", [(1024, 2048, "bf16"), (1000, 777, "f32"), (1024, 64, "f32"), (1100, 2048, "bf16"),
+                                             (60, 4099, "bf16"), (1200, 1443, "bf16"), (300, 6001, "f32")])
 def test_norm_gradient_in_place(rows, width, kind):
     """The columns' sums are those of the inputs, whichever of them dx overwrites."""
     c = draw(rows, width, kind, rows)
