@@ -18,23 +18,31 @@ __device__ __forceinline__ float ln_wave_sum(float v) {
   return v;
 }
 
-// Sums of N values over the TPR threads of a row, the same in each of them.
+// Sums of N values over the TPR threads of a row, the same in each of them: over
+// each wave, then every wave adds the waves' sums.  Two sets of those in turn, so one
+// barrier a sum is enough: who writes a set again is past the barrier of the sum
+// between, which every wave reaches only after its reads of the set.
+template <int TPR>
+struct LnRed {
+  float2 sums[2][TPR > 64 ? TPR / 64 : 1];
+};
 template <int TPR, int N>
-__device__ __forceinline__ void ln_row_sum(float (&v)[N], float2* red) {
+__device__ __forceinline__ void ln_row_sum(float (&v)[N], LnRed<TPR>& red, int& turn) {
 #pragma unroll
   for (int k = 0; k < N; ++k) v[k] = ln_wave_sum(v[k]);
   if constexpr (TPR > 64) {
-    const int wave = threadIdx.x >> 6;
-    __syncthreads();  // the previous use of red is over
-    if ((threadIdx.x & 63) == 0) red[wave] = make_float2(v[0], v[N - 1]);
+    constexpr int W = TPR / 64;
+    float2* r = red.sums[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = make_float2(v[0], v[N - 1]);
     __syncthreads();
+    const float2 u = r[threadIdx.x % W];
+    v[0] = u.x;
+    if constexpr (N == 2) v[1] = u.y;
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] = 0.f;
+    for (int m = 1; m < W; m <<= 1)
 #pragma unroll
-    for (int w = 0; w < TPR / 64; ++w) {
-      v[0] += red[w].x;
-      if constexpr (N == 2) v[1] += red[w].y;
-    }
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor(v[k], m);
   }
 }
 
@@ -144,8 +152,10 @@ constexpr int ln_threads(int tpr) { return tpr > 256 ? tpr : 256; }
 
 template <int ACT, int CUT, int TPR, int NV>
 __global__ __launch_bounds__(ln_threads(TPR), TPR > 512 ? 4 : ln_fwd_waves(ln_elems(CUT), NV)) void ln_fwd_kernel(LnFwdArgs a) {
+#pragma clang fp contract(off)  // what a row is centred by is the mean as rounded
   constexpr int E = ln_elems(CUT), RPW = TPR > 256 ? 1 : 256 / TPR;  // rows per workgroup
-  __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
+  __shared__ LnRed<TPR> red;
+  int turn = 0;
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int groups = (a.width + E - 1) / E;
   const float inv = 1.0f / float(a.width);
@@ -189,31 +199,45 @@ __global__ __launch_bounds__(ln_threads(TPR), TPR > 512 ? 4 : ln_fwd_waves(ln_el
         if (g < groups) ln_store<ACT, CUT>(a.sum, at + size_t(g) * E, a.width - E * g, x[v]);
       }
     }
-    float s[1] = {0.f}, q[1] = {0.f};
+    float s[1] = {0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int j = 0; j < E; ++j) s[0] += x[v][j];
-    ln_row_sum<TPR>(s, red);
-    const float mean = s[0] * inv;
+    ln_row_sum<TPR>(s, red, turn);
+    // The row less its mean as summed, which is off by that sum's roundings: by as
+    // much as a row far from 0 varies, or by all that a constant row does.  The
+    // centred row's own sum gives what is missing, d, to the mean and to every value
+    // (one more sum beside that of the squares).  A row whose d is not small against
+    // what it varies by, or that does not vary, is centred once more.
+    float mean = s[0] * inv, shift = mean, before = 0.f, d = 0.f, var = 0.f;
+    for (bool last = false;; last = true) {
+      float q[2] = {0.f, 0.f};  // sums of the centred values and of their squares
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      if (t + TPR * v < groups) {
+      for (int v = 0; v < NV; ++v) {
+        const int in = a.width - E * (t + TPR * v);
 #pragma unroll
         for (int j = 0; j < E; ++j) {
-          const float c = (CUT != LN_ANY || E * (t + TPR * v) + j < a.width) ? x[v][j] - mean : 0.f;
-          q[0] = fmaf(c, c, q[0]);
+          x[v][j] = (CUT == LN_ANY ? j < in : in > 0) ? x[v][j] - shift : 0.f;
+          q[0] += x[v][j];
+          q[1] = fmaf(x[v][j], x[v][j], q[1]);
         }
       }
+      ln_row_sum<TPR>(q, red, turn);
+      d = q[0] * inv;
+      var = q[1] * inv;
+      if (last || d * d <= 0x1p-12f * var) break;
+      shift = before = d;
     }
-    ln_row_sum<TPR>(q, red);
-    const float rstd = 1.0f / sqrtf(fmaf(q[0], inv, a.eps));
+    mean += before + d;
+    var = fmaf(-d, d, var);
+    const float rstd = 1.0f / sqrtf((var < 0.f ? 0.f : var) + a.eps);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int g = t + TPR * v;
       float y[E];
 #pragma unroll
-      for (int j = 0; j < E; ++j) y[j] = fmaf((x[v][j] - mean) * rstd, ga[v][j], be[v][j]);
+      for (int j = 0; j < E; ++j) y[j] = fmaf((x[v][j] - d) * rstd, ga[v][j], be[v][j]);
       if (g < groups) ln_store<ACT, CUT>(a.y, at + size_t(g) * E, a.width - E * g, y);
     }
     if (t == 0 && a.mean) {
@@ -271,7 +295,8 @@ __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
       return;
     }
   }
-  __shared__ float2 red[TPR > 64 ? TPR / 64 : 1];
+  __shared__ LnRed<TPR> red;
+  int turn = 0;
   __shared__ float cols[SUMS && RPW > 1 ? RPW : 1][SUMS && RPW > 1 ? TPR * NV * E : 1];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int groups = (a.width + E - 1) / E;
@@ -320,7 +345,7 @@ __global__ __launch_bounds__(ln_threads(TPR)) void ln_bwd_kernel(LnBwdArgs a) {
         c[1] = fmaf(d[v][j], x[v][j], c[1]);
       }
     }
-    ln_row_sum<TPR>(c, red);
+    ln_row_sum<TPR>(c, red, turn);
     const float c1 = c[0] * inv, c2 = c[1] * inv;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {

@@ -12,8 +12,10 @@
  *     y_j  = (s_j - mean) rstd gamma_j + beta_j.
  * s is rounded to the activation dtype first and the norm is that of the
  * rounded row, so the backward, which reads the stored s, sees the forward's
- * values.  Sums run in fp32 over a row held in registers (the variance over
- * the centred values).
+ * values.  Sums run in fp32 over a row held in registers: the mean's rounding
+ * is taken from the sum of the centred values and given back to the mean, the
+ * variance and y, so a row far from 0 is normed as well as one around it and a
+ * constant row gives y = beta.
  *
  * Widths 1 .. 16384, rows 0 .. 2^24; arrays are row-major and
  * dense, aligned to their element size (16-byte alignment and a width that is

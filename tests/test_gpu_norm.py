@@ -302,3 +302,46 @@ def test_norm_many_elements():
     dx, dg, db = bm.layer_norm_backward(y, x, None, mean, rstd, dx=y)
     wx = bm.layer_norm_backward(tail[0], x[-4:].clone(), None, tail[2], tail[3])[0]
     assert (dx[-4:] == wx).all() and torch.isfinite(dg).all()
+
+
+# widths of every cut and every number of threads per row
+WIDTHS = [77, 255, 300, 520, 777, 1000, 1008, 1443, 2000, 2050, 3000, 4099, 6000, 8190, 12000, 12001, 16382]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_norm_constant_rows_are_exact(width, kind):
+    """A constant row's centred values are only what its summed mean is off by, at
+    most 56 u |value|; centring twice more leaves (57 u)^2 of that, 1e-15 of the
+    value, below half a place of it: the mean is the value, y is beta, rstd is
+    eps^-1/2 with its own four operations' roundings."""
+    import torch
+    c = draw(1, width, kind, width)
+    values = torch.tensor([96.0, 1000.0, -3000.0, 3.25, 10000.0, 1e-3, 2.0 ** 20]).to(c["dt"])
+    x = values[:, None].expand(-1, width).contiguous().cuda()
+    y, _, mean, rstd = bm.layer_norm_forward(x, c["gamma"].cuda(), c["beta"].cuda(), eps=1e-5)
+    assert (mean.cpu() == values.float()).all(), mean
+    assert (np.abs(to_f64(rstd) / float(np.float32(1e-5)) ** -0.5 - 1) <= 4 * U).all(), rstd
+    be = to_f64(c["beta"])
+    assert (np.abs(to_f64(y) - be) <= 2 * half(c["dt"]) * np.abs(be) + 1e-6).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("offset", [30.0, 1e3, 1e5])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_norm_of_rows_far_from_zero(width, offset, kind):
+    """Rows that lie `offset` standard deviations from 0.  Centred values are exact
+    (both terms of the difference are within a factor 2), what they miss of the true
+    mean is known to 57 u of their mean magnitude, which is at most the deviation:
+    y is off by 60 u and 46 units of its own, whatever the offset."""
+    c = draw(6, width, kind, width, offset=offset)
+    d = {k: v.cuda() for k, v in c.items() if k != "dt"}
+    for residual in (False, True):
+        y, s, mean, rstd = bm.layer_norm_forward(d["x"], d["gamma"], d["beta"], residual=d["r"] if residual else None)
+        wy, wm, wr = ref.layer_norm(to_f64(s), to_f64(d["gamma"]), to_f64(d["beta"]), float(np.float32(1e-5)))
+        ga, be, b = np.abs(to_f64(d["gamma"])), np.abs(to_f64(d["beta"])), half(c["dt"])
+        xh = np.abs((to_f64(s) - wm[:, None]) * wr[:, None])
+        tol = ga * U * (60 + 46 * xh) + U * be
+        assert (np.abs(to_f64(y) - wy) <= tol + b * (np.abs(wy) + tol)).all(), "y"
+        assert (np.abs(to_f64(mean) - wm) <= 1.01 * U * np.abs(wm) + 60 * U / wr).all(), "mean"
+        assert (np.abs(to_f64(rstd) - wr) <= 40 * U * wr).all(), "rstd"
