@@ -345,3 +345,26 @@ def test_norm_of_rows_far_from_zero(width, offset, kind):
         assert (np.abs(to_f64(y) - wy) <= tol + b * (np.abs(wy) + tol)).all(), "y"
         assert (np.abs(to_f64(mean) - wm) <= 1.01 * U * np.abs(wm) + 60 * U / wr).all(), "mean"
         assert (np.abs(to_f64(rstd) - wr) <= 40 * U * wr).all(), "rstd"
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("size", [1e17, 1e19, 1e25, 1e37])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_norm_of_large_finite_rows(width, size, kind):
+    """Rows whose squares, or whose sum, leave fp32: the same bars as for any row,
+    powers of two apart nothing is rounded otherwise.  1e37 leaves room for eight
+    deviations below 2^127."""
+    import torch
+    c = draw(5, width, kind, width)
+    scale = torch.tensor([1.0, 1.0, 1.0, 1.0, 2.0 ** -60])[:, None]      # the last row is an ordinary one
+    z = (torch.randn(5, width, generator=torch.Generator().manual_seed(width)).clamp(-6, 6) + 1.5) * size * scale
+    z[2] = c["x"][2].float()
+    z[2, width // 2] = size                                              # one entry of a small row
+    c = dict(c, x=z.to(c["dt"]), r=c["r"] * size * 0.25)
+    d = {k: v.cuda() for k, v in c.items() if k != "dt"}
+    for residual in (False, True):
+        got = bm.layer_norm_forward(d["x"], d["gamma"], d["beta"], residual=d["r"] if residual else None)
+        check_forward(c, got, d["gamma"], d["beta"], 1e-5, residual)
+        if size < 1e30:  # gradients that stay above fp32's smallest normal number
+            check_backward(c, bm.layer_norm_backward(d["dy"], got[1], d["gamma"], got[2], got[3]), got[1], d["dy"],
+                           d["gamma"], got[2], got[3], None)
