@@ -416,21 +416,46 @@ class Layer:
                                          int(state.numel()), ctypes.byref(g), _ptr(ws), nw, _stream_handle()))
         return out
 
-    def step_substrate(self, m: int, w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None):
+    def set_scale(self, m: int, scale) -> "Layer":
+        """The factor of substrate m's codes (bmoe_layer's w_scale) in every call
+        from now on: a number, or a one-element tensor, whose reading waits for its
+        GPU.  The factor is an argument of the launches: a forward captured before
+        replays with the one it was captured with."""
+        if not 0 <= m < len(self.w_base):
+            raise ValueError(f"the layer has no substrate {m}")
+        scale = float(scale)
+        if not abs(scale) <= np.finfo(np.float32).max:
+            raise ValueError(f"substrate {m}'s scale must be finite in fp32, got {scale}")
+        self.struct.w_scale[m] = scale
+        return self
+
+    def step_substrate(self, m: int, w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None,
+                       rescale: bool = False):
         """substrate_step of latent substrate m ([d_out][d_in] fp32) with the
         codes written into this layer; weights prepared before are prepared
         again in the same buffer, which graphs captured from this layer read.
-        Returns (W', scale)."""
+        Returns (W', scale).
+
+        scale * codes stand for W'.  With rescale the layer's factor
+        follows (set_scale with the step's scale, which waits for the GPU and is
+        refused in a capture), so that the layer computes with scale * codes.
+        Without, the factor stays what it is: the layer's output and the gradient
+        of its substrate keep that factor whatever |W'| is, which is what a step
+        in a captured graph can do."""
         if not 0 <= m < len(self.w_base):
             raise ValueError(f"the layer has no substrate {m}")
         d_out, d_in = 1 << int(self.phi[m].shape[1]), 1 << int(self.theta[m].shape[1])
         if tuple(w.shape) != (d_out, d_in):
             raise ValueError(f"w has shape {tuple(w.shape)}, substrate {m} is {(d_out, d_in)}")
+        if rescale and w.is_cuda and _torch().cuda.is_current_stream_capturing():
+            raise ValueError("rescale reads the scale on the host, which a captured step cannot do")
         w, _, scale = substrate_step(w, o, step, decay, w_out=w_out, packed=self.w_base[m])
         if self._prep is not None:
             with _torch().cuda.device(w.device):
                 _check(lib().bmoe_prepare(ctypes.byref(self.struct), self.struct.prepared, self.struct.prepared_bytes,
                                           _stream_handle()))
+        if rescale:
+            self.set_scale(m, scale)
         return w, scale
 
     def kernel_names(self) -> List[str]:
@@ -706,8 +731,9 @@ def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0, w_out=None,
     """Latent substrate step W' = (1 - decay) W - step O (W [rows][cols] fp32, O
     bf16; W' = W without O) and its ternary codes at threshold mean |W'| / 2.
     Returns (W', packed [rows][cols / 16] int32 in pack_ternary's format,
-    scale: 0-d fp32 tensor mean |W'|).  w_out may be w itself (Layer.step_substrate
-    writes the codes into a layer)."""
+    scale: 0-d fp32 tensor mean |W'|, the factor under which the codes stand for
+    W').  w_out may be w itself (Layer.step_substrate writes the codes into a
+    layer)."""
     torch = _torch()
     dev, shape = w.device, w.shape
     rows, cols = shape

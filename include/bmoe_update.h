@@ -76,7 +76,10 @@ bmoe_status bmoe_orthogonalize(int32_t rows, int32_t cols, int32_t grad_dtype, c
  *   packed   [rows][cols / 16] words (16-byte aligned), written in
  *            bmoe_pack_ternary's format: w_base of bmoe_layer.
  *   scale    1 fp32, written, or NULL: the w_scale under which the codes
- *            stand for W'.
+ *            stand for W'.  bmoe_layer's w_scale is a host value that this call
+ *            does not touch: a caller whose layer computes with scale * codes
+ *            copies scale back and sets it, one whose layer keeps a fixed w_scale
+ *            (its output then does not depend on |W'|) leaves it.
  *   workspace at least bmoe_substrate_step_workspace bytes, 16-byte aligned,
  *            contents undefined after; may be NULL when that is 0 (few
  *             weights).

@@ -150,3 +150,18 @@ def test_refusals_under_host_sanitizers():
                         os.path.abspath(__file__)], cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
     tail = (r.stdout + r.stderr)[-3000:]
     assert r.returncode == 0 and "passed" in r.stdout and "ERROR: AddressSanitizer" not in r.stderr, tail
+
+
+def test_layer_scale():
+    """The factor of a substrate's codes, and what is refused for one."""
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    layer = bm.Layer(d_model=64, d_ff=0, n_experts=2, top_k=1, act="f32", ffn_act="none", renorm_gates=False,
+                     w_gate=z(2, 64), w_base_packed=[z(64, 4, dtype=torch.int32)], theta=[z(2, 6, 32)], phi=[z(2, 6, 32)],
+                     w_scale=[1.0])
+    assert layer.set_scale(0, 0.25) is layer and layer.struct.w_scale[0] == 0.25
+    layer.set_scale(0, torch.tensor(0.5))
+    for m, scale in ((1, 1.0), (-1, 1.0), (0, float("nan")), (0, float("inf")), (0, 1e39), (0, torch.tensor(float("-inf")))):
+        with pytest.raises(ValueError):
+            layer.set_scale(m, scale)
+    assert layer.struct.w_scale[0] == 0.5

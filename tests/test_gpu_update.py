@@ -381,3 +381,62 @@ def test_step_substrate_under_captured_forward(d_ff):
         inp.w_base = [ref.substrate_step(step.cpu().numpy())[1]] + list(inp.w_base[1:])
         want = bm.Layer.from_inputs(inp, device="cuda").prepare().forward(x)
         assert (y == want).all(), k
+
+
+@pytest.mark.parametrize("kw", [dict(d_model=128, d_ff=0, act="f32"), dict(d_model=128, d_ff=256, act="f32"),
+                                dict(d_model=256, d_ff=0, act="bf16"), dict(d_model=256, d_ff=512, act="bf16")])
+def test_step_substrate_rescales_the_layer(kw):
+    """After a step with rescale the layer computes with scale * codes: forward,
+    training forward and gradients equal those of a layer built with these scales,
+    and the forward is the oracle's with W = scale * codes."""
+    import torch
+    from gpu_helpers import row_rel_err, tol_for
+    inp = wl.generate(wl.small_config(n_experts=4, top_k=2, tokens=60, seed_index=730 + kw["d_model"], **kw))
+    layer = bm.Layer.from_inputs(inp, device="cuda").prepare()
+    x = to_dev(inp.x, kw["act"])
+    g = torch.Generator().manual_seed(73)
+    scales, real = [], []
+    for m, latent in enumerate(inp.w_base):
+        w = (0.3 + m) * torch.randn(latent.shape, generator=g).cuda()
+        o = torch.randn(latent.shape, generator=g).bfloat16().cuda()
+        w1, scale = layer.step_substrate(m, w, o, step=0.05, decay=0.01, rescale=True)
+        _, codes, want = ref.substrate_step(w1.cpu().numpy())
+        assert abs(layer.struct.w_scale[m] - want) <= 2.0 ** -23 * want and layer.struct.w_scale[m] == float(scale)
+        scales.append(float(scale))
+        inp.w_base[m] = codes
+        real.append(want * codes)
+    fresh = bm.Layer.from_inputs(inp, device="cuda")
+    for m, scale in enumerate(scales):
+        fresh.struct.w_scale[m] = scale
+    y, idx, _ = layer.forward(x, return_routing=True)
+    assert (y == fresh.prepare().forward(x)).all()
+    (yt, state), (ft, fstate) = layer.forward_train(x), fresh.forward_train(x)
+    dy = torch.randn(x.shape, generator=g).to(x.dtype).cuda()
+    grads, want = layer.backward(x, dy, state), fresh.backward(x, dy, fstate)
+    assert (yt == ft).all() and all((a == b).all() for a, b in zip(grads["w_base"], want["w_base"]))
+    inp.w_base = real
+    wy = ref.forward(inp, idx_override=idx.cpu().numpy())[0]
+    e = row_rel_err(to_f64(y), wy).max()
+    log(f"rescaled layer {kw}: {e:.2e}")
+    assert e <= tol_for(kw["act"]), e
+
+
+def test_step_substrate_rescale_refusals():
+    """A captured step cannot set a host value; a scale that is not finite is not
+    taken over."""
+    import torch
+    inp = wl.generate(wl.small_config(d_model=128, d_ff=0, n_experts=4, top_k=2, tokens=50, act="bf16", seed_index=740))
+    layer = bm.Layer.from_inputs(inp, device="cuda").prepare()
+    w = torch.randn(128, 128, generator=torch.Generator().manual_seed(74)).cuda()
+    layer.step_substrate(0, w)
+    assert layer.struct.w_scale[0] == 1.0
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="captured"):
+            layer.step_substrate(0, w, rescale=True)
+        layer.step_substrate(0, w)
+    w[3, 4] = float("nan")
+    with pytest.raises(ValueError, match="finite"):
+        layer.step_substrate(0, w, rescale=True)
+    assert layer.struct.w_scale[0] == 1.0
