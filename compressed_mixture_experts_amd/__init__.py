@@ -637,7 +637,8 @@ def layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, residual=Non
     """Row norm of s = x (+ residual): y = (s - mean) rstd gamma + beta.
     x, residual [rows][width] fp32 or bf16; gamma, beta [width] fp32 or None
     (ones, zeros).  Returns (y, s, mean, rstd): s is x itself without a
-    residual, mean and rstd ([rows] fp32) are None with stats=False."""
+    residual (None where y is written over x: the row that a backward reads is
+    gone), mean and rstd ([rows] fp32) are None with stats=False."""
     torch = _torch()
     dev, kind, shape = x.device, x.dtype, x.shape
     rows, width = shape
@@ -661,7 +662,9 @@ def layer_norm_forward(x, gamma=None, beta=None, eps: float = 1e-5, residual=Non
         None if gamma is None else gamma.data_ptr(), None if beta is None else beta.data_ptr(), eps,
         None if residual is None else sum_out.data_ptr(), y.data_ptr(), mean.data_ptr() if stats else None,
         rstd.data_ptr() if stats else None, _raw_stream(x)))
-    return y, x if residual is None else sum_out, mean, rstd
+    if residual is None:
+        return y, None if y.data_ptr() == x.data_ptr() and x.numel() else x, mean, rstd
+    return y, sum_out, mean, rstd
 
 
 @_on_device
@@ -671,6 +674,8 @@ def layer_norm_backward(dy, s, gamma, mean, rstd, d_sum=None, weight_grads: bool
     reaches s past the norm, added into dx).  Returns (dx like s, dgamma,
     dbeta [width] fp32; None with weight_grads=False)."""
     torch = _torch()
+    if s is None:
+        raise ValueError("s is None: the forward wrote y over the row that the backward reads")
     dev, kind, shape, f32 = dy.device, s.dtype, dy.shape, (torch.float32,)
     rows, width = shape
     _operand("s", s, shape, (torch.float32, torch.bfloat16), dev)

@@ -44,7 +44,8 @@ extern "C" {
  *   sum       [rows][width] of dtype, written with s: given exactly when
  *             residual is; may be the same buffer as x or residual.
  *   y         [rows][width] of dtype, written; may be the same buffer as x or
- *             residual (not as sum).
+ *             residual (not as sum).  Without a residual x is the row that the
+ *             backward reads: over it y serves a forward alone.
  *   mean, rstd  [rows] fp32, written, for the backward: both or neither NULL.
  * A row that holds a NaN or an infinity becomes NaN, other rows are not
  * affected.  Errors: BMOE_ERR_SHAPE (rows, width, eps), BMOE_ERR_DTYPE,

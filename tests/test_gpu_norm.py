@@ -368,3 +368,19 @@ def test_norm_of_large_finite_rows(width, size, kind):
         if size < 1e30:  # gradients that stay above fp32's smallest normal number
             check_backward(c, bm.layer_norm_backward(d["dy"], got[1], d["gamma"], got[2], got[3]), got[1], d["dy"],
                            d["gamma"], got[2], got[3], None)
+
+
+def test_norm_over_its_input_keeps_no_row():
+    """y written over x leaves no s for a backward, so none is returned."""
+    import torch
+    c = draw(7, 200, "bf16", 17)
+    x = c["x"].cuda()
+    want = bm.layer_norm_forward(x)
+    assert want[1] is x
+    z = x.clone()
+    got = bm.layer_norm_forward(z, y=z)
+    assert got[1] is None and got[0] is z and all((a == b).all() for a, b in zip(got[::2] + got[3:], want[::2] + want[3:]))
+    with pytest.raises(ValueError):
+        bm.layer_norm_backward(torch.randn(7, 200, device="cuda"), got[1], None, got[2], got[3])
+    r = bm.layer_norm_forward(x.clone(), residual=x, y=x)       # a sum of its own is kept
+    assert r[1] is not None
