@@ -60,13 +60,19 @@ constexpr int NS_K = 64;            // contraction step
 constexpr int NS_SPLIT = 16;        // most workgroups that share a tile
 constexpr int NS_SHARED = 512;      // most workgroups of a product that shares tiles
 
-// The second terms of four v = hi + lo: (v - hi) 2^5 as four e4m3 bytes.  hi is off
-// by at most 8 (X's entries stay below 2^15), so nothing saturates, and e4m3's last
-// subnormal place, 2^-9, is 2^-14 of X's: 2^-16 off at most, or 2^-4 of lo.
-constexpr float NS_LO = 32.f;
-__device__ __forceinline__ uint32_t ns_lo4(f32x4_t v, f16x4_t hi) {
-  int u = __builtin_amdgcn_cvt_pk_fp8_f32((v[0] - float(hi[0])) * NS_LO, (v[1] - float(hi[1])) * NS_LO, 0, false);
-  u = __builtin_amdgcn_cvt_pk_fp8_f32((v[2] - float(hi[2])) * NS_LO, (v[3] - float(hi[3])) * NS_LO, u, true);
+// The second terms of four v = hi + lo: (v - hi) f, f = 2^e, as four e4m3 bytes, off by
+// 2^-4 of lo or by half of e4m3's last subnormal place, 2^-10 / f.  X's entries stay
+// below 2^15, hi is off by at most 8 and e = NS_LO saturates nothing.  X_0, whose
+// roundings grow most, takes e from its largest entry: in [2^m, 2^(m+1)) hi is off by
+// at most 2^(m-11), 256 of e4m3's 448 at e = 19 - m.  m is 0 at least (||X_0|| is 2^14,
+// of at most 2^28 entries) and 14 at most.  Without that, large matrices' small entries
+// had their second terms among the subnormals: rank one came out 8.2e-3 off at 8192 x
+// 8192 and 1.3e-2 at 16384 x 16384 (now 6.2e-3 and 7.0e-3; 6.0e-3 in place of 6.6e-3 at 2048 x
+// 8192).
+constexpr int NS_LO = 5, NS_LO_MAX = 19;
+__device__ __forceinline__ uint32_t ns_lo4(f32x4_t v, f16x4_t hi, float f) {
+  int u = __builtin_amdgcn_cvt_pk_fp8_f32((v[0] - float(hi[0])) * f, (v[1] - float(hi[1])) * f, 0, false);
+  u = __builtin_amdgcn_cvt_pk_fp8_f32((v[2] - float(hi[2])) * f, (v[3] - float(hi[3])) * f, u, true);
   return uint32_t(u);
 }
 // Eight fp16 values times f as e4m3 bytes.
@@ -102,12 +108,15 @@ __device__ __forceinline__ void ns_load_grad(const void* g, size_t i, float (&v)
   }
 }
 
-// M' = mu M + G and the sum of U^2 (fp64 partial sums, one per workgroup).
+// M' = mu M + G, the sum of U^2 (fp64 partial sums, one per workgroup) and the
+// largest |U| (NS_SUMS floats behind the sums).
 template <bool BF, int W>
 __global__ __launch_bounds__(256) void ns_momentum_kernel(const void* grad, const float* mom, float* m_out, double* part,
                                                            size_t n, float mu, int nesterov) {
   __shared__ double red[4];
+  __shared__ float top[4];
   double s = 0.0;
+  float mx = 0.f;
   for (size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * W; i < n; i += size_t(gridDim.x) * 256 * W) {
     float g[W], m[W];
     ns_load_grad<BF, W>(grad, i, g);
@@ -120,6 +129,7 @@ __global__ __launch_bounds__(256) void ns_momentum_kernel(const void* grad, cons
         u = ns_u(g[j], m[j], mu, nesterov);
       }
       s = fma(double(u), double(u), s);
+      mx = fmaxf(mx, fabsf(u));
     }
     if (mom) {
       if constexpr (W == 4) *reinterpret_cast<float4*>(m_out + i) = make_float4(m[0], m[1], m[2], m[3]);
@@ -127,10 +137,19 @@ __global__ __launch_bounds__(256) void ns_momentum_kernel(const void* grad, cons
     }
   }
 #pragma unroll
-  for (int k = 1; k < 64; k <<= 1) s += __shfl_xor(s, k);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  for (int k = 1; k < 64; k <<= 1) {
+    s += __shfl_xor(s, k);
+    mx = fmaxf(mx, __shfl_xor(mx, k));
+  }
+  if ((threadIdx.x & 63) == 0) {
+    red[threadIdx.x >> 6] = s;
+    top[threadIdx.x >> 6] = mx;
+  }
   __syncthreads();
-  if (threadIdx.x == 0) part[blockIdx.x] = ((red[0] + red[1]) + red[2]) + red[3];
+  if (threadIdx.x == 0) {
+    part[blockIdx.x] = ((red[0] + red[1]) + red[2]) + red[3];
+    reinterpret_cast<float*>(part + NS_SUMS)[blockIdx.x] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+  }
 }
 
 // X_0 = U / ||U||_F times 2^14 as fp16 hi (+ lo): 64 x 64 tiles of the padded
@@ -143,12 +162,14 @@ struct NsCast {
   uint8_t* zero[3];         // rows of 2 Sp bytes to clear from Sp up to a multiple of 128: Lp of
                             // xl and of the other X's second terms, Sp of the factor's e4m3 copy
   int32_t* ticket;          // [NS_SHARED / 2], cleared
+  int32_t* lo_exp;          // the exponent of X_0's second terms, written
 };
 
 template <bool BF, int W>
 __global__ __launch_bounds__(256) void ns_cast_kernel(const void* grad, const float* mom, const double* part, int parts,
                                                        int rows, int cols, int Sp, int Lp, float mu, int nesterov, NsCast c) {
   __shared__ double red[4];
+  __shared__ float top[4];
   __shared__ _Float16 th[64][68];
   __shared__ uint32_t tl[64][17];
   const int tid = threadIdx.x;
@@ -183,14 +204,28 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(const void* grad, const fl
     }
   }
   double s = 0.0;
-  for (int p = tid; p < parts; p += 256) s += part[p];
+  float mx = 0.f;
+  for (int p = tid; p < parts; p += 256) {
+    s += part[p];
+    mx = fmaxf(mx, reinterpret_cast<const float*>(part + NS_SUMS)[p]);
+  }
 #pragma unroll
-  for (int k = 1; k < 64; k <<= 1) s += __shfl_xor(s, k);
-  if ((tid & 63) == 0) red[tid >> 6] = s;
+  for (int k = 1; k < 64; k <<= 1) {
+    s += __shfl_xor(s, k);
+    mx = fmaxf(mx, __shfl_xor(mx, k));
+  }
+  if ((tid & 63) == 0) {
+    red[tid >> 6] = s;
+    top[tid >> 6] = mx;
+  }
   __syncthreads();
   const double norm = sqrt(((red[0] + red[1]) + red[2]) + red[3]);
   // NaN for a norm that is NaN or infinite, so that all of the result is NaN
   const double scale = norm > 0.0 ? (norm < __builtin_inf() ? 16384.0 / norm : __builtin_nan("")) : (norm == 0.0 ? 0.0 : norm);
+  mx = float(double(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))) * scale);
+  const int lo_exp = min(max(NS_LO_MAX + 127 - int(__float_as_uint(mx) >> 23 & 255u), NS_LO), NS_LO_MAX);
+  const float lo_by = __uint_as_float(uint32_t(127 + lo_exp) << 23);
+  if (blockIdx.x == 0 && tid == 0) *c.lo_exp = lo_exp;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int lr = 16 * i + (tid >> 4);
@@ -201,7 +236,7 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(const void* grad, const fl
       v[j] = float(double(mom ? ns_u(g[i][j], m[i][j], mu, nesterov) : g[i][j]) * scale);
       hi[j] = _Float16(v[j]);
     }
-    const uint32_t lo = ns_lo4(v, hi);
+    const uint32_t lo = ns_lo4(v, hi, lo_by);
     *reinterpret_cast<f16x4_t*>(&th[lr][lc]) = hi;
     tl[lr][tid & 15] = lo;
     const size_t at = size_t(r0 + lr) * cp + c0 + lc;
@@ -251,7 +286,8 @@ struct NsGemm {
   const uint8_t* a8;        // NS_PROD: [M] rows of 2 K bytes, K of them the second term of a and 0
                             // up to a multiple of 128 (the offsets of a then hold here too); or null
   const uint8_t* b8;        // [N] such rows, b as e4m3
-  int32_t exp8;             // sum of a b scales 2^exp8 times that of a8 b8
+  int32_t exp8;             // sum of a b scales 2^(exp8 - e) times that of a8 b8, e the
+  const int32_t* lo_exp;    // exponent of a8's second terms: here, or NS_LO where null
   int32_t M, N, K;          // multiples of NS_K
   int32_t grid, tiles;      // workgroups; NS_SYM: tiles, else tiles of a row of tiles
   uint32_t by_tiles;        // floor(2^32 / tiles) + 1 (0 for 1): t / tiles = t by_tiles / 2^32
@@ -365,6 +401,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(
   const int nkh = KG > 1 ? nk / KG : nk;  // whole steps in fp16, then those of the second term: 128 deep
   const bool two = MODE == NS_PROD && p.a8;
   if (two) nk += (nk1 + 1) / 2;
+  int scale8 = 0;
   // a load fills 8 rows of 64; a wave's loads are all of A or all of B.  Byte
   // offsets of this lane's pieces in it; 8-row groups past the matrix (M and N
   // are multiples of 8) read its last one and are not stored
@@ -465,6 +502,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(
   load(NBUF - 1, NBUF - 1);
   if constexpr (MODE == NS_SYM) ratios(p.ra, ram, ran);
   ratios(p.rb, rbm, rbn);
+  if (two) scale8 = 127 + p.exp8 - (p.lo_exp ? *p.lo_exp : NS_LO);
   if constexpr (MODE == NS_SYM)
     asm volatile("" ::"s"(p.d), "s"(p.c), "s"(p.d8), "s"(p.f8), "s"(p.rd), "s"(p.alpha), "s"(p.beta), "s"(p.diag));
   read(0, 0, fa[0], fb[0]);
@@ -507,7 +545,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(
         return i32x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
       };
       auto mul8 = [&](int i, int j) {
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(eb[i], ea[j], acc[i][j], 0, 0, 0, 127 + p.exp8, 0, 127);
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(eb[i], ea[j], acc[i][j], 0, 0, 0, scale8, 0, 127);
       };
 #pragma unroll
       for (int i = 0; i < IN; ++i) eb[i] = read8(buf, TM + PN * wn + 16 * i);
@@ -733,7 +771,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(
           f16x4_t hi;
 #pragma unroll
           for (int r = 0; r < 4; ++r) hi[r] = _Float16(v[r]);
-          s8[(PM * wm + 16 * j + l16) * SW + (PN * wn + 16 * i) / 4 + g] = ns_lo4(v, hi);
+          s8[(PM * wm + 16 * j + l16) * SW + (PN * wn + 16 * i) / 4 + g] = ns_lo4(v, hi, float(1 << NS_LO));
         }
       __syncthreads();
       pieces([&](int r, int c) {
@@ -849,7 +887,7 @@ NsTile ns_pick(const NsGemm& p) {
 }
 
 struct NsPlan {
-  size_t part, xs, xh[2], xl[2], m[4], r[4], m8, shares, ticket, total;
+  size_t part, xs, xh[2], xl[2], m[4], r[4], m8, shares, ticket, lo_exp, total;
   int S, L, Sp, Lp;
   NsTile gram, square;      // tiles of X X^T and of the products of side S
 };
@@ -867,7 +905,7 @@ NsPlan ns_plan(int rows, int cols) {
     return at;
   };
   const size_t x = size_t(q.Sp) * q.Lp * 2, s = size_t(q.Sp) * q.Sp * 2;
-  q.part = take(NS_SUMS * 8);
+  q.part = take(NS_SUMS * 8 + NS_SUMS * 4);
   q.xs = take(x);
   for (int k = 0; k < 2; ++k) {
     q.xh[k] = take(x);
@@ -891,6 +929,7 @@ NsPlan ns_plan(int rows, int cols) {
   q.square = pick(q.Sp);
   q.shares = take(shares);
   q.ticket = take(NS_SHARED / 2 * 4);
+  q.lo_exp = take(4);
   q.total = o;
   return q;
 }
@@ -944,7 +983,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   const int blocks = int(nb < NS_SUMS ? nb : NS_SUMS);
   auto bytes = [&](size_t off) { return reinterpret_cast<uint8_t*>(ws + off); };
   int32_t* ticket = reinterpret_cast<int32_t*>(ws + q.ticket);
-  const NsCast c{at(q.xs), at(q.xh[0]), bytes(q.xl[0]), {bytes(q.xl[0]), bytes(q.xl[1]), bytes(q.m8)}, ticket};
+  int32_t* lo_exp = reinterpret_cast<int32_t*>(ws + q.lo_exp);
+  const NsCast c{at(q.xs), at(q.xh[0]), bytes(q.xl[0]), {bytes(q.xl[0]), bytes(q.xl[1]), bytes(q.m8)}, ticket, lo_exp};
   const unsigned tiles = unsigned((q.Sp / 64) * (q.Lp / 64));
   hipError_t e = hipSuccess;
   auto head = [&](auto bf, auto w) {
@@ -1023,6 +1063,7 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   prod.M = q.Lp;
   prod.N = prod.K = q.Sp;
   int k = 0;
+  bool first = true;
   auto next = [&](Sym f, float alpha, bool keep_lo) {
     NsGemm g = prod;
     g.a = at(q.xh[k]);
@@ -1030,10 +1071,12 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
     if (f.e8) {
       g.a8 = bytes(q.xl[k]);
       g.b8 = bytes(q.m8);
-      g.exp8 = f.e8 - 5;  // NS_LO = 2^5
+      g.exp8 = f.e8;
+      g.lo_exp = first ? lo_exp : nullptr;
     }
     g.rb = f.r;
     g.alpha = alpha;
+    first = false;
     k ^= 1;
     g.d = at(q.xh[k]);
     g.lo = keep_lo ? bytes(q.xl[k]) : nullptr;

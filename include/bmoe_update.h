@@ -40,8 +40,8 @@ extern "C" {
  * symmetric factors' diagonals are corrected in fp32.  Measured
  * ||O - O_exact|| / ||O_exact|| before O's rounding to bf16 (1.7e-3 by itself):
  * below 1e-3 for gradients of full rank whose singular values fall off like
- * 1 / k or slower, 3e-3 at rank min(rows, cols) / 8, 7e-3 at rank one.  M' is
- * fp32.  A NaN or an infinity in U makes all of O NaN.
+ * 1 / k or slower, 3.5e-3 at rank min(rows, cols) / 8, 6e-3 to 8e-3 at rank one,
+ * for sides of 48 to 16384.  M' is fp32.  A NaN or an infinity in U makes all of O NaN.
  *
  * rows, cols in [1, 16384].
  *   grad      [rows][cols] of grad_dtype (bmoe_dtype), read only.

@@ -440,3 +440,39 @@ def test_step_substrate_rescale_refusals():
     with pytest.raises(ValueError, match="finite"):
         layer.step_substrate(0, w, rescale=True)
     assert layer.struct.w_scale[0] == 1.0
+
+
+# Narrower bars, relative Frobenius norm, in the mean square over many entries.  A
+# rounding to fp16 is 2^-12.2 (half a place, mantissas spread evenly), to bf16 1.7e-3,
+# to e4m3 2^-5.2.
+# Full rank: about ten roundings act on settled values, whose map stretches by 2 in
+#   the mean square (its slope between -1.5 and 4 over 0.68 .. 1.21): sqrt(10) * 2 *
+#   2^-12 = 1.5e-3, with bf16's 2.3e-3.  Diagonals left as stored: 4.8e-3 at 48 x 16384.
+# Rank one: noise outside the row space grows 485-fold from X_0, 12-fold from X_3.
+#   X_0 has 2^-12.2 2^-5.2 of its own second term's rounding and of P's e4m3 copy as
+#   much at most: 2.8e-3 each; X_3, in one term, 2.1e-4 * 11.8 * 1.8 = 4.5e-3 (1.8 for
+#   ||X_3|| / ||X_5||); X_4, X_1 and X_2 1e-3 each: 6.3e-3, with bf16's 6.6e-3; half as
+#   much again for few rows.  A second term lost at X_2, where it counts least: 1.4e-2.
+# Rank S / 8: the signal grows too, 3-fold at the least, and settles before X_3: X_0's
+#   1.9e-3, X_3's 2.1e-4 * 11.8 = 2.5e-3, bf16's: 3.6e-3.  Lost at X_2: 6.9e-3.
+BARS = dict(normal=3e-3, low=5e-3, one=1e-2)
+
+
+@pytest.mark.parametrize("rows,cols", [(4096, 4096), (8192, 8192), (8192, 16384), (16384, 16384)])
+def test_orthogonalize_rank_one_of_large_sides(rows, cols):
+    """Entries of X_0 shrink with the sides, and their second terms with them: the
+    bar is the same at every size.  Rank one is its own solution, u v^T times the
+    quintic iterated on 1."""
+    import torch
+    gen = torch.Generator("cuda").manual_seed(rows + cols)
+    u, v = (torch.randn(n, generator=gen, device="cuda") for n in (rows, cols))
+    g = u[:, None] * v
+    x = 1.0
+    for _ in range(ref.NS_STEPS):
+        x = ref.NS_COEFFS[0] * x + ref.NS_COEFFS[1] * x ** 3 + ref.NS_COEFFS[2] * x ** 5
+    o = bm.orthogonalize(g)[0].double()
+    u, v = u.double(), v.double()
+    o -= (x / (u.norm() * v.norm()) * u)[:, None] * v
+    e = o.norm().item() / x
+    log(f"orthogonalize rank one {rows} x {cols}: {e:.2e}")
+    assert e <= BARS["one"], e
