@@ -457,6 +457,24 @@ def test_step_substrate_rescale_refusals():
 #   1.9e-3, X_3's 2.1e-4 * 11.8 = 2.5e-3, bf16's: 3.6e-3.  Lost at X_2: 6.9e-3.
 BARS = dict(normal=3e-3, low=5e-3, one=1e-2)
 
+# every tile of every product, whole and shared, cut and not, with even and odd depths
+# where a tile treats them differently, both orientations
+TILES = [(64, 64), (48, 16384), (16384, 48), (250, 256), (128, 5500), (5500, 120), (330, 1340), (384, 2620), (2110, 1980),
+         (1024, 1024), (4096, 1024), (320, 6592), (8250, 256), (960, 7168), (1300, 3000), (704, 11960), (2048, 8192),
+         (8190, 2040), (1275, 15030), (1536, 2750), (2750, 1530), (1020, 12928), (960, 14650), (14650, 950), (1020, 12990),
+         (960, 14528), (1020, 12800), (12800, 1000), (1020, 12730), (1150, 7610), (1150, 7800), (1470, 6840), (7030, 1470),
+         (2496, 6528)]
+
+
+@pytest.mark.parametrize("rows,cols", TILES)
+def test_orthogonalize_precision_in_every_tile(rows, cols):
+    for kind, bar in BARS.items():
+        g = matrix(kind, rows, cols, rows + 3 * cols).cuda()
+        o, want = bm.orthogonalize(g)[0], exact_on_gpu(g)
+        e = ((o.double() - want).norm() / want.norm()).item()
+        log(f"orthogonalize {kind} {rows} x {cols}: {e:.2e}")
+        assert e <= bar, (kind, e)
+
 
 @pytest.mark.parametrize("rows,cols", [(4096, 4096), (8192, 8192), (8192, 16384), (16384, 16384)])
 def test_orthogonalize_rank_one_of_large_sides(rows, cols):
