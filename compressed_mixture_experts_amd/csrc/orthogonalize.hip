@@ -53,6 +53,7 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef const __attribute__((address_space(1))) void ns_glob_t;
 typedef __attribute__((address_space(3))) void ns_lds_t;
+typedef const __attribute__((address_space(4))) int32_t ns_const_int_t;
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr int NS_SUMS = 512;        // partial sums of squares
@@ -162,7 +163,7 @@ struct NsCast {
   uint8_t* zero[3];         // rows of 2 Sp bytes to clear from Sp up to a multiple of 128: Lp of
                             // xl and of the other X's second terms, Sp of the factor's e4m3 copy
   int32_t* ticket;          // [NS_SHARED / 2], cleared
-  int32_t* lo_exp;          // the exponent of X_0's second terms, written
+  int32_t* lo_exp;          // the exponents of the second terms of X_0 and of later X, written
 };
 
 template <bool BF, int W>
@@ -225,7 +226,7 @@ __global__ __launch_bounds__(256) void ns_cast_kernel(const void* grad, const fl
   mx = float(double(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]))) * scale);
   const int lo_exp = min(max(NS_LO_MAX + 127 - int(__float_as_uint(mx) >> 23 & 255u), NS_LO), NS_LO_MAX);
   const float lo_by = __uint_as_float(uint32_t(127 + lo_exp) << 23);
-  if (blockIdx.x == 0 && tid == 0) *c.lo_exp = lo_exp;
+  if (blockIdx.x == 0 && tid < 2) c.lo_exp[tid] = tid == 0 ? lo_exp : NS_LO;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int lr = 16 * i + (tid >> 4);
@@ -287,7 +288,7 @@ struct NsGemm {
                             // up to a multiple of 128 (the offsets of a then hold here too); or null
   const uint8_t* b8;        // [N] such rows, b as e4m3
   int32_t exp8;             // sum of a b scales 2^(exp8 - e) times that of a8 b8, e the
-  const int32_t* lo_exp;    // exponent of a8's second terms: here, or NS_LO where null
+  const int32_t* lo_exp;    // exponent of a8's second terms (NS_PROD)
   int32_t M, N, K;          // multiples of NS_K
   int32_t grid, tiles;      // workgroups; NS_SYM: tiles, else tiles of a row of tiles
   uint32_t by_tiles;        // floor(2^32 / tiles) + 1 (0 for 1): t / tiles = t by_tiles / 2^32
@@ -401,7 +402,6 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(
   const int nkh = KG > 1 ? nk / KG : nk;  // whole steps in fp16, then those of the second term: 128 deep
   const bool two = MODE == NS_PROD && p.a8;
   if (two) nk += (nk1 + 1) / 2;
-  int scale8 = 0;
   // a load fills 8 rows of 64; a wave's loads are all of A or all of B.  Byte
   // offsets of this lane's pieces in it; 8-row groups past the matrix (M and N
   // are multiples of 8) read its last one and are not stored
@@ -498,11 +498,14 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void ns_gemm_kernel(
   };
 #pragma unroll
   for (int b = 0; b < NBUF - 1; ++b) load(b, b, 0, 64, b == 0);
+  // a scalar read while they arrive (behind arrive() a vector one, which waits for all
+  // loads before it: 0.4 us)
+  int scale8 = 0;
+  if constexpr (MODE == NS_PROD) scale8 = 127 + p.exp8 - *reinterpret_cast<ns_const_int_t*>(reinterpret_cast<uintptr_t>(p.lo_exp));
   arrive();
   load(NBUF - 1, NBUF - 1);
   if constexpr (MODE == NS_SYM) ratios(p.ra, ram, ran);
   ratios(p.rb, rbm, rbn);
-  if (two) scale8 = 127 + p.exp8 - (p.lo_exp ? *p.lo_exp : NS_LO);
   if constexpr (MODE == NS_SYM)
     asm volatile("" ::"s"(p.d), "s"(p.c), "s"(p.d8), "s"(p.f8), "s"(p.rd), "s"(p.alpha), "s"(p.beta), "s"(p.diag));
   read(0, 0, fa[0], fb[0]);
@@ -929,7 +932,7 @@ NsPlan ns_plan(int rows, int cols) {
   q.square = pick(q.Sp);
   q.shares = take(shares);
   q.ticket = take(NS_SHARED / 2 * 4);
-  q.lo_exp = take(4);
+  q.lo_exp = take(8);
   q.total = o;
   return q;
 }
@@ -1062,8 +1065,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
   NsGemm prod{};
   prod.M = q.Lp;
   prod.N = prod.K = q.Sp;
+  prod.lo_exp = lo_exp;
   int k = 0;
-  bool first = true;
   auto next = [&](Sym f, float alpha, bool keep_lo) {
     NsGemm g = prod;
     g.a = at(q.xh[k]);
@@ -1072,15 +1075,14 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s) {
       g.a8 = bytes(q.xl[k]);
       g.b8 = bytes(q.m8);
       g.exp8 = f.e8;
-      g.lo_exp = first ? lo_exp : nullptr;
     }
     g.rb = f.r;
     g.alpha = alpha;
-    first = false;
     k ^= 1;
     g.d = at(q.xh[k]);
     g.lo = keep_lo ? bytes(q.xl[k]) : nullptr;
     g.dt = at(q.xs);
+    prod.lo_exp = lo_exp + 1;
     return ns_go<NS_PROD>(g, ns_pick<NS_PROD>(g), s);
   };
 #define NS_DO(call)                     \
