@@ -555,9 +555,10 @@ hipError_t bwd_act(const LnBwdArgs& a, int cut, hipStream_t s) {
 
 }  // namespace
 
-// Rows' workgroups of the backward: what runs at a time (two per CU with the sums
-// of a whole row of 2048 in registers; 32768 x 2048 136 us with 512, 163 with 768,
-// 143 with 1024), no more than there are groups of 4 rows.
+// Rows' workgroups of the backward: what runs at a time with the sums of a whole row
+// of 2048 in registers, two per CU (32768 x 2048 136 us with 512, 163 with 768, 143 with
+// 1024; narrower rows' registers leave room for more, which would have to pay for their
+// partial rows), no more than there are groups of 4 rows.
 static int ln_bwd_blocks(int rows) {
   const int need = (rows + 3) / 4;
   return need < 512 ? need : 512;

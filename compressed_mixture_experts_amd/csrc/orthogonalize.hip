@@ -16,8 +16,8 @@
 // lo e4m3 (16 bits together, noise below X_3's own), whose products with P's e4m3
 // copy run at twice fp16's rate.  With X in one fp16 term throughout, a gradient
 // of rank S / 8 came out 2e-2 off, with this 3e-3; full-rank ones 1e-3.  lo in fp16
-// brings rank one from 6.5e-3 to 5e-3 and nothing else, and costs more (755 and 731
-// us at 2048 x 8192, 428 and 412 at 1300 x 6000).
+// brought rank one from 6.5e-3 to 5e-3 (lo's exponent from the data: 6e-3) and nothing
+// else, and costs more (755 and 731 us at 2048 x 8192, 428 and 412 at 1300 x 6000).
 //
 // Long matrices take the first two steps together,
 //     A_1 = P_0 A_0 P_0 = P_0 T,   Q = P_1 P_0,   X_2 = Q X_0
@@ -68,8 +68,8 @@ constexpr int NS_SHARED = 512;      // most workgroups of a product that shares 
 // at most 2^(m-11), 256 of e4m3's 448 at e = 19 - m.  m is 0 at least (||X_0|| is 2^14,
 // of at most 2^28 entries) and 14 at most.  Without that, large matrices' small entries
 // had their second terms among the subnormals: rank one came out 8.2e-3 off at 8192 x
-// 8192 and 1.3e-2 at 16384 x 16384 (now 6.2e-3 and 7.0e-3; 6.0e-3 in place of 6.6e-3 at 2048 x
-// 8192).
+// 8192 and 1.3e-2 at 16384 x 16384 (now 6.2e-3 and 7.0e-3; at 2048 x 8192 6.6e-3, now
+// 6.0e-3).
 constexpr int NS_LO = 5, NS_LO_MAX = 19;
 __device__ __forceinline__ uint32_t ns_lo4(f32x4_t v, f16x4_t hi, float f) {
   int u = __builtin_amdgcn_cvt_pk_fp8_f32((v[0] - float(hi[0])) * f, (v[1] - float(hi[1])) * f, 0, false);

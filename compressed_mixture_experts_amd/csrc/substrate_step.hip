@@ -16,9 +16,9 @@
 namespace bmoe {
 
 constexpr int SS_BLOCKS = 1024;  // most workgroups of the first pass
-// Most weights of the single workgroup, 16 per thread: as many as it takes no longer
-// for on the GPU than the two launches (us there, one and two: 16 x 64 3.3 and 3.9,
-// 64 x 256 5.2 and 4.9, 96 x 256 7.2 and 5.0); a call costs the host 9.3 and 13.4.
+// Most weights of the single workgroup, 16 per thread: about where the GPU takes as
+// long for the two launches (us there, one and two: 16 x 64 3.3 and 3.9, 64 x 256 5.2
+// and 4.9, 96 x 256 7.2 and 5.0), while a call costs the host 9.3 and 13.4.
 constexpr size_t SS_ONE = size_t(1) << 14;
 
 __device__ __forceinline__ double ss_wave_sum(double v) {

@@ -32,7 +32,8 @@ extern "C" {
  *     five times  X <- a X + (b A + c A A) X,  A = X X^T  (on the smaller side)
  *     with (a, b, c) = (3.4445, -4.7750, 2.0315):
  * every singular value of U ends between 0.68 and 1.21 unless it was smaller
- * than about 1e-3 of ||U||_F, its singular vectors stay.  O = X.
+ * than 1.5e-3 of ||U||_F (1e-3 of it ends at 0.47), its singular vectors stay.
+ * O = X.
  *
  * Precision.  Products run on the matrix cores in fp16 with fp32 sums, every
  * factor scaled by a power of two to the middle of fp16's range; X is kept as
@@ -41,7 +42,8 @@ extern "C" {
  * ||O - O_exact|| / ||O_exact|| before O's rounding to bf16 (1.7e-3 by itself):
  * below 1e-3 for gradients of full rank whose singular values fall off like
  * 1 / k or slower, 3.5e-3 at rank min(rows, cols) / 8, 6e-3 to 8e-3 at rank one,
- * for sides of 48 to 16384.  M' is fp32.  A NaN or an infinity in U makes all of O NaN.
+ * for sides of 48 to 16384.  Gradients of both types take this one path; there
+ * is none in fp32.  M' is fp32.  A NaN or an infinity in U makes all of O NaN.
  *
  * rows, cols in [1, 16384].
  *   grad      [rows][cols] of grad_dtype (bmoe_dtype), read only.
