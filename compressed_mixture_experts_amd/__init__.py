@@ -424,7 +424,7 @@ class Layer:
         if not 0 <= m < len(self.w_base):
             raise ValueError(f"the layer has no substrate {m}")
         scale = float(scale)
-        if not abs(scale) <= np.finfo(np.float32).max:
+        if not abs(scale) <= float(np.finfo(np.float32).max):
             raise ValueError(f"substrate {m}'s scale must be finite in fp32, got {scale}")
         self.struct.w_scale[m] = scale
         return self

@@ -15,8 +15,10 @@
  * values.  Sums run in fp32 over a row held in registers: the mean's rounding
  * is taken from the sum of the centred values and given back to the mean, the
  * variance and y, so a row far from 0 is normed as well as one around it and a
- * constant row gives y = beta.  Squares that leave fp32 are summed at a smaller
- * scale: a finite row is normed whatever its size (entries up to 2^127).
+ * constant row gives y = beta.  Squares that leave fp32, or vanish in it beside
+ * an eps below 2^-100, are summed at another scale: a finite row is normed
+ * whatever its size (entries up to 2^127; rstd is infinite for deviations below
+ * 2^-128).
  *
  * Widths 1 .. 16384, rows 0 .. 2^24; arrays are row-major and
  * dense, aligned to their element size (16-byte alignment and a width that is

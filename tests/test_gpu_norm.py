@@ -384,3 +384,27 @@ def test_norm_over_its_input_keeps_no_row():
         bm.layer_norm_backward(torch.randn(7, 200, device="cuda"), got[1], None, got[2], got[3])
     r = bm.layer_norm_forward(x.clone(), residual=x, y=x)       # a sum of its own is kept
     assert r[1] is not None
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("size,eps", [(1e-15, 0.0), (1e-20, 0.0), (1e-30, 0.0), (1e-20, 1e-40), (1e-20, 1e-5)])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_norm_of_small_rows(width, size, eps, kind):
+    """Rows whose squares are below fp32's normal numbers, under an eps that does not
+    cover them: the same bars as for any row (entries 1e6 times below the row's
+    deviation are still normal numbers)."""
+    import torch
+    c = draw(5, width, kind, width)
+    z = (torch.randn(5, width, generator=torch.Generator().manual_seed(width + 1)) + 0.5) * size
+    z[3] = 2.0 * size                                                    # a constant row
+    z[4] = c["x"][4].float()                                             # an ordinary one
+    x = z.to(c["dt"]).cuda()
+    got = bm.layer_norm_forward(x, eps=eps)
+    # with eps = 0 a constant row is 0 / 0
+    rows = [0, 1, 2, 4] if eps < 1e-30 else [0, 1, 2, 3, 4]
+    part = dict(c, x=c["x"][rows])
+    e = float(np.float32(eps))
+    check_forward(part, [t[rows] for t in got], None, None, e, False)
+    dy = c["dy"].cuda()
+    grads = bm.layer_norm_backward(dy, x, None, got[2], got[3])
+    check_backward(part, (grads[0][rows], None, None), x[rows], dy[rows], None, got[2][rows], got[3][rows], None)
