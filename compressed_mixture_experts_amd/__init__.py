@@ -2,7 +2,7 @@
 
 The computation runs in ``libbmoe.so`` (hand-written HIP kernels behind the C
 ABI of ``include/bmoe.h``, ``bmoe_trace.h``, ``bmoe_grad.h``, ``bmoe_train.h``,
-``bmoe_norm.h`` and ``bmoe_update.h``).  The test
+``bmoe_norm.h``, ``bmoe_update.h`` and ``bmoe_adamw.h``).  The test
 hooks of ``include/bmoe_debug.h`` live only in ``libbmoe_debug.so`` (the same
 kernels, built with -DBMOE_DEBUG_EXPORTS), loaded on first use of a
 ``dbg_*`` function.  This module only marshals arguments: torch tensors
@@ -29,7 +29,7 @@ __all__ = [
     "BmoeError", "lib", "library_path", "pack_ternary", "packed_words", "Layer",
     "dbg_butterfly", "dbg_ternary_gemm", "dbg_ternary_gemm_fp4", "butterfly_backward", "substrate_grad",
     "combine_backward", "router_backward", "gelu_backward", "substrate_input_grad",
-    "layer_norm_forward", "layer_norm_backward", "orthogonalize", "substrate_step", "STATUS",
+    "layer_norm_forward", "layer_norm_backward", "orthogonalize", "substrate_step", "AdamW", "STATUS",
     "EXPORTED_SYMBOLS", "DEBUG_SYMBOLS", "debug_lib",
 ]
 
@@ -47,7 +47,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20   # BMOE_NOALLOC_SCRATCH_BYTES of include/bmoe.
 ACT_NONE, ACT_GELU_ERF = 0, 1
 
 # exports of libbmoe.so (include/bmoe.h, bmoe_trace.h, bmoe_grad.h, bmoe_train.h,
-# bmoe_norm.h, bmoe_update.h)
+# bmoe_norm.h, bmoe_update.h, bmoe_adamw.h)
 EXPORTED_SYMBOLS = [
     "bmoe_packed_words", "bmoe_pack_ternary", "bmoe_workspace_size", "bmoe_prepared_bytes",
     "bmoe_prepare", "bmoe_route", "bmoe_forward", "bmoe_forward_noalloc", "bmoe_status_string",
@@ -61,6 +61,7 @@ EXPORTED_SYMBOLS = [
     "bmoe_layer_norm_forward", "bmoe_layer_norm_backward_workspace", "bmoe_layer_norm_backward",
     "bmoe_orthogonalize_workspace", "bmoe_orthogonalize",
     "bmoe_substrate_step_workspace", "bmoe_substrate_step",
+    "bmoe_adamw_step", "bmoe_adamw_moments",
 ]
 # exported by libbmoe_debug.so only (include/bmoe_debug.h)
 DEBUG_SYMBOLS = ["bmoe_dbg_butterfly", "bmoe_dbg_ternary_gemm", "bmoe_dbg_ternary_gemm_fp4"]
@@ -154,6 +155,8 @@ def _load(path: str, debug: bool) -> ctypes.CDLL:
     L.bmoe_orthogonalize.argtypes = [c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_f, c_i32, c_vp, c_vp, c_sz, c_vp]
     L.bmoe_substrate_step_workspace.argtypes = [c_i32, c_i32, ctypes.POINTER(c_sz)]
     L.bmoe_substrate_step.argtypes = [c_i32, c_i32, c_vp, c_vp, c_d, c_d, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]
+    L.bmoe_adamw_step.argtypes = [c_vp, c_i32, c_vp, c_vp]
+    L.bmoe_adamw_moments.argtypes = [c_vp, c_i32, c_i32, c_vp, c_vp, c_vp]
     ret = [n for n in EXPORTED_SYMBOLS if n not in ("bmoe_packed_words", "bmoe_prepared_bytes",
                                                     "bmoe_status_string", "bmoe_last_error")]
     if debug:
@@ -784,3 +787,6 @@ def dbg_ternary_gemm_fp4(a, w_packed, n_out: int, alpha: float = 1.0):
     _check(D.bmoe_dbg_ternary_gemm_fp4(M, n_out, K, _ptr(a), _ptr(w_packed), _ptr(scratch),
                                        float(alpha), _ptr(z), _stream_handle()), D)
     return z
+
+
+from .blocks import AdamW  # noqa: E402

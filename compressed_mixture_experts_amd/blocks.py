@@ -1,0 +1,203 @@
+"""Operators around an expert layer (include/bmoe_adamw.h): argument marshalling only,
+as in the package's other calls."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import numpy as np
+
+from . import BF16, F32, _check, _raw_stream, _torch, lib
+
+# bmoe_adamw_tensor of include/bmoe_adamw.h
+_ADAMW_TENSOR = np.dtype([
+    ("param", np.uint64), ("grad", np.uint64), ("m", np.uint64), ("v", np.uint64), ("m_exp", np.uint64), ("v_exp", np.uint64),
+    ("copy", np.uint64), ("n", np.int64), ("lr_scale", np.float32), ("weight_decay", np.float32), ("grad_dtype", np.int32),
+    ("bits", np.int32)])
+
+
+class _AdamWArgs(ctypes.Structure):
+    """bmoe_adamw_args of include/bmoe_adamw.h."""
+    _fields_ = [
+        ("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+        ("step", ctypes.c_int64), ("step_device", ctypes.c_void_p), ("lr_device", ctypes.c_void_p),
+        ("grad_scale", ctypes.c_void_p), ("seed", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+def _listed(name, what, count, default=None):
+    """`what` as a list of `count`: a number (or None) is everybody's."""
+    if what is None:
+        return [default] * count
+    if isinstance(what, (list, tuple)):
+        if len(what) != count:
+            raise ValueError(f"{name} has {len(what)} entries for {count} parameters")
+        return list(what)
+    return [what] * count
+
+
+def _tensor(name, t, kind, shape, device):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is {t!r}, expected a tensor")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected a GPU tensor on {device}")
+    if t.dtype != kind:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {kind}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+class AdamW:
+    """AdamW over a list of fp32 tensors on one GPU, all of them in one launch for
+    every 40 (bmoe_adamw_step): what `Layer.backward` gives gradients for besides the
+    latent substrates (angles, gate matrix), norm weights, dense projections.
+
+        opt = bmoe.AdamW([layer.theta[0], layer.phi[0], gamma], lr=1e-3, weight_decay=[0.0, 0.0, 0.0])
+        opt.step([grads["theta"][0], grads["phi"][0], dgamma])
+
+    params           the tensors, updated in place by every step.
+    weight_decay, lr_scale, bits, copies   one for all tensors or a list of them: the
+                     decoupled decay, a factor on lr, 32 or 8 bits for the moments (8:
+                     bmoe_adamw.h's codes), a bf16 tensor that gets the new values.
+    lr               a number, which may be set anew between steps (`opt.lr`), or a
+                     one-element fp32 tensor that every step reads on the GPU.
+    m, v             the moments to go on from (fp32; with 8 bits uint8 codes and their
+                     blocks' exponents m_exp, v_exp [ceil(n / 256)] uint8), used as they
+                     are and updated in place; None: zeros.
+    steps            the steps already taken.
+    capturable       count the steps on the GPU, so that a step captured in a graph
+                     counts on in every replay; without, a step in a capture is refused.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01, *, lr_scale=1.0, bits=32,
+                 copies=None, seed: int = 0, m=None, v=None, m_exp=None, v_exp=None, steps: int = 0, capturable: bool = False):
+        torch = _torch()
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("AdamW needs at least one parameter")
+        if not isinstance(self.params[0], torch.Tensor) or not self.params[0].is_cuda:
+            raise ValueError("AdamW needs GPU tensors")
+        count, dev = len(self.params), self.params[0].device
+        self.device, self.lr, self.betas, self.eps, self.seed = dev, lr, tuple(betas), float(eps), int(seed)
+        if len(self.betas) != 2:
+            raise ValueError("betas are two numbers")
+        if not 0 <= self.seed < 1 << 32:
+            raise ValueError("seed must fit 32 bits")
+        if steps < 0:
+            raise ValueError("steps must not be negative")
+        f32, u8 = torch.float32, torch.uint8
+        self.bits = _listed("bits", bits, count)
+        self._decay, self._scale = _listed("weight_decay", weight_decay, count, 0.0), _listed("lr_scale", lr_scale, count, 1.0)
+        self.copies = _listed("copies", copies, count) if isinstance(copies, (list, tuple)) or copies is None else [copies]
+        if len(self.copies) != count:
+            raise ValueError(f"copies has {len(self.copies)} entries for {count} parameters")
+        given = [_listed(n, x, count) if isinstance(x, (list, tuple)) or x is None else [x] for n, x in
+                 (("m", m), ("v", v), ("m_exp", m_exp), ("v_exp", v_exp))]
+        self.m, self.v, self.m_exp, self.v_exp = [], [], [], []
+        for i, p in enumerate(self.params):
+            _tensor(f"params[{i}]", p, f32, p.shape, dev)
+            if self.copies[i] is not None:
+                _tensor(f"copies[{i}]", self.copies[i], torch.bfloat16, p.shape, dev)
+            if self.bits[i] not in (32, 8):
+                raise ValueError(f"bits[{i}] is {self.bits[i]}, expected 32 or 8")
+            eight = self.bits[i] == 8
+            blocks = torch.Size([(p.numel() + 255) // 256])
+            for name, have, out, kind, shape, wanted in (
+                    ("m", given[0], self.m, u8 if eight else f32, p.shape, True), ("v", given[1], self.v, u8 if eight else f32, p.shape, True),
+                    ("m_exp", given[2], self.m_exp, u8, blocks, eight), ("v_exp", given[3], self.v_exp, u8, blocks, eight)):
+                x = have[i] if i < len(have) else None
+                if not wanted:
+                    if x is not None:
+                        raise ValueError(f"{name}[{i}] is for moments in 8 bits")
+                    out.append(None)
+                elif x is None:
+                    if eight and (given[0][i] is None) != (have[i] is None):
+                        raise ValueError(f"m, v, m_exp and v_exp of parameter {i} go together")
+                    out.append(torch.zeros(shape, dtype=kind, device=dev))
+                else:
+                    out.append(_tensor(f"{name}[{i}]", x, kind, shape, dev))
+            if (given[0][i] is None) != (given[1][i] is None):
+                raise ValueError(f"m and v of parameter {i} go together")
+        t = np.zeros(count, dtype=_ADAMW_TENSOR)
+        for name, tensors in (("param", self.params), ("m", self.m), ("v", self.v), ("m_exp", self.m_exp), ("v_exp", self.v_exp),
+                              ("copy", self.copies)):
+            t[name] = [0 if x is None else x.data_ptr() for x in tensors]
+        t["n"] = [p.numel() for p in self.params]
+        t["lr_scale"], t["weight_decay"], t["bits"] = self._scale, self._decay, self.bits
+        self._table = t
+        self._shapes = [p.shape for p in self.params]
+        self._steps = int(steps)
+        self._counter = torch.full((1,), self._steps, dtype=torch.int64, device=dev) if capturable else None
+
+    @property
+    def steps(self) -> int:
+        """The steps taken (capturable: read from the GPU, which waits for it)."""
+        return self._steps if self._counter is None else int(self._counter.item())
+
+    def step(self, grads, grad_scale=None) -> None:
+        """One step: grads a list like params (fp32 or bf16; None: that tensor is left
+        as it is), grad_scale a one-element fp32 tensor that multiplies all of them
+        (what clips them, or takes a loss's scale out again)."""
+        torch = _torch()
+        f32, bf16, table, dev = torch.float32, torch.bfloat16, self._table, self.device
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        index = dev.index
+        if not all(g is None or (g.is_cuda and g.get_device() == index and g.shape == s and g.is_contiguous() and
+                                 (g.dtype is f32 or g.dtype is bf16)) for g, s in zip(grads, self._shapes)):
+            for i, (g, s) in enumerate(zip(grads, self._shapes)):
+                if g is not None:
+                    _tensor(f"grads[{i}]", g, bf16 if getattr(g, "dtype", None) == bf16 else f32, s, dev)
+        table["grad"] = [0 if g is None else g.data_ptr() for g in grads]
+        table["grad_dtype"] = [BF16 if g is not None and g.dtype is bf16 else F32 for g in grads]
+        a = _AdamWArgs()
+        a.beta1, a.beta2 = self.betas
+        a.eps, a.seed = self.eps, self.seed
+        if isinstance(self.lr, torch.Tensor):
+            a.lr_device = _tensor("lr", self.lr.reshape(-1), f32, torch.Size([1]), dev).data_ptr()
+        else:
+            a.lr = float(self.lr)
+        if grad_scale is not None:
+            a.grad_scale = _tensor("grad_scale", grad_scale.reshape(-1), f32, torch.Size([1]), dev).data_ptr()
+        with torch.cuda.device(dev):
+            if self._counter is not None:
+                a.step_device = self._counter.data_ptr()
+            elif torch.cuda.is_current_stream_capturing():
+                raise ValueError("a captured step counts on the GPU: AdamW(capturable=True)")
+            else:
+                a.step = self._steps + 1
+            _check(lib().bmoe_adamw_step(table.ctypes.data, len(table), ctypes.byref(a), _raw_stream(self.params[0])))
+        self._steps += 1
+
+    def moments(self, m_out=None, v_out=None):
+        """The moments' values as two lists: the fp32 tensors themselves, and for codes of
+        8 bits new fp32 tensors, or those of m_out and v_out (lists of fp32 or of bf16
+        tensors, which hold the values exactly; not for moments of 32 bits)."""
+        torch = _torch()
+        coded = [i for i, b in enumerate(self.bits) if b == 8]
+        kind = torch.float32
+        for name, outs in (("m_out", m_out), ("v_out", v_out)):
+            if outs is not None and len(outs) != len(self.params):
+                raise ValueError(f"{name} has {len(outs)} entries for {len(self.params)} parameters")
+        first = next((o[i] for o in (m_out, v_out) if o is not None for i in coded if o[i] is not None), None)
+        if first is not None and first.dtype == torch.bfloat16:
+            kind = torch.bfloat16
+        ms, vs = list(self.m), list(self.v)
+        for name, outs, out in (("m_out", m_out, ms), ("v_out", v_out, vs)):
+            for i, p in enumerate(self.params):
+                x = None if outs is None else outs[i]
+                if self.bits[i] != 8:
+                    if x is not None:
+                        raise ValueError(f"{name}[{i}]: the moments of parameter {i} are no codes")
+                else:
+                    out[i] = torch.empty(p.shape, dtype=kind, device=self.device) if x is None else _tensor(f"{name}[{i}]", x, kind, p.shape, self.device)
+        if coded:
+            table = self._table[coded]
+            pointers = [np.array([out[i].data_ptr() for i in coded], dtype=np.uint64) for out in (ms, vs)]
+            with torch.cuda.device(self.device):
+                _check(lib().bmoe_adamw_moments(table.ctypes.data, len(table), BF16 if kind == torch.bfloat16 else F32,
+                                                pointers[0].ctypes.data, pointers[1].ctypes.data, _raw_stream(self.params[0])))
+        return ms, vs

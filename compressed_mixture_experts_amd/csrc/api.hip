@@ -1,9 +1,10 @@
-// Host side of the C ABI declared in include/bmoe.h, include/bmoe_trace.h,
-// include/bmoe_grad.h, include/bmoe_norm.h, include/bmoe_train.h,
-// include/bmoe_update.h and (built with -DBMOE_DEBUG_EXPORTS only)
+// Host side of the C ABI declared in include/bmoe.h, include/bmoe_adamw.h,
+// include/bmoe_trace.h, include/bmoe_grad.h, include/bmoe_norm.h,
+// include/bmoe_train.h, include/bmoe_update.h and (built with -DBMOE_DEBUG_EXPORTS only)
 // include/bmoe_debug.h: argument validation (all before any enqueue),
 // workspace planning, and the launch sequence of the forward pass on the
 // caller's stream.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -14,6 +15,7 @@
 #include <vector>
 
 #include "bmoe.h"
+#include "bmoe_adamw.h"
 #include "bmoe_debug.h"
 #include "bmoe_grad.h"
 #include "bmoe_norm.h"
@@ -1690,6 +1692,170 @@ bmoe_status bmoe_substrate_step(int32_t rows, int32_t cols, const float* w, cons
                       1.0 - decay, n};
   BMOE_HIP(launch_sub_step(a, stream));
   return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- AdamW
+namespace {
+
+constexpr int32_t kMaxTensors = 1 << 20;
+constexpr int64_t kMaxValues = int64_t(1) << 40;
+
+// Sorts every kind's ranges by address, which they mostly are already, and looks for a
+// written one that overlaps any other.  The kinds below `written` are those.
+bool disjoint(std::vector<std::vector<Range>>& kinds, size_t written) {
+  struct Mark {
+    uintptr_t lo, hi;
+    bool out;
+  };
+  std::vector<Mark> all;
+  size_t n = 0;
+  for (const auto& k : kinds) n += k.size();
+  all.reserve(n);
+  auto less = [](const Mark& a, const Mark& b) { return a.lo < b.lo; };
+  for (size_t k = 0; k < kinds.size(); ++k) {
+    const size_t at = all.size();
+    for (const Range& r : kinds[k])
+      if (r.p && r.bytes) all.push_back({reinterpret_cast<uintptr_t>(r.p), reinterpret_cast<uintptr_t>(r.p) + r.bytes, k < written});
+    const auto mid = all.begin() + std::ptrdiff_t(at);
+    if (!std::is_sorted(mid, all.end(), less)) std::sort(mid, all.end(), less);
+    std::inplace_merge(all.begin(), mid, all.end(), less);
+  }
+  uintptr_t out = 0, in = 0;   // ends of what was written and read so far
+  for (const Mark& m : all) {
+    if (m.lo < out || (m.out && m.lo < in)) return false;
+    (m.out ? out : in) = std::max(m.out ? out : in, m.hi);
+  }
+  return true;
+}
+
+bmoe_status check_adamw_tensor(const bmoe_adamw_tensor& t, int32_t i) {
+  if (t.n < 0 || t.n > kMaxValues) return fail(BMOE_ERR_SHAPE, "tensor %d: n=%lld must be in [0, 2^40]", i, (long long)t.n);
+  if (t.bits != 32 && t.bits != 8) return fail(BMOE_ERR_DTYPE, "tensor %d: bits=%d must be 32 or 8", i, t.bits);
+  if (t.n > 0 && t.bits == 8 && (!t.m_exp || !t.v_exp)) return fail(BMOE_ERR_NULL, "tensor %d: m_exp / v_exp is NULL", i);
+  if (t.n > 0 && (!t.m || !t.v)) return fail(BMOE_ERR_NULL, "tensor %d: m / v is NULL", i);
+  return BMOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+bmoe_status bmoe_adamw_step(const bmoe_adamw_tensor* tensors, int32_t count, const bmoe_adamw_args* args,
+                            hipStream_t stream) try {
+  if (count < 0 || count > kMaxTensors) return fail(BMOE_ERR_SHAPE, "count=%d must be in [0, %d]", count, kMaxTensors);
+  if (!args || (count > 0 && !tensors)) return fail(BMOE_ERR_NULL, "tensors / args is NULL");
+  const bmoe_adamw_args& g = *args;
+  if (!g.lr_device && !std::isfinite(g.lr)) return fail(BMOE_ERR_SHAPE, "lr=%g must be finite", g.lr);
+  if (!(g.beta1 >= 0.0 && g.beta1 < 1.0) || !(g.beta2 >= 0.0 && g.beta2 < 1.0))
+    return fail(BMOE_ERR_SHAPE, "beta1=%g and beta2=%g must be in [0, 1)", g.beta1, g.beta2);
+  if (g.eps != 0.0 && !(g.eps >= 0x1p-126 && g.eps <= 0x1p126))
+    return fail(BMOE_ERR_SHAPE, "eps=%g must be 0 or in [2^-126, 2^126]", g.eps);
+  if (!g.step_device && g.step < 1) return fail(BMOE_ERR_SHAPE, "step=%lld must be at least 1", (long long)g.step);
+  if (g.reserved != 0) return fail(BMOE_ERR_SHAPE, "reserved field must be 0");
+  if (!aligned(g.step_device, 8) || !aligned(g.lr_device, 4) || !aligned(g.grad_scale, 4))
+    return fail(BMOE_ERR_ALIGN, "step_device must be 8-byte aligned, lr_device and grad_scale 4-byte");
+  std::vector<AwTensor> list;
+  list.reserve(size_t(count));
+  enum { P, M, V, ME, VE, COPY, ONES, GRAD, SCALARS, KINDS };
+  std::vector<std::vector<Range>> kinds(KINDS);
+  for (int k = 0; k < KINDS; ++k) kinds[size_t(k)].reserve(k == ONES || k == SCALARS ? 2 : size_t(count));
+  for (int32_t i = 0; i < count; ++i) {
+    const bmoe_adamw_tensor& t = tensors[i];
+    const bmoe_status st = check_adamw_tensor(t, i);
+    if (st != BMOE_OK) return st;
+    if (t.grad_dtype != BMOE_F32 && t.grad_dtype != BMOE_BF16)
+      return fail(BMOE_ERR_DTYPE, "tensor %d: grad_dtype=%d is unknown", i, t.grad_dtype);
+    if (!std::isfinite(t.lr_scale) || !std::isfinite(t.weight_decay))
+      return fail(BMOE_ERR_SHAPE, "tensor %d: lr_scale=%g and weight_decay=%g must be finite", i, double(t.lr_scale),
+                  double(t.weight_decay));
+    if (t.n == 0 || !t.grad) continue;
+    if (!t.param) return fail(BMOE_ERR_NULL, "tensor %d: param is NULL", i);
+    const size_t n = size_t(t.n), gs = act_size(t.grad_dtype), ms = t.bits == 8 ? 1 : 4, nb = (n + 255) / 256;
+    if (!aligned(t.param, 4) || !aligned(t.grad, gs) || !aligned(t.m, ms) || !aligned(t.v, ms) || !aligned(t.copy, 2))
+      return fail(BMOE_ERR_ALIGN, "tensor %d: param, grad, m, v and copy must be aligned to their element size", i);
+    const bool eight = t.bits == 8;
+    kinds[P].push_back({t.param, 4 * n});
+    kinds[M].push_back({t.m, ms * n});
+    kinds[V].push_back({t.v, ms * n});
+    if (eight) {
+      kinds[ME].push_back({t.m_exp, nb});
+      kinds[VE].push_back({t.v_exp, nb});
+    }
+    kinds[COPY].push_back({t.copy, 2 * n});
+    kinds[GRAD].push_back({t.grad, gs * n});
+    const bool fast = aligned(t.param, 16) && aligned(t.grad, 4 * gs) && aligned(t.m, 4 * ms) && aligned(t.v, 4 * ms) && aligned(t.copy, 8);
+    list.push_back({t.param, t.grad, t.m, t.v, t.m_exp, t.v_exp, static_cast<uint16_t*>(t.copy), t.n, t.lr_scale, t.weight_decay,
+                    uint32_t(i), uint32_t((t.grad_dtype == BMOE_BF16 ? AW_GRAD_BF16 : 0) | (eight ? AW_EIGHT : 0) | (fast ? AW_ALIGNED : 0))});
+  }
+  kinds[ONES].push_back({g.step_device, 8});
+  kinds[SCALARS].push_back({g.lr_device, 4});
+  kinds[SCALARS].push_back({g.grad_scale, 4});
+  if (!disjoint(kinds, GRAD)) return fail(BMOE_ERR_ALIAS, "an array that is written overlaps another one");
+  if (list.empty() && !g.step_device) return ok();
+  const bmoe_status st = check_device();
+  if (st != BMOE_OK) return st;
+  AwScalars s{};
+  s.beta1 = float(g.beta1);
+  s.rest1 = float(1.0 - g.beta1);
+  s.beta2 = float(g.beta2);
+  s.rest2 = float(1.0 - g.beta2);
+  s.eps = float(g.eps);
+  s.lr = float(g.lr);
+  s.log1 = std::log(g.beta1);
+  s.log2 = std::log(g.beta2);
+  s.step = g.step;
+  if (!g.step_device) {
+    s.by1 = float(-1.0 / std::expm1(double(g.step) * s.log1));
+    s.root2 = float(1.0 / std::sqrt(-std::expm1(double(g.step) * s.log2)));
+  }
+  s.step_device = g.step_device;
+  s.lr_device = g.lr_device;
+  s.grad_scale = g.grad_scale;
+  s.seed = g.seed;
+  BMOE_HIP(launch_adamw(list.data(), int(list.size()), s, g.step_device, stream));
+  return ok();
+} catch (...) {
+  return fail(BMOE_ERR_HIP, "out of host memory");
+}
+
+bmoe_status bmoe_adamw_moments(const bmoe_adamw_tensor* tensors, int32_t count, int32_t out_dtype, void* const* m_out,
+                               void* const* v_out, hipStream_t stream) try {
+  if (count < 0 || count > kMaxTensors) return fail(BMOE_ERR_SHAPE, "count=%d must be in [0, %d]", count, kMaxTensors);
+  if (out_dtype != BMOE_F32 && out_dtype != BMOE_BF16) return fail(BMOE_ERR_DTYPE, "out_dtype=%d is unknown", out_dtype);
+  if (count > 0 && (!tensors || !m_out || !v_out)) return fail(BMOE_ERR_NULL, "tensors / m_out / v_out is NULL");
+  const size_t os = act_size(out_dtype);
+  std::vector<AwTensor> list;
+  list.reserve(size_t(count));
+  std::vector<std::vector<Range>> kinds(6);
+  for (int32_t i = 0; i < count; ++i) {
+    const bmoe_adamw_tensor& t = tensors[i];
+    const bmoe_status st = check_adamw_tensor(t, i);
+    if (st != BMOE_OK) return st;
+    if (t.bits != 8) return fail(BMOE_ERR_DTYPE, "tensor %d: its moments are no codes", i);
+    if (t.n == 0 || (!m_out[i] && !v_out[i])) continue;
+    if (!aligned(m_out[i], os) || !aligned(v_out[i], os))
+      return fail(BMOE_ERR_ALIGN, "tensor %d: m_out and v_out must be aligned to their element size", i);
+    const size_t n = size_t(t.n), nb = (n + 255) / 256;
+    kinds[0].push_back({m_out[i], os * n});
+    kinds[1].push_back({v_out[i], os * n});
+    kinds[2].push_back({t.m, n});
+    kinds[3].push_back({t.v, n});
+    kinds[4].push_back({t.m_exp, nb});
+    kinds[5].push_back({t.v_exp, nb});
+    const bool fast = aligned(t.m, 4) && aligned(t.v, 4) && aligned(m_out[i], 4 * os) && aligned(v_out[i], 4 * os);
+    list.push_back({static_cast<float*>(m_out[i]), nullptr, t.m, t.v, t.m_exp, t.v_exp, static_cast<uint16_t*>(v_out[i]), t.n, 0.f, 0.f,
+                    uint32_t(i), uint32_t(fast ? AW_ALIGNED : 0)});
+  }
+  if (!disjoint(kinds, 2)) return fail(BMOE_ERR_ALIAS, "an array that is written overlaps another one");
+  if (list.empty()) return ok();
+  const bmoe_status st = check_device();
+  if (st != BMOE_OK) return st;
+  BMOE_HIP(launch_adamw_values(list.data(), int(list.size()), out_dtype == BMOE_BF16, stream));
+  return ok();
+} catch (...) {
+  return fail(BMOE_ERR_HIP, "out of host memory");
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
 // Launchers of the training-step operators (include/bmoe_norm.h,
-// include/bmoe_update.h).
+// include/bmoe_update.h, include/bmoe_adamw.h).
 #pragma once
 
 #include "common.hpp"
@@ -63,5 +63,37 @@ struct OrthoArgs {
 };
 size_t ortho_workspace(int rows, int cols);
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t s);
+
+// AdamW (adamw.hip).
+enum AwFlags { AW_GRAD_BF16 = 1, AW_EIGHT = 2, AW_ALIGNED = 4 };
+constexpr int AW_TENSORS = 40;  // of a launch
+struct AwTensor {
+  float* p;                 // [n]
+  const void* g;            // [n]
+  void* m;                  // [n] fp32 or codes
+  void* v;
+  uint8_t* me;              // a byte a block of 256 with codes
+  uint8_t* ve;
+  uint16_t* copy;           // [n] bf16 or null
+  int64_t n;
+  float lr_scale, decay;
+  uint32_t index;           // the tensor's place in the call
+  uint32_t flags;
+};
+struct AwScalars {
+  float beta1, rest1, beta2, rest2, eps;   // rest = 1 - beta
+  float lr;
+  float by1, root2;         // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  double log1, log2;        // log(beta)
+  int64_t step;
+  const int64_t* step_device;
+  const float* lr_device;
+  const float* grad_scale;
+  uint32_t seed;
+};
+// count_up: raised by 1 first, or null
+hipError_t launch_adamw(const AwTensor* tensors, int count, const AwScalars& s, int64_t* count_up, hipStream_t stream);
+// codes' values: of m to p and of v to copy (arrays of the given type, null: not wanted)
+hipError_t launch_adamw_values(const AwTensor* tensors, int count, bool bf16, hipStream_t stream);
 
 }  // namespace bmoe

@@ -611,3 +611,56 @@ def substrate_step(w, o=None, step: float = 0.0, decay: float = 0.0):
     scale = mag.sum() / mag.size
     codes = np.where(2.0 * mag > scale, np.sign(w), 0.0).astype(np.int8)
     return w, codes, scale
+
+
+# ---------------------------------------------------------------- AdamW
+ADAMW_BLOCK, ADAMW_M_TOP, ADAMW_V_TOP = 256, 13, 29
+
+
+def adamw(p, g, m, v, t, lr, betas=(0.9, 0.999), eps: float = 1e-8, decay: float = 0.0):
+    """AdamW step number t in fp64: (p', m', v')."""
+    m = betas[0] * m + (1.0 - betas[0]) * g
+    v = betas[1] * v + (1.0 - betas[1]) * g * g
+    step = (m / (1.0 - betas[0] ** t)) / (np.sqrt(v / (1.0 - betas[1] ** t)) + eps)
+    return p - lr * decay * p - lr * step, m, v
+
+
+def _adamw_mix(h):
+    h = np.asarray(h, dtype=np.uint64) & np.uint64(0xFFFFFFFF)
+    for shift, by in ((15, 0x6A09E667), (13, 0x3C6EF373)):
+        h = ((h ^ (h >> np.uint64(shift))) * np.uint64(by)) & np.uint64(0xFFFFFFFF)
+    return h ^ (h >> np.uint64(16))
+
+
+def adamw_random(n: int, t: int, index: int, seed: int):
+    """The two fractions in [0, 1) of each of n values: (for m, for v)."""
+    mask = 0xFFFFFFFF
+    key = int(_adamw_mix((t * 0x9E3779B1 + int(_adamw_mix((index * 0xBB67AE85 + seed) & mask))) & mask))
+    i = np.arange(n, dtype=np.uint64)
+    h = _adamw_mix(((i & np.uint64(mask)) * np.uint64(0x9E3779B1) + (i >> np.uint64(32)) * np.uint64(0xBB67AE85) + np.uint64(key)) & np.uint64(mask))
+    return (h & np.uint64(0xFFFF)).astype(np.float64) / 65536.0, (h >> np.uint64(16)).astype(np.float64) / 65536.0
+
+
+def adamw_exponents(x):
+    """Exponent of the largest finite value of each block, as the stored byte."""
+    size = np.abs(np.where(np.isfinite(x), x, 0.0))
+    size = np.pad(size, (0, -len(size) % ADAMW_BLOCK)).reshape(-1, ADAMW_BLOCK).max(axis=1)
+    e = np.where(size > 0, np.frexp(size)[1] - 1, -126)
+    return (np.clip(e, -126, 127) + 127).astype(np.uint8)
+
+
+def adamw_codes(x, exps, top: int, r):
+    """Codes of |x| at the blocks' stored exponents, rounded up by the fractions r (of
+    values only: signs, NaN codes and v's lowest code are the caller's)."""
+    e = exps.astype(np.int64).repeat(ADAMW_BLOCK)[: len(x)] - 127 - top
+    size = np.abs(x)
+    k = np.where(size > 0, np.maximum(np.frexp(size)[1] - 1 - e, 0), 0)
+    return np.floor(np.ldexp(size, -(k + e - 3)) + r).astype(np.int64) + 8 * k
+
+
+def adamw_values(codes, exps, top: int):
+    """What the codes (without sign) stand for."""
+    e = exps.astype(np.int64).repeat(ADAMW_BLOCK)[: len(codes)] - 127 - top
+    c = codes.astype(np.int64)
+    k = np.maximum((c >> 3) - 1, 0)
+    return np.ldexp((c - 8 * k).astype(np.float64), k + e - 3)

@@ -1,0 +1,139 @@
+"""Argument errors of the operators around a layer (include/bmoe_adamw.h): each is
+found on the host before anything is enqueued, so the pointers here are never followed.
+No GPU needed."""
+import ctypes
+import os
+import subprocess
+import sys
+
+import numpy as np
+import pytest
+
+import compressed_mixture_experts_amd as bm
+from compressed_mixture_experts_amd import blocks
+from compressed_mixture_experts_amd import build as bbuild
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+NULL, SHAPE, DTYPE, ALIGN, ALIAS, WORKSPACE = 1, 2, 3, 4, 5, 6
+MB = 1 << 20
+
+
+def ptr(k):
+    """Made-up address of array k, far from every other one."""
+    return (k + 1) * 64 * MB
+
+
+def tensors(changes=(), second=()):
+    """Two tensors of 1000 values, of 32 and 8 bits."""
+    t = np.zeros(2, dtype=blocks._ADAMW_TENSOR)
+    for i, (bits, change) in enumerate(((32, changes), (8, second))):
+        row = dict(param=ptr(10 * i), grad=ptr(10 * i + 1), m=ptr(10 * i + 2), v=ptr(10 * i + 3), m_exp=ptr(10 * i + 4) if bits == 8 else 0,
+                   v_exp=ptr(10 * i + 5) if bits == 8 else 0, copy=ptr(10 * i + 6), n=1000, lr_scale=1.0, weight_decay=0.0, grad_dtype=0,
+                   bits=bits)
+        row.update(change)
+        for k, x in row.items():
+            t[k][i] = x
+    return t
+
+
+ARGS = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1, step_device=None, lr_device=None, grad_scale=None, seed=0, reserved=0)
+
+
+def step(t, **change):
+    a = blocks._AdamWArgs(**dict(ARGS, **change))
+    return bm.lib().bmoe_adamw_step(t.ctypes.data, len(t), ctypes.byref(a), None)
+
+
+REFUSED_TENSORS = [
+    (dict(n=-1), {}, SHAPE), (dict(n=(1 << 40) + 1), {}, SHAPE), (dict(lr_scale=float("nan")), {}, SHAPE),
+    (dict(weight_decay=float("inf")), {}, SHAPE), (dict(bits=16), {}, DTYPE), (dict(grad_dtype=2), {}, DTYPE),
+    (dict(param=0), {}, NULL), (dict(m=0), {}, NULL), (dict(v=0), {}, NULL), ({}, dict(m_exp=0), NULL), ({}, dict(v_exp=0), NULL),
+    (dict(param=ptr(0) + 2), {}, ALIGN), (dict(grad=ptr(1) + 1), {}, ALIGN), (dict(m=ptr(2) + 2), {}, ALIGN), (dict(copy=ptr(6) + 1), {}, ALIGN),
+    (dict(grad=ptr(1) + 1, grad_dtype=1), {}, ALIGN),
+    # within a tensor, and between two
+    (dict(grad=ptr(0) + 4), {}, ALIAS), (dict(m=ptr(0)), {}, ALIAS), (dict(v=ptr(2)), {}, ALIAS), (dict(copy=ptr(1) + 2), {}, ALIAS),
+    ({}, dict(m_exp=ptr(15)), ALIAS), ({}, dict(v_exp=ptr(12) + 999), ALIAS), ({}, dict(param=ptr(0) + 3996), ALIAS),
+    ({}, dict(grad=ptr(3)), ALIAS), ({}, dict(copy=ptr(6) + 1998), ALIAS), (dict(grad=ptr(13)), {}, ALIAS), ({}, dict(m=ptr(0) - 999), ALIAS),
+]
+
+
+@pytest.mark.parametrize("first,second,status", REFUSED_TENSORS, ids=lambda v: str(v)[:50])
+def test_adamw_tensor_refusals(first, second, status):
+    assert step(tensors(first, second)) == status
+    assert bm.lib().bmoe_last_error() != b""
+
+
+REFUSED_ARGS = [
+    (dict(lr=float("nan")), SHAPE), (dict(lr=float("inf")), SHAPE), (dict(beta1=1.0), SHAPE), (dict(beta1=-0.1), SHAPE),
+    (dict(beta2=1.0), SHAPE), (dict(beta2=float("nan")), SHAPE), (dict(eps=-1e-8), SHAPE), (dict(eps=float("nan")), SHAPE),
+    (dict(eps=1e-40), SHAPE), (dict(eps=float("inf")), SHAPE), (dict(step=0), SHAPE), (dict(reserved=1), SHAPE),
+    (dict(step_device=ptr(40) + 4), ALIGN), (dict(lr_device=ptr(40) + 2), ALIGN), (dict(grad_scale=ptr(40) + 1), ALIGN),
+    (dict(step_device=ptr(0)), ALIAS), (dict(lr_device=ptr(0) + 8), ALIAS), (dict(grad_scale=ptr(2)), ALIAS),
+    (dict(step_device=ptr(40), lr_device=ptr(40) + 4), ALIAS),
+]
+
+
+@pytest.mark.parametrize("change,status", REFUSED_ARGS, ids=lambda v: str(v)[:50])
+def test_adamw_argument_refusals(change, status):
+    assert step(tensors(), **change) == status
+
+
+def test_adamw_nothing_to_do():
+    """No tensors, no values, no gradients: nothing is launched, no GPU is needed."""
+    L = bm.lib()
+    a = blocks._AdamWArgs(**ARGS)
+    assert L.bmoe_adamw_step(None, 0, ctypes.byref(a), None) == 0
+    assert step(tensors(dict(n=0, param=0, m=0, v=0), dict(grad=0))) == 0
+    assert L.bmoe_adamw_step(None, 2, ctypes.byref(a), None) == NULL
+    assert L.bmoe_adamw_step(None, 0, None, None) == NULL
+    assert L.bmoe_adamw_step(None, -1, ctypes.byref(a), None) == SHAPE
+    # what is read may be read twice: refused for another reason
+    t = tensors(dict(grad=ptr(11)))
+    assert step(t, beta1=2.0) == SHAPE
+
+
+def moments(t, m_out, v_out, kind=0):
+    m, v = np.array(m_out, dtype=np.uint64), np.array(v_out, dtype=np.uint64)
+    return bm.lib().bmoe_adamw_moments(t.ctypes.data, len(t), kind, m.ctypes.data, v.ctypes.data, None)
+
+
+def test_adamw_moments_refusals():
+    t = tensors(second={})[1:].copy()
+    assert moments(t, [ptr(30)], [ptr(31)], kind=2) == DTYPE
+    assert moments(tensors(), [ptr(30), ptr(31)], [ptr(32), ptr(33)]) == DTYPE   # the first has no codes
+    assert moments(t, [ptr(30) + 2], [ptr(31)]) == ALIGN and moments(t, [ptr(30)], [ptr(31) + 1], kind=1) == ALIGN
+    assert moments(t, [ptr(30)], [ptr(30) + 4]) == ALIAS and moments(t, [ptr(12)], [0]) == ALIAS
+    assert moments(t, [0], [ptr(15) - 4]) == ALIAS
+    assert moments(t, [0], [0]) == 0
+    assert bm.lib().bmoe_adamw_moments(None, 1, 0, None, None, None) == NULL
+    assert bm.lib().bmoe_adamw_moments(None, -1, 0, None, None, None) == SHAPE
+
+
+def test_adamw_struct_is_the_header_s():
+    """Sizes of the two structures as the C compiler lays them out: 7 pointers, a 64-bit
+    number and four 32-bit ones; 4 doubles, a 64-bit number, 3 pointers, two 32-bit numbers."""
+    assert blocks._ADAMW_TENSOR.itemsize == 7 * 8 + 8 + 4 * 4 and ctypes.sizeof(blocks._AdamWArgs) == 4 * 8 + 8 + 3 * 8 + 2 * 4
+
+
+def test_adamw_binding_refuses_cpu_tensors():
+    torch = pytest.importorskip("torch")
+    for params in ([torch.zeros(4)], [], [None]):
+        with pytest.raises(ValueError):
+            bm.AdamW(params)
+
+
+def test_refusals_under_host_sanitizers():
+    """This file again against the library whose host code is sanitized."""
+    rt = bbuild.sanitizer_runtime()
+    if os.environ.get("BMOE_LIBRARY"):
+        pytest.skip("already running against a chosen library")
+    if not os.path.exists(bbuild.LIB_HOSTSAN) or not rt:
+        pytest.skip("libbmoe_hostsan.so or the sanitizer runtime is missing (build with the package build)")
+    env = dict(os.environ, BMOE_LIBRARY=bbuild.LIB_HOSTSAN, LD_PRELOAD=rt,
+               ASAN_OPTIONS="detect_leaks=0:abort_on_error=1:halt_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1",
+               HIP_VISIBLE_DEVICES=os.environ.get("HIP_VISIBLE_DEVICES", ""))
+    r = subprocess.run([sys.executable, "-m", "pytest", "-q", "-x", "-p", "no:cacheprovider", "-k", "not binding",
+                        os.path.abspath(__file__)], cwd=ROOT, env=env, capture_output=True, text=True, timeout=600)
+    tail = (r.stdout + r.stderr)[-3000:]
+    assert r.returncode == 0 and "passed" in r.stdout and "ERROR: AddressSanitizer" not in r.stderr, tail

@@ -1,0 +1,48 @@
+"""Pins of the fp64 oracle's operators around a layer: closed forms, differences and
+invariants."""
+import numpy as np
+
+from oracle import ref
+
+
+def test_adamw_first_step_is_the_gradients_sign():
+    """Without moments the first step's m / sqrt(v) is the gradient's sign."""
+    g = np.array([3.0, -2e-3, 5e-9, 0.0])
+    p, m, v = ref.adamw(np.ones(4), g, np.zeros(4), np.zeros(4), 1, 0.1, eps=0.0 + 1e-30)
+    assert np.allclose(p, 1 - 0.1 * np.sign(g)) and np.allclose(m, 0.1 * g) and np.allclose(v, 1e-3 * g * g)
+    assert np.allclose(ref.adamw(2 * np.ones(4), 0 * g, 0 * g, 0 * g, 1, 0.1, decay=0.5)[0], 1.9)
+
+
+def test_adamw_code_values_round_to_themselves():
+    """Every code's value has that code whatever the fraction, and the values grow with
+    their codes by steps of a factor of 9/8 at most above the first octave."""
+    exps = np.array([100], dtype=np.uint8)
+    for top, codes in ((13, np.arange(0, 121)), (29, np.arange(0, 249))):
+        x = ref.adamw_values(codes, exps, top)
+        assert (np.diff(x) > 0).all() and (x[9:] / x[8:-1] <= 9 / 8).all() and x[0] == 0
+        assert x[8 * top + 8] == 2.0 ** (100 - 127) and x[1] == 2.0 ** (100 - 127 - top - 3)
+        for r in (0.0, 0.5, 1 - 2.0 ** -16):
+            assert (ref.adamw_codes(x, exps, top, r) == codes).all()
+
+
+def test_adamw_codes_keep_the_mean():
+    """Rounding by fractions is unbiased: the mean over all 2^16 of them is the value."""
+    exps = np.array([127], dtype=np.uint8)
+    r = np.arange(65536) / 65536.0
+    for top, xs in ((13, (0.7, 1.3, 1.9999, 3e-4, 2e-5)), (29, (0.7, 1.0627, 3e-6, 1e-9, 3e-10))):
+        for x in xs:
+            block = np.full(256, x)
+            got = np.concatenate([ref.adamw_values(ref.adamw_codes(block, exps, top, r[i:i + 256]), exps, top) for i in range(0, 65536, 256)])
+            assert abs(got.mean() - x) <= 2.0 ** -16 * max(x / 8, 2.0 ** (-top - 3))
+
+
+def test_adamw_random_is_uniform():
+    """Means and variances of both fractions, and their correlation with each other, the
+    next value's and the next step's: within 5 standard deviations."""
+    n = 1 << 16
+    rows = [ref.adamw_random(n, t, i, s) for t, i, s in ((1, 0, 0), (2, 0, 0), (1, 1, 0), (1, 0, 1))]
+    flat = [f for pair in rows for f in pair]
+    for k, f in enumerate(flat):
+        assert abs(f.mean() - 0.5) < 5 * np.sqrt(1 / 12 / n) and abs(f.var() - 1 / 12) < 5 * np.sqrt(1 / 180 / n)
+        for h in flat[:k] + [np.roll(f, 1)]:
+            assert abs(np.corrcoef(f, h)[0, 1]) < 5 / np.sqrt(n)
