@@ -2,8 +2,8 @@
 as in the package's other calls."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
-import math
 
 import numpy as np
 
@@ -48,6 +48,15 @@ def _tensor(name, t, kind, shape, device):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _device(index: int):
+    """The GPU `index` as the current one (2 us less where it is)."""
+    torch = _torch()
+    return _HERE if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
 class AdamW:
@@ -127,8 +136,10 @@ class AdamW:
             t[name] = [0 if x is None else x.data_ptr() for x in tensors]
         t["n"] = [p.numel() for p in self.params]
         t["lr_scale"], t["weight_decay"], t["bits"] = self._scale, self._decay, self.bits
-        self._table = t
+        self._table, self._table_at = t, t.ctypes.data
+        self._grad, self._grad_dtype = t["grad"], t["grad_dtype"]   # views of it
         self._shapes = [p.shape for p in self.params]
+        self._coded = [i for i, b in enumerate(self.bits) if b == 8]
         self._steps = int(steps)
         self._counter = torch.full((1,), self._steps, dtype=torch.int64, device=dev) if capturable else None
 
@@ -151,8 +162,8 @@ class AdamW:
             for i, (g, s) in enumerate(zip(grads, self._shapes)):
                 if g is not None:
                     _tensor(f"grads[{i}]", g, bf16 if getattr(g, "dtype", None) == bf16 else f32, s, dev)
-        table["grad"] = [0 if g is None else g.data_ptr() for g in grads]
-        table["grad_dtype"] = [BF16 if g is not None and g.dtype is bf16 else F32 for g in grads]
+        self._grad[:] = [0 if g is None else g.data_ptr() for g in grads]
+        self._grad_dtype[:] = [BF16 if g is not None and g.dtype is bf16 else F32 for g in grads]
         a = _AdamWArgs()
         a.beta1, a.beta2 = self.betas
         a.eps, a.seed = self.eps, self.seed
@@ -162,14 +173,14 @@ class AdamW:
             a.lr = float(self.lr)
         if grad_scale is not None:
             a.grad_scale = _tensor("grad_scale", grad_scale.reshape(-1), f32, torch.Size([1]), dev).data_ptr()
-        with torch.cuda.device(dev):
+        with _device(index):
             if self._counter is not None:
                 a.step_device = self._counter.data_ptr()
             elif torch.cuda.is_current_stream_capturing():
                 raise ValueError("a captured step counts on the GPU: AdamW(capturable=True)")
             else:
                 a.step = self._steps + 1
-            _check(lib().bmoe_adamw_step(table.ctypes.data, len(table), ctypes.byref(a), _raw_stream(self.params[0])))
+            _check(lib().bmoe_adamw_step(self._table_at, len(table), ctypes.byref(a), _raw_stream(self.params[0])))
         self._steps += 1
 
     def moments(self, m_out=None, v_out=None):
@@ -177,27 +188,31 @@ class AdamW:
         8 bits new fp32 tensors, or those of m_out and v_out (lists of fp32 or of bf16
         tensors, which hold the values exactly; not for moments of 32 bits)."""
         torch = _torch()
-        coded = [i for i, b in enumerate(self.bits) if b == 8]
-        kind = torch.float32
+        coded, kind, bf16 = self._coded, torch.float32, torch.bfloat16
+        index, count = self.device.index, len(self.params)
         for name, outs in (("m_out", m_out), ("v_out", v_out)):
-            if outs is not None and len(outs) != len(self.params):
-                raise ValueError(f"{name} has {len(outs)} entries for {len(self.params)} parameters")
+            if outs is not None and len(outs) != count:
+                raise ValueError(f"{name} has {len(outs)} entries for {count} parameters")
         first = next((o[i] for o in (m_out, v_out) if o is not None for i in coded if o[i] is not None), None)
-        if first is not None and first.dtype == torch.bfloat16:
-            kind = torch.bfloat16
+        if first is not None and first.dtype == bf16:
+            kind = bf16
         ms, vs = list(self.m), list(self.v)
         for name, outs, out in (("m_out", m_out, ms), ("v_out", v_out, vs)):
-            for i, p in enumerate(self.params):
-                x = None if outs is None else outs[i]
-                if self.bits[i] != 8:
-                    if x is not None:
-                        raise ValueError(f"{name}[{i}]: the moments of parameter {i} are no codes")
-                else:
-                    out[i] = torch.empty(p.shape, dtype=kind, device=self.device) if x is None else _tensor(f"{name}[{i}]", x, kind, p.shape, self.device)
+            if outs is None:
+                outs = [None] * count
+            elif len(coded) < count and any(x is not None and b != 8 for x, b in zip(outs, self.bits)):
+                raise ValueError(f"{name} is for moments in 8 bits: None elsewhere")
+            for i in coded:
+                x = outs[i]
+                if x is None:
+                    x = torch.empty(self._shapes[i], dtype=kind, device=self.device)
+                elif not (x.is_cuda and x.dtype is kind and x.get_device() == index and x.shape == self._shapes[i] and x.is_contiguous()):
+                    _tensor(f"{name}[{i}]", x, kind, self._shapes[i], self.device)
+                out[i] = x
         if coded:
             table = self._table[coded]
             pointers = [np.array([out[i].data_ptr() for i in coded], dtype=np.uint64) for out in (ms, vs)]
-            with torch.cuda.device(self.device):
+            with _device(index):
                 _check(lib().bmoe_adamw_moments(table.ctypes.data, len(table), BF16 if kind == torch.bfloat16 else F32,
                                                 pointers[0].ctypes.data, pointers[1].ctypes.data, _raw_stream(self.params[0])))
         return ms, vs
