@@ -2,7 +2,7 @@
 
 The computation runs in ``libbmoe.so`` (hand-written HIP kernels behind the C
 ABI of ``include/bmoe.h``, ``bmoe_trace.h``, ``bmoe_grad.h``, ``bmoe_train.h``,
-``bmoe_norm.h``, ``bmoe_update.h`` and ``bmoe_adamw.h``).  The test
+``bmoe_norm.h``, ``bmoe_update.h``, ``bmoe_adamw.h`` and ``bmoe_block.h``).  The test
 hooks of ``include/bmoe_debug.h`` live only in ``libbmoe_debug.so`` (the same
 kernels, built with -DBMOE_DEBUG_EXPORTS), loaded on first use of a
 ``dbg_*`` function.  This module only marshals arguments: torch tensors
@@ -29,7 +29,8 @@ __all__ = [
     "BmoeError", "lib", "library_path", "pack_ternary", "packed_words", "Layer",
     "dbg_butterfly", "dbg_ternary_gemm", "dbg_ternary_gemm_fp4", "butterfly_backward", "substrate_grad",
     "combine_backward", "router_backward", "gelu_backward", "substrate_input_grad",
-    "layer_norm_forward", "layer_norm_backward", "orthogonalize", "substrate_step", "AdamW", "STATUS",
+    "layer_norm_forward", "layer_norm_backward", "orthogonalize", "substrate_step", "AdamW",
+    "block_norm_forward", "block_norm_backward", "STATUS",
     "EXPORTED_SYMBOLS", "DEBUG_SYMBOLS", "debug_lib",
 ]
 
@@ -47,7 +48,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20   # BMOE_NOALLOC_SCRATCH_BYTES of include/bmoe.
 ACT_NONE, ACT_GELU_ERF = 0, 1
 
 # exports of libbmoe.so (include/bmoe.h, bmoe_trace.h, bmoe_grad.h, bmoe_train.h,
-# bmoe_norm.h, bmoe_update.h, bmoe_adamw.h)
+# bmoe_norm.h, bmoe_update.h, bmoe_adamw.h, bmoe_block.h)
 EXPORTED_SYMBOLS = [
     "bmoe_packed_words", "bmoe_pack_ternary", "bmoe_workspace_size", "bmoe_prepared_bytes",
     "bmoe_prepare", "bmoe_route", "bmoe_forward", "bmoe_forward_noalloc", "bmoe_status_string",
@@ -62,6 +63,7 @@ EXPORTED_SYMBOLS = [
     "bmoe_orthogonalize_workspace", "bmoe_orthogonalize",
     "bmoe_substrate_step_workspace", "bmoe_substrate_step",
     "bmoe_adamw_step", "bmoe_adamw_moments",
+    "bmoe_block_norm_forward", "bmoe_block_norm_backward_workspace", "bmoe_block_norm_backward",
 ]
 # exported by libbmoe_debug.so only (include/bmoe_debug.h)
 DEBUG_SYMBOLS = ["bmoe_dbg_butterfly", "bmoe_dbg_ternary_gemm", "bmoe_dbg_ternary_gemm_fp4"]
@@ -157,6 +159,9 @@ def _load(path: str, debug: bool) -> ctypes.CDLL:
     L.bmoe_substrate_step.argtypes = [c_i32, c_i32, c_vp, c_vp, c_d, c_d, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]
     L.bmoe_adamw_step.argtypes = [c_vp, c_i32, c_vp, c_vp]
     L.bmoe_adamw_moments.argtypes = [c_vp, c_i32, c_i32, c_vp, c_vp, c_vp]
+    L.bmoe_block_norm_forward.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]
+    L.bmoe_block_norm_backward_workspace.argtypes = [c_vp, ctypes.POINTER(c_sz)]
+    L.bmoe_block_norm_backward.argtypes = [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]
     ret = [n for n in EXPORTED_SYMBOLS if n not in ("bmoe_packed_words", "bmoe_prepared_bytes",
                                                     "bmoe_status_string", "bmoe_last_error")]
     if debug:
@@ -789,4 +794,4 @@ def dbg_ternary_gemm_fp4(a, w_packed, n_out: int, alpha: float = 1.0):
     return z
 
 
-from .blocks import AdamW  # noqa: E402
+from .blocks import AdamW, block_norm_backward, block_norm_forward  # noqa: E402

@@ -1,5 +1,5 @@
-"""Operators around an expert layer (include/bmoe_adamw.h): argument marshalling only,
-as in the package's other calls."""
+"""Operators around an expert layer (include/bmoe_adamw.h, bmoe_block.h): argument
+marshalling only, as in the package's other calls."""
 from __future__ import annotations
 
 import contextlib
@@ -7,7 +7,7 @@ import ctypes
 
 import numpy as np
 
-from . import BF16, F32, _check, _raw_stream, _torch, lib
+from . import BF16, F32, _check, _on_device, _operand, _raw_stream, _torch, lib
 
 # bmoe_adamw_tensor of include/bmoe_adamw.h
 _ADAMW_TENSOR = np.dtype([
@@ -216,3 +216,127 @@ class AdamW:
                 _check(lib().bmoe_adamw_moments(table.ctypes.data, len(table), BF16 if kind == torch.bfloat16 else F32,
                                                 pointers[0].ctypes.data, pointers[1].ctypes.data, _raw_stream(self.params[0])))
         return ms, vs
+
+
+class _BlockNorm(ctypes.Structure):
+    """bmoe_block_norm of include/bmoe_block.h."""
+    _fields_ = [
+        ("rows", ctypes.c_int32), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32), ("kind", ctypes.c_int32),
+        ("post", ctypes.c_int32), ("gate_kind", ctypes.c_int32), ("alpha", ctypes.c_float), ("scale", ctypes.c_float),
+        ("eps", ctypes.c_float), ("reserved", ctypes.c_int32), ("gate", ctypes.c_void_p), ("gamma_post", ctypes.c_void_p),
+        ("beta_post", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("beta", ctypes.c_void_p)]
+
+
+class _BlockNormGrads(ctypes.Structure):
+    """bmoe_block_norm_grads of include/bmoe_block.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gamma_post", "beta_post", "gate", "gamma", "beta")]
+
+
+_NORM_KINDS = {"layer": 0, "rms": 1}
+
+
+def _block_norm(b, gate, alpha, scale, post, kind, gamma_post, beta_post, gamma, beta, eps):
+    """Check the weights and describe the call."""
+    torch = _torch()
+    dev, f32 = b.device, (torch.float32,)
+    rows, width = b.shape
+    _operand("b", b, b.shape, (torch.float32, torch.bfloat16), dev)
+    if kind not in _NORM_KINDS:
+        raise ValueError(f"kind is {kind!r}, expected 'layer' or 'rms'")
+    n = _BlockNorm()
+    n.rows, n.width, n.dtype, n.kind, n.post = rows, width, BF16 if b.dtype is torch.bfloat16 else F32, _NORM_KINDS[kind], 1 if post else 0
+    n.alpha, n.scale, n.eps = alpha, scale, eps
+    if gate is not None:
+        if gate.dim() == 1:
+            n.gate_kind = 1
+            _operand("gate", gate, (width,), f32, dev)
+        else:
+            n.gate_kind = 2
+            _operand("gate", gate, b.shape, (b.dtype,), dev)
+        n.gate = gate.data_ptr()
+    if gamma_post is not None:
+        n.gamma_post = _operand("gamma_post", gamma_post, (width,), f32, dev).data_ptr()
+    if beta_post is not None:
+        n.beta_post = _operand("beta_post", beta_post, (width,), f32, dev).data_ptr()
+    if gamma is not None:
+        n.gamma = _operand("gamma", gamma, (width,), f32, dev).data_ptr()
+    if beta is not None:
+        n.beta = _operand("beta", beta, (width,), f32, dev).data_ptr()
+    return n
+
+
+@_on_device
+def block_norm_forward(b, residual=None, gate=None, alpha: float = 1.0, scale: float = 1.0, post: bool = True, kind: str = "layer",
+                       gamma_post=None, beta_post=None, gamma=None, beta=None, eps: float = 1e-5, stats: bool = True, s_out=None,
+                       y=None):
+    """From a block's output b [rows][width] (fp32 or bf16) to the next block's input:
+        z = norm(b) gamma_post + beta_post   (z = b with post=False)
+        s = alpha residual + scale gate z,   y = norm(s) gamma + beta
+    with layer norms or (kind="rms", without betas) RMS norms.  gate: None, [width] fp32
+    or [rows][width] like b; gammas and betas [width] fp32 or None (ones, zeros).  Returns
+    (y, s, stats): stats [rows][4] fp32 for the backward (None with stats=False).  s_out may be
+    residual itself, and y either input that is not needed any more."""
+    torch = _torch()
+    n = _block_norm(b, gate, alpha, scale, post, kind, gamma_post, beta_post, gamma, beta, eps)
+    dev, shape, own = b.device, b.shape, (b.dtype,)
+    if residual is not None:
+        _operand("residual", residual, shape, own, dev)
+    s_out = torch.empty_like(b) if s_out is None else _operand("s_out", s_out, shape, own, dev)
+    y = torch.empty_like(b) if y is None else _operand("y", y, shape, own, dev)
+    st = torch.empty((shape[0], 4), dtype=torch.float32, device=dev) if stats else None
+    _check(lib().bmoe_block_norm_forward(ctypes.byref(n), b.data_ptr(), None if residual is None else residual.data_ptr(),
+                                         s_out.data_ptr(), y.data_ptr(), None if st is None else st.data_ptr(), _raw_stream(b)))
+    return y, s_out, st
+
+
+@_on_device
+def block_norm_backward(dy, b, s, stats, gate=None, alpha: float = 1.0, scale: float = 1.0, post: bool = True, kind: str = "layer",
+                        gamma_post=None, beta_post=None, gamma=None, d_sum=None, residual: bool = True, weight_grads: bool = True,
+                        db=None, dr=None):
+    """Backward of block_norm_forward at its s and stats: dy [rows][width] fp32 or of b's
+    dtype, d_sum like b or None (gradient that reaches s past the norm in front of the next
+    block).  Returns a dict of b, residual (None with residual=False), gate, gamma_post,
+    beta_post, gamma and beta: the gradients, like b the first two and a gate of rows, fp32
+    [width] the others, None for what the forward has no use for (betas of an RMS norm,
+    post's without it, a gate that was not given; weight_grads=False: all but the first
+    two).  db and dr may be b, s, d_sum or a dy of their dtype themselves."""
+    torch = _torch()
+    if b.dim() != 2:
+        raise ValueError(f"b has shape {tuple(b.shape)}, expected two dimensions")
+    dev, own = dy.device, (b.dtype,)
+    if b.device != dev:
+        raise ValueError(f"b is on {b.device}, expected {dev}")
+    n = _block_norm(b, gate, alpha, scale, post, kind, gamma_post, beta_post, gamma, None, 0.0)
+    shape = b.shape
+    rows, width = shape
+    _operand("dy", dy, shape, (torch.float32, b.dtype), dev)
+    _operand("s", s, shape, own, dev)
+    _operand("stats", stats, (rows, 4), (torch.float32,), dev)
+    if d_sum is not None:
+        _operand("d_sum", d_sum, shape, own, dev)
+    out = dict.fromkeys(("b", "residual", "gate", "gamma_post", "beta_post", "gamma", "beta"))
+    out["b"] = torch.empty_like(b) if db is None else _operand("db", db, shape, own, dev)
+    if residual:
+        out["residual"] = torch.empty_like(b) if dr is None else _operand("dr", dr, shape, own, dev)
+    elif dr is not None:
+        raise ValueError("dr needs residual=True")
+    g, ws, nbytes = None, None, 0
+    if weight_grads:
+        layer = kind == "layer"
+        names = ["gamma"] + (["beta"] if layer else []) + (["gamma_post"] if post else []) + (["beta_post"] if post and layer else [])
+        if gate is not None and gate.dim() == 1:
+            names.append("gate")
+        for name, x in zip(names, torch.empty((len(names), width), dtype=torch.float32, device=dev).unbind(0)):
+            out[name] = x
+        if gate is not None and gate.dim() == 2:
+            out["gate"] = torch.empty_like(b)
+        g = _BlockNormGrads(*[None if out[k] is None else out[k].data_ptr() for k in ("gamma_post", "beta_post", "gate", "gamma", "beta")])
+        size = ctypes.c_size_t(0)
+        _check(lib().bmoe_block_norm_backward_workspace(ctypes.byref(n), ctypes.byref(size)))
+        nbytes = size.value
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _check(lib().bmoe_block_norm_backward(
+        ctypes.byref(n), BF16 if dy.dtype is torch.bfloat16 else F32, dy.data_ptr(), b.data_ptr(), s.data_ptr(), stats.data_ptr(),
+        None if d_sum is None else d_sum.data_ptr(), out["b"].data_ptr(), None if out["residual"] is None else out["residual"].data_ptr(),
+        None if g is None else ctypes.byref(g), None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dy)))
+    return out

@@ -1,5 +1,5 @@
 // Host side of the C ABI declared in include/bmoe.h, include/bmoe_adamw.h,
-// include/bmoe_trace.h, include/bmoe_grad.h, include/bmoe_norm.h,
+// include/bmoe_block.h, include/bmoe_trace.h, include/bmoe_grad.h, include/bmoe_norm.h,
 // include/bmoe_train.h, include/bmoe_update.h and (built with -DBMOE_DEBUG_EXPORTS only)
 // include/bmoe_debug.h: argument validation (all before any enqueue),
 // workspace planning, and the launch sequence of the forward pass on the
@@ -16,6 +16,7 @@
 
 #include "bmoe.h"
 #include "bmoe_adamw.h"
+#include "bmoe_block.h"
 #include "bmoe_debug.h"
 #include "bmoe_grad.h"
 #include "bmoe_norm.h"
@@ -1856,6 +1857,138 @@ bmoe_status bmoe_adamw_moments(const bmoe_adamw_tensor* tensors, int32_t count, 
   return ok();
 } catch (...) {
   return fail(BMOE_ERR_HIP, "out of host memory");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- norms around a block
+namespace {
+
+bmoe_status check_block_norm(const bmoe_block_norm* n) {
+  if (!n) return fail(BMOE_ERR_NULL, "the description is NULL");
+  const bmoe_status st = check_norm_shape(n->rows, n->width);
+  if (st != BMOE_OK) return st;
+  if (n->dtype != BMOE_F32 && n->dtype != BMOE_BF16) return fail(BMOE_ERR_DTYPE, "dtype=%d is unknown", n->dtype);
+  if (n->kind != BMOE_NORM_LAYER && n->kind != BMOE_NORM_RMS) return fail(BMOE_ERR_DTYPE, "kind=%d is unknown", n->kind);
+  if (n->gate_kind < BMOE_GATE_NONE || n->gate_kind > BMOE_GATE_ROWS) return fail(BMOE_ERR_DTYPE, "gate_kind=%d is unknown", n->gate_kind);
+  if (n->post != 0 && n->post != 1) return fail(BMOE_ERR_SHAPE, "post=%d must be 0 or 1", n->post);
+  if (!(n->eps >= 0.f) || std::isinf(n->eps)) return fail(BMOE_ERR_SHAPE, "eps=%g must be finite and not negative", double(n->eps));
+  if (!std::isfinite(n->alpha) || !std::isfinite(n->scale))
+    return fail(BMOE_ERR_SHAPE, "alpha=%g and scale=%g must be finite", double(n->alpha), double(n->scale));
+  if (n->reserved != 0) return fail(BMOE_ERR_SHAPE, "reserved field must be 0");
+  if (!n->post && (n->gamma_post || n->beta_post)) return fail(BMOE_ERR_SHAPE, "gamma_post and beta_post need post 1");
+  if (n->kind == BMOE_NORM_RMS && (n->beta || n->beta_post)) return fail(BMOE_ERR_SHAPE, "an RMS norm has no beta");
+  if (n->gate_kind == BMOE_GATE_NONE && n->gate) return fail(BMOE_ERR_SHAPE, "gate needs a gate_kind");
+  if (n->gate_kind != BMOE_GATE_NONE && !n->gate && (n->rows > 0 || n->gate_kind == BMOE_GATE_CHANNEL))
+    return fail(BMOE_ERR_NULL, "gate is NULL");
+  if (!aligned(n->gate, n->gate_kind == BMOE_GATE_ROWS ? act_size(n->dtype) : 4))
+    return fail(BMOE_ERR_ALIGN, "gate must be aligned to its element size");
+  if (!aligned(n->gamma_post, 4) || !aligned(n->beta_post, 4) || !aligned(n->gamma, 4) || !aligned(n->beta, 4))
+    return fail(BMOE_ERR_ALIGN, "gamma_post, beta_post, gamma and beta must be 4-byte aligned");
+  return BMOE_OK;
+}
+
+// What both directions read beside their rows.
+struct BlockWeights {
+  Range gate, gp, bp, ga, be;
+  explicit BlockWeights(const bmoe_block_norm* n) {
+    const size_t wb = size_t(n->width) * 4;
+    gate = {n->gate, n->gate_kind == BMOE_GATE_ROWS ? size_t(n->rows) * n->width * act_size(n->dtype) : wb};
+    gp = {n->gamma_post, wb};
+    bp = {n->beta_post, wb};
+    ga = {n->gamma, wb};
+    be = {n->beta, wb};
+  }
+  bool hit(Range r) const { return overlaps_any(r, {gate, gp, bp, ga, be}); }
+};
+
+}  // namespace
+
+extern "C" {
+
+bmoe_status bmoe_block_norm_forward(const bmoe_block_norm* n, const void* b, const void* r, void* s, void* y,
+                                    float* stats, hipStream_t stream) {
+  bmoe_status st = check_block_norm(n);
+  if (st != BMOE_OK) return st;
+  if (n->rows == 0) return ok();
+  if (!b || !s || !y) return fail(BMOE_ERR_NULL, "b / s / y is NULL");
+  const size_t es = act_size(n->dtype), nb = size_t(n->rows) * n->width * es;
+  if (!aligned(b, es) || !aligned(r, es) || !aligned(s, es) || !aligned(y, es))
+    return fail(BMOE_ERR_ALIGN, "b, r, s and y must be aligned to their element size");
+  if (!aligned(stats, 16)) return fail(BMOE_ERR_ALIGN, "stats must be 16-byte aligned");
+  const Range rb{b, nb}, rr{r, nb}, rs{s, nb}, ry{y, nb}, rst{stats, size_t(n->rows) * 16};
+  const BlockWeights w(n);
+  if (overlaps_any(ry, {rb, rr}, true) || overlaps_any(ry, {rs, rst}) || w.hit(ry))
+    return fail(BMOE_ERR_ALIAS, "y overlaps another array (it may be b or r itself)");
+  if (overlaps_any(rs, {rb, rr}, true) || overlaps_any(rs, {rst}) || w.hit(rs))
+    return fail(BMOE_ERR_ALIAS, "s overlaps another array (it may be b or r itself)");
+  if (overlaps_any(rst, {rb, rr}) || w.hit(rst)) return fail(BMOE_ERR_ALIAS, "stats overlaps another array");
+  st = check_device();
+  if (st != BMOE_OK) return st;
+  const BnFwdArgs a{b, r, n->gate, n->gamma_post, n->beta_post, n->gamma, n->beta, s, y, reinterpret_cast<float4*>(stats),
+                    n->alpha, n->scale, n->eps, n->rows, n->width, n->kind == BMOE_NORM_LAYER, n->post, n->gate_kind};
+  BMOE_HIP(launch_block_norm_fwd(a, n->dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, stream));
+  return ok();
+}
+
+bmoe_status bmoe_block_norm_backward_workspace(const bmoe_block_norm* n, size_t* bytes) {
+  if (!bytes) return fail(BMOE_ERR_NULL, "bytes is NULL");
+  if (!n) return fail(BMOE_ERR_NULL, "the description is NULL");
+  const bmoe_status st = check_norm_shape(n->rows, n->width);
+  if (st != BMOE_OK) return st;
+  *bytes = bn_bwd_workspace(n->rows, n->width);
+  return ok();
+}
+
+bmoe_status bmoe_block_norm_backward(const bmoe_block_norm* n, int32_t dy_dtype, const void* dy, const void* b,
+                                     const void* s, const float* stats, const void* d_sum, void* db, void* dr,
+                                     const bmoe_block_norm_grads* grads, void* workspace, size_t workspace_bytes,
+                                     hipStream_t stream) {
+  bmoe_status st = check_block_norm(n);
+  if (st != BMOE_OK) return st;
+  if (dy_dtype != BMOE_F32 && dy_dtype != n->dtype) return fail(BMOE_ERR_DTYPE, "dy_dtype=%d must be fp32 or dtype", dy_dtype);
+  const bmoe_block_norm_grads none{};
+  const bmoe_block_norm_grads& g = grads ? *grads : none;
+  const bool row_gate = n->gate_kind == BMOE_GATE_ROWS;
+  if ((g.beta || g.beta_post) && n->kind == BMOE_NORM_RMS) return fail(BMOE_ERR_SHAPE, "an RMS norm has no beta");
+  if ((g.gamma_post || g.beta_post) && !n->post) return fail(BMOE_ERR_SHAPE, "gradients of gamma_post and beta_post need post 1");
+  if (g.gate && n->gate_kind == BMOE_GATE_NONE) return fail(BMOE_ERR_SHAPE, "the gradient of a gate needs one");
+  const bool sums = g.gamma_post || g.beta_post || g.gamma || g.beta || (g.gate && !row_gate);
+  if (n->rows == 0 && !sums) return ok();
+  if (n->rows > 0 && (!dy || !b || !s || !stats || !db)) return fail(BMOE_ERR_NULL, "dy / b / s / stats / db is NULL");
+  const size_t need = sums ? bn_bwd_workspace(n->rows, n->width) : 0;
+  if (need > 0 && !workspace) return fail(BMOE_ERR_NULL, "workspace is NULL");
+  const size_t es = act_size(n->dtype), ds = act_size(dy_dtype), count = size_t(n->rows) * n->width, nb = count * es, wb = size_t(n->width) * 4;
+  if (n->rows > 0 && (!aligned(dy, ds) || !aligned(b, es) || !aligned(s, es) || !aligned(d_sum, es) || !aligned(db, es) || !aligned(dr, es)))
+    return fail(BMOE_ERR_ALIGN, "dy, b, s, d_sum, db and dr must be aligned to their element size");
+  if (n->rows > 0 && !aligned(stats, 16)) return fail(BMOE_ERR_ALIGN, "stats must be 16-byte aligned");
+  if (!aligned(g.gamma_post, 4) || !aligned(g.beta_post, 4) || !aligned(g.gamma, 4) || !aligned(g.beta, 4) || !aligned(g.gate, row_gate ? es : 4))
+    return fail(BMOE_ERR_ALIGN, "the weights' gradients must be aligned to their element size");
+  if (need > 0 && !aligned(workspace, 16)) return fail(BMOE_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (workspace_bytes < need) return fail(BMOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  const Range rdy{dy, count * ds}, rb{b, nb}, rs{s, nb}, rst{stats, size_t(n->rows) * 16}, rd{d_sum, nb}, rdb{db, nb}, rdr{dr, nb},
+      rws{workspace, need};
+  const BlockWeights w(n);
+  const Range out[] = {{g.gamma_post, wb}, {g.beta_post, wb}, {g.gate, row_gate ? nb : wb}, {g.gamma, wb}, {g.beta, wb}};
+  for (const Range& x : {rdb, rdr})
+    if (overlaps_any(x, {rb, rs, rd}, true) || overlaps_any(x, {rdy}, ds == es) || overlaps_any(x, {rst, rws}) || w.hit(x) ||
+        overlaps_any(x, {out[0], out[1], out[2], out[3], out[4]}))
+      return fail(BMOE_ERR_ALIAS, "db / dr overlaps another array (it may be b, s, d_sum or a dy of its dtype itself)");
+  if (overlap(rdb, rdr)) return fail(BMOE_ERR_ALIAS, "db overlaps dr");
+  for (int i = 0; i < 5; ++i) {
+    if (overlaps_any(out[i], {rdy, rb, rs, rst, rd, rws}) || w.hit(out[i])) return fail(BMOE_ERR_ALIAS, "a weight's gradient overlaps another array");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return fail(BMOE_ERR_ALIAS, "two weights' gradients overlap");
+  }
+  if (overlaps_any(rws, {rdy, rb, rs, rst, rd}) || w.hit(rws)) return fail(BMOE_ERR_ALIAS, "the workspace overlaps an input");
+  st = check_device();
+  if (st != BMOE_OK) return st;
+  const BnBwdArgs a{dy, b, s, reinterpret_cast<const float4*>(stats), d_sum, n->gate, n->gamma_post, n->beta_post, n->gamma, db, dr,
+                    row_gate ? g.gate : nullptr, g.gamma_post, g.beta_post, row_gate ? nullptr : static_cast<float*>(g.gate), g.gamma, g.beta,
+                    sums ? static_cast<float*>(workspace) : nullptr, n->alpha, n->scale, n->rows, n->width, n->kind == BMOE_NORM_LAYER,
+                    n->post, n->gate_kind};
+  BMOE_HIP(launch_block_norm_bwd(a, n->dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, dy_dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, stream));
+  return ok();
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
 // Launchers of the training-step operators (include/bmoe_norm.h,
-// include/bmoe_update.h, include/bmoe_adamw.h).
+// include/bmoe_update.h, include/bmoe_adamw.h, include/bmoe_block.h).
 #pragma once
 
 #include "common.hpp"
@@ -95,5 +95,47 @@ struct AwScalars {
 hipError_t launch_adamw(const AwTensor* tensors, int count, const AwScalars& s, int64_t* count_up, hipStream_t stream);
 // codes' values: of m to p and of v to copy (arrays of the given type, null: not wanted)
 hipError_t launch_adamw_values(const AwTensor* tensors, int count, bool bf16, hipStream_t stream);
+
+// Norms around a block (block_norm.hip).
+enum BnGate { BN_GATE_NONE = 0, BN_GATE_CHANNEL = 1, BN_GATE_ROWS = 2 };
+struct BnFwdArgs {
+  const void* b;            // [rows][width]
+  const void* r;            // [rows][width] or null
+  const void* gate;         // [width] fp32, [rows][width] or null
+  const float* gamma_post;  // [width] or null, as the next three
+  const float* beta_post;
+  const float* gamma;
+  const float* beta;
+  void* s;                  // [rows][width]
+  void* y;                  // [rows][width]
+  float4* stats;            // [rows] or null
+  float alpha, scale, eps;
+  int32_t rows, width, layer, post, gate_kind;
+};
+struct BnBwdArgs {
+  const void* dy;           // [rows][width], its own dtype
+  const void* b;            // [rows][width]
+  const void* s;            // [rows][width]
+  const float4* stats;      // [rows]
+  const void* d_sum;        // [rows][width] or null
+  const void* gate;         // as in the forward
+  const float* gamma_post;
+  const float* beta_post;
+  const float* gamma;
+  void* db;                 // [rows][width]
+  void* dr;                 // [rows][width] or null
+  void* d_gate;             // [rows][width] with a gate of rows, or null
+  float* d_gamma_post;      // [width] or null, as the next four
+  float* d_beta_post;
+  float* d_gate_channel;
+  float* d_gamma;
+  float* d_beta;
+  float* part;              // the workspace, null without any of those five
+  float alpha, scale;
+  int32_t rows, width, layer, post, gate_kind;
+};
+size_t bn_bwd_workspace(int rows, int width);
+hipError_t launch_block_norm_fwd(const BnFwdArgs& a, int act, hipStream_t s);
+hipError_t launch_block_norm_bwd(const BnBwdArgs& a, int act, int dact, hipStream_t s);
 
 }  // namespace bmoe

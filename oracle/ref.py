@@ -664,3 +664,45 @@ def adamw_values(codes, exps, top: int):
     c = codes.astype(np.int64)
     k = np.maximum((c >> 3) - 1, 0)
     return np.ldexp((c - 8 * k).astype(np.float64), k + e - 3)
+
+
+# ---------------------------------------------------------------- norms around a block
+def row_norm(a, kind: str, eps: float):
+    """(normed rows, mean, 1 / deviation); a mean of 0 for "rms"."""
+    mean = a.mean(axis=1) if kind == "layer" else np.zeros(len(a))
+    c = a - mean[:, None]
+    rstd = 1.0 / np.sqrt((c * c).mean(axis=1) + eps)
+    return c * rstd[:, None], mean, rstd
+
+
+def block_norm(b, r, gate, alpha, scale, post, kind, gp, bp, eps):
+    """(s before it is stored, mean, 1 / deviation) of the norm behind a block, gate and
+    residual; y is row_norm of the stored s with gamma and beta."""
+    z, mean, rstd = (row_norm(b, kind, eps) if post else (b, np.zeros(len(b)), np.zeros(len(b))))
+    if post:
+        z = z * (1.0 if gp is None else gp) + (0.0 if bp is None else bp)
+    s = scale * (z if gate is None else z * gate)
+    return (s if r is None else s + alpha * r), mean, rstd
+
+
+def row_norm_backward(v, xhat, rstd, kind: str):
+    c = v.mean(axis=1, keepdims=True) if kind == "layer" else 0.0
+    return rstd[:, None] * (v - c - xhat * (v * xhat).mean(axis=1, keepdims=True))
+
+
+def block_norm_backward(dy, b, s, stats, gate, alpha, scale, post, kind, gp, bp, ga, d_sum=None):
+    """Gradients of sum(dy y) + sum(d_sum s) at the given stats, in b, r, gate (its shape), gp,
+    bp, ga and be, and that in s, as a dict."""
+    one = lambda x: 1.0 if x is None else x  # noqa: E731
+    shat = (s - stats[:, 2:3]) * stats[:, 3:4]
+    ds = row_norm_backward(dy * one(ga), shat, stats[:, 3], kind) + (0.0 if d_sum is None else d_sum)
+    out = {"s": ds, "residual": alpha * ds, "gamma": (dy * shat).sum(axis=0), "beta": dy.sum(axis=0)}
+    bhat = (b - stats[:, 0:1]) * stats[:, 1:2] if post else b
+    z = bhat * one(gp) + (0.0 if bp is None else bp) if post else b
+    dz = scale * ds
+    if gate is not None:
+        out["gate"] = (dz * z).sum(axis=0) if gate.ndim == 1 else dz * z
+        dz = dz * gate
+    out["gamma_post"], out["beta_post"] = (dz * bhat).sum(axis=0), dz.sum(axis=0)
+    out["b"] = row_norm_backward(dz * one(gp), bhat, stats[:, 1], kind) if post else dz
+    return out

@@ -1,4 +1,4 @@
-"""Argument errors of the operators around a layer (include/bmoe_adamw.h): each is
+"""Argument errors of the operators around a layer (include/bmoe_adamw.h, bmoe_block.h): each is
 found on the host before anything is enqueued, so the pointers here are never followed.
 No GPU needed."""
 import ctypes
@@ -120,6 +120,87 @@ def test_adamw_binding_refuses_cpu_tensors():
     for params in ([torch.zeros(4)], [], [None]):
         with pytest.raises(ValueError):
             bm.AdamW(params)
+
+
+NORM = dict(rows=2000, width=64, dtype=0, kind=0, post=1, gate_kind=1, alpha=1.0, scale=1.0, eps=1e-5, reserved=0, gate=ptr(0),
+            gamma_post=ptr(1), beta_post=ptr(2), gamma=ptr(3), beta=ptr(4))
+FWD = dict(b=ptr(5), r=ptr(6), s=ptr(7), y=ptr(8), stats=ptr(9))
+BWD = dict(dy_dtype=0, dy=ptr(5), b=ptr(6), s=ptr(7), stats=ptr(8), d_sum=ptr(9), db=ptr(10), dr=ptr(11), grads=None, ws=ptr(12), ws_bytes=1 << 40)
+GRADS = dict(gamma_post=ptr(13), beta_post=ptr(14), gate=ptr(15), gamma=ptr(16), beta=ptr(17))
+
+
+def block_forward(norm={}, **change):
+    n = blocks._BlockNorm(**dict(NORM, **norm))
+    return bm.lib().bmoe_block_norm_forward(ctypes.byref(n), *dict(FWD, **change).values(), None)
+
+
+def block_backward(norm={}, grads={}, **change):
+    n = blocks._BlockNorm(**dict(NORM, beta=None, **norm) if "beta" not in norm else dict(NORM, **norm))
+    g = blocks._BlockNormGrads(**dict(GRADS, **grads))
+    args = dict(BWD, grads=ctypes.addressof(g))
+    args.update(change)
+    return bm.lib().bmoe_block_norm_backward(ctypes.byref(n), *args.values(), None)
+
+
+BLOCK_NORM_REFUSED = [
+    (dict(rows=-1), SHAPE), (dict(rows=(1 << 24) + 1), SHAPE), (dict(width=0), SHAPE), (dict(width=16385), SHAPE), (dict(post=2), SHAPE),
+    (dict(eps=-1.0), SHAPE), (dict(eps=float("nan")), SHAPE), (dict(alpha=float("inf")), SHAPE), (dict(scale=float("nan")), SHAPE),
+    (dict(reserved=1), SHAPE), (dict(post=0), SHAPE), (dict(post=0, gamma_post=None), SHAPE), (dict(kind=1), SHAPE), (dict(gate_kind=0), SHAPE),
+    (dict(dtype=2), DTYPE), (dict(kind=2), DTYPE), (dict(gate_kind=3), DTYPE), (dict(gate_kind=-1), DTYPE), (dict(gate=None), NULL),
+    (dict(gate=ptr(0) + 2), ALIGN), (dict(gate=ptr(0) + 1, gate_kind=2, dtype=1), ALIGN), (dict(gamma=ptr(3) + 2), ALIGN),
+    (dict(beta_post=ptr(2) + 1), ALIGN),
+]
+
+
+@pytest.mark.parametrize("change,status", BLOCK_NORM_REFUSED, ids=lambda v: str(v)[:60])
+def test_block_norm_description_refusals(change, status):
+    assert block_forward(change) == status
+    assert block_backward(change) == status
+    assert bm.lib().bmoe_last_error() != b""
+
+
+BLOCK_FORWARD_REFUSED = [
+    (dict(b=None), NULL), (dict(s=None), NULL), (dict(y=None), NULL), (dict(b=ptr(5) + 2), ALIGN), (dict(r=ptr(6) + 1), ALIGN), (dict(stats=ptr(9) + 8), ALIGN),
+    (dict(y=ptr(7)), ALIAS), (dict(y=ptr(5) + 4), ALIAS), (dict(s=ptr(6) - 4), ALIAS), (dict(s=ptr(3)), ALIAS), (dict(y=ptr(0)), ALIAS),
+    (dict(stats=ptr(5)), ALIAS), (dict(stats=ptr(7) + 16), ALIAS), (dict(stats=ptr(1)), ALIAS), (dict(y=ptr(9) + 16), ALIAS),
+]
+
+
+@pytest.mark.parametrize("change,status", BLOCK_FORWARD_REFUSED, ids=lambda v: str(v)[:60])
+def test_block_norm_forward_refusals(change, status):
+    assert block_forward(**change) == status
+
+
+BLOCK_BACKWARD_REFUSED = [
+    ({}, {}, dict(dy_dtype=1), DTYPE), ({}, {}, dict(dy_dtype=2), DTYPE), ({}, {}, dict(dy=None), NULL), ({}, {}, dict(b=None), NULL),
+    ({}, {}, dict(s=None), NULL), ({}, {}, dict(stats=None), NULL), ({}, {}, dict(db=None), NULL), ({}, {}, dict(ws=None), NULL),
+    ({}, {}, dict(ws_bytes=100), WORKSPACE), ({}, {}, dict(ws=ptr(12) + 8), ALIGN), ({}, {}, dict(stats=ptr(8) + 4), ALIGN),
+    ({}, {}, dict(dr=ptr(11) + 2), ALIGN), ({}, dict(gamma=ptr(16) + 2), {}, ALIGN),
+    (dict(kind=1, beta_post=None), {}, {}, SHAPE), (dict(post=0, gamma_post=None, beta_post=None), {}, {}, SHAPE),
+    (dict(gate_kind=0, gate=None), {}, {}, SHAPE),
+    ({}, {}, dict(db=ptr(6) + 4), ALIAS), ({}, {}, dict(db=ptr(11)), ALIAS), ({}, {}, dict(dr=ptr(8)), ALIAS), ({}, {}, dict(dr=ptr(12)), ALIAS),
+    ({}, {}, dict(db=ptr(0)), ALIAS), ({}, dict(gamma=ptr(5)), {}, ALIAS), ({}, dict(beta=ptr(16)), {}, ALIAS), ({}, dict(gate=ptr(0)), {}, ALIAS),
+    ({}, dict(gate=ptr(10)), {}, ALIAS), ({}, {}, dict(ws=ptr(9)), ALIAS), ({}, {}, dict(ws=ptr(3) - 16), ALIAS), (dict(dtype=1), {}, dict(db=ptr(5)), ALIAS),
+]
+
+
+@pytest.mark.parametrize("norm,grads,change,status", BLOCK_BACKWARD_REFUSED, ids=lambda v: str(v)[:60])
+def test_block_norm_backward_refusals(norm, grads, change, status):
+    assert block_backward(norm, grads, **change) == status
+
+
+def test_block_norm_nothing_to_do_and_sizes():
+    n = ctypes.c_size_t(77)
+    none = dict.fromkeys(GRADS)
+    assert block_forward(dict(rows=0), b=None, s=None, y=None) == 0
+    assert block_backward(dict(rows=0), none, dy=None, b=None, s=None, stats=None, db=None, dr=None, ws=None, ws_bytes=0) == 0
+    for rows, width, status in ((-1, 64, SHAPE), (4, 0, SHAPE), (1 << 24, 16384, 0), (0, 64, 0)):
+        d = blocks._BlockNorm(**dict(NORM, rows=rows, width=width))
+        assert bm.lib().bmoe_block_norm_backward_workspace(ctypes.byref(d), ctypes.byref(n)) == status
+    assert n.value == 0   # of no rows
+    assert bm.lib().bmoe_block_norm_backward_workspace(None, ctypes.byref(n)) == NULL
+    assert bm.lib().bmoe_block_norm_backward_workspace(ctypes.byref(d), None) == NULL
+    assert ctypes.sizeof(blocks._BlockNorm) == 10 * 4 + 5 * 8 and ctypes.sizeof(blocks._BlockNormGrads) == 5 * 8
 
 
 def test_refusals_under_host_sanitizers():

@@ -46,3 +46,36 @@ def test_adamw_random_is_uniform():
         assert abs(f.mean() - 0.5) < 5 * np.sqrt(1 / 12 / n) and abs(f.var() - 1 / 12) < 5 * np.sqrt(1 / 180 / n)
         for h in flat[:k] + [np.roll(f, 1)]:
             assert abs(np.corrcoef(f, h)[0, 1]) < 5 / np.sqrt(n)
+
+
+def test_block_norm_backward_matches_differences():
+    r = np.random.default_rng(4)
+    n, w, eps = 4, 6, 1e-3
+    for kind in ("layer", "rms"):
+        for post in (True, False):
+            for gates in (None, r.standard_normal(w), r.standard_normal((n, w))):
+                x = {"b": r.standard_normal((n, w)) + 1, "residual": r.standard_normal((n, w)), "gate": gates}
+                x["gamma_post"], x["beta_post"] = (r.standard_normal(w), r.standard_normal(w) if kind == "layer" else None) if post else (None, None)
+                x["gamma"], x["beta"] = r.standard_normal(w), r.standard_normal(w) if kind == "layer" else None
+                dy, dsum = r.standard_normal((n, w)), r.standard_normal((n, w))
+
+                def forward(x):
+                    s, m1, r1 = ref.block_norm(x["b"], x["residual"], x["gate"], 0.7, 1.3, post, kind, x["gamma_post"], x["beta_post"], eps)
+                    y, m2, r2 = ref.row_norm(s, kind, eps)
+                    y = y * x["gamma"] + (0 if x["beta"] is None else x["beta"])
+                    return s, y, np.stack([m1, r1, m2, r2], 1)
+
+                def loss(x):
+                    s, y, _ = forward(x)
+                    return (dy * y).sum() + (dsum * s).sum()
+
+                s, _, stats = forward(x)
+                got = ref.block_norm_backward(dy, x["b"], s, stats, gates, 0.7, 1.3, post, kind, x["gamma_post"], x["beta_post"], x["gamma"], dsum)
+                for name, a in x.items():
+                    if a is None:
+                        continue
+                    for i in np.ndindex(a.shape):
+                        up, dn = dict(x, **{name: a.copy()}), dict(x, **{name: a.copy()})
+                        up[name][i] += 1e-5
+                        dn[name][i] -= 1e-5
+                        assert abs((loss(up) - loss(dn)) / 2e-5 - got[name][i]) < 1e-6, (kind, post, name)
