@@ -68,7 +68,10 @@ __global__ __launch_bounds__(ln_threads(TPR), TPR > 512 ? 4 : ln_fwd_waves(ln_el
         if (g < groups) ln_store<ACT, CUT>(a.sum, at + size_t(g) * E, a.width - E * g, x[v]);
       }
     }
-    const LnStats st = ln_centre<CUT, TPR>(x, a.width, t, a.eps, red, turn);
+    const LnStats st = ln_centre<TPR>(x, a.width, a.eps, red, turn, [&](int v, int j) {
+      const int in = a.width - E * (t + TPR * v);
+      return CUT == LN_ANY ? j < in : in > 0;
+    });
     const float rstd = st.rstd, d = st.off;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {

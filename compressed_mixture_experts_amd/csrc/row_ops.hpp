@@ -10,15 +10,32 @@
 
 namespace bmoe {
 
-// Sum over a wave's 64 lanes, the same value in every lane (fixed order).
+// Sum over the LANES lanes of a wave that share a row, the same value in each of them
+// (the tree of exchanges with the lanes 1, 2, 4, .. away, within the register file).
+template <int CTRL>
+__device__ __forceinline__ float ln_dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int LANES>
 __device__ __forceinline__ float ln_wave_sum(float v) {
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+  static_assert(LANES == 16 || LANES == 32 || LANES == 64, "rows of lanes");
+  v = ln_dpp_add<0xB1>(v);    // quad_perm 1 0 3 2
+  v = ln_dpp_add<0x4E>(v);    // quad_perm 2 3 0 1
+  v = ln_dpp_add<0x141>(v);   // row_half_mirror: the other four of eight
+  v = ln_dpp_add<0x140>(v);   // row_mirror: the other eight of sixteen
+  if constexpr (LANES >= 32) {
+    const auto u = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(u[0]) + __uint_as_float(u[1]);
+  }
+  if constexpr (LANES == 64) {
+    const auto u = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(u[0]) + __uint_as_float(u[1]);
+  }
   return v;
 }
 
 // Sums of N values over the TPR threads of a row, the same in each of them: over
-// each wave, then every wave adds the waves' sums.  Two sets of those in turn, so one
+// each wave, then every wave adds the waves' sums (TPR a power of two).  Two sets of those in turn, so one
 // barrier a sum is enough: who writes a set again is past the barrier of the sum
 // between, which every wave reaches only after its reads of the set.
 template <int TPR>
@@ -28,12 +45,12 @@ struct LnRed {
 template <int TPR, int N>
 __device__ __forceinline__ void ln_row_sum(float (&v)[N], LnRed<TPR>& red, int& turn) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = ln_wave_sum(v[k]);
+  for (int k = 0; k < N; ++k) v[k] = ln_wave_sum<(TPR < 64 ? TPR : 64)>(v[k]);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
     float2* r = red.sums[turn];
     turn ^= 1;
-    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = make_float2(v[0], v[N - 1]);
+    if ((threadIdx.x & 63) == 0) r[threadIdx.x % TPR / 64] = make_float2(v[0], v[N - 1]);
     __syncthreads();
     const float2 u = r[threadIdx.x % W];
     v[0] = u.x;
@@ -146,8 +163,9 @@ __device__ __forceinline__ void ln_round(float* v) {
 struct LnStats {
   float mean, off, rstd, unit;
 };
-template <int CUT, int TPR, int NV, int E>
-__device__ __forceinline__ LnStats ln_centre(float (&x)[NV][E], int width, int t, float eps, LnRed<TPR>& red, int& turn) {
+// on(v, j): whether x[v][j] is the row's; what is not is 0 and stays it.
+template <int TPR, int NV, int E, typename On>
+__device__ __forceinline__ LnStats ln_centre(float (&x)[NV][E], int width, float eps, LnRed<TPR>& red, int& turn, On&& on) {
 #pragma clang fp contract(off)  // what a row is centred by is the mean as rounded
   const float inv = 1.0f / float(width);
   float s[1] = {0.f};  // in parts of the mean, which no finite row's sum of leaves fp32
@@ -162,15 +180,13 @@ __device__ __forceinline__ LnStats ln_centre(float (&x)[NV][E], int width, int t
     constexpr bool W = decltype(whole)::value;
     float q[W ? 2 : 1] = {};
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int in = width - E * (t + TPR * v);  // past the row everything stays 0
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
       for (int j = 0; j < E; ++j) {
-        x[v][j] -= (CUT == LN_ANY ? j < in : in > 0) ? by : 0.f;
+        x[v][j] -= on(v, j) ? by : 0.f;
         if constexpr (W) q[1] = fmaf(x[v][j], inv, q[1]);
         q[0] = fmaf(x[v][j], x[v][j], q[0]);
       }
-    }
     ln_row_sum<TPR>(q, red, turn);
     var = q[0] * inv;
     if constexpr (W) d = q[1];
