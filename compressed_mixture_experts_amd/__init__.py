@@ -2,7 +2,8 @@
 
 The computation runs in ``libbmoe.so`` (hand-written HIP kernels behind the C
 ABI of ``include/bmoe.h``, ``bmoe_trace.h``, ``bmoe_grad.h``, ``bmoe_train.h``,
-``bmoe_norm.h``, ``bmoe_update.h``, ``bmoe_adamw.h`` and ``bmoe_block.h``).  The test
+``bmoe_norm.h``, ``bmoe_update.h``, ``bmoe_adamw.h``, ``bmoe_block.h`` and
+``bmoe_ffn.h``).  The test
 hooks of ``include/bmoe_debug.h`` live only in ``libbmoe_debug.so`` (the same
 kernels, built with -DBMOE_DEBUG_EXPORTS), loaded on first use of a
 ``dbg_*`` function.  This module only marshals arguments: torch tensors
@@ -30,7 +31,7 @@ __all__ = [
     "dbg_butterfly", "dbg_ternary_gemm", "dbg_ternary_gemm_fp4", "butterfly_backward", "substrate_grad",
     "combine_backward", "router_backward", "gelu_backward", "substrate_input_grad",
     "layer_norm_forward", "layer_norm_backward", "orthogonalize", "substrate_step", "AdamW",
-    "block_norm_forward", "block_norm_backward", "STATUS",
+    "block_norm_forward", "block_norm_backward", "gated_ffn_forward", "gated_ffn_forward_train", "gated_ffn_backward", "STATUS",
     "EXPORTED_SYMBOLS", "DEBUG_SYMBOLS", "debug_lib",
 ]
 
@@ -48,7 +49,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20   # BMOE_NOALLOC_SCRATCH_BYTES of include/bmoe.
 ACT_NONE, ACT_GELU_ERF = 0, 1
 
 # exports of libbmoe.so (include/bmoe.h, bmoe_trace.h, bmoe_grad.h, bmoe_train.h,
-# bmoe_norm.h, bmoe_update.h, bmoe_adamw.h, bmoe_block.h)
+# bmoe_norm.h, bmoe_update.h, bmoe_adamw.h, bmoe_block.h, bmoe_ffn.h)
 EXPORTED_SYMBOLS = [
     "bmoe_packed_words", "bmoe_pack_ternary", "bmoe_workspace_size", "bmoe_prepared_bytes",
     "bmoe_prepare", "bmoe_route", "bmoe_forward", "bmoe_forward_noalloc", "bmoe_status_string",
@@ -64,6 +65,8 @@ EXPORTED_SYMBOLS = [
     "bmoe_substrate_step_workspace", "bmoe_substrate_step",
     "bmoe_adamw_step", "bmoe_adamw_moments",
     "bmoe_block_norm_forward", "bmoe_block_norm_backward_workspace", "bmoe_block_norm_backward",
+    "bmoe_gated_ffn_state_size", "bmoe_gated_ffn_forward_workspace", "bmoe_gated_ffn_forward",
+    "bmoe_gated_ffn_backward_workspace", "bmoe_gated_ffn_backward",
 ]
 # exported by libbmoe_debug.so only (include/bmoe_debug.h)
 DEBUG_SYMBOLS = ["bmoe_dbg_butterfly", "bmoe_dbg_ternary_gemm", "bmoe_dbg_ternary_gemm_fp4"]
@@ -162,6 +165,12 @@ def _load(path: str, debug: bool) -> ctypes.CDLL:
     L.bmoe_block_norm_forward.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]
     L.bmoe_block_norm_backward_workspace.argtypes = [c_vp, ctypes.POINTER(c_sz)]
     L.bmoe_block_norm_backward.argtypes = [c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]
+    L.bmoe_gated_ffn_state_size.argtypes = [c_i32, c_i32, ctypes.POINTER(c_sz)]
+    L.bmoe_gated_ffn_forward_workspace.argtypes = [c_i32, c_i32, c_i32, c_i32, ctypes.POINTER(c_sz)]
+    L.bmoe_gated_ffn_forward.argtypes = [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_sz, c_vp]
+    L.bmoe_gated_ffn_backward_workspace.argtypes = [c_i32, c_i32, c_i32, ctypes.POINTER(c_sz)]
+    L.bmoe_gated_ffn_backward.argtypes = [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                          c_sz, c_vp]
     ret = [n for n in EXPORTED_SYMBOLS if n not in ("bmoe_packed_words", "bmoe_prepared_bytes",
                                                     "bmoe_status_string", "bmoe_last_error")]
     if debug:
@@ -632,10 +641,10 @@ def _raw_stream(t) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_bytes(name: str, a: int, b: int) -> int:
-    """What the library's size query `name` says for (a, b): sizes alone decide."""
+def _workspace_bytes(name: str, *sizes: int) -> int:
+    """What the library's size query `name` says for the sizes: they alone decide."""
     n = ctypes.c_size_t(0)
-    _check(getattr(lib(), name)(a, b, ctypes.byref(n)))
+    _check(getattr(lib(), name)(*sizes, ctypes.byref(n)))
     return int(n.value)
 
 
@@ -794,4 +803,5 @@ def dbg_ternary_gemm_fp4(a, w_packed, n_out: int, alpha: float = 1.0):
     return z
 
 
-from .blocks import AdamW, block_norm_backward, block_norm_forward  # noqa: E402
+from .blocks import (AdamW, block_norm_backward, block_norm_forward, gated_ffn_backward,  # noqa: E402
+                     gated_ffn_forward, gated_ffn_forward_train)

@@ -1,5 +1,5 @@
-"""Operators around an expert layer (include/bmoe_adamw.h, bmoe_block.h): argument
-marshalling only, as in the package's other calls."""
+"""Operators around an expert layer (include/bmoe_adamw.h, bmoe_block.h,
+bmoe_ffn.h): argument marshalling only, as in the package's other calls."""
 from __future__ import annotations
 
 import contextlib
@@ -7,7 +7,7 @@ import ctypes
 
 import numpy as np
 
-from . import BF16, F32, _check, _on_device, _operand, _raw_stream, _torch, lib
+from . import BF16, F32, _check, _on_device, _operand, _raw_stream, _torch, _workspace_bytes, lib
 
 # bmoe_adamw_tensor of include/bmoe_adamw.h
 _ADAMW_TENSOR = np.dtype([
@@ -340,3 +340,85 @@ def block_norm_backward(dy, b, s, stats, gate=None, alpha: float = 1.0, scale: f
         None if d_sum is None else d_sum.data_ptr(), out["b"].data_ptr(), None if out["residual"] is None else out["residual"].data_ptr(),
         None if g is None else ctypes.byref(g), None if ws is None else ws.data_ptr(), nbytes, _raw_stream(dy)))
     return out
+
+
+_GATED_ACTS = {"silu": 0, "gelu": 1}
+
+
+def _ffn(x, w_in, w_down, act):
+    """Check what all three calls have: (tokens, d, ff, act's number, bf16)."""
+    torch = _torch()
+    bf16, dev = (torch.bfloat16,), x.device
+    tokens, d = x.shape
+    _operand("x", x, x.shape, bf16, dev)
+    if w_down.dim() != 2:
+        raise ValueError(f"w_down has shape {tuple(w_down.shape)}, expected two dimensions")
+    ff = w_down.shape[1]
+    _operand("w_down", w_down, (d, ff), bf16, dev)
+    _operand("w_in", w_in, (2 * ff, d), bf16, dev)
+    if act not in _GATED_ACTS:
+        raise ValueError(f"act is {act!r}, expected 'silu' or 'gelu'")
+    return tokens, d, ff, _GATED_ACTS[act], bf16
+
+
+def _ffn_forward(x, w_in, w_down, act, add, y, train):
+    torch = _torch()
+    tokens, d, ff, kind, bf16 = _ffn(x, w_in, w_down, act)
+    dev = x.device
+    if add is not None:
+        _operand("add", add, x.shape, bf16, dev)
+    y = torch.empty_like(x) if y is None else _operand("y", y, x.shape, bf16, dev)
+    state = torch.empty(7 * tokens * ff, dtype=torch.uint8, device=dev) if train else None
+    nbytes = _workspace_bytes("bmoe_gated_ffn_forward_workspace", tokens, d, ff, 1 if train else 0)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    _check(lib().bmoe_gated_ffn_forward(tokens, d, ff, kind, x.data_ptr(), w_in.data_ptr(), w_down.data_ptr(),
+                                        None if add is None else add.data_ptr(), y.data_ptr(), None if state is None else state.data_ptr(),
+                                        7 * tokens * ff, None if ws is None else ws.data_ptr(), nbytes, _raw_stream(x)))
+    return y, state
+
+
+@_on_device
+def gated_ffn_forward(x, w_in, w_down, act: str = "silu", add=None, y=None):
+    """Dense gated feed-forward block on the rows of x [tokens][d]: with Wg the first and Wu
+    the second half of w_in [2 ff][d],
+        y = (act(x Wg^T) * (x Wu^T)) w_down^T (+ add)
+    for act "silu" or "gelu" (exact).  Everything bf16, d and ff multiples of 8; w_down [d][ff].
+    add [tokens][d] is added before the one rounding (a ButterflyMoE layer's output, to
+    which this is the shared expert); y may be add itself."""
+    return _ffn_forward(x, w_in, w_down, act, add, y, False)[0]
+
+
+@_on_device
+def gated_ffn_forward_train(x, w_in, w_down, act: str = "silu", add=None, y=None):
+    """gated_ffn_forward and the state that gated_ffn_backward reads (an opaque device
+    buffer, 7 bytes for each token and hidden unit).  Returns (y, state)."""
+    return _ffn_forward(x, w_in, w_down, act, add, y, True)
+
+
+@_on_device
+def gated_ffn_backward(x, w_in, w_down, dy, state, act: str = "silu", dx_add=None, input_grad: bool = True, weight_grads: bool = True,
+                       dx=None, dw_in=None, dw_down=None):
+    """Gradients of sum(dy * y) at the state of gated_ffn_forward_train: (dx [tokens][d],
+    dw_in, dw_down like the weights), bf16, None for those not wanted.  dx_add [tokens][d]
+    fp32 is added into dx before its rounding (the input gradient of Layer.backward for the
+    same x).  The gradient of the forward's add is dy."""
+    torch = _torch()
+    tokens, d, ff, kind, bf16 = _ffn(x, w_in, w_down, act)
+    dev = x.device
+    _operand("dy", dy, x.shape, bf16, dev)
+    _operand("state", state, (7 * tokens * ff,), (torch.uint8,), dev)
+    if dx_add is not None:
+        _operand("dx_add", dx_add, x.shape, (torch.float32,), dev)
+    if input_grad:
+        dx = torch.empty_like(x) if dx is None else _operand("dx", dx, x.shape, bf16, dev)
+    if weight_grads:
+        dw_in = torch.empty_like(w_in) if dw_in is None else _operand("dw_in", dw_in, w_in.shape, bf16, dev)
+        dw_down = torch.empty_like(w_down) if dw_down is None else _operand("dw_down", dw_down, w_down.shape, bf16, dev)
+    if (not input_grad and dx is not None) or (not weight_grads and (dw_in is not None or dw_down is not None)):
+        raise ValueError("an output is given for a gradient that is not wanted")
+    nbytes = _workspace_bytes("bmoe_gated_ffn_backward_workspace", tokens, d, ff)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    _check(lib().bmoe_gated_ffn_backward(tokens, d, ff, kind, x.data_ptr(), w_in.data_ptr(), w_down.data_ptr(), dy.data_ptr(), state.data_ptr(),
+                                         7 * tokens * ff, at(dx_add), at(dx), at(dw_in), at(dw_down), at(ws), nbytes, _raw_stream(x)))
+    return dx, dw_in, dw_down

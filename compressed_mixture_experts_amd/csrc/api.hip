@@ -1,5 +1,5 @@
 // Host side of the C ABI declared in include/bmoe.h, include/bmoe_adamw.h,
-// include/bmoe_block.h, include/bmoe_trace.h, include/bmoe_grad.h, include/bmoe_norm.h,
+// include/bmoe_block.h, include/bmoe_ffn.h, include/bmoe_trace.h, include/bmoe_grad.h, include/bmoe_norm.h,
 // include/bmoe_train.h, include/bmoe_update.h and (built with -DBMOE_DEBUG_EXPORTS only)
 // include/bmoe_debug.h: argument validation (all before any enqueue),
 // workspace planning, and the launch sequence of the forward pass on the
@@ -18,6 +18,7 @@
 #include "bmoe_adamw.h"
 #include "bmoe_block.h"
 #include "bmoe_debug.h"
+#include "bmoe_ffn.h"
 #include "bmoe_grad.h"
 #include "bmoe_norm.h"
 #include "bmoe_trace.h"
@@ -1988,6 +1989,119 @@ bmoe_status bmoe_block_norm_backward(const bmoe_block_norm* n, int32_t dy_dtype,
                     sums ? static_cast<float*>(workspace) : nullptr, n->alpha, n->scale, n->rows, n->width, n->kind == BMOE_NORM_LAYER,
                     n->post, n->gate_kind};
   BMOE_HIP(launch_block_norm_bwd(a, n->dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, dy_dtype == BMOE_BF16 ? ACT_BF16 : ACT_F32, stream));
+  return ok();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- gated feed-forward block
+namespace {
+
+bmoe_status check_ffn(int32_t tokens, int32_t d, int32_t ff) {
+  if (tokens < 0 || tokens > kMaxTokens) return fail(BMOE_ERR_SHAPE, "tokens=%d must be in [0, %d]", tokens, kMaxTokens);
+  if (d < 8 || d > 16384 || d % 8 != 0 || ff < 8 || ff > 65536 || ff % 8 != 0 || int64_t(d) * ff > int64_t(1) << 29)
+    return fail(BMOE_ERR_SHAPE, "d=%d and ff=%d: need positive multiples of 8, d <= 16384, ff <= 65536, d ff <= 2^29", d, ff);
+  if (int64_t(tokens) * (d > ff ? d : ff) > int64_t(1) << 36)
+    return fail(BMOE_ERR_SHAPE, "tokens=%d of d=%d, ff=%d: more than 2^36 values", tokens, d, ff);
+  return BMOE_OK;
+}
+
+size_t ffn_state(int32_t tokens, int32_t ff) { return size_t(tokens) * ff * 7; }
+
+}  // namespace
+
+extern "C" {
+
+bmoe_status bmoe_gated_ffn_state_size(int32_t tokens, int32_t ff, size_t* bytes) {
+  if (!bytes) return fail(BMOE_ERR_NULL, "bytes is NULL");
+  const bmoe_status st = check_ffn(tokens, 8, ff);
+  if (st != BMOE_OK) return st;
+  *bytes = ffn_state(tokens, ff);
+  return ok();
+}
+
+bmoe_status bmoe_gated_ffn_forward_workspace(int32_t tokens, int32_t d, int32_t ff, int32_t with_state, size_t* bytes) {
+  if (!bytes) return fail(BMOE_ERR_NULL, "bytes is NULL");
+  const bmoe_status st = check_ffn(tokens, d, ff);
+  if (st != BMOE_OK) return st;
+  if (with_state != 0 && with_state != 1) return fail(BMOE_ERR_SHAPE, "with_state=%d must be 0 or 1", with_state);
+  *bytes = gf_forward_workspace(tokens, d, ff, with_state == 1);
+  return ok();
+}
+
+bmoe_status bmoe_gated_ffn_forward(int32_t tokens, int32_t d, int32_t ff, int32_t act, const void* x, const void* w_in,
+                                   const void* w_down, const void* add, void* y, void* state, size_t state_bytes,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  bmoe_status st = check_ffn(tokens, d, ff);
+  if (st != BMOE_OK) return st;
+  if (act != BMOE_GATED_SILU && act != BMOE_GATED_GELU) return fail(BMOE_ERR_DTYPE, "act=%d is unknown", act);
+  if (tokens == 0) return ok();
+  if (!x || !w_in || !w_down || !y) return fail(BMOE_ERR_NULL, "x / w_in / w_down / y is NULL");
+  const size_t need = gf_forward_workspace(tokens, d, ff, state != nullptr);
+  if (need > 0 && !workspace) return fail(BMOE_ERR_NULL, "workspace is NULL");
+  if (!aligned(x, 16) || !aligned(w_in, 16) || !aligned(w_down, 16) || !aligned(add, 16) || !aligned(y, 16) || !aligned(state, 16) ||
+      (need > 0 && !aligned(workspace, 16)))
+    return fail(BMOE_ERR_ALIGN, "every array must be 16-byte aligned");
+  if (state && state_bytes < ffn_state(tokens, ff))
+    return fail(BMOE_ERR_WORKSPACE, "state has %zu bytes, %zu needed", state_bytes, ffn_state(tokens, ff));
+  if (workspace_bytes < need) return fail(BMOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  const size_t nx = size_t(tokens) * d * 2, nw = size_t(d) * ff * 2;
+  const Range rx{x, nx}, ri{w_in, 2 * nw}, rd{w_down, nw}, ra{add, nx}, ry{y, nx}, rs{state, ffn_state(tokens, ff)}, rws{workspace, need};
+  if (overlaps_any(ry, {ra}, true) || overlaps_any(ry, {rx, ri, rd, rs, rws}))
+    return fail(BMOE_ERR_ALIAS, "y overlaps another array (it may be add itself)");
+  if (overlaps_any(rs, {rx, ri, rd, ra, rws}) || overlaps_any(rws, {rx, ri, rd, ra}))
+    return fail(BMOE_ERR_ALIAS, "state or the workspace overlaps another array");
+  st = check_device();
+  if (st != BMOE_OK) return st;
+  auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
+  const GfFwdArgs a{u16(x), u16(w_in), u16(w_down), u16(add), static_cast<uint16_t*>(y), static_cast<uint16_t*>(state), workspace, tokens, d,
+                    ff, act == BMOE_GATED_GELU};
+  BMOE_HIP(launch_gated_ffn_forward(a, stream));
+  return ok();
+}
+
+bmoe_status bmoe_gated_ffn_backward_workspace(int32_t tokens, int32_t d, int32_t ff, size_t* bytes) {
+  if (!bytes) return fail(BMOE_ERR_NULL, "bytes is NULL");
+  const bmoe_status st = check_ffn(tokens, d, ff);
+  if (st != BMOE_OK) return st;
+  *bytes = gf_backward_workspace(tokens, d, ff);
+  return ok();
+}
+
+bmoe_status bmoe_gated_ffn_backward(int32_t tokens, int32_t d, int32_t ff, int32_t act, const void* x, const void* w_in,
+                                    const void* w_down, const void* dy, const void* state, size_t state_bytes,
+                                    const float* dx_add, void* dx, void* dw_in, void* dw_down, void* workspace,
+                                    size_t workspace_bytes, hipStream_t stream) {
+  bmoe_status st = check_ffn(tokens, d, ff);
+  if (st != BMOE_OK) return st;
+  if (act != BMOE_GATED_SILU && act != BMOE_GATED_GELU) return fail(BMOE_ERR_DTYPE, "act=%d is unknown", act);
+  if (!dx && !dw_in && !dw_down) return ok();
+  const size_t need = gf_backward_workspace(tokens, d, ff);
+  if (tokens > 0 && (!x || !w_in || !w_down || !dy || !state || !workspace))
+    return fail(BMOE_ERR_NULL, "x / w_in / w_down / dy / state / workspace is NULL");
+  if (!aligned(dw_in, 16) || !aligned(dw_down, 16) ||
+      (tokens > 0 && (!aligned(x, 16) || !aligned(w_in, 16) || !aligned(w_down, 16) || !aligned(dy, 16) || !aligned(state, 16) ||
+                      !aligned(dx_add, 16) || !aligned(dx, 16) || !aligned(workspace, 16))))
+    return fail(BMOE_ERR_ALIGN, "every array must be 16-byte aligned");
+  if (state_bytes < ffn_state(tokens, ff))
+    return fail(BMOE_ERR_WORKSPACE, "state has %zu bytes, %zu needed", state_bytes, ffn_state(tokens, ff));
+  if (workspace_bytes < need) return fail(BMOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+  const size_t nx = size_t(tokens) * d * 2, nw = size_t(d) * ff * 2;
+  const Range in[] = {{x, nx}, {w_in, 2 * nw}, {w_down, nw}, {dy, nx}, {state, ffn_state(tokens, ff)}, {dx_add, 2 * nx}};
+  const Range out[] = {{dx, nx}, {dw_in, 2 * nw}, {dw_down, nw}, {workspace, need}};
+  for (int i = 0; i < 4; ++i) {
+    if (overlaps_any(out[i], {in[0], in[1], in[2], in[3], in[4], in[5]}))
+      return fail(BMOE_ERR_ALIAS, "dx, dw_in, dw_down or the workspace overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return fail(BMOE_ERR_ALIAS, "two of dx, dw_in, dw_down and the workspace overlap");
+  }
+  st = check_device();
+  if (st != BMOE_OK) return st;
+  auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
+  auto w16 = [](void* p) { return static_cast<uint16_t*>(p); };
+  const GfBwdArgs a{u16(x), u16(w_in), u16(w_down), u16(dy), u16(state), dx_add, w16(dx), w16(dw_in), w16(dw_down), workspace, tokens, d, ff,
+                    act == BMOE_GATED_GELU};
+  BMOE_HIP(launch_gated_ffn_backward(a, stream));
   return ok();
 }
 

@@ -1,0 +1,753 @@
+// Dense gated feed-forward block (include/bmoe_ffn.h).
+//
+// Six matrix products over bf16 with fp32 sums, all by one kernel template:
+//     forward   g | u = x Wg^T | x Wu^T -> h        y = h Wd^T
+//     backward  dh = dy Wd -> dg | du               dx = [dg du] [Wg; Wu]
+//               [dWg; dWu] = [dg du]^T x            dWd = dy^T h
+// An operand has the contraction contiguous (x, h, dy and the weights of the forward) or
+// its other side (the weights of the backward's first two, everything in the last two).
+// Operand tiles of 64-deep steps come straight into LDS (16 bytes per lane) in a ring of
+// steps, in the layout they have in memory; those of the second kind are turned on the
+// way from LDS to registers (ds_read_b64_tr_b16), so no transposed copy of anything is
+// written.
+#include "butterfly_impl.hpp"
+#include "step_ops.hpp"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace bmoe {
+
+typedef const __attribute__((address_space(1))) void gf_glob_t;
+typedef __attribute__((address_space(3))) void gf_lds_t;
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t gf_lds4_t;
+
+constexpr int GF_K = 64;          // contraction step
+constexpr int GF_CUS = 256;       // of a whole MI355X
+constexpr int GF_SPLIT = 16;      // most workgroups that share a tile's depth
+constexpr int GF_FEW = 32;        // most tokens of the kernel that reads weights straight into registers
+
+// what the places of a step past a ragged depth are filled with
+__device__ const uint4 gf_zeros = {0, 0, 0, 0};
+
+enum GfEpilogue { GF_OUT, GF_PART, GF_GATE, GF_GRAD };
+enum GfActivation { GF_SILU = 0, GF_GELU = 1 };
+
+struct GfGemm {
+  const uint16_t* a;        // [M][K], or [K][M] (AT)
+  const uint16_t* b;        // [N][K], or [K][N] (BT); GF_GATE: [2 ff][K], N = 2 ff
+  int32_t lda, ldb;         // elements of a row of each
+  int32_t M, N, K;
+  int32_t nm, nn, band;     // tile rows and columns, tile rows of a band
+  int32_t split, per;       // workgroups that share a tile's depth, steps of each
+  uint16_t* out;            // GF_OUT [M][N]; GF_GATE h [M][ff]; GF_GRAD [M][2 ff] dg | du
+  const uint16_t* add16;    // GF_OUT: [M][N] or null
+  const float* add32;       // the same
+  float* part;              // GF_PART: [split][M][N]
+  uint16_t* pa;             // GF_GATE: [M][2 ff], u act'(g) and act(g), or null; GF_GRAD: read
+  uint8_t* fine;            // [M][ff] four more bits of both
+  int32_t ff;
+};
+
+__device__ __forceinline__ float gf_sigmoid(float g) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g)); }
+// GELU is the layers' own up to the end of its tail's range, where that is 2.6e-8, and 0 or g
+// beyond.
+__device__ __forceinline__ float gf_gelu(float g) { return fabsf(g) > 5.75f ? (g > 0.f ? g : g * 0.f) : gelu_erf(g); }
+template <int F>
+__device__ __forceinline__ float gf_act(float g) {
+  return F == GF_GELU ? gf_gelu(g) : g * gf_sigmoid(g);
+}
+// act(g) and its derivative
+template <int F>
+__device__ __forceinline__ float2 gf_act_slope(float g) {
+  if constexpr (F == GF_GELU) {
+    const float slope = 0.5f * (1.0f + erf_as(g * 0.70710678118654752f)) +
+                        g * 0.39894228040143268f * __builtin_amdgcn_exp2f(-0.72134752044448170f * g * g);
+    return make_float2(gf_gelu(g), slope);
+  }
+  const float s = gf_sigmoid(g);
+  return make_float2(g * s, s * fmaf(g, 1.0f - s, 1.0f));
+}
+
+// The two factors of dh that the backward takes, p = u act'(g) for dg and a = act(g) for du, are
+// kept to 12 significant bits: as bf16, truncated, and a byte with the next four bits of
+// both.  In bf16 alone their rounding would count in dx and dw_in as much as those of dg
+// and du themselves (3.0e-3 off in all, with these 2.4e-3), in fp32 they would be three more
+// bytes to write and read.
+struct GfKept {
+  uint32_t p, a;            // fp32 values with the four bits behind bf16's, rounded
+};
+__device__ __forceinline__ GfKept gf_keep(float p, float a) { return {__float_as_uint(p) + 0x800u, __float_as_uint(a) + 0x800u}; }
+__device__ __forceinline__ uint32_t gf_fine(GfKept v) { return (v.p >> 12 & 15u) | (v.a >> 8 & 0xF0u); }
+__device__ __forceinline__ float gf_kept_p(uint32_t bf16, uint32_t fine) { return __uint_as_float(bf16 << 16 | (fine & 15u) << 12); }
+__device__ __forceinline__ float gf_kept_a(uint32_t bf16, uint32_t fine) { return __uint_as_float(bf16 << 16 | (fine & 0xF0u) << 8); }
+
+// One workgroup per T x T tile of D[m][n] = sum_k A[m][k] B[n][k], WM x WN waves of
+// T / WM x T / WN each (MFMA blocks of 16 x 16 x 32), NBUF steps in the ring.
+//
+// LDS, contraction contiguous: [T rows][64], 16-byte chunk c of row r at c ^ (r % 8); a lane
+// reads its 8 values of depth as one 16-byte chunk.  Other side contiguous: [64 depths][T],
+// chunk c of depth k at c ^ 2 (k % 8); 16 lanes read 4 depths of 16 rows as 8 bytes each
+// and get 4 depths of their row.
+//
+// A step is two 32-deep halves with a set of fragments each: the reads of the next half
+// are issued among the products of the current one, and the barrier that frees a ring
+// place stands between the halves.  The first step of a depth that is no multiple of 64 is
+// the short one: it is loaded ahead of the loop, so the loop has no case for it.
+template <bool AT, bool BT, int EPI, int F, int T, int WM, int WN, int NBUF>
+__global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
+  constexpr int NW = WM * WN, NT = 64 * NW;
+  constexpr int PM = T / WM, PN = T / WN, IM = PM / 16, IN = PN / 16;
+  constexpr int STAGE = 2 * T * GF_K;            // halves of a ring place: A's, then B's
+  constexpr int LPW = 2 * T / 8 / NW;            // loads per wave and step
+  static_assert(T / 8 % LPW == 0, "no wave loads both operands");
+  static_assert(EPI != GF_GATE || IN % 2 == 0, "gate and up blocks in pairs");
+  extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int wm = wave % WM, wn = wave / WM;
+  // an XCD's workgroups take the same share of a block of tiles: bands of tile rows,
+  // column by column within a band
+  int t = xcd_remap(blockIdx.x, gridDim.x);
+  const int tiles = p.nm * p.nn, share = t / tiles;
+  t -= share * tiles;
+  const int r0 = t / (p.band * p.nn) * p.band;
+  t -= r0 * p.nn;
+  const int hh = min(p.band, p.nm - r0);
+  const int tn = t / hh, tm = r0 + t - tn * hh;
+  const int m0 = tm * T, n0 = tn * T;
+  const int nk1 = (p.K + GF_K - 1) / GF_K, short_by = nk1 * GF_K - p.K;
+  const int k0 = share * p.per, nk = min(p.per, nk1 - k0);
+
+  // this wave's loads: all of A or all of B, byte offsets of this lane's pieces from the
+  // tile's first element; rows and columns past the matrix read its last ones and are
+  // not stored
+  const bool isb = wave * LPW >= T / 8;
+  uint32_t off[LPW];
+  int deep[LPW];            // depth within a step of the lane's first value
+  const char* base;
+  size_t advance;           // bytes of a step
+  {
+    auto place = [&](auto turned, const uint16_t* q, int ld, int first, int count, bool gate) {
+      constexpr bool TURNED = decltype(turned)::value;
+      base = reinterpret_cast<const char*>(q + (TURNED ? size_t(first) : gate ? size_t(0) : size_t(first) * ld));
+      advance = TURNED ? size_t(GF_K) * ld * 2 : GF_K * 2;
+#pragma unroll
+      for (int j = 0; j < LPW; ++j) {
+        const int w = wave * LPW + j - (isb ? T / 8 : 0);
+        if constexpr (TURNED) {
+          constexpr int RC = T / 8, RPL = 64 / RC;
+          const int k = w * RPL + lane / RC, c = (lane % RC) ^ (2 * (k & (T / 16 - 1) & 7));
+          off[j] = 2u * (uint32_t(k) * uint32_t(ld) + uint32_t(min(first + 8 * c, count - 8) - first));
+          deep[j] = k;
+        } else {
+          const int row = 8 * w + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
+          uint32_t at;
+          if (gate) {   // blocks of 16 rows of Wg and Wu in turn
+            const int half = min(first / 2 + 16 * (row >> 5) + (row & 15), p.ff - 1);
+            at = uint32_t(half + (row & 16 ? p.ff : 0));
+          } else {
+            at = uint32_t(min(first + row, count - 1) - first);
+          }
+          off[j] = 2u * (at * uint32_t(ld) + 8u * c);
+          deep[j] = 8 * c;
+        }
+      }
+    };
+    if (isb) place(std::integral_constant<bool, BT>{}, p.b, p.ldb, n0, p.N, EPI == GF_GATE);
+    else place(std::integral_constant<bool, AT>{}, p.a, p.lda, m0, p.M, false);
+  }
+  // bytes that the first step is short by: the steps behind it start that much earlier
+  const size_t back = short_by ? advance / GF_K * short_by : 0;
+  auto load = [&](int kt, int buf) {
+    const int s = k0 + min(kt, nk - 1);   // past the last one: the last one again, never read
+    const char* src = base + size_t(s) * advance - (s > 0 ? back : 0);
+    uint16_t* dst = sm + buf * STAGE + wave * LPW * 512;
+#pragma unroll
+    for (int j = 0; j < LPW; ++j)
+      __builtin_amdgcn_global_load_lds((gf_glob_t*)(src + off[j]), (gf_lds_t*)(dst + 512 * j), 16, 0, 0);
+  };
+  // step 0 of the whole depth: zeros behind its last value
+  auto load_short = [&](int buf) {
+    uint16_t* dst = sm + buf * STAGE + wave * LPW * 512;
+#pragma unroll
+    for (int j = 0; j < LPW; ++j) {
+      const char* at = deep[j] < GF_K - short_by ? base + off[j] : reinterpret_cast<const char*>(&gf_zeros);
+      __builtin_amdgcn_global_load_lds((gf_glob_t*)at, (gf_lds_t*)(dst + 512 * j), 16, 0, 0);
+    }
+  };
+
+  f32x4_t acc[IN][IM];
+#pragma unroll
+  for (int i = 0; i < IN; ++i)
+#pragma unroll
+    for (int j = 0; j < IM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  bf16x8_t fa[2][IM], fb[2][IN];
+  // one operand's fragments of half h: COUNT blocks of 16 rows from `row` on
+  auto read_one = [&](auto turned, const uint16_t* tile, int row, int h, auto& f) {
+    constexpr int COUNT = sizeof(f) / sizeof(f[0]);
+    if constexpr (decltype(turned)::value) {
+      const int k = 32 * h + 8 * g + (l16 >> 2), s = l16 >> 1 & 1;
+      const int swz = 2 * ((l16 >> 2) & (T / 16 - 1)), more = T >= 128 ? 64 : 0;   // 4 depths on: chunk ^ 8
+#pragma unroll
+      for (int j = 0; j < COUNT; ++j) {
+        const int at = 8 * ((row / 8 + 2 * j + s) ^ swz) + 4 * (l16 & 1);
+        const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gf_lds4_t*)(tile + k * T + at));
+        const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gf_lds4_t*)(tile + (k + 4) * T + (at ^ more)));
+        typedef short i16x8_t __attribute__((ext_vector_type(8)));
+        f[j] = __builtin_bit_cast(bf16x8_t, i16x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+      }
+    } else {
+      const uint16_t* q = tile + (row + l16) * GF_K + 8 * ((4 * h + g) ^ (l16 & 7));
+#pragma unroll
+      for (int j = 0; j < COUNT; ++j) f[j] = *reinterpret_cast<const bf16x8_t*>(q + 16 * j * GF_K);
+    }
+  };
+  auto read = [&](int buf, int h, bf16x8_t (&a)[IM], bf16x8_t (&b)[IN]) {
+    read_one(std::integral_constant<bool, AT>{}, sm + buf * STAGE, PM * wm, h, a);
+    read_one(std::integral_constant<bool, BT>{}, sm + buf * STAGE + T * GF_K, PN * wn, h, b);
+  };
+  auto mul = [&](const bf16x8_t (&a)[IM], const bf16x8_t (&b)[IN]) {
+#pragma unroll
+    for (int i = 0; i < IN; ++i)
+#pragma unroll
+      for (int j = 0; j < IM; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i], a[j], acc[i][j], 0, 0, 0);
+  };
+  // order of a region: the reads behind the first products, the loads among the others
+  auto spread = [&](auto loads) {
+    constexpr int NL = decltype(loads)::value, READS = (AT ? 2 : 1) * IM + (BT ? 2 : 1) * IN, MULS = IM * IN;
+    constexpr int FIRST = READS < MULS / 2 ? READS : MULS / 2, PER = (READS + FIRST - 1) / FIRST;
+    constexpr int REST = MULS - FIRST, GAP = NL > 0 && REST / std::max(NL, 1) > 0 ? REST / std::max(NL, 1) : 1;
+#pragma unroll
+    for (int m = 0; m < FIRST; ++m) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+    }
+#pragma unroll
+    for (int m = 0; m < NL; ++m) {
+      __builtin_amdgcn_sched_group_barrier(0x008, GAP, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, MULS, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // this wave's reads are done and its loads of all but the newest steps have arrived;
+  // then the same of every wave
+  auto arrive = [&]() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * LPW) : "memory");
+  };
+  if (k0 == 0 && short_by) {
+    load_short(0);
+    if (nk == 1) {   // the loads past it read no more than it has
+#pragma unroll
+      for (int j = 0; j < LPW; ++j) off[j] = deep[j] < GF_K - short_by ? off[j] : 0;
+    }
+  } else {
+    load(0, 0);
+  }
+#pragma unroll
+  for (int b = 1; b < NBUF - 1; ++b) load(b, b);
+  arrive();
+  load(NBUF - 1, NBUF - 1);
+  read(0, 0, fa[0], fb[0]);
+  int buf = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+    const int next = buf + 1 == NBUF ? 0 : buf + 1;
+    read(buf, 1, fa[1], fb[1]);
+    mul(fa[0], fb[0]);
+    spread(std::integral_constant<int, 0>{});
+    arrive();
+    read(next, 0, fa[0], fb[0]);
+    load(kt + NBUF, buf);
+    mul(fa[1], fb[1]);
+    spread(std::integral_constant<int, LPW>{});
+    buf = next;
+  }
+  // loads past the last step may still be writing to the ring
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // acc[i][j][r] = D[m0 + PM wm + 16 j + l16][n0 + PN wn + 16 i + 4 g + r]
+  if constexpr (EPI == GF_PART) {
+    float* out = p.part + size_t(share) * p.M * p.N;
+#pragma unroll
+    for (int j = 0; j < IM; ++j) {
+      const int m = m0 + PM * wm + 16 * j + l16;
+#pragma unroll
+      for (int i = 0; i < IN; ++i) {
+        const int n = n0 + PN * wn + 16 * i + 4 * g;
+        if (m < p.M && n < p.N) *reinterpret_cast<f32x4_t*>(out + size_t(m) * p.N + n) = acc[i][j];
+      }
+    }
+    return;
+  }
+  uint16_t* st = sm;
+  // bf16 values f(i, j) of this lane's blocks (i a multiple of BY, columns 16 / BY apart)
+  // to a staged tile of W columns, and that in rows of 16 bytes to dst, W columns from c0 on
+  // inside `cols`
+  auto put = [&](auto by, uint16_t* dst, int ld, int c0, int cols, auto&& f) {
+    constexpr int BY = decltype(by)::value, W = T / BY, ST = W + 4;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < IM; ++j)
+#pragma unroll
+      for (int i = 0; i < IN; i += BY)
+        *reinterpret_cast<uint2*>(st + (PM * wm + 16 * j + l16) * ST + (PN * wn + 16 * i) / BY + 4 * g) = f(i, j);
+    __syncthreads();
+#pragma unroll 4
+    for (int q = 0; q < T * W / 8 / NT; ++q) {
+      const int k = tid + NT * q, r = k / (W / 8), c = 8 * (k % (W / 8));
+      if (m0 + r >= p.M || c0 + c >= cols) continue;
+      const uint2 lo = *reinterpret_cast<const uint2*>(st + r * ST + c), hi = *reinterpret_cast<const uint2*>(st + r * ST + c + 4);
+      *reinterpret_cast<uint4*>(dst + size_t(m0 + r) * ld + c0 + c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+    }
+  };
+  auto pack = [](f32x4_t v) { return make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])); };
+  auto four = [](const uint16_t* q) {
+    const uint2 u = *reinterpret_cast<const uint2*>(q);
+    return f32x4_t{bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y)};
+  };
+  using one = std::integral_constant<int, 1>;
+  using two = std::integral_constant<int, 2>;
+  if constexpr (EPI == GF_OUT) {
+    if (p.add16 || p.add32) {
+#pragma unroll
+      for (int j = 0; j < IM; ++j) {
+        const int m = m0 + PM * wm + 16 * j + l16;
+#pragma unroll
+        for (int i = 0; i < IN; ++i) {
+          const int n = n0 + PN * wn + 16 * i + 4 * g;
+          if (m >= p.M || n >= p.N) continue;
+          const size_t at = size_t(m) * p.N + n;
+          if (p.add16) acc[i][j] += four(p.add16 + at);
+          if (p.add32) acc[i][j] += *reinterpret_cast<const f32x4_t*>(p.add32 + at);
+        }
+      }
+    }
+    put(one{}, p.out, p.N, n0, p.N, [&](int i, int j) { return pack(acc[i][j]); });
+  } else if constexpr (EPI == GF_GATE) {
+    const int c0 = n0 / 2;
+    if (!p.pa) {
+      put(two{}, p.out, p.ff, c0, p.ff, [&](int i, int j) {
+        f32x4_t h;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) h[r] = gf_act<F>(acc[i][j][r]) * acc[i + 1][j][r];
+        return pack(h);
+      });
+      return;
+    }
+    // h and the kept factors take the places of g and u
+    uint2 h[IN / 2][IM];
+#pragma unroll
+    for (int j = 0; j < IM; ++j)
+#pragma unroll
+      for (int i = 0; i < IN; i += 2) {
+        f32x4_t o;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float2 f = gf_act_slope<F>(acc[i][j][r]);
+          const float u = acc[i + 1][j][r];
+          o[r] = f.x * u;
+          const GfKept k = gf_keep(u * f.y, f.x);
+          acc[i][j][r] = __uint_as_float(k.p);
+          acc[i + 1][j][r] = __uint_as_float(k.a);
+        }
+        h[i / 2][j] = pack(o);
+        asm volatile("" : "+v"(acc[i][j]), "+v"(acc[i + 1][j]));
+      }
+    auto upper = [](f32x4_t v) {
+      return make_uint2(__float_as_uint(v[0]) >> 16 | (__float_as_uint(v[1]) & 0xFFFF0000u),
+                        __float_as_uint(v[2]) >> 16 | (__float_as_uint(v[3]) & 0xFFFF0000u));
+    };
+    put(two{}, p.out, p.ff, c0, p.ff, [&](int i, int j) { return h[i / 2][j]; });
+    put(two{}, p.pa, 2 * p.ff, c0, p.ff, [&](int i, int j) { return upper(acc[i][j]); });
+    put(two{}, p.pa + p.ff, 2 * p.ff, c0, p.ff, [&](int i, int j) { return upper(acc[i + 1][j]); });
+    constexpr int W = T / 2, ST = W / 4 + 1;   // columns, 4-byte words of a staged row
+    uint32_t* bytes = reinterpret_cast<uint32_t*>(sm);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < IM; ++j)
+#pragma unroll
+      for (int i = 0; i < IN; i += 2) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v |= gf_fine(GfKept{__float_as_uint(acc[i][j][r]), __float_as_uint(acc[i + 1][j][r])}) << (8 * r);
+        bytes[(PM * wm + 16 * j + l16) * ST + (PN * wn + 16 * i) / 8 + g] = v;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < T * W / 8 / NT; ++q) {
+      const int k = tid + NT * q, r = k / (W / 8), c = 8 * (k % (W / 8));
+      if (m0 + r >= p.M || c0 + c >= p.ff) continue;
+      *reinterpret_cast<uint2*>(p.fine + size_t(m0 + r) * p.ff + c0 + c) = make_uint2(bytes[r * ST + c / 4], bytes[r * ST + c / 4 + 1]);
+    }
+  } else if constexpr (EPI == GF_GRAD) {
+    // acc is dh; dg and du take its place as bf16
+#pragma unroll
+    for (int j = 0; j < IM; ++j) {
+      const size_t m = min(m0 + PM * wm + 16 * j + l16, p.M - 1);
+      uint2 pv[IN], av[IN];
+      uint32_t fv[IN];
+#pragma unroll
+      for (int i = 0; i < IN; ++i) {
+        const int n = min(n0 + PN * wn + 16 * i + 4 * g, p.ff - 4);
+        pv[i] = *reinterpret_cast<const uint2*>(p.pa + m * 2 * p.ff + n);
+        av[i] = *reinterpret_cast<const uint2*>(p.pa + m * 2 * p.ff + p.ff + n);
+        fv[i] = *reinterpret_cast<const uint32_t*>(p.fine + m * p.ff + n);
+      }
+#pragma unroll
+      for (int i = 0; i < IN; ++i) {
+        f32x4_t dg, du;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t x = (r & 2 ? pv[i].y : pv[i].x) >> (16 * (r & 1)), y = (r & 2 ? av[i].y : av[i].x) >> (16 * (r & 1));
+          dg[r] = acc[i][j][r] * gf_kept_p(x, fv[i] >> (8 * r));
+          du[r] = acc[i][j][r] * gf_kept_a(y, fv[i] >> (8 * r));
+        }
+        const uint2 x = pack(dg), y = pack(du);
+        acc[i][j] = __builtin_bit_cast(f32x4_t, make_uint4(x.x, x.y, y.x, y.y));
+        asm volatile("" : "+v"(acc[i][j]));   // here, not where du is stored: its factors and dh would live until then
+      }
+      // one row of blocks at a time: the loads of all would take the registers
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    put(one{}, p.out, 2 * p.ff, n0, p.ff, [&](int i, int j) {
+      const uint4 u = __builtin_bit_cast(uint4, acc[i][j]);
+      return make_uint2(u.x, u.y);
+    });
+    put(one{}, p.out + p.ff, 2 * p.ff, n0, p.ff, [&](int i, int j) {
+      const uint4 u = __builtin_bit_cast(uint4, acc[i][j]);
+      return make_uint2(u.z, u.w);
+    });
+  }
+}
+
+// The shares' sums, added in order, and what is added to them.
+__global__ __launch_bounds__(256) void gf_reduce_kernel(const float* part, int split, size_t n, uint16_t* out,
+                                                        const uint16_t* add16, const float* add32) {
+  const size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  f32x4_t s = *reinterpret_cast<const f32x4_t*>(part + i);
+#pragma unroll 4
+  for (int k = 1; k < split; ++k) s += *reinterpret_cast<const f32x4_t*>(part + k * n + i);
+  if (add16) {
+    const uint2 u = *reinterpret_cast<const uint2*>(add16 + i);
+    s += f32x4_t{bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y)};
+  }
+  if (add32) s += *reinterpret_cast<const f32x4_t*>(add32 + i);
+  *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+}
+
+// Few tokens: bound by the weights' bytes.  A workgroup takes 16 rows of a weight (GATE: of
+// Wg and of Wu), its waves a part of the depth each; weights come from memory into
+// registers as MFMA operands, 16 bytes per lane, U steps of 32 on their way at a time, and
+// the tokens' rows, which the caches hold, the same way.  NT blocks of 16 tokens.
+struct GfFew {
+  const uint16_t* x;        // [M][K]
+  const uint16_t* w;        // [R][K], GATE: [2 R][K]
+  const uint16_t* add;      // [M][R] or null
+  uint16_t* out;            // [M][R]
+  uint16_t* pa;             // GATE: [M][2 R] or null
+  uint8_t* fine;            // GATE: [M][R] when pa is set
+  int32_t M, R, K;
+};
+template <bool GATE, int F, int NT>
+__global__ __launch_bounds__(1024) void gf_few_kernel(GfFew p) {
+  constexpr int NWT = GATE ? 2 : 1, U = GATE || NT > 1 ? 4 : 8;
+  extern __shared__ __attribute__((aligned(16))) float red[];   // [waves][NWT][NT][16 tokens][20]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+  const int l16 = lane & 15, g = lane >> 4, row0 = 16 * blockIdx.x;
+  const int steps = (p.K + 31) / 32, per = (steps + waves - 1) / waves, s0 = wave * per, s1 = min(s0 + per, steps);
+  const uint16_t* w[NWT];
+  const uint16_t* x[NT];
+#pragma unroll
+  for (int k = 0; k < NWT; ++k) w[k] = p.w + size_t(min(row0 + l16, p.R - 1) + k * p.R) * p.K + 8 * g;
+#pragma unroll
+  for (int k = 0; k < NT; ++k) x[k] = p.x + size_t(min(16 * k + l16, p.M - 1)) * p.K + 8 * g;
+  f32x4_t acc[NWT][NT] = {};
+  const bf16x8_t zero = {};
+  auto round = [&](int s, auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
+    bf16x8_t fw[U][NWT], fx[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // depths past the end are read at the last whole chunk and made zero
+      const int k = 32 * (s + u), at = WHOLE ? k : min(k, p.K - 8 - 8 * g);
+#pragma unroll
+      for (int i = 0; i < NWT; ++i) fw[u][i] = *reinterpret_cast<const bf16x8_t*>(w[i] + at);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) fx[u][i] = *reinterpret_cast<const bf16x8_t*>(x[i] + at);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!WHOLE) {
+        const bool in = s + u < s1 && 32 * (s + u) + 8 * g < p.K;
+#pragma unroll
+        for (int i = 0; i < NWT; ++i) fw[u][i] = in ? fw[u][i] : zero;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) fx[u][i] = in ? fx[u][i] : zero;
+      }
+#pragma unroll
+      for (int i = 0; i < NWT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[u][i], fx[u][j], acc[i][j], 0, 0, 0);
+    }
+  };
+  int s = s0;
+  for (; s + U <= s1 && 32 * (s + U) <= p.K; s += U) round(s, std::true_type{});
+  for (; s < s1; s += U) round(s, std::false_type{});
+  // acc[i][j][r] = D[row 4 g + r][token 16 j + l16]
+#pragma unroll
+  for (int i = 0; i < NWT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *reinterpret_cast<f32x4_t*>(red + (((wave * NWT + i) * NT + j) * 16 + l16) * 20 + 4 * g) = acc[i][j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < 256 * NT; e += blockDim.x) {
+    const int r = e & 15, m = e >> 4;
+    if (m >= p.M || row0 + r >= p.R) continue;
+    float v[NWT] = {};
+    for (int k = 0; k < waves; ++k)
+#pragma unroll
+      for (int i = 0; i < NWT; ++i) v[i] += red[((k * NWT + i) * NT * 16 + m) * 20 + r];
+    const size_t at = size_t(m) * p.R + row0 + r;
+    if constexpr (GATE) {
+      if (p.pa) {
+        const float2 f = gf_act_slope<F>(v[0]);
+        const GfKept k = gf_keep(v[1] * f.y, f.x);
+        p.pa[at + size_t(m) * p.R] = uint16_t(k.p >> 16);
+        p.pa[at + size_t(m + 1) * p.R] = uint16_t(k.a >> 16);
+        p.fine[at] = uint8_t(gf_fine(k));
+      }
+      v[0] = gf_act<F>(v[0]) * v[1];
+    } else if (p.add) {
+      v[0] += load1<ACT_BF16>(p.add, at);
+    }
+    p.out[at] = uint16_t(pack_bf16x2(v[0], v[0]));
+  }
+}
+
+__global__ __launch_bounds__(256) void gf_zero_kernel(uint16_t* out, size_t n) {
+  for (size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * 8; i < n; i += size_t(gridDim.x) * 2048)
+    *reinterpret_cast<uint4*>(out + i) = make_uint4(0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ host
+namespace {
+
+struct GfTile {
+  int side, split;
+};
+
+int64_t gf_tiles(int M, int N, int side) { return int64_t((M + side - 1) / side) * ((N + side - 1) / side); }
+
+// A product's tile side and the workgroups that share a tile's depth, by a time estimate in
+// microseconds: rounds of workgroups over the CUs, a step of 64 by the lone workgroup of
+// a CU or by each of two, a tile's beginning and end; shares are written and read again in
+// fp32 by a launch behind.
+GfTile gf_pick(int M, int N, int K, bool may_split) {
+  struct Side {
+    int side, per_cu;
+    double step, once;
+  };
+  GfTile best{0, 1};
+  double least = 0;
+  const int steps = (K + GF_K - 1) / GF_K;
+  for (const Side s : {Side{64, 2, 0.29, 2.0}, Side{128, 1, 0.41, 3.0}, Side{256, 1, 1.2, 5.0}}) {
+    const int64_t tiles = gf_tiles(M, N, s.side);
+    for (int split = 1; split <= (may_split ? GF_SPLIT : 1); ++split) {
+      const int per = (steps + split - 1) / split;
+      if (split > 1 && ((split - 1) * per >= steps || per < 4)) continue;
+      const double rounds = double((tiles * split + GF_CUS * s.per_cu - 1) / (GF_CUS * s.per_cu));
+      double time = rounds * (per * s.step + s.once);
+      if (split > 1) time += 3.0 + double(M) * N * split * 8 / 4e6;
+      if (!best.side || time < least) {
+        best = GfTile{s.side, split};
+        least = time;
+      }
+    }
+  }
+  return best;
+}
+
+size_t gf_part_bytes(int M, int N, GfTile t) { return t.split > 1 ? size_t(t.split) * M * N * 4 : 0; }
+size_t gf_round(size_t bytes) { return (bytes + 255) / 256 * 256; }
+
+template <bool AT, bool BT, int EPI, int F, int T, int WM, int WN, int NBUF>
+hipError_t gf_go(GfGemm p, hipStream_t s) {
+  constexpr size_t ring = size_t(NBUF) * 2 * T * GF_K * 2, stage = size_t(T) * (T + 4) * 2;
+  constexpr size_t lds = ring > stage ? ring : stage;
+  const auto kernel = gf_gemm_kernel<AT, BT, EPI, F, T, WM, WN, NBUF>;
+  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
+  if (e != hipSuccess) return e;
+  p.nm = (p.M + T - 1) / T;
+  p.nn = (p.N + T - 1) / T;
+  p.band = std::min(p.nm, 8);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(int64_t(p.nm) * p.nn * p.split)), dim3(64 * WM * WN), lds, s, p);
+  return hipGetLastError();
+}
+
+template <bool AT, bool BT, int EPI, int F = GF_SILU>
+hipError_t gf_side(const GfGemm& p, int side, hipStream_t s) {
+  if (side == 64) return gf_go<AT, BT, EPI, F, 64, 2, 2, 4>(p, s);
+  if (side == 128) return gf_go<AT, BT, EPI, F, 128, 2, 4, 3>(p, s);
+  return gf_go<AT, BT, EPI, F, 256, 2, 4, 2>(p, s);
+}
+
+// A product whose result is written as it is (plus what is added), in shares where the
+// estimate says so.
+template <bool AT, bool BT>
+hipError_t gf_product(GfGemm p, float* part, hipStream_t s) {
+  const GfTile t = gf_pick(p.M, p.N, p.K, true);
+  p.split = t.split;
+  p.per = ((p.K + GF_K - 1) / GF_K + t.split - 1) / t.split;
+  if (t.split == 1) return gf_side<AT, BT, GF_OUT>(p, t.side, s);
+  p.part = part;
+  const hipError_t e = gf_side<AT, BT, GF_PART>(p, t.side, s);
+  if (e != hipSuccess) return e;
+  const size_t n = size_t(p.M) * p.N;
+  hipLaunchKernelGGL(gf_reduce_kernel, dim3(unsigned((n / 4 + 255) / 256)), dim3(256), 0, s, part, t.split, n, p.out, p.add16, p.add32);
+  return hipGetLastError();
+}
+
+template <bool GATE, int F = GF_SILU>
+hipError_t gf_few(const GfFew& p, hipStream_t s) {
+  // waves of a workgroup: 2048 in all (eight to a CU), down to 4 steps of the depth each
+  const int groups = (p.R + 15) / 16, steps = (p.K + 31) / 32;
+  int waves = 4;
+  while (waves < 16 && groups * waves < 2048 && steps / waves > 4) waves *= 2;
+  const int nt = p.M > 16 ? 2 : 1;
+  const size_t lds = size_t(waves) * (GATE ? 2 : 1) * nt * 16 * 20 * 4;
+  const auto kernel = nt == 2 ? gf_few_kernel<GATE, F, 2> : gf_few_kernel<GATE, F, 1>;
+  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(kernel, dim3(unsigned(groups)), dim3(64 * waves), lds, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t gf_forward_workspace(int tokens, int d, int ff, bool with_state) {
+  if (tokens == 0) return 0;
+  const size_t h = with_state ? 0 : gf_round(size_t(tokens) * ff * 2);
+  return h + (tokens <= GF_FEW ? 0 : gf_part_bytes(tokens, d, gf_pick(tokens, d, ff, true)));
+}
+
+hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
+  const int M = a.tokens;
+  if (M == 0) return hipSuccess;
+  // of the state: the kept factors, h, the factors' further bits
+  uint16_t* pa = a.state;
+  uint8_t* fine = reinterpret_cast<uint8_t*>(a.state + size_t(M) * 3 * a.ff);
+  char* ws = static_cast<char*>(a.ws);
+  uint16_t* h = a.state ? a.state + size_t(M) * 2 * a.ff : reinterpret_cast<uint16_t*>(ws);
+  float* part = reinterpret_cast<float*>(ws + (a.state ? 0 : gf_round(size_t(M) * a.ff * 2)));
+  if (M <= GF_FEW) {
+    const GfFew gate{a.x, a.w_in, nullptr, h, pa, fine, M, a.ff, a.d};
+    const hipError_t e = a.gelu ? gf_few<true, GF_GELU>(gate, s) : gf_few<true, GF_SILU>(gate, s);
+    return e != hipSuccess ? e : gf_few<false>(GfFew{h, a.w_down, a.add, a.y, nullptr, nullptr, M, a.d, a.ff}, s);
+  }
+  GfGemm p{};
+  p.a = a.x;
+  p.b = a.w_in;
+  p.lda = p.ldb = p.K = a.d;
+  p.M = M;
+  p.N = 2 * a.ff;
+  p.split = 1;
+  p.per = (p.K + GF_K - 1) / GF_K;
+  p.out = h;
+  p.pa = pa;
+  p.fine = fine;
+  p.ff = a.ff;
+  const int side = gf_pick(M, p.N, p.K, false).side;
+  hipError_t e = a.gelu ? gf_side<false, false, GF_GATE, GF_GELU>(p, side, s) : gf_side<false, false, GF_GATE, GF_SILU>(p, side, s);
+  if (e != hipSuccess) return e;
+  p = GfGemm{};
+  p.a = h;
+  p.b = a.w_down;
+  p.lda = p.ldb = p.K = a.ff;
+  p.M = M;
+  p.N = a.d;
+  p.out = a.y;
+  p.add16 = a.add;
+  return gf_product<false, false>(p, part, s);
+}
+
+size_t gf_backward_workspace(int tokens, int d, int ff) {
+  if (tokens == 0) return 0;
+  const size_t part = std::max({gf_part_bytes(tokens, d, gf_pick(tokens, d, 2 * ff, true)),
+                                gf_part_bytes(2 * ff, d, gf_pick(2 * ff, d, tokens, true)),
+                                gf_part_bytes(d, ff, gf_pick(d, ff, tokens, true))});
+  return gf_round(size_t(tokens) * 2 * ff * 2) + part;
+}
+
+hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
+  const int M = a.tokens;
+  if (M == 0) {
+    for (auto [p, n] : {std::pair<uint16_t*, size_t>{a.dw_in, size_t(2) * a.ff * a.d}, {a.dw_down, size_t(a.d) * a.ff}}) {
+      if (!p) continue;
+      hipLaunchKernelGGL(gf_zero_kernel, dim3(unsigned(std::min<size_t>((n + 2047) / 2048, 1024))), dim3(256), 0, s, p, n);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
+  const uint16_t* h = a.state + size_t(M) * 2 * a.ff;
+  uint16_t* dgu = static_cast<uint16_t*>(a.ws);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(a.ws) + gf_round(size_t(M) * 2 * a.ff * 2));
+  hipError_t e = hipSuccess;
+  if (a.dx || a.dw_in) {
+    GfGemm p{};
+    p.a = a.dy;
+    p.b = a.w_down;
+    p.lda = p.K = a.d;
+    p.ldb = p.N = p.ff = a.ff;
+    p.M = M;
+    p.split = 1;
+    p.per = (p.K + GF_K - 1) / GF_K;
+    p.out = dgu;
+    p.pa = const_cast<uint16_t*>(a.state);
+    p.fine = reinterpret_cast<uint8_t*>(p.pa + size_t(M) * 3 * a.ff);
+    const int side = gf_pick(M, p.N, p.K, false).side;
+    e = a.gelu ? gf_side<false, true, GF_GRAD, GF_GELU>(p, side, s) : gf_side<false, true, GF_GRAD, GF_SILU>(p, side, s);
+    if (e != hipSuccess) return e;
+  }
+  if (a.dx) {
+    GfGemm p{};
+    p.a = dgu;
+    p.b = a.w_in;
+    p.lda = p.K = 2 * a.ff;
+    p.ldb = p.N = a.d;
+    p.M = M;
+    p.out = a.dx;
+    p.add32 = a.dx_add;
+    e = gf_product<false, true>(p, part, s);
+    if (e != hipSuccess) return e;
+  }
+  if (a.dw_in) {
+    GfGemm p{};
+    p.a = dgu;
+    p.b = a.x;
+    p.lda = p.M = 2 * a.ff;
+    p.ldb = p.N = a.d;
+    p.K = M;
+    p.out = a.dw_in;
+    e = gf_product<true, true>(p, part, s);
+    if (e != hipSuccess) return e;
+  }
+  if (a.dw_down) {
+    GfGemm p{};
+    p.a = a.dy;
+    p.b = h;
+    p.lda = p.M = a.d;
+    p.ldb = p.N = a.ff;
+    p.K = M;
+    p.out = a.dw_down;
+    e = gf_product<true, true>(p, part, s);
+  }
+  return e;
+}
+
+}  // namespace bmoe

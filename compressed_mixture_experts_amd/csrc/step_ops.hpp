@@ -1,5 +1,6 @@
 // Launchers of the training-step operators (include/bmoe_norm.h,
-// include/bmoe_update.h, include/bmoe_adamw.h, include/bmoe_block.h).
+// include/bmoe_update.h, include/bmoe_adamw.h, include/bmoe_block.h,
+// include/bmoe_ffn.h).
 #pragma once
 
 #include "common.hpp"
@@ -137,5 +138,34 @@ struct BnBwdArgs {
 size_t bn_bwd_workspace(int rows, int width);
 hipError_t launch_block_norm_fwd(const BnFwdArgs& a, int act, hipStream_t s);
 hipError_t launch_block_norm_bwd(const BnBwdArgs& a, int act, int dact, hipStream_t s);
+
+// Dense gated feed-forward block (gated_ffn.hip), bf16.
+struct GfFwdArgs {
+  const uint16_t* x;        // [tokens][d]
+  const uint16_t* w_in;     // [2 ff][d]
+  const uint16_t* w_down;   // [d][ff]
+  const uint16_t* add;      // [tokens][d] or null
+  uint16_t* y;              // [tokens][d]
+  uint16_t* state;          // [tokens][2 ff], [tokens][ff], then bytes [tokens][ff]; or null
+  void* ws;
+  int32_t tokens, d, ff, gelu;
+};
+struct GfBwdArgs {
+  const uint16_t* x;
+  const uint16_t* w_in;
+  const uint16_t* w_down;
+  const uint16_t* dy;       // [tokens][d]
+  const uint16_t* state;
+  const float* dx_add;      // [tokens][d] or null
+  uint16_t* dx;             // [tokens][d] or null
+  uint16_t* dw_in;          // [2 ff][d] or null
+  uint16_t* dw_down;        // [d][ff] or null
+  void* ws;
+  int32_t tokens, d, ff, gelu;
+};
+size_t gf_forward_workspace(int tokens, int d, int ff, bool with_state);
+size_t gf_backward_workspace(int tokens, int d, int ff);
+hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s);
+hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s);
 
 }  // namespace bmoe

@@ -706,3 +706,31 @@ def block_norm_backward(dy, b, s, stats, gate, alpha, scale, post, kind, gp, bp,
     out["gamma_post"], out["beta_post"] = (dz * bhat).sum(axis=0), dz.sum(axis=0)
     out["b"] = row_norm_backward(dz * one(gp), bhat, stats[:, 1], kind) if post else dz
     return out
+
+
+# ---------------------------------------------------------------- gated feed-forward block
+def gated_act(g, act: str):
+    """(act(g), act'(g)) of "silu" or "gelu"."""
+    if act == "silu":
+        s = 1.0 / (1.0 + np.exp(-g))
+        return g * s, s * (1.0 + g * (1.0 - s))
+    cdf = 0.5 * (1.0 + np.vectorize(math.erf)(g / math.sqrt(2.0)))
+    return g * cdf, cdf + g * np.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi)
+
+
+def gated_ffn(x, w_in, w_down, act: str):
+    """(y, g, u, h) of the dense gated feed-forward block."""
+    ff = w_down.shape[1]
+    gu = x @ w_in.T
+    g, u = gu[:, :ff], gu[:, ff:]
+    h = gated_act(g, act)[0] * u
+    return h @ w_down.T, g, u, h
+
+
+def gated_ffn_backward(x, w_in, w_down, dy, act: str):
+    """Gradients of sum(dy y): (dx, dw_in, dw_down)."""
+    _, g, u, h = gated_ffn(x, w_in, w_down, act)
+    a, slope = gated_act(g, act)
+    dh = dy @ w_down
+    dgu = np.concatenate([dh * u * slope, dh * a], axis=1)
+    return dgu @ w_in, dgu.T @ x, dy.T @ h

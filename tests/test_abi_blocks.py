@@ -1,4 +1,5 @@
-"""Argument errors of the operators around a layer (include/bmoe_adamw.h, bmoe_block.h): each is
+"""Argument errors of the operators around a layer (include/bmoe_adamw.h, bmoe_block.h,
+bmoe_ffn.h): each is
 found on the host before anything is enqueued, so the pointers here are never followed.
 No GPU needed."""
 import ctypes
@@ -201,6 +202,57 @@ def test_block_norm_nothing_to_do_and_sizes():
     assert bm.lib().bmoe_block_norm_backward_workspace(None, ctypes.byref(n)) == NULL
     assert bm.lib().bmoe_block_norm_backward_workspace(ctypes.byref(d), None) == NULL
     assert ctypes.sizeof(blocks._BlockNorm) == 10 * 4 + 5 * 8 and ctypes.sizeof(blocks._BlockNormGrads) == 5 * 8
+
+
+FFN = dict(tokens=100, d=64, ff=128, act=0, x=ptr(0), w_in=ptr(1), w_down=ptr(2), add=ptr(3), y=ptr(4), state=ptr(5), state_bytes=1 << 40,
+           ws=ptr(6), ws_bytes=1 << 40, stream=None)
+FFN_BWD = dict(tokens=100, d=64, ff=128, act=0, x=ptr(0), w_in=ptr(1), w_down=ptr(2), dy=ptr(3), state=ptr(4), state_bytes=1 << 40, dx_add=ptr(5),
+               dx=ptr(6), dw_in=ptr(7), dw_down=ptr(8), ws=ptr(9), ws_bytes=1 << 40, stream=None)
+
+FFN_SHAPES = [dict(tokens=-1), dict(tokens=(1 << 24) + 1), dict(d=0), dict(d=12), dict(d=16392), dict(ff=0), dict(ff=20), dict(ff=65544),
+              dict(d=16384, ff=65536), dict(tokens=1 << 24, ff=4104), dict(d=-8)]
+FFN_REFUSED = [(c, SHAPE) for c in FFN_SHAPES] + [
+    (dict(act=2), DTYPE), (dict(act=-1), DTYPE), (dict(x=None), NULL), (dict(w_in=None), NULL), (dict(w_down=None), NULL), (dict(y=None), NULL),
+    (dict(state=None, ws=None), NULL), (dict(x=ptr(0) + 8), ALIGN), (dict(add=ptr(3) + 2), ALIGN), (dict(state=ptr(5) + 4), ALIGN),
+    (dict(state=None, ws=ptr(6) + 8), ALIGN), (dict(state_bytes=100 * 7 * 128 - 1), WORKSPACE), (dict(state=None, ws_bytes=100), WORKSPACE),
+    (dict(y=ptr(0)), ALIAS), (dict(y=ptr(3) + 16), ALIAS), (dict(y=ptr(5)), ALIAS), (dict(state=ptr(1)), ALIAS), (dict(state=ptr(2) - 16), ALIAS),
+    (dict(state=None, ws=ptr(0)), ALIAS), (dict(state=None, ws=ptr(4)), ALIAS),
+]
+
+
+@pytest.mark.parametrize("change,status", FFN_REFUSED, ids=lambda v: str(v)[:60])
+def test_gated_ffn_forward_refusals(change, status):
+    assert bm.lib().bmoe_gated_ffn_forward(*dict(FFN, **change).values()) == status
+    assert bm.lib().bmoe_last_error() != b""
+
+
+FFN_BWD_REFUSED = [(c, SHAPE) for c in FFN_SHAPES] + [
+    (dict(act=3), DTYPE), (dict(x=None), NULL), (dict(dy=None), NULL), (dict(state=None), NULL), (dict(ws=None), NULL), (dict(w_in=None), NULL),
+    (dict(dx=ptr(6) + 8), ALIGN), (dict(dw_in=ptr(7) + 2), ALIGN), (dict(dx_add=ptr(5) + 4), ALIGN), (dict(ws=ptr(9) + 8), ALIGN),
+    (dict(state_bytes=100), WORKSPACE), (dict(ws_bytes=1000), WORKSPACE), (dict(dx=ptr(3)), ALIAS), (dict(dx=ptr(5)), ALIAS), (dict(dw_in=ptr(1)), ALIAS),
+    (dict(dw_down=ptr(7) + 64), ALIAS), (dict(ws=ptr(4)), ALIAS), (dict(ws=ptr(8)), ALIAS), (dict(dw_down=ptr(0) + 16), ALIAS),
+]
+
+
+@pytest.mark.parametrize("change,status", FFN_BWD_REFUSED, ids=lambda v: str(v)[:60])
+def test_gated_ffn_backward_refusals(change, status):
+    assert bm.lib().bmoe_gated_ffn_backward(*dict(FFN_BWD, **change).values()) == status
+
+
+def test_gated_ffn_sizes_and_nothing_to_do():
+    L, n = bm.lib(), ctypes.c_size_t(77)
+    assert L.bmoe_gated_ffn_forward(*dict(FFN, tokens=0, x=None, y=None).values()) == 0
+    assert L.bmoe_gated_ffn_backward(*dict(FFN_BWD, dx=None, dw_in=None, dw_down=None, x=None).values()) == 0
+    assert L.bmoe_gated_ffn_state_size(10, 64, ctypes.byref(n)) == 0 and n.value == 10 * 7 * 64
+    assert L.bmoe_gated_ffn_state_size(10, 64, None) == NULL and L.bmoe_gated_ffn_state_size(10, 63, ctypes.byref(n)) == SHAPE
+    assert L.bmoe_gated_ffn_forward_workspace(10, 64, 64, 2, ctypes.byref(n)) == SHAPE
+    # few tokens need the activated product alone, and with a state nothing
+    for tokens in (1, 32):
+        assert L.bmoe_gated_ffn_forward_workspace(tokens, 64, 64, 1, ctypes.byref(n)) == 0 and n.value == 0
+        assert L.bmoe_gated_ffn_forward_workspace(tokens, 64, 64, 0, ctypes.byref(n)) == 0 and tokens * 128 <= n.value < tokens * 128 + 256
+    for tokens, d, ff in ((1, 8, 8), (33, 2048, 8192), (1 << 20, 2048, 8192), (4096, 16384, 32768)):
+        for call in ((L.bmoe_gated_ffn_forward_workspace, (tokens, d, ff, 0)), (L.bmoe_gated_ffn_backward_workspace, (tokens, d, ff))):
+            assert call[0](*call[1], ctypes.byref(n)) == 0 and tokens * ff * 2 <= n.value < tokens * ff * 4 + (4 << 30)
 
 
 def test_refusals_under_host_sanitizers():

@@ -79,3 +79,25 @@ def test_block_norm_backward_matches_differences():
                         up[name][i] += 1e-5
                         dn[name][i] -= 1e-5
                         assert abs((loss(up) - loss(dn)) / 2e-5 - got[name][i]) < 1e-6, (kind, post, name)
+
+
+def test_gated_ffn_backward_matches_differences():
+    r = np.random.default_rng(6)
+    for act in ("silu", "gelu"):
+        args = [r.standard_normal((3, 4)), r.standard_normal((10, 4)), r.standard_normal((4, 5))]
+        dy = r.standard_normal((3, 4))
+        for k, grad in enumerate(ref.gated_ffn_backward(*args, dy, act)):
+            for i in np.ndindex(args[k].shape):
+                up, dn = [a.copy() for a in args], [a.copy() for a in args]
+                up[k][i] += 1e-5
+                dn[k][i] -= 1e-5
+                diff = ((dy * ref.gated_ffn(*up, act)[0]).sum() - (dy * ref.gated_ffn(*dn, act)[0]).sum()) / 2e-5
+                assert abs(diff - grad[i]) < 1e-7, (act, k)
+
+
+def test_gated_activations():
+    g = np.array([-40.0, -1.0, 0.0, 1.0, 40.0])
+    a, s = ref.gated_act(g, "silu")
+    assert np.allclose(a, [0, -0.2689414213699951, 0, 0.7310585786300049, 40]) and s[2] == 0.5 and np.isclose(s[4], 1)
+    a, s = ref.gated_act(g, "gelu")
+    assert np.allclose(a, [0, -0.15865525393145707, 0, 0.8413447460685429, 40]) and s[2] == 0.5 and np.isclose(s[4], 1)
