@@ -336,45 +336,41 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
       });
       return;
     }
-    // h and the kept factors take the places of g and u
-    uint2 h[IN / 2][IM];
+    // h, the kept factors and their further bits take the places of g and u: 7 of 8 words
 #pragma unroll
     for (int j = 0; j < IM; ++j)
 #pragma unroll
       for (int i = 0; i < IN; i += 2) {
         f32x4_t o;
+        uint32_t kp[4], ka[4], fine = 0;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const float2 f = gf_act_slope<F>(acc[i][j][r]);
           const float u = acc[i + 1][j][r];
           o[r] = f.x * u;
           const GfKept k = gf_keep(u * f.y, f.x);
-          acc[i][j][r] = __uint_as_float(k.p);
-          acc[i + 1][j][r] = __uint_as_float(k.a);
+          kp[r] = k.p;
+          ka[r] = k.a;
+          fine |= gf_fine(k) << (8 * r);
         }
-        h[i / 2][j] = pack(o);
-        asm volatile("" : "+v"(acc[i][j]), "+v"(acc[i + 1][j]));
+        auto upper = [](uint32_t x, uint32_t y) { return x >> 16 | (y & 0xFFFF0000u); };
+        const uint2 h = pack(o);
+        acc[i][j] = __builtin_bit_cast(f32x4_t, make_uint4(h.x, h.y, upper(kp[0], kp[1]), upper(kp[2], kp[3])));
+        acc[i + 1][j] = __builtin_bit_cast(f32x4_t, make_uint4(upper(ka[0], ka[1]), upper(ka[2], ka[3]), fine, 0));
+        asm volatile("" : "+v"(acc[i][j]), "+v"(acc[i + 1][j]));   // here, not where they are stored
       }
-    auto upper = [](f32x4_t v) {
-      return make_uint2(__float_as_uint(v[0]) >> 16 | (__float_as_uint(v[1]) & 0xFFFF0000u),
-                        __float_as_uint(v[2]) >> 16 | (__float_as_uint(v[3]) & 0xFFFF0000u));
-    };
-    put(two{}, p.out, p.ff, c0, p.ff, [&](int i, int j) { return h[i / 2][j]; });
-    put(two{}, p.pa, 2 * p.ff, c0, p.ff, [&](int i, int j) { return upper(acc[i][j]); });
-    put(two{}, p.pa + p.ff, 2 * p.ff, c0, p.ff, [&](int i, int j) { return upper(acc[i + 1][j]); });
+    auto words = [](f32x4_t v) { return __builtin_bit_cast(uint4, v); };
+    put(two{}, p.out, p.ff, c0, p.ff, [&](int i, int j) { return make_uint2(words(acc[i][j]).x, words(acc[i][j]).y); });
+    put(two{}, p.pa, 2 * p.ff, c0, p.ff, [&](int i, int j) { return make_uint2(words(acc[i][j]).z, words(acc[i][j]).w); });
+    put(two{}, p.pa + p.ff, 2 * p.ff, c0, p.ff, [&](int i, int j) { return make_uint2(words(acc[i + 1][j]).x, words(acc[i + 1][j]).y); });
     constexpr int W = T / 2, ST = W / 4 + 1;   // columns, 4-byte words of a staged row
     uint32_t* bytes = reinterpret_cast<uint32_t*>(sm);
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < IM; ++j)
 #pragma unroll
-      for (int i = 0; i < IN; i += 2) {
-        uint32_t v = 0;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          v |= gf_fine(GfKept{__float_as_uint(acc[i][j][r]), __float_as_uint(acc[i + 1][j][r])}) << (8 * r);
-        bytes[(PM * wm + 16 * j + l16) * ST + (PN * wn + 16 * i) / 8 + g] = v;
-      }
+      for (int i = 0; i < IN; i += 2)
+        bytes[(PM * wm + 16 * j + l16) * ST + (PN * wn + 16 * i) / 8 + g] = words(acc[i + 1][j]).z;
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < T * W / 8 / NT; ++q) {
