@@ -88,7 +88,7 @@ __device__ __forceinline__ float gf_kept_a(uint32_t bf16, uint32_t fine) { retur
 //
 // LDS, contraction contiguous: [T rows][64], 16-byte chunk c of row r at c ^ (r % 8); a lane
 // reads its 8 values of depth as one 16-byte chunk.  Other side contiguous: [64 depths][T],
-// chunk c of depth k at c ^ 2 (k % 8); 16 lanes read 4 depths of 16 rows as 8 bytes each
+// chunk c of depth k at c ^ 2 (k % 4); 16 lanes read 4 depths of 16 rows as 8 bytes each
 // and get 4 depths of their row.
 //
 // A step is two 32-deep halves with a set of fragments each: the reads of the next half
@@ -138,7 +138,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
         const int w = wave * LPW + j - (isb ? T / 8 : 0);
         if constexpr (TURNED) {
           constexpr int RC = T / 8, RPL = 64 / RC;
-          const int k = w * RPL + lane / RC, c = (lane % RC) ^ (2 * (k & (T / 16 - 1) & 7));
+          const int k = w * RPL + lane / RC, c = (lane % RC) ^ (2 * (k & 3));
           off[j] = 2u * (uint32_t(k) * uint32_t(ld) + uint32_t(min(first + 8 * c, count - 8) - first));
           deep[j] = k;
         } else {
@@ -163,10 +163,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
   auto load = [&](int kt, int buf) {
     const int s = k0 + min(kt, nk - 1);   // past the last one: the last one again, never read
     const char* src = base + size_t(s) * advance - (s > 0 ? back : 0);
+    // the step's address in scalar registers, the lane's offsets as they are: an address of 64
+    // bits per lane and load takes 16 registers and an addition each
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(src), 0, -1, 0x00027000);
     uint16_t* dst = sm + buf * STAGE + wave * LPW * 512;
 #pragma unroll
     for (int j = 0; j < LPW; ++j)
-      __builtin_amdgcn_global_load_lds((gf_glob_t*)(src + off[j]), (gf_lds_t*)(dst + 512 * j), 16, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (gf_lds_t*)(dst + 512 * j), 16, int(off[j]), 0, 0, 0);
   };
   // step 0 of the whole depth: zeros behind its last value
   auto load_short = [&](int buf) {
@@ -188,13 +191,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
   auto read_one = [&](auto turned, const uint16_t* tile, int row, int h, auto& f) {
     constexpr int COUNT = sizeof(f) / sizeof(f[0]);
     if constexpr (decltype(turned)::value) {
-      const int k = 32 * h + 8 * g + (l16 >> 2), s = l16 >> 1 & 1;
-      const int swz = 2 * ((l16 >> 2) & (T / 16 - 1)), more = T >= 128 ? 64 : 0;   // 4 depths on: chunk ^ 8
+      // of four blocks next to each other; the others are 64 values on
+      constexpr int FOUR = COUNT < 4 ? COUNT : 4;
+      const uint16_t* q[FOUR];
+#pragma unroll
+      for (int j = 0; j < FOUR; ++j)
+        q[j] = tile + (8 * g + (l16 >> 2)) * T + 16 * ((row / 16 + j) ^ (l16 >> 2)) + 4 * (l16 & 3);
 #pragma unroll
       for (int j = 0; j < COUNT; ++j) {
-        const int at = 8 * ((row / 8 + 2 * j + s) ^ swz) + 4 * (l16 & 1);
-        const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gf_lds4_t*)(tile + k * T + at));
-        const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gf_lds4_t*)(tile + (k + 4) * T + (at ^ more)));
+        const uint16_t* at = q[j % FOUR] + 32 * h * T + 64 * (j / FOUR);
+        const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gf_lds4_t*)at);
+        const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gf_lds4_t*)(at + 4 * T));
         typedef short i16x8_t __attribute__((ext_vector_type(8)));
         f[j] = __builtin_bit_cast(bf16x8_t, i16x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
       }
