@@ -23,7 +23,6 @@ typedef __attribute__((address_space(3))) void gf_lds_t;
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t gf_lds4_t;
 
-constexpr int GF_K = 64;          // contraction step
 constexpr int GF_CUS = 256;       // of a whole MI355X
 constexpr int GF_SPLIT = 16;      // most workgroups that share a tile's depth
 constexpr int GF_FEW = 32;        // most tokens of the kernel that reads weights straight into registers
@@ -83,25 +82,27 @@ __device__ __forceinline__ uint32_t gf_fine(GfKept v) { return (v.p >> 12 & 15u)
 __device__ __forceinline__ float gf_kept_p(uint32_t bf16, uint32_t fine) { return __uint_as_float(bf16 << 16 | (fine & 15u) << 12); }
 __device__ __forceinline__ float gf_kept_a(uint32_t bf16, uint32_t fine) { return __uint_as_float(bf16 << 16 | (fine & 0xF0u) << 8); }
 
-// One workgroup per T x T tile of D[m][n] = sum_k A[m][k] B[n][k], WM x WN waves of
-// T / WM x T / WN each (MFMA blocks of 16 x 16 x 32), NBUF steps in the ring.
+// One workgroup per TM x TN tile of D[m][n] = sum_k A[m][k] B[n][k], WM x WN waves of
+// TM / WM x TN / WN each (MFMA blocks of 16 x 16 x 32), NBUF steps of depth BK in the ring.
 //
-// LDS, contraction contiguous: [T rows][64], 16-byte chunk c of row r at c ^ (r % 8); a lane
-// reads its 8 values of depth as one 16-byte chunk.  Other side contiguous: [64 depths][T],
-// chunk c of depth k at c ^ 2 (k % 4); 16 lanes read 4 depths of 16 rows as 8 bytes each
-// and get 4 depths of their row.
+// LDS, contraction contiguous: [rows][BK], 16-byte chunk c of row r at c ^ (r % 8), in steps
+// of 32 at c ^ (r / 2 % 4); a lane reads its 8 values of depth as one 16-byte chunk.  Other
+// side contiguous: [BK depths][rows], chunk c of depth k at c ^ 2 (k % 4); 16 lanes read 4
+// depths of 16 rows as 8 bytes each and get 4 depths of their row.
 //
-// A step is two 32-deep halves with a set of fragments each: the reads of the next half
+// A step's 32-deep halves have a set of fragments each in turn: the reads of the next half
 // are issued among the products of the current one, and the barrier that frees a ring
-// place stands between the halves.  The first step of a depth that is no multiple of 64 is
-// the short one: it is loaded ahead of the loop, so the loop has no case for it.
-template <bool AT, bool BT, int EPI, int F, int T, int WM, int WN, int NBUF>
+// place stands in front of a step's last products.  The first step of a depth that is no
+// multiple of BK is the short one: it is loaded ahead of the loop, so the loop has no case
+// for it.
+template <bool AT, bool BT, int EPI, int F, int TM, int TN, int BK, int WM, int WN, int NBUF>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
+#if defined(__HIP_DEVICE_COMPILE__)   // the host's pass knows no buffer resources and would drop the kernel
   constexpr int NW = WM * WN, NT = 64 * NW;
-  constexpr int PM = T / WM, PN = T / WN, IM = PM / 16, IN = PN / 16;
-  constexpr int STAGE = 2 * T * GF_K;            // halves of a ring place: A's, then B's
-  constexpr int LPW = 2 * T / 8 / NW;            // loads per wave and step
-  static_assert(T / 8 % LPW == 0, "no wave loads both operands");
+  constexpr int PM = TM / WM, PN = TN / WN, IM = PM / 16, IN = PN / 16, H = BK / 32;
+  constexpr int STAGE = (TM + TN) * BK;          // halves of a ring place: A's, then B's
+  constexpr int LA = TM * BK / 512 / NW, LB = TN * BK / 512 / NW;   // loads per wave and step
+  static_assert(TM * BK % (512 * NW) == 0 && TN * BK % (512 * NW) == 0, "whole loads per wave");
   static_assert(EPI != GF_GATE || IN % 2 == 0, "gate and up blocks in pairs");
   extern __shared__ __attribute__((aligned(16))) uint16_t sm[];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -116,69 +117,71 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
   t -= r0 * p.nn;
   const int hh = min(p.band, p.nm - r0);
   const int tn = t / hh, tm = r0 + t - tn * hh;
-  const int m0 = tm * T, n0 = tn * T;
-  const int nk1 = (p.K + GF_K - 1) / GF_K, short_by = nk1 * GF_K - p.K;
+  const int m0 = tm * TM, n0 = tn * TN;
+  const int nk1 = (p.K + BK - 1) / BK, short_by = nk1 * BK - p.K;
   const int k0 = share * p.per, nk = min(p.per, nk1 - k0);
 
-  // this wave's loads: all of A or all of B, byte offsets of this lane's pieces from the
-  // tile's first element; rows and columns past the matrix read its last ones and are
-  // not stored
-  const bool isb = wave * LPW >= T / 8;
-  uint32_t off[LPW];
-  int deep[LPW];            // depth within a step of the lane's first value
-  const char* base;
-  size_t advance;           // bytes of a step
-  {
-    auto place = [&](auto turned, const uint16_t* q, int ld, int first, int count, bool gate) {
-      constexpr bool TURNED = decltype(turned)::value;
-      base = reinterpret_cast<const char*>(q + (TURNED ? size_t(first) : gate ? size_t(0) : size_t(first) * ld));
-      advance = TURNED ? size_t(GF_K) * ld * 2 : GF_K * 2;
+  // one operand's loads of this wave: byte offsets of this lane's pieces from the tile's
+  // first element; rows and columns past the matrix read its last ones and are not stored
+  auto place = [&](auto turned, auto side, const uint16_t* q, int ld, int first, int count, bool gate, auto& off, auto& deep, size_t& advance) {
+    constexpr bool TURNED = decltype(turned)::value;
+    constexpr int T = decltype(side)::value, L = T * BK / 512 / NW;
+    advance = TURNED ? size_t(BK) * ld * 2 : BK * 2;
 #pragma unroll
-      for (int j = 0; j < LPW; ++j) {
-        const int w = wave * LPW + j - (isb ? T / 8 : 0);
-        if constexpr (TURNED) {
-          constexpr int RC = T / 8, RPL = 64 / RC;
-          const int k = w * RPL + lane / RC, c = (lane % RC) ^ (2 * (k & 3));
-          off[j] = 2u * (uint32_t(k) * uint32_t(ld) + uint32_t(min(first + 8 * c, count - 8) - first));
-          deep[j] = k;
+    for (int j = 0; j < L; ++j) {
+      const int w = wave * L + j;
+      if constexpr (TURNED) {
+        constexpr int RC = T / 8, RPL = 64 / RC;
+        const int k = w * RPL + lane / RC, c = (lane % RC) ^ (2 * (k & 3));
+        off[j] = 2u * (uint32_t(k) * uint32_t(ld) + uint32_t(min(first + 8 * c, count - 8) - first));
+        deep[j] = k;
+      } else {
+        constexpr int RC = BK / 8, RPL = 64 / RC;
+        const int r = lane / RC, row = w * RPL + r, c = (lane % RC) ^ (BK == 64 ? r & 7 : r >> 1 & 3);
+        uint32_t at;
+        if (gate) {   // blocks of 16 rows of Wg and Wu in turn
+          const int half = min(first / 2 + 16 * (row >> 5) + (row & 15), p.ff - 1);
+          at = uint32_t(half + (row & 16 ? p.ff : 0));
         } else {
-          const int row = 8 * w + (lane >> 3), c = (lane & 7) ^ (lane >> 3);
-          uint32_t at;
-          if (gate) {   // blocks of 16 rows of Wg and Wu in turn
-            const int half = min(first / 2 + 16 * (row >> 5) + (row & 15), p.ff - 1);
-            at = uint32_t(half + (row & 16 ? p.ff : 0));
-          } else {
-            at = uint32_t(min(first + row, count - 1) - first);
-          }
-          off[j] = 2u * (at * uint32_t(ld) + 8u * c);
-          deep[j] = 8 * c;
+          at = uint32_t(min(first + row, count - 1) - first);
         }
+        off[j] = 2u * (at * uint32_t(ld) + 8u * c);
+        deep[j] = 8 * c;
       }
-    };
-    if (isb) place(std::integral_constant<bool, BT>{}, p.b, p.ldb, n0, p.N, EPI == GF_GATE);
-    else place(std::integral_constant<bool, AT>{}, p.a, p.lda, m0, p.M, false);
-  }
-  // bytes that the first step is short by: the steps behind it start that much earlier
-  const size_t back = short_by ? advance / GF_K * short_by : 0;
+    }
+    return reinterpret_cast<const char*>(q + (TURNED ? size_t(first) : gate ? size_t(0) : size_t(first) * ld));
+  };
+  uint32_t aoff[LA], boff[LB];
+  int adeep[LA], bdeep[LB];   // depth within a step of the lane's first value
+  size_t astep, bstep;        // bytes of a step
+  const char* abase = place(std::integral_constant<bool, AT>{}, std::integral_constant<int, TM>{}, p.a, p.lda, m0, p.M, false, aoff, adeep, astep);
+  const char* bbase = place(std::integral_constant<bool, BT>{}, std::integral_constant<int, TN>{}, p.b, p.ldb, n0, p.N, EPI == GF_GATE, boff, bdeep, bstep);
+  auto place_of = [&](int buf, bool b) { return sm + buf * STAGE + (b ? TM * BK + wave * LB * 512 : wave * LA * 512); };
   auto load = [&](int kt, int buf) {
     const int s = k0 + min(kt, nk - 1);   // past the last one: the last one again, never read
-    const char* src = base + size_t(s) * advance - (s > 0 ? back : 0);
-    // the step's address in scalar registers, the lane's offsets as they are: an address of 64
-    // bits per lane and load takes 16 registers and an addition each
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(src), 0, -1, 0x00027000);
-    uint16_t* dst = sm + buf * STAGE + wave * LPW * 512;
+    // bytes that the first step is short by: the steps behind it start that much earlier.
+    // The step's address is in scalar registers, the lane's offsets as they are: an address of
+    // 64 bits per lane and load takes 16 registers and an addition each
+    auto at = [&](const char* base, size_t step) {
+      return const_cast<char*>(base + size_t(s) * step - (s > 0 ? step / BK * short_by : 0));
+    };
+    const auto ra = __builtin_amdgcn_make_buffer_rsrc(at(abase, astep), 0, -1, 0x00027000);
+    const auto rb = __builtin_amdgcn_make_buffer_rsrc(at(bbase, bstep), 0, -1, 0x00027000);
 #pragma unroll
-    for (int j = 0; j < LPW; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (gf_lds_t*)(dst + 512 * j), 16, int(off[j]), 0, 0, 0);
+    for (int j = 0; j < LA; ++j) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (gf_lds_t*)(place_of(buf, false) + 512 * j), 16, int(aoff[j]), 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < LB; ++j) __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (gf_lds_t*)(place_of(buf, true) + 512 * j), 16, int(boff[j]), 0, 0, 0);
   };
   // step 0 of the whole depth: zeros behind its last value
-  auto load_short = [&](int buf) {
-    uint16_t* dst = sm + buf * STAGE + wave * LPW * 512;
+  auto load_short = [&]() {
+    auto one = [&](const char* base, uint32_t off, int deep, uint16_t* dst) {
+      const char* at = deep < BK - short_by ? base + off : reinterpret_cast<const char*>(&gf_zeros);
+      __builtin_amdgcn_global_load_lds((gf_glob_t*)at, (gf_lds_t*)dst, 16, 0, 0);
+    };
 #pragma unroll
-    for (int j = 0; j < LPW; ++j) {
-      const char* at = deep[j] < GF_K - short_by ? base + off[j] : reinterpret_cast<const char*>(&gf_zeros);
-      __builtin_amdgcn_global_load_lds((gf_glob_t*)at, (gf_lds_t*)(dst + 512 * j), 16, 0, 0);
-    }
+    for (int j = 0; j < LA; ++j) one(abase, aoff[j], adeep[j], place_of(0, false) + 512 * j);
+#pragma unroll
+    for (int j = 0; j < LB; ++j) one(bbase, boff[j], bdeep[j], place_of(0, true) + 512 * j);
   };
 
   f32x4_t acc[IN][IM];
@@ -188,8 +191,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
     for (int j = 0; j < IM; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   bf16x8_t fa[2][IM], fb[2][IN];
   // one operand's fragments of half h: COUNT blocks of 16 rows from `row` on
-  auto read_one = [&](auto turned, const uint16_t* tile, int row, int h, auto& f) {
-    constexpr int COUNT = sizeof(f) / sizeof(f[0]);
+  auto read_one = [&](auto turned, auto side, const uint16_t* tile, int row, int h, auto& f) {
+    constexpr int T = decltype(side)::value, COUNT = sizeof(f) / sizeof(f[0]);
     if constexpr (decltype(turned)::value) {
       // of four blocks next to each other; the others are 64 values on
       constexpr int FOUR = COUNT < 4 ? COUNT : 4;
@@ -206,14 +209,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
         f[j] = __builtin_bit_cast(bf16x8_t, i16x8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
       }
     } else {
-      const uint16_t* q = tile + (row + l16) * GF_K + 8 * ((4 * h + g) ^ (l16 & 7));
+      const uint16_t* q = tile + (row + l16) * BK + 8 * ((4 * h + g) ^ (BK == 64 ? l16 & 7 : l16 >> 1 & 3));
 #pragma unroll
-      for (int j = 0; j < COUNT; ++j) f[j] = *reinterpret_cast<const bf16x8_t*>(q + 16 * j * GF_K);
+      for (int j = 0; j < COUNT; ++j) f[j] = *reinterpret_cast<const bf16x8_t*>(q + 16 * j * BK);
     }
   };
   auto read = [&](int buf, int h, bf16x8_t (&a)[IM], bf16x8_t (&b)[IN]) {
-    read_one(std::integral_constant<bool, AT>{}, sm + buf * STAGE, PM * wm, h, a);
-    read_one(std::integral_constant<bool, BT>{}, sm + buf * STAGE + T * GF_K, PN * wn, h, b);
+    read_one(std::integral_constant<bool, AT>{}, std::integral_constant<int, TM>{}, sm + buf * STAGE, PM * wm, h, a);
+    read_one(std::integral_constant<bool, BT>{}, std::integral_constant<int, TN>{}, sm + buf * STAGE + TM * BK, PN * wn, h, b);
   };
   auto mul = [&](const bf16x8_t (&a)[IM], const bf16x8_t (&b)[IN]) {
 #pragma unroll
@@ -242,13 +245,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
   // this wave's reads are done and its loads of all but the newest steps have arrived;
   // then the same of every wave
   auto arrive = [&]() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * LPW) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NBUF - 2) * (LA + LB)) : "memory");
   };
   if (k0 == 0 && short_by) {
-    load_short(0);
+    load_short();
     if (nk == 1) {   // the loads past it read no more than it has
 #pragma unroll
-      for (int j = 0; j < LPW; ++j) off[j] = deep[j] < GF_K - short_by ? off[j] : 0;
+      for (int j = 0; j < LA; ++j) aoff[j] = adeep[j] < BK - short_by ? aoff[j] : 0;
+#pragma unroll
+      for (int j = 0; j < LB; ++j) boff[j] = bdeep[j] < BK - short_by ? boff[j] : 0;
     }
   } else {
     load(0, 0);
@@ -259,17 +264,34 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
   load(NBUF - 1, NBUF - 1);
   read(0, 0, fa[0], fb[0]);
   int buf = 0;
-  for (int kt = 0; kt < nk; ++kt) {
+  // a step whose first half is in the fragments `set`
+  auto step = [&](int kt, auto set) {
+    constexpr int P = decltype(set)::value;
     const int next = buf + 1 == NBUF ? 0 : buf + 1;
-    read(buf, 1, fa[1], fb[1]);
-    mul(fa[0], fb[0]);
-    spread(std::integral_constant<int, 0>{});
+    if constexpr (H == 2) {
+      read(buf, 1, fa[1 - P], fb[1 - P]);
+      mul(fa[P], fb[P]);
+      spread(std::integral_constant<int, 0>{});
+    }
+    constexpr int Q = H == 2 ? 1 - P : P;
     arrive();
-    read(next, 0, fa[0], fb[0]);
+    read(next, 0, fa[1 - Q], fb[1 - Q]);
     load(kt + NBUF, buf);
-    mul(fa[1], fb[1]);
-    spread(std::integral_constant<int, LPW>{});
+    mul(fa[Q], fb[Q]);
+    spread(std::integral_constant<int, LA + LB>{});
     buf = next;
+  };
+  using even = std::integral_constant<int, 0>;
+  using odd = std::integral_constant<int, 1>;
+  if constexpr (H == 2) {
+    for (int kt = 0; kt < nk; ++kt) step(kt, even{});
+  } else {
+    int kt = 0;
+    for (; kt + 1 < nk; kt += 2) {
+      step(kt, even{});
+      step(kt + 1, odd{});
+    }
+    if (kt < nk) step(kt, even{});
   }
   // loads past the last step may still be writing to the ring
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -293,7 +315,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
   // to a staged tile of W columns, and that in rows of 16 bytes to dst, W columns from c0 on
   // inside `cols`
   auto put = [&](auto by, uint16_t* dst, int ld, int c0, int cols, auto&& f) {
-    constexpr int BY = decltype(by)::value, W = T / BY, ST = W + 4;
+    constexpr int BY = decltype(by)::value, W = TN / BY, ST = W + 4;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < IM; ++j)
@@ -302,7 +324,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
         *reinterpret_cast<uint2*>(st + (PM * wm + 16 * j + l16) * ST + (PN * wn + 16 * i) / BY + 4 * g) = f(i, j);
     __syncthreads();
 #pragma unroll 4
-    for (int q = 0; q < T * W / 8 / NT; ++q) {
+    for (int q = 0; q < TM * W / 8 / NT; ++q) {
       const int k = tid + NT * q, r = k / (W / 8), c = 8 * (k % (W / 8));
       if (m0 + r >= p.M || c0 + c >= cols) continue;
       const uint2 lo = *reinterpret_cast<const uint2*>(st + r * ST + c), hi = *reinterpret_cast<const uint2*>(st + r * ST + c + 4);
@@ -367,64 +389,92 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
         asm volatile("" : "+v"(acc[i][j]), "+v"(acc[i + 1][j]));   // here, not where they are stored
       }
     auto words = [](f32x4_t v) { return __builtin_bit_cast(uint4, v); };
-    put(two{}, p.out, p.ff, c0, p.ff, [&](int i, int j) { return make_uint2(words(acc[i][j]).x, words(acc[i][j]).y); });
-    put(two{}, p.pa, 2 * p.ff, c0, p.ff, [&](int i, int j) { return make_uint2(words(acc[i][j]).z, words(acc[i][j]).w); });
-    put(two{}, p.pa + p.ff, 2 * p.ff, c0, p.ff, [&](int i, int j) { return make_uint2(words(acc[i + 1][j]).x, words(acc[i + 1][j]).y); });
-    constexpr int W = T / 2, ST = W / 4 + 1;   // columns, 4-byte words of a staged row
-    uint32_t* bytes = reinterpret_cast<uint32_t*>(sm);
+    // both factors beside each other, then h and the bytes
+    constexpr int W = TN / 2, SF = TN + 4, SH = W + 4, SB = W / 4 + 1;   // halves, halves, words of a staged row
+    uint32_t* bytes = reinterpret_cast<uint32_t*>(sm + TM * SH);
+    auto each = [&](auto&& f) {   // f(row, column of this lane's first value, i, j)
+#pragma unroll
+      for (int j = 0; j < IM; ++j)
+#pragma unroll
+        for (int i = 0; i < IN; i += 2) f(PM * wm + 16 * j + l16, (PN * wn + 16 * i) / 2 + 4 * g, i, j);
+    };
+    auto eight = [&](int at) {
+      const uint2 lo = *reinterpret_cast<const uint2*>(st + at), hi = *reinterpret_cast<const uint2*>(st + at + 4);
+      return make_uint4(lo.x, lo.y, hi.x, hi.y);
+    };
+    each([&](int r, int c, int i, int j) {
+      *reinterpret_cast<uint2*>(st + r * SF + c) = make_uint2(words(acc[i][j]).z, words(acc[i][j]).w);
+      *reinterpret_cast<uint2*>(st + r * SF + W + c) = make_uint2(words(acc[i + 1][j]).x, words(acc[i + 1][j]).y);
+    });
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < IM; ++j)
-#pragma unroll
-      for (int i = 0; i < IN; i += 2)
-        bytes[(PM * wm + 16 * j + l16) * ST + (PN * wn + 16 * i) / 8 + g] = words(acc[i + 1][j]).z;
+#pragma unroll 4
+    for (int q = 0; q < TM * TN / 8 / NT; ++q) {
+      const int k = tid + NT * q, r = k / (TN / 8), c = 8 * (k % (TN / 8)), h = c0 + c % W;
+      if (m0 + r < p.M && h < p.ff) *reinterpret_cast<uint4*>(p.pa + size_t(m0 + r) * 2 * p.ff + (c < W ? 0 : p.ff) + h) = eight(r * SF + c);
+    }
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < T * W / 8 / NT; ++q) {
+    each([&](int r, int c, int i, int j) {
+      *reinterpret_cast<uint2*>(st + r * SH + c) = make_uint2(words(acc[i][j]).x, words(acc[i][j]).y);
+      bytes[r * SB + c / 4] = words(acc[i + 1][j]).z;
+    });
+    __syncthreads();
+#pragma unroll 4
+    for (int q = 0; q < TM * W / 8 / NT; ++q) {
       const int k = tid + NT * q, r = k / (W / 8), c = 8 * (k % (W / 8));
       if (m0 + r >= p.M || c0 + c >= p.ff) continue;
-      *reinterpret_cast<uint2*>(p.fine + size_t(m0 + r) * p.ff + c0 + c) = make_uint2(bytes[r * ST + c / 4], bytes[r * ST + c / 4 + 1]);
+      const size_t at = size_t(m0 + r) * p.ff + c0 + c;
+      *reinterpret_cast<uint4*>(p.out + at) = eight(r * SH + c);
+      *reinterpret_cast<uint2*>(p.fine + at) = make_uint2(bytes[r * SB + c / 4], bytes[r * SB + c / 4 + 1]);
     }
   } else if constexpr (EPI == GF_GRAD) {
-    // acc is dh; dg and du take its place as bf16
+    // dh goes through LDS in fp32, PM rows at a time, so that its factors are read and dg and
+    // du written in whole rows; the factors are on their way while it does
+    constexpr int ST = TN + 4, PIECES = PM * TN / 8 / NT, PER = PIECES < 4 ? PIECES : 4;
+    float* dh = reinterpret_cast<float*>(sm);
 #pragma unroll
-    for (int j = 0; j < IM; ++j) {
-      const size_t m = min(m0 + PM * wm + 16 * j + l16, p.M - 1);
-      uint2 pv[IN], av[IN];
-      uint32_t fv[IN];
+    for (int part = 0; part < WM; ++part) {
+      if (part > 0) __syncthreads();
+      if (wm == part) {
 #pragma unroll
-      for (int i = 0; i < IN; ++i) {
-        const int n = min(n0 + PN * wn + 16 * i + 4 * g, p.ff - 4);
-        pv[i] = *reinterpret_cast<const uint2*>(p.pa + m * 2 * p.ff + n);
-        av[i] = *reinterpret_cast<const uint2*>(p.pa + m * 2 * p.ff + p.ff + n);
-        fv[i] = *reinterpret_cast<const uint32_t*>(p.fine + m * p.ff + n);
+        for (int j = 0; j < IM; ++j)
+#pragma unroll
+          for (int i = 0; i < IN; ++i) *reinterpret_cast<f32x4_t*>(dh + (16 * j + l16) * ST + PN * wn + 16 * i + 4 * g) = acc[i][j];
       }
 #pragma unroll
-      for (int i = 0; i < IN; ++i) {
-        f32x4_t dg, du;
+      for (int q0 = 0; q0 < PIECES; q0 += PER) {
+        uint4 pv[PER], av[PER];
+        uint2 fv[PER];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t x = (r & 2 ? pv[i].y : pv[i].x) >> (16 * (r & 1)), y = (r & 2 ? av[i].y : av[i].x) >> (16 * (r & 1));
-          dg[r] = acc[i][j][r] * gf_kept_p(x, fv[i] >> (8 * r));
-          du[r] = acc[i][j][r] * gf_kept_a(y, fv[i] >> (8 * r));
+        for (int q = 0; q < PER; ++q) {
+          const int k = tid + NT * (q0 + q), r = k / (TN / 8), c = 8 * (k % (TN / 8));
+          const size_t m = min(m0 + PM * part + r, p.M - 1);
+          const int n = min(n0 + c, p.ff - 8);
+          pv[q] = *reinterpret_cast<const uint4*>(p.pa + m * 2 * p.ff + n);
+          av[q] = *reinterpret_cast<const uint4*>(p.pa + m * 2 * p.ff + p.ff + n);
+          fv[q] = *reinterpret_cast<const uint2*>(p.fine + m * p.ff + n);
         }
-        const uint2 x = pack(dg), y = pack(du);
-        acc[i][j] = __builtin_bit_cast(f32x4_t, make_uint4(x.x, x.y, y.x, y.y));
-        asm volatile("" : "+v"(acc[i][j]));   // here, not where du is stored: its factors and dh would live until then
+        if (q0 == 0) __syncthreads();
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+          const int k = tid + NT * (q0 + q), r = k / (TN / 8), c = 8 * (k % (TN / 8));
+          const uint32_t pw[4] = {pv[q].x, pv[q].y, pv[q].z, pv[q].w}, aw[4] = {av[q].x, av[q].y, av[q].z, av[q].w}, fw[2] = {fv[q].x, fv[q].y};
+          uint32_t dg[4], du[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 d = *reinterpret_cast<const float2*>(dh + r * ST + c + 2 * e);
+            const uint32_t f = fw[e / 2] >> (16 * (e & 1));
+            dg[e] = pack_bf16x2(d.x * gf_kept_p(pw[e], f), d.y * gf_kept_p(pw[e] >> 16, f >> 8));
+            du[e] = pack_bf16x2(d.x * gf_kept_a(aw[e], f), d.y * gf_kept_a(aw[e] >> 16, f >> 8));
+          }
+          if (m0 + PM * part + r >= p.M || n0 + c >= p.ff) continue;
+          uint16_t* out = p.out + size_t(m0 + PM * part + r) * 2 * p.ff + n0 + c;
+          *reinterpret_cast<uint4*>(out) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+          *reinterpret_cast<uint4*>(out + p.ff) = make_uint4(du[0], du[1], du[2], du[3]);
+        }
       }
-      // one row of blocks at a time: the loads of all would take the registers
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
     }
-    put(one{}, p.out, 2 * p.ff, n0, p.ff, [&](int i, int j) {
-      const uint4 u = __builtin_bit_cast(uint4, acc[i][j]);
-      return make_uint2(u.x, u.y);
-    });
-    put(one{}, p.out + p.ff, 2 * p.ff, n0, p.ff, [&](int i, int j) {
-      const uint4 u = __builtin_bit_cast(uint4, acc[i][j]);
-      return make_uint2(u.z, u.w);
-    });
   }
+#endif
 }
 
 // The shares' sums, added in order, and what is added to them.
@@ -557,7 +607,7 @@ GfTile gf_pick(int M, int N, int K, bool may_split) {
   };
   GfTile best{0, 1};
   double least = 0;
-  const int steps = (K + GF_K - 1) / GF_K;
+  const int steps = (K + 63) / 64;
   for (const Side s : {Side{64, 2, 0.29, 2.0}, Side{128, 1, 0.41, 3.0}, Side{256, 1, 1.2, 5.0}}) {
     const int64_t tiles = gf_tiles(M, N, s.side);
     for (int split = 1; split <= (may_split ? GF_SPLIT : 1); ++split) {
@@ -578,15 +628,18 @@ GfTile gf_pick(int M, int N, int K, bool may_split) {
 size_t gf_part_bytes(int M, int N, GfTile t) { return t.split > 1 ? size_t(t.split) * M * N * 4 : 0; }
 size_t gf_round(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
-template <bool AT, bool BT, int EPI, int F, int T, int WM, int WN, int NBUF>
+template <bool AT, bool BT, int EPI, int F, int TM, int TN, int BK, int WM, int WN, int NBUF>
 hipError_t gf_go(GfGemm p, hipStream_t s) {
-  constexpr size_t ring = size_t(NBUF) * 2 * T * GF_K * 2, stage = size_t(T) * (T + 4) * 2;
+  // the ring; staged tiles of bf16, or of fp32 in WM parts
+  constexpr size_t ring = size_t(NBUF) * (TM + TN) * BK * 2;
+  constexpr size_t stage = EPI == GF_GRAD ? size_t(TM / WM) * (TN + 4) * 4 : size_t(TM) * (TN + 4) * 2;
   constexpr size_t lds = ring > stage ? ring : stage;
-  const auto kernel = gf_gemm_kernel<AT, BT, EPI, F, T, WM, WN, NBUF>;
+  const auto kernel = gf_gemm_kernel<AT, BT, EPI, F, TM, TN, BK, WM, WN, NBUF>;
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
   if (e != hipSuccess) return e;
-  p.nm = (p.M + T - 1) / T;
-  p.nn = (p.N + T - 1) / T;
+  p.nm = (p.M + TM - 1) / TM;
+  p.nn = (p.N + TN - 1) / TN;
+  p.per = ((p.K + BK - 1) / BK + p.split - 1) / p.split;
   p.band = std::min(p.nm, 8);
   hipLaunchKernelGGL(kernel, dim3(unsigned(int64_t(p.nm) * p.nn * p.split)), dim3(64 * WM * WN), lds, s, p);
   return hipGetLastError();
@@ -594,9 +647,9 @@ hipError_t gf_go(GfGemm p, hipStream_t s) {
 
 template <bool AT, bool BT, int EPI, int F = GF_SILU>
 hipError_t gf_side(const GfGemm& p, int side, hipStream_t s) {
-  if (side == 64) return gf_go<AT, BT, EPI, F, 64, 2, 2, 4>(p, s);
-  if (side == 128) return gf_go<AT, BT, EPI, F, 128, 2, 4, 3>(p, s);
-  return gf_go<AT, BT, EPI, F, 256, 2, 4, 2>(p, s);
+  if (side == 64) return gf_go<AT, BT, EPI, F, 64, 64, 64, 2, 2, 4>(p, s);
+  if (side == 128) return gf_go<AT, BT, EPI, F, 128, 128, 64, 2, 4, 3>(p, s);
+  return gf_go<AT, BT, EPI, F, 256, 256, 64, 2, 4, 2>(p, s);
 }
 
 // A product whose result is written as it is (plus what is added), in shares where the
@@ -605,7 +658,6 @@ template <bool AT, bool BT>
 hipError_t gf_product(GfGemm p, float* part, hipStream_t s) {
   const GfTile t = gf_pick(p.M, p.N, p.K, true);
   p.split = t.split;
-  p.per = ((p.K + GF_K - 1) / GF_K + t.split - 1) / t.split;
   if (t.split == 1) return gf_side<AT, BT, GF_OUT>(p, t.side, s);
   p.part = part;
   const hipError_t e = gf_side<AT, BT, GF_PART>(p, t.side, s);
@@ -659,7 +711,6 @@ hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
   p.M = M;
   p.N = 2 * a.ff;
   p.split = 1;
-  p.per = (p.K + GF_K - 1) / GF_K;
   p.out = h;
   p.pa = pa;
   p.fine = fine;
@@ -709,8 +760,7 @@ hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
     p.ldb = p.N = p.ff = a.ff;
     p.M = M;
     p.split = 1;
-    p.per = (p.K + GF_K - 1) / GF_K;
-    p.out = dgu;
+      p.out = dgu;
     p.pa = const_cast<uint16_t*>(a.state);
     p.fine = reinterpret_cast<uint8_t*>(p.pa + size_t(M) * 3 * a.ff);
     const int side = gf_pick(M, p.N, p.K, false).side;
