@@ -11,6 +11,7 @@
 // way from LDS to registers (ds_read_b64_tr_b16), so no transposed copy of anything is
 // written.
 #include "butterfly_impl.hpp"
+#include "row_ops.hpp"
 #include "step_ops.hpp"
 
 #include <algorithm>
@@ -25,7 +26,7 @@ typedef __attribute__((address_space(3))) i16x4_t gf_lds4_t;
 
 constexpr int GF_CUS = 256;       // of a whole MI355X
 constexpr int GF_SPLIT = 16;      // most workgroups that share a tile's depth
-constexpr int GF_FEW = 32;        // most tokens of the kernel that reads weights straight into registers
+constexpr int GF_FEW = 4;         // most tokens of the kernel that takes them one by one
 
 // what the places of a step past a ragged depth are filled with
 __device__ const uint4 gf_zeros = {0, 0, 0, 0};
@@ -493,10 +494,13 @@ __global__ __launch_bounds__(256) void gf_reduce_kernel(const float* part, int s
   *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
 }
 
-// Few tokens: bound by the weights' bytes.  A workgroup takes 16 rows of a weight (GATE: of
-// Wg and of Wu), its waves a part of the depth each; weights come from memory into
-// registers as MFMA operands, 16 bytes per lane, U steps of 32 on their way at a time, and
-// the tokens' rows, which the caches hold, the same way.  NT blocks of 16 tokens.
+// Few tokens: bound by the weights' bytes, each of which is read once, a row's 1024 at a
+// time by a wave (16 bytes per lane), and multiplied in fp32 without the matrix cores: with
+// TOK tokens 8 + 8 TOK operations on 8 weights, 6 us of the 20 that 100 MB take at TOK = 4.
+// (One token, d 2048, ff 8192: 23 us, 4.3 TB/s with both launches; as operands of MFMA,
+// 64 bytes of 16 rows at a time, 30, in tiles of 64 28.  8 tokens: 39, in tiles 28.)
+// A wave takes four rows (GATE: two of Wg and of Wu each), DEEP steps of 512 of their depth
+// on their way at a time; `parts` waves of a workgroup share the depth of the same rows.
 struct GfFew {
   const uint16_t* x;        // [M][K]
   const uint16_t* w;        // [R][K], GATE: [2 R][K]
@@ -504,82 +508,93 @@ struct GfFew {
   uint16_t* out;            // [M][R]
   uint16_t* pa;             // GATE: [M][2 R] or null
   uint8_t* fine;            // GATE: [M][R] when pa is set
-  int32_t M, R, K;
+  int32_t M, R, K, parts;
 };
-template <bool GATE, int F, int NT>
-__global__ __launch_bounds__(1024) void gf_few_kernel(GfFew p) {
-  constexpr int NWT = GATE ? 2 : 1, U = GATE || NT > 1 ? 4 : 8;
-  extern __shared__ __attribute__((aligned(16))) float red[];   // [waves][NWT][NT][16 tokens][20]
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
-  const int l16 = lane & 15, g = lane >> 4, row0 = 16 * blockIdx.x;
-  const int steps = (p.K + 31) / 32, per = (steps + waves - 1) / waves, s0 = wave * per, s1 = min(s0 + per, steps);
-  const uint16_t* w[NWT];
-  const uint16_t* x[NT];
+constexpr int GF_FEW_WAVES = 8;
+template <bool GATE, int F, int TOK>
+__global__ __launch_bounds__(64 * GF_FEW_WAVES) void gf_few_kernel(GfFew p) {
+  constexpr int ROWS = GATE ? 2 : 4, DEEP = TOK > 2 ? 2 : 4;
+  __shared__ float red[GF_FEW_WAVES][4][TOK];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int groups = GF_FEW_WAVES / p.parts, part = wave % p.parts;
+  const int row0 = (blockIdx.x * groups + wave / p.parts) * ROWS;
+  const int steps = (p.K + 511) / 512, per = (steps + p.parts - 1) / p.parts, s0 = part * per, s1 = min(s0 + per, steps);
+  const uint16_t* w[4];
+  const uint16_t* x[TOK];
 #pragma unroll
-  for (int k = 0; k < NWT; ++k) w[k] = p.w + size_t(min(row0 + l16, p.R - 1) + k * p.R) * p.K + 8 * g;
+  for (int r = 0; r < 4; ++r) w[r] = p.w + size_t(min(row0 + r % ROWS, p.R - 1) + r / ROWS * p.R) * p.K;
 #pragma unroll
-  for (int k = 0; k < NT; ++k) x[k] = p.x + size_t(min(16 * k + l16, p.M - 1)) * p.K + 8 * g;
-  f32x4_t acc[NWT][NT] = {};
-  const bf16x8_t zero = {};
-  auto round = [&](int s, auto whole) {
-    constexpr bool WHOLE = decltype(whole)::value;
-    bf16x8_t fw[U][NWT], fx[U][NT];
+  for (int m = 0; m < TOK; ++m) x[m] = p.x + size_t(min(m, p.M - 1)) * p.K;
+  float acc[4][TOK] = {};
+  for (int s = s0; s < s1; s += DEEP) {
+    uint4 wv[DEEP][4], xv[DEEP][TOK];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      // depths past the end are read at the last whole chunk and made zero
-      const int k = 32 * (s + u), at = WHOLE ? k : min(k, p.K - 8 - 8 * g);
+    for (int u = 0; u < DEEP; ++u) {
+      const int at = min(512 * (s + u) + 8 * lane, p.K - 8);   // past the end the last one, which counts as zeros
 #pragma unroll
-      for (int i = 0; i < NWT; ++i) fw[u][i] = *reinterpret_cast<const bf16x8_t*>(w[i] + at);
+      for (int r = 0; r < 4; ++r) wv[u][r] = *reinterpret_cast<const uint4*>(w[r] + at);
 #pragma unroll
-      for (int i = 0; i < NT; ++i) fx[u][i] = *reinterpret_cast<const bf16x8_t*>(x[i] + at);
+      for (int m = 0; m < TOK; ++m) xv[u][m] = *reinterpret_cast<const uint4*>(x[m] + at);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!WHOLE) {
-        const bool in = s + u < s1 && 32 * (s + u) + 8 * g < p.K;
+    for (int u = 0; u < DEEP; ++u) {
+      const bool in = s + u < s1 && 512 * (s + u) + 8 * lane < p.K;
+      float xf[TOK][8];
 #pragma unroll
-        for (int i = 0; i < NWT; ++i) fw[u][i] = in ? fw[u][i] : zero;
+      for (int m = 0; m < TOK; ++m) {
+        const uint32_t q[4] = {xv[u][m].x, xv[u][m].y, xv[u][m].z, xv[u][m].w};
 #pragma unroll
-        for (int i = 0; i < NT; ++i) fx[u][i] = in ? fx[u][i] : zero;
+        for (int e = 0; e < 4; ++e) {
+          xf[m][2 * e] = in ? bf16lo(q[e]) : 0.f;
+          xf[m][2 * e + 1] = in ? bf16hi(q[e]) : 0.f;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < NWT; ++i)
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t q[4] = {wv[u][r].x, wv[u][r].y, wv[u][r].z, wv[u][r].w};
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[u][i], fx[u][j], acc[i][j], 0, 0, 0);
-    }
-  };
-  int s = s0;
-  for (; s + U <= s1 && 32 * (s + U) <= p.K; s += U) round(s, std::true_type{});
-  for (; s < s1; s += U) round(s, std::false_type{});
-  // acc[i][j][r] = D[row 4 g + r][token 16 j + l16]
+        for (int e = 0; e < 4; ++e) {
+          const float lo = in ? bf16lo(q[e]) : 0.f, hi = in ? bf16hi(q[e]) : 0.f;
 #pragma unroll
-  for (int i = 0; i < NWT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      *reinterpret_cast<f32x4_t*>(red + (((wave * NWT + i) * NT + j) * 16 + l16) * 20 + 4 * g) = acc[i][j];
-  __syncthreads();
-  for (int e = threadIdx.x; e < 256 * NT; e += blockDim.x) {
-    const int r = e & 15, m = e >> 4;
-    if (m >= p.M || row0 + r >= p.R) continue;
-    float v[NWT] = {};
-    for (int k = 0; k < waves; ++k)
-#pragma unroll
-      for (int i = 0; i < NWT; ++i) v[i] += red[((k * NWT + i) * NT * 16 + m) * 20 + r];
-    const size_t at = size_t(m) * p.R + row0 + r;
-    if constexpr (GATE) {
-      if (p.pa) {
-        const float2 f = gf_act_slope<F>(v[0]);
-        const GfKept k = gf_keep(v[1] * f.y, f.x);
-        p.pa[at + size_t(m) * p.R] = uint16_t(k.p >> 16);
-        p.pa[at + size_t(m + 1) * p.R] = uint16_t(k.a >> 16);
-        p.fine[at] = uint8_t(gf_fine(k));
+          for (int m = 0; m < TOK; ++m) {
+            acc[r][m] = fmaf(lo, xf[m][2 * e], acc[r][m]);
+            acc[r][m] = fmaf(hi, xf[m][2 * e + 1], acc[r][m]);
+          }
+        }
       }
-      v[0] = gf_act<F>(v[0]) * v[1];
-    } else if (p.add) {
-      v[0] += load1<ACT_BF16>(p.add, at);
     }
-    p.out[at] = uint16_t(pack_bf16x2(v[0], v[0]));
   }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int m = 0; m < TOK; ++m) {
+      const float v = ln_wave_sum<64>(acc[r][m]);
+      if (lane == 0) red[wave][r][m] = v;
+    }
+  __syncthreads();
+  // one value of the result each
+  const int e = threadIdx.x, m = e % TOK, r = e / TOK % ROWS, group = e / (TOK * ROWS);
+  const int row = (blockIdx.x * groups + group) * ROWS + r;
+  if (group >= groups || m >= p.M || row >= p.R) return;
+  float v = 0.f, u = 0.f;
+  for (int k = group * p.parts; k < (group + 1) * p.parts; ++k) {
+    v += red[k][r][m];
+    if (GATE) u += red[k][(ROWS + r) & 3][m];
+  }
+  const size_t at = size_t(m) * p.R + row;
+  if constexpr (GATE) {
+    if (p.pa) {
+      const float2 f = gf_act_slope<F>(v);
+      const GfKept k = gf_keep(u * f.y, f.x);
+      p.pa[at + size_t(m) * p.R] = uint16_t(k.p >> 16);
+      p.pa[at + size_t(m + 1) * p.R] = uint16_t(k.a >> 16);
+      p.fine[at] = uint8_t(gf_fine(k));
+    }
+    v = gf_act<F>(v) * u;
+  } else if (p.add) {
+    v += load1<ACT_BF16>(p.add, at);
+  }
+  p.out[at] = uint16_t(pack_bf16x2(v, v));
 }
 
 __global__ __launch_bounds__(256) void gf_zero_kernel(uint16_t* out, size_t n) {
@@ -590,34 +605,49 @@ __global__ __launch_bounds__(256) void gf_zero_kernel(uint16_t* out, size_t n) {
 // ------------------------------------------------------------------ host
 namespace {
 
+// Tiles a product may have.  GF_128 has eight waves of 64 x 32 and a CU of its own, GF_128_2
+// four of 64 x 64 and shares the CU with a second workgroup.
+enum GfTiling { GF_64, GF_128, GF_128_2, GF_256 };
 struct GfTile {
-  int side, split;
+  GfTiling tiling;
+  int split;
 };
+constexpr int gf_tile_side(GfTiling t) { return t == GF_64 ? 64 : t == GF_256 ? 256 : 128; }
 
-int64_t gf_tiles(int M, int N, int side) { return int64_t((M + side - 1) / side) * ((N + side - 1) / side); }
-
-// A product's tile side and the workgroups that share a tile's depth, by a time estimate in
+// A product's tiles and the workgroups that share a tile's depth, by a time estimate in
 // microseconds: rounds of workgroups over the CUs, a step of 64 by the lone workgroup of
 // a CU or by each of two, a tile's beginning and end; shares are written and read again in
-// fp32 by a launch behind.
-GfTile gf_pick(int M, int N, int K, bool may_split) {
-  struct Side {
-    int side, per_cu;
-    double step, once;
+// fp32 by a launch behind.  Operands turned in LDS take longer, their reads being half as
+// wide.  The constants are fitted to 16 products of 0.6 to 1100 GFLOP, each with every
+// tile and split forced (M x N x K, us: 16384 x 2048 x 8192 as x W^T, 256 405, 128_2 467, 128 516,
+// 64 777; 2736 x 512 x 4001 as dy^T x, 128_2 in 5 shares 27.5, 64 39.2; 4096 x 1024 x 4096 128 32.8,
+// 128_2 in 2 shares 41.1, 64 46.2; 256 x 2048 x 8192 64 in 2 shares 17.7, 128 in 8 18.3); a
+// pick is within a tenth of the best of them.
+GfTile gf_pick(int M, int N, int K, bool turned, bool may_split) {
+  struct Option {
+    GfTiling tiling;
+    int per_cu;
+    double lone[2], shared[2], once;   // steps: plain, turned
   };
-  GfTile best{0, 1};
+  constexpr Option options[] = {{GF_64, 2, {0.2, 0.45}, {0.42, 0.62}, 3.0},
+                                {GF_128, 1, {0.48, 0.8}, {0, 0}, 2.0},
+                                {GF_128_2, 2, {0.66, 0.8}, {0.91, 1.1}, 3.0},
+                                {GF_256, 1, {1.58, 1.8}, {0, 0}, 4.0}};
+  GfTile best{GF_64, 1};
   double least = 0;
   const int steps = (K + 63) / 64;
-  for (const Side s : {Side{64, 2, 0.29, 2.0}, Side{128, 1, 0.41, 3.0}, Side{256, 1, 1.2, 5.0}}) {
-    const int64_t tiles = gf_tiles(M, N, s.side);
+  for (const Option& o : options) {
+    const int side = gf_tile_side(o.tiling);
+    const int64_t tiles = int64_t((M + side - 1) / side) * ((N + side - 1) / side);
     for (int split = 1; split <= (may_split ? GF_SPLIT : 1); ++split) {
       const int per = (steps + split - 1) / split;
-      if (split > 1 && ((split - 1) * per >= steps || per < 4)) continue;
-      const double rounds = double((tiles * split + GF_CUS * s.per_cu - 1) / (GF_CUS * s.per_cu));
-      double time = rounds * (per * s.step + s.once);
-      if (split > 1) time += 3.0 + double(M) * N * split * 8 / 4e6;
-      if (!best.side || time < least) {
-        best = GfTile{s.side, split};
+      if (split > 1 && ((split - 1) * per >= steps || per < 4)) break;
+      const int64_t n = tiles * split;
+      const double step = o.per_cu == 1 || n <= GF_CUS ? o.lone[turned] : o.shared[turned];
+      double time = double((n + GF_CUS * o.per_cu - 1) / (GF_CUS * o.per_cu)) * (per * step + o.once);
+      if (split > 1) time += 3.0 + double(M) * N * split / 1e6;
+      if (least == 0 || time < least) {
+        best = GfTile{o.tiling, split};
         least = time;
       }
     }
@@ -646,9 +676,10 @@ hipError_t gf_go(GfGemm p, hipStream_t s) {
 }
 
 template <bool AT, bool BT, int EPI, int F = GF_SILU>
-hipError_t gf_side(const GfGemm& p, int side, hipStream_t s) {
-  if (side == 64) return gf_go<AT, BT, EPI, F, 64, 64, 64, 2, 2, 4>(p, s);
-  if (side == 128) return gf_go<AT, BT, EPI, F, 128, 128, 64, 2, 4, 3>(p, s);
+hipError_t gf_tiled(const GfGemm& p, GfTiling t, hipStream_t s) {
+  if (t == GF_64) return gf_go<AT, BT, EPI, F, 64, 64, 64, 2, 2, 4>(p, s);
+  if (t == GF_128) return gf_go<AT, BT, EPI, F, 128, 128, 64, 2, 4, 3>(p, s);
+  if (t == GF_128_2) return gf_go<AT, BT, EPI, F, 128, 128, 64, 2, 2, 2>(p, s);
   return gf_go<AT, BT, EPI, F, 256, 256, 64, 2, 4, 2>(p, s);
 }
 
@@ -656,11 +687,11 @@ hipError_t gf_side(const GfGemm& p, int side, hipStream_t s) {
 // estimate says so.
 template <bool AT, bool BT>
 hipError_t gf_product(GfGemm p, float* part, hipStream_t s) {
-  const GfTile t = gf_pick(p.M, p.N, p.K, true);
+  const GfTile t = gf_pick(p.M, p.N, p.K, AT || BT, true);
   p.split = t.split;
-  if (t.split == 1) return gf_side<AT, BT, GF_OUT>(p, t.side, s);
+  if (t.split == 1) return gf_tiled<AT, BT, GF_OUT>(p, t.tiling, s);
   p.part = part;
-  const hipError_t e = gf_side<AT, BT, GF_PART>(p, t.side, s);
+  const hipError_t e = gf_tiled<AT, BT, GF_PART>(p, t.tiling, s);
   if (e != hipSuccess) return e;
   const size_t n = size_t(p.M) * p.N;
   hipLaunchKernelGGL(gf_reduce_kernel, dim3(unsigned((n / 4 + 255) / 256)), dim3(256), 0, s, part, t.split, n, p.out, p.add16, p.add32);
@@ -668,17 +699,14 @@ hipError_t gf_product(GfGemm p, float* part, hipStream_t s) {
 }
 
 template <bool GATE, int F = GF_SILU>
-hipError_t gf_few(const GfFew& p, hipStream_t s) {
-  // waves of a workgroup: 2048 in all (eight to a CU), down to 4 steps of the depth each
-  const int groups = (p.R + 15) / 16, steps = (p.K + 31) / 32;
-  int waves = 4;
-  while (waves < 16 && groups * waves < 2048 && steps / waves > 4) waves *= 2;
-  const int nt = p.M > 16 ? 2 : 1;
-  const size_t lds = size_t(waves) * (GATE ? 2 : 1) * nt * 16 * 20 * 4;
-  const auto kernel = nt == 2 ? gf_few_kernel<GATE, F, 2> : gf_few_kernel<GATE, F, 1>;
-  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(kernel, dim3(unsigned(groups)), dim3(64 * waves), lds, s, p);
+hipError_t gf_few(GfFew p, hipStream_t s) {
+  // waves that share rows: 4096 in all (16 to a CU), down to one step of the depth each
+  const int blocks = (p.R + (GATE ? 1 : 3)) / (GATE ? 2 : 4), steps = (p.K + 511) / 512;
+  p.parts = 1;
+  while (p.parts < GF_FEW_WAVES && int64_t(blocks) * p.parts < 4096 && 2 * p.parts <= steps) p.parts *= 2;
+  const int groups = GF_FEW_WAVES / p.parts;
+  const auto kernel = p.M == 1 ? gf_few_kernel<GATE, F, 1> : p.M == 2 ? gf_few_kernel<GATE, F, 2> : gf_few_kernel<GATE, F, 4>;
+  hipLaunchKernelGGL(kernel, dim3(unsigned((blocks + groups - 1) / groups)), dim3(64 * GF_FEW_WAVES), 0, s, p);
   return hipGetLastError();
 }
 
@@ -687,7 +715,7 @@ hipError_t gf_few(const GfFew& p, hipStream_t s) {
 size_t gf_forward_workspace(int tokens, int d, int ff, bool with_state) {
   if (tokens == 0) return 0;
   const size_t h = with_state ? 0 : gf_round(size_t(tokens) * ff * 2);
-  return h + (tokens <= GF_FEW ? 0 : gf_part_bytes(tokens, d, gf_pick(tokens, d, ff, true)));
+  return h + (tokens <= GF_FEW ? 0 : gf_part_bytes(tokens, d, gf_pick(tokens, d, ff, false, true)));
 }
 
 hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
@@ -700,9 +728,9 @@ hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
   uint16_t* h = a.state ? a.state + size_t(M) * 2 * a.ff : reinterpret_cast<uint16_t*>(ws);
   float* part = reinterpret_cast<float*>(ws + (a.state ? 0 : gf_round(size_t(M) * a.ff * 2)));
   if (M <= GF_FEW) {
-    const GfFew gate{a.x, a.w_in, nullptr, h, pa, fine, M, a.ff, a.d};
+    const GfFew gate{a.x, a.w_in, nullptr, h, pa, fine, M, a.ff, a.d, 1};
     const hipError_t e = a.gelu ? gf_few<true, GF_GELU>(gate, s) : gf_few<true, GF_SILU>(gate, s);
-    return e != hipSuccess ? e : gf_few<false>(GfFew{h, a.w_down, a.add, a.y, nullptr, nullptr, M, a.d, a.ff}, s);
+    return e != hipSuccess ? e : gf_few<false>(GfFew{h, a.w_down, a.add, a.y, nullptr, nullptr, M, a.d, a.ff, 1}, s);
   }
   GfGemm p{};
   p.a = a.x;
@@ -715,8 +743,8 @@ hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
   p.pa = pa;
   p.fine = fine;
   p.ff = a.ff;
-  const int side = gf_pick(M, p.N, p.K, false).side;
-  hipError_t e = a.gelu ? gf_side<false, false, GF_GATE, GF_GELU>(p, side, s) : gf_side<false, false, GF_GATE, GF_SILU>(p, side, s);
+  const GfTiling tiling = gf_pick(M, p.N, p.K, false, false).tiling;
+  hipError_t e = a.gelu ? gf_tiled<false, false, GF_GATE, GF_GELU>(p, tiling, s) : gf_tiled<false, false, GF_GATE, GF_SILU>(p, tiling, s);
   if (e != hipSuccess) return e;
   p = GfGemm{};
   p.a = h;
@@ -731,9 +759,9 @@ hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
 
 size_t gf_backward_workspace(int tokens, int d, int ff) {
   if (tokens == 0) return 0;
-  const size_t part = std::max({gf_part_bytes(tokens, d, gf_pick(tokens, d, 2 * ff, true)),
-                                gf_part_bytes(2 * ff, d, gf_pick(2 * ff, d, tokens, true)),
-                                gf_part_bytes(d, ff, gf_pick(d, ff, tokens, true))});
+  const size_t part = std::max({gf_part_bytes(tokens, d, gf_pick(tokens, d, 2 * ff, true, true)),
+                                gf_part_bytes(2 * ff, d, gf_pick(2 * ff, d, tokens, true, true)),
+                                gf_part_bytes(d, ff, gf_pick(d, ff, tokens, true, true))});
   return gf_round(size_t(tokens) * 2 * ff * 2) + part;
 }
 
@@ -763,8 +791,8 @@ hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
       p.out = dgu;
     p.pa = const_cast<uint16_t*>(a.state);
     p.fine = reinterpret_cast<uint8_t*>(p.pa + size_t(M) * 3 * a.ff);
-    const int side = gf_pick(M, p.N, p.K, false).side;
-    e = a.gelu ? gf_side<false, true, GF_GRAD, GF_GELU>(p, side, s) : gf_side<false, true, GF_GRAD, GF_SILU>(p, side, s);
+    const GfTiling tiling = gf_pick(M, p.N, p.K, true, false).tiling;
+    e = a.gelu ? gf_tiled<false, true, GF_GRAD, GF_GELU>(p, tiling, s) : gf_tiled<false, true, GF_GRAD, GF_SILU>(p, tiling, s);
     if (e != hipSuccess) return e;
   }
   if (a.dx) {

@@ -103,8 +103,10 @@ class Want:
 
 
 SHAPES = [
-    # few tokens: both numbers of blocks, depths that are no multiple of 32 or of a wave's share
-    (1, 8, 8), (1, 64, 128), (2, 72, 40), (15, 24, 264), (16, 128, 64), (17, 200, 136), (32, 512, 1000), (31, 1024, 2048), (5, 2048, 24),
+    # few tokens, one by one: depths below and beside whole steps of 512, shared among 1 to 8 waves
+    (1, 8, 8), (1, 64, 128), (2, 72, 40), (1, 520, 1032), (3, 512, 4104), (4, 2048, 264), (1, 1000, 16), (4, 8, 3000),
+    # the fewest of the others
+    (15, 24, 264), (16, 128, 64), (17, 200, 136), (32, 512, 1000), (31, 1024, 2048), (5, 2048, 24),
     # tiles of 64 and 128, ragged in every direction, depths below one step
     (33, 8, 8), (64, 64, 64), (65, 72, 136), (100, 16, 32), (127, 136, 8), (128, 128, 256), (129, 520, 264), (257, 264, 72), (300, 40, 1000),
     (1000, 256, 512), (1001, 512, 1368), (2000, 24, 56), (77, 1024, 2048),
@@ -153,7 +155,7 @@ def test_gate_closed_and_open():
     u = x.double() @ wi[ff:].double().T
     h = 128.0 * u * (torch.arange(ff, device="cuda") % 2 == 0)
     for act in ("silu", "gelu"):
-        for n in (7, tokens):
+        for n in (2, 7, tokens):
             y, state = bm.gated_ffn_forward_train(x[:n], wi, wd, act)
             want = h[:n] @ wd.double().T
             assert (y.double() == want.to(torch.bfloat16).double()).all()
@@ -168,7 +170,7 @@ def test_gate_closed_and_open():
 def test_bad_rows_stay_alone():
     """NaN and infinity in one token reach its own rows alone, at every tile's edge."""
     import torch
-    for tokens in (20, 100, 300):
+    for tokens in (4, 20, 100, 300):
         c = draw(tokens, 72, 136, 5)
         want, _ = bm.gated_ffn_forward_train(c["x"], c["w_in"], c["w_down"])
         for row, bad in ((0, float("nan")), (tokens - 1, float("inf")), (tokens // 2, float("nan"))):
@@ -188,7 +190,7 @@ def test_no_tokens_and_in_place():
     y, state = bm.gated_ffn_forward_train(z, c["w_in"], c["w_down"])
     dx, dwi, dwd = bm.gated_ffn_backward(z, c["w_in"], c["w_down"], z, state)
     assert y.shape == dx.shape == (0, 64) and (dwi == 0).all() and (dwd == 0).all()
-    for tokens in (9, 50):
+    for tokens in (3, 9, 50):
         want = bm.gated_ffn_forward(c["x"][:tokens], c["w_in"], c["w_down"], add=c["add"][:tokens])
         add = c["add"][:tokens].clone()
         assert bm.gated_ffn_forward(c["x"][:tokens], c["w_in"], c["w_down"], add=add, y=add) is add and (add == want).all()
