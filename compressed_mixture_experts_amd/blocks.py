@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import numpy as np
 
@@ -140,6 +141,7 @@ class AdamW:
         self._grad, self._grad_dtype = t["grad"], t["grad_dtype"]   # views of it
         self._shapes = [p.shape for p in self.params]
         self._coded = [i for i, b in enumerate(self.bits) if b == 8]
+        self._coded_shapes = [self._shapes[i] for i in self._coded]
         self._steps = int(steps)
         self._counter = torch.full((1,), self._steps, dtype=torch.int64, device=dev) if capturable else None
 
@@ -147,6 +149,15 @@ class AdamW:
     def steps(self) -> int:
         """The steps taken (capturable: read from the GPU, which waits for it)."""
         return self._steps if self._counter is None else int(self._counter.item())
+
+    def _fit(self, tensors, shapes, kinds) -> bool:
+        """Whether all are tensors of these shapes and types, dense on this GPU (a tenth of a
+        microsecond for each, where checks that name what is wrong take one)."""
+        torch = _torch()
+        if not all(map(torch.is_tensor, tensors)):
+            return False
+        return (set(map(torch.Tensor.get_device, tensors)) == {self.device.index} and [t.shape for t in tensors] == shapes and
+                {t.dtype for t in tensors} <= kinds and all(map(torch.Tensor.is_contiguous, tensors)))
 
     def step(self, grads, grad_scale=None) -> None:
         """One step: grads a list like params (fp32 or bf16; None: that tensor is left
@@ -157,13 +168,12 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         index = dev.index
-        if not all(g is None or (g.is_cuda and g.get_device() == index and g.shape == s and g.is_contiguous() and
-                                 (g.dtype is f32 or g.dtype is bf16)) for g, s in zip(grads, self._shapes)):
+        if not self._fit(grads, self._shapes, {f32, bf16}):
             for i, (g, s) in enumerate(zip(grads, self._shapes)):
                 if g is not None:
                     _tensor(f"grads[{i}]", g, bf16 if getattr(g, "dtype", None) == bf16 else f32, s, dev)
         self._grad[:] = [0 if g is None else g.data_ptr() for g in grads]
-        self._grad_dtype[:] = [BF16 if g is not None and g.dtype is bf16 else F32 for g in grads]
+        self._grad_dtype[:] = [F32 if g is None or g.dtype is f32 else BF16 for g in grads]
         a = _AdamWArgs()
         a.beta1, a.beta2 = self.betas
         a.eps, a.seed = self.eps, self.seed
@@ -202,12 +212,12 @@ class AdamW:
                 outs = [None] * count
             elif len(coded) < count and any(x is not None and b != 8 for x, b in zip(outs, self.bits)):
                 raise ValueError(f"{name} is for moments in 8 bits: None elsewhere")
-            for i in coded:
-                x = outs[i]
-                if x is None:
-                    x = torch.empty(self._shapes[i], dtype=kind, device=self.device)
-                elif not (x.is_cuda and x.dtype is kind and x.get_device() == index and x.shape == self._shapes[i] and x.is_contiguous()):
-                    _tensor(f"{name}[{i}]", x, kind, self._shapes[i], self.device)
+            given = [outs[i] for i in coded]
+            if not self._fit(given, self._coded_shapes, {kind}):
+                for k, (i, x) in enumerate(zip(coded, given)):
+                    given[k] = (torch.empty(self._shapes[i], dtype=kind, device=self.device) if x is None else
+                                _tensor(f"{name}[{i}]", x, kind, self._shapes[i], self.device))
+            for i, x in zip(coded, given):
                 out[i] = x
         if coded:
             table = self._table[coded]
@@ -289,6 +299,15 @@ def block_norm_forward(b, residual=None, gate=None, alpha: float = 1.0, scale: f
     return y, s_out, st
 
 
+@functools.lru_cache(maxsize=4096)
+def _block_norm_workspace(rows: int, width: int) -> int:
+    """bmoe_block_norm_backward_workspace: sizes alone decide."""
+    n, size = _BlockNorm(), ctypes.c_size_t(0)
+    n.rows, n.width = rows, width
+    _check(lib().bmoe_block_norm_backward_workspace(ctypes.byref(n), ctypes.byref(size)))
+    return int(size.value)
+
+
 @_on_device
 def block_norm_backward(dy, b, s, stats, gate=None, alpha: float = 1.0, scale: float = 1.0, post: bool = True, kind: str = "layer",
                         gamma_post=None, beta_post=None, gamma=None, d_sum=None, residual: bool = True, weight_grads: bool = True,
@@ -331,9 +350,7 @@ def block_norm_backward(dy, b, s, stats, gate=None, alpha: float = 1.0, scale: f
         if gate is not None and gate.dim() == 2:
             out["gate"] = torch.empty_like(b)
         g = _BlockNormGrads(*[None if out[k] is None else out[k].data_ptr() for k in ("gamma_post", "beta_post", "gate", "gamma", "beta")])
-        size = ctypes.c_size_t(0)
-        _check(lib().bmoe_block_norm_backward_workspace(ctypes.byref(n), ctypes.byref(size)))
-        nbytes = size.value
+        nbytes = _block_norm_workspace(rows, width)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     _check(lib().bmoe_block_norm_backward(
         ctypes.byref(n), BF16 if dy.dtype is torch.bfloat16 else F32, dy.data_ptr(), b.data_ptr(), s.data_ptr(), stats.data_ptr(),
