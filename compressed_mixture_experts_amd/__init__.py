@@ -315,6 +315,16 @@ class Layer:
         self.struct.prepared, self.struct.prepared_bytes = _ptr(view), need
         return self
 
+    def refresh(self):
+        """Build the prepared weights again, after the layer's angles, gate matrix or codes
+        changed (an optimiser's step), in the buffer that there is: graphs captured from
+        this layer read that one.  A no-op without prepared weights."""
+        if self._prep is not None:
+            with _torch().cuda.device(self.w_gate.device):
+                _check(lib().bmoe_prepare(ctypes.byref(self.struct), self.struct.prepared, self.struct.prepared_bytes,
+                                          _stream_handle()))
+        return self
+
     def unprepare(self):
         """Go back to building the prepared data inside every forward."""
         self.struct.prepared, self.struct.prepared_bytes = None, 0
@@ -467,10 +477,7 @@ class Layer:
         if rescale and w.is_cuda and _torch().cuda.is_current_stream_capturing():
             raise ValueError("rescale reads the scale on the host, which a captured step cannot do")
         w, _, scale = substrate_step(w, o, step, decay, w_out=w_out, packed=self.w_base[m])
-        if self._prep is not None:
-            with _torch().cuda.device(w.device):
-                _check(lib().bmoe_prepare(ctypes.byref(self.struct), self.struct.prepared, self.struct.prepared_bytes,
-                                          _stream_handle()))
+        self.refresh()
         if rescale:
             self.set_scale(m, scale)
         return w, scale

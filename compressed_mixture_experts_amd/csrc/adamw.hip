@@ -323,7 +323,7 @@ hipError_t aw_launches(const AwTensor* tensors, int count, const AwScalars& s, i
     blocks = 0;
     return hipGetLastError();
   };
-  constexpr int64_t kMost = int64_t(1) << 30;   // workgroups of a launch
+  constexpr int64_t kMost = (int64_t(1) << 24) - 1;   // workgroups of a launch: its threads fit 32 bits
   for (int k = 0; k < count; ++k) {
     const int64_t need = (tensors[k].n + a.run - 1) / a.run;
     if (need == 0) continue;

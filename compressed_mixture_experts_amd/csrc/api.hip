@@ -1702,7 +1702,7 @@ bmoe_status bmoe_substrate_step(int32_t rows, int32_t cols, const float* w, cons
 namespace {
 
 constexpr int32_t kMaxTensors = 1 << 20;
-constexpr int64_t kMaxValues = int64_t(1) << 40;
+constexpr int64_t kMaxValues = int64_t(1) << 33;   // 2^23 workgroups of 256
 
 // Sorts every kind's ranges by address, which they mostly are already, and looks for a
 // written one that overlaps any other.  The kinds below `written` are those.
@@ -1733,7 +1733,7 @@ bool disjoint(std::vector<std::vector<Range>>& kinds, size_t written) {
 }
 
 bmoe_status check_adamw_tensor(const bmoe_adamw_tensor& t, int32_t i) {
-  if (t.n < 0 || t.n > kMaxValues) return fail(BMOE_ERR_SHAPE, "tensor %d: n=%lld must be in [0, 2^40]", i, (long long)t.n);
+  if (t.n < 0 || t.n > kMaxValues) return fail(BMOE_ERR_SHAPE, "tensor %d: n=%lld must be in [0, 2^33]", i, (long long)t.n);
   if (t.bits != 32 && t.bits != 8) return fail(BMOE_ERR_DTYPE, "tensor %d: bits=%d must be 32 or 8", i, t.bits);
   if (t.n > 0 && t.bits == 8 && (!t.m_exp || !t.v_exp)) return fail(BMOE_ERR_NULL, "tensor %d: m_exp / v_exp is NULL", i);
   if (t.n > 0 && (!t.m || !t.v)) return fail(BMOE_ERR_NULL, "tensor %d: m / v is NULL", i);

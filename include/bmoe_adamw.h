@@ -55,7 +55,7 @@ typedef struct bmoe_adamw_tensor {
   uint8_t* m_exp;        /* [ceil(n / 256)], updated, with 8 bits; else NULL */
   uint8_t* v_exp;        /* the same */
   void* copy;            /* [n] bf16, written, or NULL */
-  int64_t n;             /* 0 .. 2^40 */
+  int64_t n;             /* 0 .. 2^33 */
   float lr_scale;        /* finite */
   float weight_decay;    /* finite */
   int32_t grad_dtype;    /* bmoe_dtype */

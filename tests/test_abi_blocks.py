@@ -46,7 +46,7 @@ def step(t, **change):
 
 
 REFUSED_TENSORS = [
-    (dict(n=-1), {}, SHAPE), (dict(n=(1 << 40) + 1), {}, SHAPE), (dict(lr_scale=float("nan")), {}, SHAPE),
+    (dict(n=-1), {}, SHAPE), (dict(n=(1 << 33) + 1), {}, SHAPE), (dict(lr_scale=float("nan")), {}, SHAPE),
     (dict(weight_decay=float("inf")), {}, SHAPE), (dict(bits=16), {}, DTYPE), (dict(grad_dtype=2), {}, DTYPE),
     (dict(param=0), {}, NULL), (dict(m=0), {}, NULL), (dict(v=0), {}, NULL), ({}, dict(m_exp=0), NULL), ({}, dict(v_exp=0), NULL),
     (dict(param=ptr(0) + 2), {}, ALIGN), (dict(grad=ptr(1) + 1), {}, ALIGN), (dict(m=ptr(2) + 2), {}, ALIGN), (dict(copy=ptr(6) + 1), {}, ALIGN),

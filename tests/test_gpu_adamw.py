@@ -278,6 +278,14 @@ def test_another_stream_and_given_moments():
     assert (a.params[0] == b.params[0]).all() and (a.m[0] == b.m[0]).all() and a.steps == b.steps == 2
 
 
+def test_empty_tensors():
+    import torch
+    z = torch.zeros(0, device="cuda")
+    opt = bm.AdamW([z, torch.ones(5, device="cuda")], bits=[8, 32])
+    opt.step([z.clone(), torch.ones(5, device="cuda")])
+    assert (opt.params[1] < 1).all() and opt.moments()[0][0].shape == (0,)
+
+
 def test_binding_refusals():
     import torch
     z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)  # noqa: E731
