@@ -6,7 +6,7 @@
 //               [dWg; dWu] = [dg du]^T x            dWd = dy^T h
 // An operand has the contraction contiguous (x, h, dy and the weights of the forward) or
 // its other side (the weights of the backward's first two, everything in the last two).
-// Operand tiles of 64-deep steps come straight into LDS (16 bytes per lane) in a ring of
+// Operand tiles of 64-deep or 32-deep steps come straight into LDS (16 bytes per lane) in a ring of
 // steps, in the layout they have in memory; those of the second kind are turned on the
 // way from LDS to registers (ds_read_b64_tr_b16), so no transposed copy of anything is
 // written.
@@ -497,15 +497,20 @@ __global__ __launch_bounds__(256) void gf_reduce_kernel(const float* part, int s
 // Few tokens: bound by the weights' bytes, each of which is read once, a row's 1024 at a
 // time by a wave (16 bytes per lane), and multiplied in fp32 without the matrix cores: with
 // TOK tokens 8 + 8 TOK operations on 8 weights, 6 us of the 20 that 100 MB take at TOK = 4.
-// (One token, d 2048, ff 8192: 23 us, 4.3 TB/s with both launches; as operands of MFMA,
+// (One token, d 2048, ff 8192: 22.5 us, 4.5 TB/s with both launches; as operands of MFMA,
 // 64 bytes of 16 rows at a time, 30, in tiles of 64 28.  8 tokens: 39, in tiles 28.)
 // A wave takes four rows (GATE: two of Wg and of Wu each), DEEP steps of 512 of their depth
-// on their way at a time; `parts` waves of a workgroup share the depth of the same rows.
+// on their way at a time: of a short depth more would be loaded for nothing (four steps:
+// one token 23.8 us, at d 1024, ff 4096 11.6 instead of 9.7, four tokens 13.0 instead of
+// 11.6).  `parts` waves of a workgroup share the depth of the same rows.
+// h stays fp32 between the launches: no matrix core asks for it in bf16, and it comes out of
+// the L2 (four tokens 27.0 us, in bf16 25.5).
 struct GfFew {
-  const uint16_t* x;        // [M][K]
+  const uint16_t* x;        // [M][K], GATE
+  float* h;                 // GATE: [M][R], written; otherwise [M][K], read
   const uint16_t* w;        // [R][K], GATE: [2 R][K]
   const uint16_t* add;      // [M][R] or null
-  uint16_t* out;            // [M][R]
+  uint16_t* out;            // [M][R], GATE: or null
   uint16_t* pa;             // GATE: [M][2 R] or null
   uint8_t* fine;            // GATE: [M][R] when pa is set
   int32_t M, R, K, parts;
@@ -513,28 +518,31 @@ struct GfFew {
 constexpr int GF_FEW_WAVES = 8;
 template <bool GATE, int F, int TOK>
 __global__ __launch_bounds__(64 * GF_FEW_WAVES) void gf_few_kernel(GfFew p) {
-  constexpr int ROWS = GATE ? 2 : 4, DEEP = TOK > 2 ? 2 : 4;
+  constexpr int ROWS = GATE ? 2 : 4, DEEP = TOK > (GATE ? 2 : 1) ? 1 : 2;
   __shared__ float red[GF_FEW_WAVES][4][TOK];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int groups = GF_FEW_WAVES / p.parts, part = wave % p.parts;
   const int row0 = (blockIdx.x * groups + wave / p.parts) * ROWS;
   const int steps = (p.K + 511) / 512, per = (steps + p.parts - 1) / p.parts, s0 = part * per, s1 = min(s0 + per, steps);
   const uint16_t* w[4];
-  const uint16_t* x[TOK];
+  constexpr int XV = GATE ? 1 : 2;   // of 16 bytes for 8 values of x or h
+  const uint4* x[TOK];
 #pragma unroll
   for (int r = 0; r < 4; ++r) w[r] = p.w + size_t(min(row0 + r % ROWS, p.R - 1) + r / ROWS * p.R) * p.K;
 #pragma unroll
-  for (int m = 0; m < TOK; ++m) x[m] = p.x + size_t(min(m, p.M - 1)) * p.K;
+  for (int m = 0; m < TOK; ++m) x[m] = reinterpret_cast<const uint4*>(GATE ? static_cast<const void*>(p.x) : p.h) + size_t(min(m, p.M - 1)) * p.K / 8 * XV;
   float acc[4][TOK] = {};
   for (int s = s0; s < s1; s += DEEP) {
-    uint4 wv[DEEP][4], xv[DEEP][TOK];
+    uint4 wv[DEEP][4], xv[DEEP][TOK][XV];
 #pragma unroll
     for (int u = 0; u < DEEP; ++u) {
       const int at = min(512 * (s + u) + 8 * lane, p.K - 8);   // past the end the last one, which counts as zeros
 #pragma unroll
       for (int r = 0; r < 4; ++r) wv[u][r] = *reinterpret_cast<const uint4*>(w[r] + at);
 #pragma unroll
-      for (int m = 0; m < TOK; ++m) xv[u][m] = *reinterpret_cast<const uint4*>(x[m] + at);
+      for (int m = 0; m < TOK; ++m)
+#pragma unroll
+        for (int v = 0; v < XV; ++v) xv[u][m][v] = x[m][at / 8 * XV + v];
     }
 #pragma unroll
     for (int u = 0; u < DEEP; ++u) {
@@ -542,11 +550,18 @@ __global__ __launch_bounds__(64 * GF_FEW_WAVES) void gf_few_kernel(GfFew p) {
       float xf[TOK][8];
 #pragma unroll
       for (int m = 0; m < TOK; ++m) {
-        const uint32_t q[4] = {xv[u][m].x, xv[u][m].y, xv[u][m].z, xv[u][m].w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          xf[m][2 * e] = in ? bf16lo(q[e]) : 0.f;
-          xf[m][2 * e + 1] = in ? bf16hi(q[e]) : 0.f;
+        for (int v = 0; v < XV; ++v) {
+          const uint32_t q[4] = {xv[u][m][v].x, xv[u][m][v].y, xv[u][m][v].z, xv[u][m][v].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (GATE) {
+              xf[m][2 * e] = in ? bf16lo(q[e]) : 0.f;
+              xf[m][2 * e + 1] = in ? bf16hi(q[e]) : 0.f;
+            } else {
+              xf[m][4 * v + e] = in ? __uint_as_float(q[e]) : 0.f;
+            }
+          }
         }
       }
 #pragma unroll
@@ -591,6 +606,8 @@ __global__ __launch_bounds__(64 * GF_FEW_WAVES) void gf_few_kernel(GfFew p) {
       p.fine[at] = uint8_t(gf_fine(k));
     }
     v = gf_act<F>(v) * u;
+    p.h[at] = v;
+    if (!p.out) return;
   } else if (p.add) {
     v += load1<ACT_BF16>(p.add, at);
   }
@@ -632,7 +649,7 @@ GfTile gf_pick(int M, int N, int K, bool turned, bool may_split) {
   constexpr Option options[] = {{GF_64, 2, {0.2, 0.45}, {0.42, 0.62}, 3.0},
                                 {GF_128, 1, {0.48, 0.8}, {0, 0}, 2.0},
                                 {GF_128_2, 2, {0.66, 0.8}, {0.91, 1.1}, 3.0},
-                                {GF_256, 1, {1.58, 1.8}, {0, 0}, 4.0}};
+                                {GF_256, 1, {1.58, 1.71}, {0, 0}, 4.0}};
   GfTile best{GF_64, 1};
   double least = 0;
   const int steps = (K + 63) / 64;
@@ -641,6 +658,7 @@ GfTile gf_pick(int M, int N, int K, bool turned, bool may_split) {
     const int64_t tiles = int64_t((M + side - 1) / side) * ((N + side - 1) / side);
     for (int split = 1; split <= (may_split ? GF_SPLIT : 1); ++split) {
       const int per = (steps + split - 1) / split;
+      // no share without a step, and then none of twice as many steps of 32 either, nor of one less
       if (split > 1 && ((split - 1) * per >= steps || per < 4)) break;
       const int64_t n = tiles * split;
       const double step = o.per_cu == 1 || n <= GF_CUS ? o.lone[turned] : o.shared[turned];
@@ -680,7 +698,12 @@ hipError_t gf_tiled(const GfGemm& p, GfTiling t, hipStream_t s) {
   if (t == GF_64) return gf_go<AT, BT, EPI, F, 64, 64, 64, 2, 2, 4>(p, s);
   if (t == GF_128) return gf_go<AT, BT, EPI, F, 128, 128, 64, 2, 4, 3>(p, s);
   if (t == GF_128_2) return gf_go<AT, BT, EPI, F, 128, 128, 64, 2, 2, 2>(p, s);
-  return gf_go<AT, BT, EPI, F, 256, 256, 64, 2, 4, 2>(p, s);
+  // Steps of 32 in a ring of four load three quarters of the ring ahead where steps of 64 in
+  // the same LDS load half; with a turned operand that is the faster (dx of 16384 x 2048 x 8192
+  // 955 us against 1006, dg | du 675 against 698, dW_in and dW_down 715 against 735 on average),
+  // with none the doubled barriers cost as much (h 1109 against 1097, y 487 both).
+  if constexpr (BT) return gf_go<AT, BT, EPI, F, 256, 256, 32, 2, 4, 4>(p, s);
+  else return gf_go<AT, BT, EPI, F, 256, 256, 64, 2, 4, 2>(p, s);
 }
 
 // A product whose result is written as it is (plus what is added), in shares where the
@@ -714,8 +737,9 @@ hipError_t gf_few(GfFew p, hipStream_t s) {
 
 size_t gf_forward_workspace(int tokens, int d, int ff, bool with_state) {
   if (tokens == 0) return 0;
+  if (tokens <= GF_FEW) return size_t(tokens) * ff * 4;
   const size_t h = with_state ? 0 : gf_round(size_t(tokens) * ff * 2);
-  return h + (tokens <= GF_FEW ? 0 : gf_part_bytes(tokens, d, gf_pick(tokens, d, ff, false, true)));
+  return h + gf_part_bytes(tokens, d, gf_pick(tokens, d, ff, false, true));
 }
 
 hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
@@ -728,9 +752,10 @@ hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
   uint16_t* h = a.state ? a.state + size_t(M) * 2 * a.ff : reinterpret_cast<uint16_t*>(ws);
   float* part = reinterpret_cast<float*>(ws + (a.state ? 0 : gf_round(size_t(M) * a.ff * 2)));
   if (M <= GF_FEW) {
-    const GfFew gate{a.x, a.w_in, nullptr, h, pa, fine, M, a.ff, a.d, 1};
+    float* h32 = reinterpret_cast<float*>(ws);
+    const GfFew gate{a.x, h32, a.w_in, nullptr, a.state ? h : nullptr, pa, fine, M, a.ff, a.d, 1};
     const hipError_t e = a.gelu ? gf_few<true, GF_GELU>(gate, s) : gf_few<true, GF_SILU>(gate, s);
-    return e != hipSuccess ? e : gf_few<false>(GfFew{h, a.w_down, a.add, a.y, nullptr, nullptr, M, a.d, a.ff, 1}, s);
+    return e != hipSuccess ? e : gf_few<false>(GfFew{nullptr, h32, a.w_down, a.add, a.y, nullptr, nullptr, M, a.d, a.ff, 1}, s);
   }
   GfGemm p{};
   p.a = a.x;
@@ -788,7 +813,7 @@ hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
     p.ldb = p.N = p.ff = a.ff;
     p.M = M;
     p.split = 1;
-      p.out = dgu;
+    p.out = dgu;
     p.pa = const_cast<uint16_t*>(a.state);
     p.fine = reinterpret_cast<uint8_t*>(p.pa + size_t(M) * 3 * a.ff);
     const GfTiling tiling = gf_pick(M, p.N, p.K, true, false).tiling;

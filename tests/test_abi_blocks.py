@@ -246,10 +246,10 @@ def test_gated_ffn_sizes_and_nothing_to_do():
     assert L.bmoe_gated_ffn_state_size(10, 64, ctypes.byref(n)) == 0 and n.value == 10 * 7 * 64
     assert L.bmoe_gated_ffn_state_size(10, 64, None) == NULL and L.bmoe_gated_ffn_state_size(10, 63, ctypes.byref(n)) == SHAPE
     assert L.bmoe_gated_ffn_forward_workspace(10, 64, 64, 2, ctypes.byref(n)) == SHAPE
-    # few tokens need the activated product alone, and with a state nothing
+    # few tokens keep the activated product in fp32, with a state or without
     for tokens in (1, 4):
-        assert L.bmoe_gated_ffn_forward_workspace(tokens, 64, 64, 1, ctypes.byref(n)) == 0 and n.value == 0
-        assert L.bmoe_gated_ffn_forward_workspace(tokens, 64, 64, 0, ctypes.byref(n)) == 0 and tokens * 128 <= n.value < tokens * 128 + 256
+        for with_state in (0, 1):
+            assert L.bmoe_gated_ffn_forward_workspace(tokens, 64, 64, with_state, ctypes.byref(n)) == 0 and n.value == tokens * 256
     for tokens, d, ff in ((1, 8, 8), (33, 2048, 8192), (1 << 20, 2048, 8192), (4096, 16384, 32768)):
         for call in ((L.bmoe_gated_ffn_forward_workspace, (tokens, d, ff, 0)), (L.bmoe_gated_ffn_backward_workspace, (tokens, d, ff))):
             assert call[0](*call[1], ctypes.byref(n)) == 0 and tokens * ff * 2 <= n.value < tokens * ff * 4 + (4 << 30)
