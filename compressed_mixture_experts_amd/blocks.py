@@ -72,11 +72,14 @@ class AdamW:
     weight_decay, lr_scale, bits, copies   one for all tensors or a list of them: the
                      decoupled decay, a factor on lr, 32 or 8 bits for the moments (8:
                      bmoe_adamw.h's codes), a bf16 tensor that gets the new values.
-    lr               a number, which may be set anew between steps (`opt.lr`), or a
-                     one-element fp32 tensor that every step reads on the GPU.
+    lr               a number, which may be set anew between steps (`opt.lr`; a captured
+                     step keeps its own), or a one-element fp32 tensor that every step
+                     reads on the GPU.
     m, v             the moments to go on from (fp32; with 8 bits uint8 codes and their
                      blocks' exponents m_exp, v_exp [ceil(n / 256)] uint8), used as they
-                     are and updated in place; None: zeros.
+                     are and updated in place; None: zeros.  `opt.m`, `opt.v` and so on
+                     list the tensors in use, whose values may be set.  (Parameters and
+                     copies may get other memory between steps, the moments not.)
     steps            the steps already taken.
     capturable       count the steps on the GPU, so that a step captured in a graph
                      counts on in every replay; without, a step in a capture is refused.
@@ -101,10 +104,8 @@ class AdamW:
         f32, u8 = torch.float32, torch.uint8
         self.bits = _listed("bits", bits, count)
         self._decay, self._scale = _listed("weight_decay", weight_decay, count, 0.0), _listed("lr_scale", lr_scale, count, 1.0)
-        self.copies = _listed("copies", copies, count) if isinstance(copies, (list, tuple)) or copies is None else [copies]
-        if len(self.copies) != count:
-            raise ValueError(f"copies has {len(self.copies)} entries for {count} parameters")
-        given = [_listed(n, x, count) if isinstance(x, (list, tuple)) or x is None else [x] for n, x in
+        self.copies = _listed("copies", [copies] if isinstance(copies, torch.Tensor) else copies, count)
+        given = [_listed(n, [x] if isinstance(x, torch.Tensor) else x, count) for n, x in
                  (("m", m), ("v", v), ("m_exp", m_exp), ("v_exp", v_exp))]
         self.m, self.v, self.m_exp, self.v_exp = [], [], [], []
         for i, p in enumerate(self.params):
@@ -118,7 +119,7 @@ class AdamW:
             for name, have, out, kind, shape, wanted in (
                     ("m", given[0], self.m, u8 if eight else f32, p.shape, True), ("v", given[1], self.v, u8 if eight else f32, p.shape, True),
                     ("m_exp", given[2], self.m_exp, u8, blocks, eight), ("v_exp", given[3], self.v_exp, u8, blocks, eight)):
-                x = have[i] if i < len(have) else None
+                x = have[i]
                 if not wanted:
                     if x is not None:
                         raise ValueError(f"{name}[{i}] is for moments in 8 bits")
@@ -128,22 +129,32 @@ class AdamW:
                         raise ValueError(f"m, v, m_exp and v_exp of parameter {i} go together")
                     out.append(torch.zeros(shape, dtype=kind, device=dev))
                 else:
-                    out.append(_tensor(f"{name}[{i}]", x, kind, shape, dev))
+                    out.append(_tensor(f"{name}[{i}]", x, kind, shape, dev).detach())   # this memory, whatever x is given later
             if (given[0][i] is None) != (given[1][i] is None):
                 raise ValueError(f"m and v of parameter {i} go together")
+        # what its owner may give other memory (`tensor.data = ..`, a module's `.to`)
+        self._owned = [(f"{name}[{i}]", x, x.dtype, x.shape) for name, tensors in (("params", self.params), ("copies", self.copies))
+                       for i, x in enumerate(tensors) if x is not None]
+        self._owned_tensors = [o[1] for o in self._owned]
         t = np.zeros(count, dtype=_ADAMW_TENSOR)
-        for name, tensors in (("param", self.params), ("m", self.m), ("v", self.v), ("m_exp", self.m_exp), ("v_exp", self.v_exp),
-                              ("copy", self.copies)):
+        self._table = t
+        for name, tensors in (("m", self.m), ("v", self.v), ("m_exp", self.m_exp), ("v_exp", self.v_exp)):
             t[name] = [0 if x is None else x.data_ptr() for x in tensors]
+        self._take_addresses()
         t["n"] = [p.numel() for p in self.params]
         t["lr_scale"], t["weight_decay"], t["bits"] = self._scale, self._decay, self.bits
-        self._table, self._table_at = t, t.ctypes.data
+        self._table_at = t.ctypes.data
         self._grad, self._grad_dtype = t["grad"], t["grad_dtype"]   # views of it
         self._shapes = [p.shape for p in self.params]
         self._coded = [i for i, b in enumerate(self.bits) if b == 8]
         self._coded_shapes = [self._shapes[i] for i in self._coded]
         self._steps = int(steps)
         self._counter = torch.full((1,), self._steps, dtype=torch.int64, device=dev) if capturable else None
+
+    def _take_addresses(self):
+        for name, tensors in (("param", self.params), ("copy", self.copies)):
+            self._table[name] = [0 if x is None else x.data_ptr() for x in tensors]
+        self._addresses = [x.data_ptr() for x in self._owned_tensors]
 
     @property
     def steps(self) -> int:
@@ -168,6 +179,10 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         index = dev.index
+        if list(map(torch.Tensor.data_ptr, self._owned_tensors)) != self._addresses:   # taken where they are now
+            for name, x, kind, shape in self._owned:
+                _tensor(name, x, kind, shape, dev)
+            self._take_addresses()
         if not self._fit(grads, self._shapes, {f32, bf16}):
             for i, (g, s) in enumerate(zip(grads, self._shapes)):
                 if g is not None:

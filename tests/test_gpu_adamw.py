@@ -278,6 +278,36 @@ def test_another_stream_and_given_moments():
     assert (a.params[0] == b.params[0]).all() and (a.m[0] == b.m[0]).all() and a.steps == b.steps == 2
 
 
+def test_memory_that_moved():
+    """A tensor that its owner gives other memory is taken from there, or refused."""
+    import torch
+    for bits in (32, 8):
+        (a, gs), (b, _) = (make([300, 70], ["f32"], bits, 31, copies=[torch.zeros(300, dtype=torch.bfloat16, device="cuda"), None])
+                           for _ in range(2))
+        for opt in (a, b):
+            opt.step(gs)
+        old, kept = b.params[0].data, b.params[0].data.clone()
+        b.params[0].data = old.clone()
+        b.copies[0].data = b.copies[0].data.clone()
+        for opt in (a, b):
+            opt.step(gs)
+        torch.cuda.synchronize()
+        assert (old == kept).all() and all((x == y).all() for x, y in zip(a.params, b.params)) and (a.copies[0] == b.copies[0]).all()
+        assert all((x == y).all() for p, q in zip(a.moments(), b.moments()) for x, y in zip(p, q))
+        b.params[1].data = torch.zeros(70, device="cuda", dtype=torch.bfloat16)
+        with pytest.raises(ValueError, match=r"params\[1\]"):
+            b.step(gs)
+        assert b.steps == 2
+    # moments that were given: their memory stays in use
+    m = torch.zeros(300, device="cuda")
+    opt = bm.AdamW([torch.zeros(300, device="cuda")], m=[m], v=[torch.zeros(300, device="cuda")])
+    opt.step([torch.ones(300, device="cuda")])
+    assert (m == opt.m[0]).all() and (m > 0).all()
+    m.data = torch.ones(300, device="cuda")
+    opt.step([torch.zeros(300, device="cuda")])
+    assert (m == 1).all() and (opt.m[0] < 0.1).all()
+
+
 def test_empty_tensors():
     import torch
     z = torch.zeros(0, device="cuda")
