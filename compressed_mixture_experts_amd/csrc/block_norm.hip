@@ -120,9 +120,11 @@ struct BnWeight {
   }
 };
 
-// Threads of a workgroup: whole rows.  The backward's partial rows are as many as its
-// workgroups, so those of narrow rows are as large as the registers allow.
-constexpr int bn_fwd_threads(int tpr) { return tpr > 256 ? tpr : 256; }
+// Threads of a workgroup: whole rows.  In the forward a row that takes barriers has the
+// workgroup to itself, so that what its size asks for (LnStats) is everybody's (8192 x 1024
+// fp32 26.3 us, with two rows to a workgroup 27.8).  The backward's partial rows are as many
+// as its workgroups, so those of narrow rows are as large as the registers allow.
+constexpr int bn_fwd_threads(int tpr) { return tpr > 64 ? tpr : 256; }
 constexpr int bn_fwd_waves(int tpr) { return tpr > 256 ? 4 : BN_FWD_WAVES; }
 // (Rows that share barriers wait for each other: with three of 2048 to a workgroup 32768 x
 // 2048 takes 191 us in place of 180, 1024 x 2048 22 in place of 25.)
@@ -131,7 +133,7 @@ constexpr int bn_bwd_threads(int tpr) { return tpr <= 128 ? 256 * BN_BWD_WAVES :
 template <int ACT, int CUT, int TPR, int NV>
 __global__ __launch_bounds__(bn_fwd_threads(TPR), bn_fwd_waves(TPR)) void bn_fwd_kernel(BnFwdArgs a) {
   constexpr int E = 8, RPW = bn_fwd_threads(TPR) / TPR;
-  __shared__ LnRed<TPR> red[TPR > 64 ? RPW : 1];
+  __shared__ LnRed<TPR> red;
   int turn = 0;
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR, width = a.width;
   const BnCols<CUT, TPR> cols{width, t};
@@ -157,8 +159,7 @@ __global__ __launch_bounds__(bn_fwd_threads(TPR), bn_fwd_waves(TPR)) void bn_fwd
     for (int v = 0; v < NV; ++v) fold(v, wp[v], wq[v]);
   }
   auto on = [&](int v, int j) { return cols.on(v, j); };
-  // all rows of a workgroup at a time, since they share its barriers; past the last row
-  // that one again, not stored
+  // past the last row that one again, not stored
   for (int base = blockIdx.x * RPW; base < a.rows; base += gridDim.x * RPW) {
     const int row = min(base + sub, a.rows - 1);
     const bool live = base + sub < a.rows;
@@ -180,8 +181,7 @@ __global__ __launch_bounds__(bn_fwd_threads(TPR), bn_fwd_waves(TPR)) void bn_fwd
 #pragma unroll
       for (int j = 0; j < E; ++j) x[v][j] = on(v, j) ? x[v][j] : 0.f;
     auto normed = [&]() {
-      LnRed<TPR>& mine = red[TPR > 64 ? sub : 0];
-      return a.layer ? ln_centre<TPR>(x, width, a.eps, mine, turn, on) : bn_root<TPR>(x, width, a.eps, mine, turn);
+      return a.layer ? ln_centre<TPR>(x, width, a.eps, red, turn, on) : bn_root<TPR>(x, width, a.eps, red, turn);
     };
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
     if (a.post) {
@@ -252,6 +252,8 @@ __global__ __launch_bounds__(bn_bwd_threads(TPR), bn_bwd_waves(TPR)) void bn_bwd
   using Weight = BnWeight<CUT, TPR, NV, (TPR < 1024)>;
   const Weight wgp(a.gamma_post, 1.f, cols), wbp(a.beta_post, 0.f, cols),
       wgc(a.gate_kind == BN_GATE_CHANNEL ? a.gate : nullptr, 1.f, cols), wga(a.gamma, 1.f, cols);
+  // all rows of a workgroup at a time, since they share its barriers; past the last row
+  // that one again, not stored
   for (int base = blockIdx.x * RPW; base < a.rows; base += gridDim.x * RPW) {
     const int row = min(base + sub, a.rows - 1);
     const bool live = base + sub < a.rows;

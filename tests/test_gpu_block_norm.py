@@ -218,6 +218,28 @@ def test_rows_of_any_size(width, kind):
         check_forward(sub, tuple(x[keep] for x in got), 1.0, 1.0, True, eps)
 
 
+@pytest.mark.parametrize("width", [20, 200, 500, 777, 1024, 2049])
+def test_a_row_does_not_depend_on_its_neighbours(width):
+    """Rows of all sizes beside each other, and the same rows in another order."""
+    import torch
+    c = draw(4500, width, "f32", "layer", "rows", True, width)
+    r = np.random.default_rng(width)
+    size = np.array([1.0, 1e30, 1.0, 1e-30, 1e19, 1.0, 1e-24])[r.integers(0, 7, 4500)].astype(np.float32)
+    c["b"] *= torch.from_numpy(size).cuda()[:, None]
+    c["b"][::13] += 1e3
+    c["b"][::101, width // 2] = float("nan")
+    turn = torch.from_numpy(r.permutation(4500)).cuda()
+    for kind in ("layer", "rms"):
+        kw = dict(kind=kind, gamma_post=c["gp"], gamma=c["ga"], eps=0.0)
+        got = bm.block_norm_forward(c["b"], c["r"], gate=c["gate"], **kw)
+        again = bm.block_norm_forward(c["b"][turn], c["r"][turn], gate=c["gate"][turn], **kw)
+        one = bm.block_norm_backward(c["dy"], c["b"], got[1], got[2], gate=c["gate"], d_sum=c["ds"], weight_grads=False, **{k: v for k, v in kw.items() if k != "eps"})
+        two = bm.block_norm_backward(c["dy"][turn], c["b"][turn], again[1], again[2], gate=c["gate"][turn], d_sum=c["ds"][turn], weight_grads=False,
+                                     **{k: v for k, v in kw.items() if k != "eps"})
+        for x, y in list(zip(got, again)) + [(one[k], two[k]) for k in ("b", "residual")]:
+            assert torch.equal(x[turn].view(torch.int32), y.view(torch.int32)) or torch.equal(x[turn].nan_to_num(7.0), y.nan_to_num(7.0))
+
+
 def test_bad_rows_stay_alone_and_no_rows():
     import torch
     c = draw(6, 300, "bf16", "layer", "channel", True, 9)
