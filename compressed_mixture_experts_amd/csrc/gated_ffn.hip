@@ -96,9 +96,9 @@ __device__ __forceinline__ float gf_kept_a(uint32_t bf16, uint32_t fine) { retur
 // place stands in front of a step's last products.  The first step of a depth that is no
 // multiple of BK is the short one: it is loaded ahead of the loop, so the loop has no case
 // for it.
+#if defined(__HIP_DEVICE_COMPILE__)   // the host's pass knows no buffer resources and would drop the kernels
 template <bool AT, bool BT, int EPI, int F, int TM, int TN, int BK, int WM, int WN, int NBUF>
-__global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
-#if defined(__HIP_DEVICE_COMPILE__)   // the host's pass knows no buffer resources and would drop the kernel
+__device__ __forceinline__ void gf_gemm(const GfGemm& p, int bid) {
   constexpr int NW = WM * WN, NT = 64 * NW;
   constexpr int PM = TM / WM, PN = TN / WN, IM = PM / 16, IN = PN / 16, H = BK / 32;
   constexpr int STAGE = (TM + TN) * BK;          // halves of a ring place: A's, then B's
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
   const int wm = wave % WM, wn = wave / WM;
   // an XCD's workgroups take the same share of a block of tiles: bands of tile rows,
   // column by column within a band
-  int t = xcd_remap(blockIdx.x, gridDim.x);
+  int t = xcd_remap(bid, p.nm * p.nn * p.split);
   const int tiles = p.nm * p.nn, share = t / tiles;
   t -= share * tiles;
   const int r0 = t / (p.band * p.nn) * p.band;
@@ -475,23 +475,60 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
       }
     }
   }
+}
+#endif
+
+template <bool AT, bool BT, int EPI, int F, int TM, int TN, int BK, int WM, int WN, int NBUF>
+__global__ __launch_bounds__(64 * WM * WN, 2) void gf_gemm_kernel(GfGemm p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  gf_gemm<AT, BT, EPI, F, TM, TN, BK, WM, WN, NBUF>(p, blockIdx.x);
 #endif
 }
 
-// The shares' sums, added in order, and what is added to them.
-__global__ __launch_bounds__(256) void gf_reduce_kernel(const float* part, int split, size_t n, uint16_t* out,
-                                                        const uint16_t* add16, const float* add32) {
-  const size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  f32x4_t s = *reinterpret_cast<const f32x4_t*>(part + i);
+// dx, dW_in and dW_down, those of them that are wanted, in one launch: where one of them leaves CUs without work, the next
+// one's workgroups take them (gf_group_pick).
+struct GfGroup {
+  GfGemm job[3];
+  int32_t start[3];         // first workgroups, multiples of 8: a job's XCDs are the launch's
+};
+template <int EPI, int TM, int TN, int BK, int WM, int WN, int NBUF>
+__global__ __launch_bounds__(64 * WM * WN, 2) void gf_group_kernel(GfGroup g) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const int bid = blockIdx.x, k = bid < g.start[1] ? 0 : bid < g.start[2] ? 1 : 2;
+  const GfGemm p = g.job[k];
+  if (bid - g.start[k] >= p.nm * p.nn * p.split) return;
+  if (k == 0) gf_gemm<false, true, EPI, 0, TM, TN, BK, WM, WN, NBUF>(p, bid);
+  else gf_gemm<true, true, EPI, 0, TM, TN, BK, WM, WN, NBUF>(p, bid - g.start[k]);
+#endif
+}
+
+// The shares' sums of up to three products, added in order, and what is added to them.
+struct GfSum {
+  const float* part;
+  uint16_t* out;
+  const uint16_t* add16;    // or null
+  const float* add32;       // or null
+  size_t n;
+  int32_t split, blocks;
+};
+struct GfSums {
+  GfSum of[3];
+};
+__global__ __launch_bounds__(256) void gf_reduce_kernel(GfSums g) {
+  int b = blockIdx.x, w = 0;
+  while (w < 2 && b >= g.of[w].blocks) b -= g.of[w++].blocks;
+  const GfSum p = g.of[w];
+  const size_t i = (size_t(b) * 256 + threadIdx.x) * 4;
+  if (i >= p.n) return;
+  f32x4_t s = *reinterpret_cast<const f32x4_t*>(p.part + i);
 #pragma unroll 4
-  for (int k = 1; k < split; ++k) s += *reinterpret_cast<const f32x4_t*>(part + k * n + i);
-  if (add16) {
-    const uint2 u = *reinterpret_cast<const uint2*>(add16 + i);
+  for (int k = 1; k < p.split; ++k) s += *reinterpret_cast<const f32x4_t*>(p.part + k * p.n + i);
+  if (p.add16) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p.add16 + i);
     s += f32x4_t{bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y)};
   }
-  if (add32) s += *reinterpret_cast<const f32x4_t*>(add32 + i);
-  *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+  if (p.add32) s += *reinterpret_cast<const f32x4_t*>(p.add32 + i);
+  *reinterpret_cast<uint2*>(p.out + i) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
 }
 
 // Few tokens: bound by the weights' bytes, each of which is read once, a row's 1024 at a
@@ -628,6 +665,7 @@ enum GfTiling { GF_64, GF_128, GF_128_2, GF_256 };
 struct GfTile {
   GfTiling tiling;
   int split;
+  double time;
 };
 constexpr int gf_tile_side(GfTiling t) { return t == GF_64 ? 64 : t == GF_256 ? 256 : 128; }
 
@@ -650,8 +688,7 @@ GfTile gf_pick(int M, int N, int K, bool turned, bool may_split) {
                                 {GF_128, 1, {0.48, 0.8}, {0, 0}, 2.0},
                                 {GF_128_2, 2, {0.66, 0.8}, {0.91, 1.1}, 3.0},
                                 {GF_256, 1, {1.58, 1.71}, {0, 0}, 4.0}};
-  GfTile best{GF_64, 1};
-  double least = 0;
+  GfTile best{GF_64, 1, 0};
   const int steps = (K + 63) / 64;
   for (const Option& o : options) {
     const int side = gf_tile_side(o.tiling);
@@ -664,46 +701,67 @@ GfTile gf_pick(int M, int N, int K, bool turned, bool may_split) {
       const double step = o.per_cu == 1 || n <= GF_CUS ? o.lone[turned] : o.shared[turned];
       double time = double((n + GF_CUS * o.per_cu - 1) / (GF_CUS * o.per_cu)) * (per * step + o.once);
       if (split > 1) time += 3.0 + double(M) * N * split / 1e6;
-      if (least == 0 || time < least) {
-        best = GfTile{o.tiling, split};
-        least = time;
-      }
+      if (best.time == 0 || time < best.time) best = GfTile{o.tiling, split, time};
     }
   }
   return best;
 }
 
-size_t gf_part_bytes(int M, int N, GfTile t) { return t.split > 1 ? size_t(t.split) * M * N * 4 : 0; }
 size_t gf_round(size_t bytes) { return (bytes + 255) / 256 * 256; }
+size_t gf_part_bytes(int M, int N, int split) { return gf_round(size_t(split) * M * N * 4); }
+size_t gf_pick_bytes(int M, int N, int K, bool turned) {
+  const int split = gf_pick(M, N, K, turned, true).split;
+  return split > 1 ? gf_part_bytes(M, N, split) : 0;
+}
 
-template <bool AT, bool BT, int EPI, int F, int TM, int TN, int BK, int WM, int WN, int NBUF>
+// A product's tiles and steps; its workgroups.
+int gf_plan(GfGemm& p, int side, int step) {
+  p.nm = (p.M + side - 1) / side;
+  p.nn = (p.N + side - 1) / side;
+  p.per = ((p.K + step - 1) / step + p.split - 1) / p.split;
+  p.band = std::min(p.nm, 8);
+  return p.nm * p.nn * p.split;
+}
+
+template <bool AT, bool BT, int EPI, int F, int T, int BK, int WM, int WN, int NBUF>
 hipError_t gf_go(GfGemm p, hipStream_t s) {
   // the ring; staged tiles of bf16, or of fp32 in WM parts
-  constexpr size_t ring = size_t(NBUF) * (TM + TN) * BK * 2;
-  constexpr size_t stage = EPI == GF_GRAD ? size_t(TM / WM) * (TN + 4) * 4 : size_t(TM) * (TN + 4) * 2;
+  constexpr size_t ring = size_t(NBUF) * 2 * T * BK * 2;
+  constexpr size_t stage = EPI == GF_GRAD ? size_t(T / WM) * (T + 4) * 4 : size_t(T) * (T + 4) * 2;
   constexpr size_t lds = ring > stage ? ring : stage;
-  const auto kernel = gf_gemm_kernel<AT, BT, EPI, F, TM, TN, BK, WM, WN, NBUF>;
+  const auto kernel = gf_gemm_kernel<AT, BT, EPI, F, T, T, BK, WM, WN, NBUF>;
   const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
   if (e != hipSuccess) return e;
-  p.nm = (p.M + TM - 1) / TM;
-  p.nn = (p.N + TN - 1) / TN;
-  p.per = ((p.K + BK - 1) / BK + p.split - 1) / p.split;
-  p.band = std::min(p.nm, 8);
-  hipLaunchKernelGGL(kernel, dim3(unsigned(int64_t(p.nm) * p.nn * p.split)), dim3(64 * WM * WN), lds, s, p);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(gf_plan(p, T, BK))), dim3(64 * WM * WN), lds, s, p);
   return hipGetLastError();
 }
 
 template <bool AT, bool BT, int EPI, int F = GF_SILU>
 hipError_t gf_tiled(const GfGemm& p, GfTiling t, hipStream_t s) {
-  if (t == GF_64) return gf_go<AT, BT, EPI, F, 64, 64, 64, 2, 2, 4>(p, s);
-  if (t == GF_128) return gf_go<AT, BT, EPI, F, 128, 128, 64, 2, 4, 3>(p, s);
-  if (t == GF_128_2) return gf_go<AT, BT, EPI, F, 128, 128, 64, 2, 2, 2>(p, s);
+  if (t == GF_64) return gf_go<AT, BT, EPI, F, 64, 64, 2, 2, 4>(p, s);
+  if (t == GF_128) return gf_go<AT, BT, EPI, F, 128, 64, 2, 4, 3>(p, s);
+  if (t == GF_128_2) return gf_go<AT, BT, EPI, F, 128, 64, 2, 2, 2>(p, s);
   // Steps of 32 in a ring of four load three quarters of the ring ahead where steps of 64 in
   // the same LDS load half; with a turned operand that is the faster (dx of 16384 x 2048 x 8192
   // 955 us against 1006, dg | du 675 against 698, dW_in and dW_down 715 against 735 on average),
   // with none the doubled barriers cost as much (h 1109 against 1097, y 487 both).
-  if constexpr (BT) return gf_go<AT, BT, EPI, F, 256, 256, 32, 2, 4, 4>(p, s);
-  else return gf_go<AT, BT, EPI, F, 256, 256, 64, 2, 4, 2>(p, s);
+  if constexpr (BT) return gf_go<AT, BT, EPI, F, 256, 32, 2, 4, 4>(p, s);
+  else return gf_go<AT, BT, EPI, F, 256, 64, 2, 4, 2>(p, s);
+}
+
+// The second launch of products written as partial sums.
+hipError_t gf_reduce(const GfGemm* p, int count, hipStream_t s) {
+  GfSums g{};
+  unsigned blocks = 0;
+  for (int k = 0; k < count; ++k) {
+    if (p[k].M == 0) continue;
+    const size_t n = size_t(p[k].M) * p[k].N;
+    g.of[k] = GfSum{p[k].part, p[k].out, p[k].add16, p[k].add32, n, p[k].split, int32_t((n / 4 + 255) / 256)};
+    blocks += unsigned(g.of[k].blocks);
+  }
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(gf_reduce_kernel, dim3(blocks), dim3(256), 0, s, g);
+  return hipGetLastError();
 }
 
 // A product whose result is written as it is (plus what is added), in shares where the
@@ -715,10 +773,7 @@ hipError_t gf_product(GfGemm p, float* part, hipStream_t s) {
   if (t.split == 1) return gf_tiled<AT, BT, GF_OUT>(p, t.tiling, s);
   p.part = part;
   const hipError_t e = gf_tiled<AT, BT, GF_PART>(p, t.tiling, s);
-  if (e != hipSuccess) return e;
-  const size_t n = size_t(p.M) * p.N;
-  hipLaunchKernelGGL(gf_reduce_kernel, dim3(unsigned((n / 4 + 255) / 256)), dim3(256), 0, s, part, t.split, n, p.out, p.add16, p.add32);
-  return hipGetLastError();
+  return e != hipSuccess ? e : gf_reduce(&p, 1, s);
 }
 
 template <bool GATE, int F = GF_SILU>
@@ -733,13 +788,107 @@ hipError_t gf_few(GfFew p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The backward's last three products in one launch: 0 where they are better off one by one.
+struct GfTogether {
+  int side;                 // 0, 128 (two workgroups to a CU) or 256
+  bool parts;               // all of them as partial sums, also those in one share
+  int split[3];
+};
+// their M, N and K
+void gf_three(int tokens, int d, int ff, int (&m)[3], int (&n)[3], int (&k)[3]) {
+  m[0] = tokens; n[0] = d; k[0] = 2 * ff;
+  m[1] = 2 * ff; n[1] = d; k[1] = tokens;
+  m[2] = d; n[2] = ff; k[2] = tokens;
+}
+// By gf_pick's estimate, with the workgroups dealt out in order to whatever place is free first
+// (whole backward one by one and together, us: 4001 x 512 x 1368 94 and 69, 2354 x 1984 x 832 108
+// and 84, 4503 x 1536 x 5696 619 and 479, 677 x 1024 x 320 35 and 23; 16384 x 512 x 2048 315 and 294;
+// taken all the same: 8192 x 512 x 2048 161 and 174, 15899 x 1088 x 4096 1056 and 1067, which the
+// last 3 % leave out).
+GfTogether gf_group_pick(int tokens, int d, int ff) {
+  int m[3], n[3], k[3];
+  gf_three(tokens, d, ff, m, n, k);
+  GfTogether best{0, false, {1, 1, 1}};
+  double least = 0;
+  for (int j = 0; j < 3; ++j) least += 0.97 * gf_pick(m[j], n[j], k[j], true, true).time;
+  for (const int side : {128, 256}) {
+    const int places = side == 128 ? 2 * GF_CUS : GF_CUS;
+    int64_t tiles[3], all = 0;
+    int steps[3];
+    for (int j = 0; j < 3; ++j) {
+      tiles[j] = int64_t((m[j] + side - 1) / side) * ((n[j] + side - 1) / side);
+      steps[j] = (k[j] + 63) / 64;
+      all += tiles[j];
+    }
+    if (all > 4 * places) continue;   // what the last ones leave empty is little
+    for (int s = 0; s < 3 * GF_SPLIT; ++s) {   // steps of a workgroup: those of one product in 1 .. GF_SPLIT shares
+      const int per = (steps[s / GF_SPLIT] + s % GF_SPLIT) / (s % GF_SPLIT + 1);
+      if (per < 4) continue;
+      int split[3];
+      int64_t count = 0;
+      double sums = 0;
+      for (int j = 0; j < 3; ++j) {
+        split[j] = std::min((steps[j] + per - 1) / per, GF_SPLIT);
+        const int own = (steps[j] + split[j] - 1) / split[j];
+        split[j] = (steps[j] + own - 1) / own;
+        count += tiles[j] * split[j];
+        sums += 1.4 * double(m[j]) * n[j] * split[j] / 1e6;
+      }
+      const bool parts = split[0] > 1 || split[1] > 1 || split[2] > 1;
+      if (count > 8 * places) continue;
+      const double step = side == 256 ? 1.71 : count <= GF_CUS ? 0.8 : 1.1, once = side == 256 ? 4.0 : 3.0;
+      // places by when they are free
+      struct { double at; int64_t n; } free[8] = {{0, places}};
+      int kinds = 1;
+      double last = 0;
+      for (int j = 0; j < 3; ++j) {
+        const double takes = ((steps[j] + split[j] - 1) / split[j]) * step + once;
+        for (int64_t left = tiles[j] * split[j]; left > 0;) {
+          int f = 0;
+          for (int q = 1; q < kinds; ++q)
+            if (free[q].at < free[f].at) f = q;
+          const int64_t now = std::min(left, free[f].n);
+          const double until = free[f].at + takes;
+          last = std::max(last, until);
+          left -= now;
+          free[f].n -= now;
+          if (free[f].n == 0) free[f] = free[--kinds];
+          free[kinds++] = {until, now};
+        }
+      }
+      const double time = last + (parts ? 3.0 + sums : 0.0);
+      if (time < least) {
+        least = time;
+        best = GfTogether{side, parts, {split[0], split[1], split[2]}};
+      }
+    }
+  }
+  return best;
+}
+
+template <int EPI, int T, int BK, int WM, int WN, int NBUF>
+hipError_t gf_group_go(GfGroup& g, hipStream_t s) {
+  constexpr size_t ring = size_t(NBUF) * 2 * T * BK * 2, stage = size_t(T) * (T + 4) * 2, lds = ring > stage ? ring : stage;
+  const auto kernel = gf_group_kernel<EPI, T, T, BK, WM, WN, NBUF>;
+  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(kernel), lds);
+  if (e != hipSuccess) return e;
+  int blocks = 0;
+  for (int k = 0; k < 3; ++k) {
+    g.start[k] = (blocks + 7) / 8 * 8;
+    if (!g.job[k].out) g.job[k].M = 0;   // not wanted
+    blocks = g.start[k] + gf_plan(g.job[k], T, BK);
+  }
+  hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(64 * WM * WN), lds, s, g);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t gf_forward_workspace(int tokens, int d, int ff, bool with_state) {
   if (tokens == 0) return 0;
   if (tokens <= GF_FEW) return size_t(tokens) * ff * 4;
   const size_t h = with_state ? 0 : gf_round(size_t(tokens) * ff * 2);
-  return h + gf_part_bytes(tokens, d, gf_pick(tokens, d, ff, false, true));
+  return h + gf_pick_bytes(tokens, d, ff, false);
 }
 
 hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
@@ -784,10 +933,15 @@ hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
 
 size_t gf_backward_workspace(int tokens, int d, int ff) {
   if (tokens == 0) return 0;
-  const size_t part = std::max({gf_part_bytes(tokens, d, gf_pick(tokens, d, 2 * ff, true, true)),
-                                gf_part_bytes(2 * ff, d, gf_pick(2 * ff, d, tokens, true, true)),
-                                gf_part_bytes(d, ff, gf_pick(d, ff, tokens, true, true))});
-  return gf_round(size_t(tokens) * 2 * ff * 2) + part;
+  int m[3], n[3], k[3];
+  gf_three(tokens, d, ff, m, n, k);
+  const GfTogether t = gf_group_pick(tokens, d, ff);
+  size_t one = 0, all = 0;
+  for (int j = 0; j < 3; ++j) {
+    one = std::max(one, gf_pick_bytes(m[j], n[j], k[j], true));
+    if (t.parts) all += gf_part_bytes(m[j], n[j], t.split[j]);
+  }
+  return gf_round(size_t(tokens) * 2 * ff * 2) + std::max(one, all);
 }
 
 hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
@@ -820,39 +974,34 @@ hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
     e = a.gelu ? gf_tiled<false, true, GF_GRAD, GF_GELU>(p, tiling, s) : gf_tiled<false, true, GF_GRAD, GF_SILU>(p, tiling, s);
     if (e != hipSuccess) return e;
   }
-  if (a.dx) {
-    GfGemm p{};
-    p.a = dgu;
-    p.b = a.w_in;
-    p.lda = p.K = 2 * a.ff;
-    p.ldb = p.N = a.d;
-    p.M = M;
-    p.out = a.dx;
-    p.add32 = a.dx_add;
-    e = gf_product<false, true>(p, part, s);
-    if (e != hipSuccess) return e;
+  GfGroup g{};
+  GfGemm &dx = g.job[0], &dw_in = g.job[1], &dw_down = g.job[2];
+  dx.a = dw_in.a = dgu;
+  dx.lda = dx.K = dw_in.lda = dw_in.M = 2 * a.ff;
+  dx.b = a.w_in;
+  dw_in.b = a.x;
+  dx.ldb = dx.N = dw_in.ldb = dw_in.N = dw_down.lda = dw_down.M = a.d;
+  dx.M = dw_in.K = dw_down.K = M;
+  dw_down.a = a.dy;
+  dw_down.b = h;
+  dw_down.ldb = dw_down.N = a.ff;
+  dx.add32 = a.dx_add;
+  dx.out = a.dx;
+  dw_in.out = a.dw_in;
+  dw_down.out = a.dw_down;
+  if (const GfTogether t = gf_group_pick(M, a.d, a.ff); t.side) {
+    for (int k = 0; k < 3; ++k) {
+      g.job[k].split = t.split[k];
+      g.job[k].part = part;
+      if (t.parts) part += gf_part_bytes(g.job[k].M, g.job[k].N, t.split[k]) / 4;
+    }
+    if (!t.parts) return t.side == 128 ? gf_group_go<GF_OUT, 128, 64, 2, 2, 2>(g, s) : gf_group_go<GF_OUT, 256, 32, 2, 4, 4>(g, s);
+    e = t.side == 128 ? gf_group_go<GF_PART, 128, 64, 2, 2, 2>(g, s) : gf_group_go<GF_PART, 256, 32, 2, 4, 4>(g, s);
+    return e != hipSuccess ? e : gf_reduce(g.job, 3, s);
   }
-  if (a.dw_in) {
-    GfGemm p{};
-    p.a = dgu;
-    p.b = a.x;
-    p.lda = p.M = 2 * a.ff;
-    p.ldb = p.N = a.d;
-    p.K = M;
-    p.out = a.dw_in;
-    e = gf_product<true, true>(p, part, s);
-    if (e != hipSuccess) return e;
-  }
-  if (a.dw_down) {
-    GfGemm p{};
-    p.a = a.dy;
-    p.b = h;
-    p.lda = p.M = a.d;
-    p.ldb = p.N = a.ff;
-    p.K = M;
-    p.out = a.dw_down;
-    e = gf_product<true, true>(p, part, s);
-  }
+  if (a.dx) e = gf_product<false, true>(dx, part, s);
+  if (e == hipSuccess && a.dw_in) e = gf_product<true, true>(dw_in, part, s);
+  if (e == hipSuccess && a.dw_down) e = gf_product<true, true>(dw_down, part, s);
   return e;
 }
 
