@@ -83,13 +83,22 @@ __device__ __forceinline__ uint32_t gf_fine(GfKept v) { return (v.p >> 12 & 15u)
 __device__ __forceinline__ float gf_kept_p(uint32_t bf16, uint32_t fine) { return __uint_as_float(bf16 << 16 | (fine & 15u) << 12); }
 __device__ __forceinline__ float gf_kept_a(uint32_t bf16, uint32_t fine) { return __uint_as_float(bf16 << 16 | (fine & 0xF0u) << 8); }
 
+// Where chunk 0 of depth k lies in rows of T values whose other side is contiguous: the 32
+// lanes that LDS serves at a time read 32 bytes each of depths 0 .. 3 and 8 .. 11, which are
+// in eight places of the banks this way.  (With 8 .. 11 where 0 .. 3 are, LDS is busy twice as
+// long in dW_in of 16384 x 2048 x 8192, half of it with conflicts, and the product 1.8 % slower.)
+template <int T>
+__device__ __forceinline__ int gf_turned_swizzle(int k) {
+  return (2 * (k & 3)) ^ ((T == 64 ? 2 : 8) * (k >> 3 & 1));
+}
+
 // One workgroup per TM x TN tile of D[m][n] = sum_k A[m][k] B[n][k], WM x WN waves of
 // TM / WM x TN / WN each (MFMA blocks of 16 x 16 x 32), NBUF steps of depth BK in the ring.
 //
 // LDS, contraction contiguous: [rows][BK], 16-byte chunk c of row r at c ^ (r % 8), in steps
 // of 32 at c ^ (r / 2 % 4); a lane reads its 8 values of depth as one 16-byte chunk.  Other
-// side contiguous: [BK depths][rows], chunk c of depth k at c ^ 2 (k % 4); 16 lanes read 4
-// depths of 16 rows as 8 bytes each and get 4 depths of their row.
+// side contiguous: [BK depths][rows], chunk c of depth k at c ^ gf_turned_swizzle(k); 16 lanes
+// read 4 depths of 16 rows as 8 bytes each and get 4 depths of their row.
 //
 // A step's 32-deep halves have a set of fragments each in turn: the reads of the next half
 // are issued among the products of the current one, and the barrier that frees a ring
@@ -98,7 +107,7 @@ __device__ __forceinline__ float gf_kept_a(uint32_t bf16, uint32_t fine) { retur
 // for it.
 #if defined(__HIP_DEVICE_COMPILE__)   // the host's pass knows no buffer resources and would drop the kernels
 template <bool AT, bool BT, int EPI, int F, int TM, int TN, int BK, int WM, int WN, int NBUF>
-__device__ __forceinline__ void gf_gemm(const GfGemm& p, int bid) {
+__device__ __forceinline__ void gf_gemm(const GfGemm p, int bid) {
   constexpr int NW = WM * WN, NT = 64 * NW;
   constexpr int PM = TM / WM, PN = TN / WN, IM = PM / 16, IN = PN / 16, H = BK / 32;
   constexpr int STAGE = (TM + TN) * BK;          // halves of a ring place: A's, then B's
@@ -133,7 +142,7 @@ __device__ __forceinline__ void gf_gemm(const GfGemm& p, int bid) {
       const int w = wave * L + j;
       if constexpr (TURNED) {
         constexpr int RC = T / 8, RPL = 64 / RC;
-        const int k = w * RPL + lane / RC, c = (lane % RC) ^ (2 * (k & 3));
+        const int k = w * RPL + lane / RC, c = (lane % RC) ^ gf_turned_swizzle<T>(k);
         off[j] = 2u * (uint32_t(k) * uint32_t(ld) + uint32_t(min(first + 8 * c, count - 8) - first));
         deep[j] = k;
       } else {
@@ -195,15 +204,11 @@ __device__ __forceinline__ void gf_gemm(const GfGemm& p, int bid) {
   auto read_one = [&](auto turned, auto side, const uint16_t* tile, int row, int h, auto& f) {
     constexpr int T = decltype(side)::value, COUNT = sizeof(f) / sizeof(f[0]);
     if constexpr (decltype(turned)::value) {
-      // of four blocks next to each other; the others are 64 values on
-      constexpr int FOUR = COUNT < 4 ? COUNT : 4;
-      const uint16_t* q[FOUR];
-#pragma unroll
-      for (int j = 0; j < FOUR; ++j)
-        q[j] = tile + (8 * g + (l16 >> 2)) * T + 16 * ((row / 16 + j) ^ (l16 >> 2)) + 4 * (l16 & 3);
+      const int k = 8 * g + (l16 >> 2);   // further depths of this lane's have its place too
+      const uint16_t* q = tile + k * T + 4 * (l16 & 3);
 #pragma unroll
       for (int j = 0; j < COUNT; ++j) {
-        const uint16_t* at = q[j % FOUR] + 32 * h * T + 64 * (j / FOUR);
+        const uint16_t* at = q + ((row + 16 * j) ^ (8 * gf_turned_swizzle<T>(k))) + 32 * h * T;
         const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gf_lds4_t*)at);
         const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((gf_lds4_t*)(at + 4 * T));
         typedef short i16x8_t __attribute__((ext_vector_type(8)));
