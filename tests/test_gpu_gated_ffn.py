@@ -248,3 +248,27 @@ def test_binding_refusals():
         bm.gated_ffn_forward(x, wi, wd, y=x)
     with pytest.raises(bm.BmoeError, match="ALIAS"):
         bm.gated_ffn_backward(x, wi, wd, x, state, dx=x)
+
+
+@pytest.mark.parametrize("tokens,d,ff", [(3, 256, 512), (300, 40, 1000), (1000, 256, 512), (4001, 512, 1368), (257, 264, 72)])
+def test_each_gradient_alone(tokens, d, ff):
+    """The C call with any of dx, dw_in and dw_down left out: the others as with all of them,
+    in one launch or in several."""
+    import ctypes
+    import itertools
+    import torch
+    c = draw(tokens, d, ff, 21)
+    y, state = bm.gated_ffn_forward_train(c["x"], c["w_in"], c["w_down"])
+    want = bm.gated_ffn_backward(c["x"], c["w_in"], c["w_down"], y, state)
+    n = ctypes.c_size_t(0)
+    assert bm.lib().bmoe_gated_ffn_backward_workspace(tokens, d, ff, ctypes.byref(n)) == 0
+    for keep in itertools.product((False, True), repeat=3):
+        ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+        out = [torch.full_like(w, 7.0) for w in want]
+        assert bm.lib().bmoe_gated_ffn_backward(
+            tokens, d, ff, 0, c["x"].data_ptr(), c["w_in"].data_ptr(), c["w_down"].data_ptr(), y.data_ptr(), state.data_ptr(),
+            state.numel(), None, *[o.data_ptr() if k else None for o, k in zip(out, keep)], ws.data_ptr(), n.value,
+            torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        for o, w, k in zip(out, want, keep):
+            assert (o == w).all() if k else (o == 7.0).all()
