@@ -161,14 +161,16 @@ class AdamW:
         """The steps taken (capturable: read from the GPU, which waits for it)."""
         return self._steps if self._counter is None else int(self._counter.item())
 
-    def _fit(self, tensors, shapes, kinds) -> bool:
-        """Whether all are tensors of these shapes and types, dense on this GPU (a tenth of a
-        microsecond for each, where checks that name what is wrong take one)."""
+    def _fit(self, tensors, shapes):
+        """The types of tensors that all are of these shapes, dense and on this GPU (a tenth of
+        a microsecond for each, where checks that name what is wrong take one); None where
+        one is not, or is of a class of its own."""
         torch = _torch()
-        if not all(map(torch.is_tensor, tensors)):
-            return False
-        return (set(map(torch.Tensor.get_device, tensors)) == {self.device.index} and [t.shape for t in tensors] == shapes and
-                {t.dtype for t in tensors} <= kinds and all(map(torch.Tensor.is_contiguous, tensors)))
+        t = torch.Tensor
+        if (set(map(type, tensors)) <= {t, torch.nn.Parameter} and set(map(t.get_device, tensors)) == {self.device.index} and
+                list(map(t.size, tensors)) == shapes and all(map(t.is_contiguous, tensors))):
+            return set(map(t.dtype.__get__, tensors))
+        return None
 
     def step(self, grads, grad_scale=None) -> None:
         """One step: grads a list like params (fp32 or bf16; None: that tensor is left
@@ -183,12 +185,18 @@ class AdamW:
             for name, x, kind, shape in self._owned:
                 _tensor(name, x, kind, shape, dev)
             self._take_addresses()
-        if not self._fit(grads, self._shapes, {f32, bf16}):
+        kinds = self._fit(grads, self._shapes)
+        if kinds is None or not kinds <= {f32, bf16}:
             for i, (g, s) in enumerate(zip(grads, self._shapes)):
                 if g is not None:
                     _tensor(f"grads[{i}]", g, bf16 if getattr(g, "dtype", None) == bf16 else f32, s, dev)
-        self._grad[:] = [0 if g is None else g.data_ptr() for g in grads]
-        self._grad_dtype[:] = [F32 if g is None or g.dtype is f32 else BF16 for g in grads]
+            kinds = None
+        if kinds is None or len(kinds) > 1:
+            self._grad[:] = [0 if g is None else g.data_ptr() for g in grads]
+            self._grad_dtype[:] = [F32 if g is None or g.dtype is f32 else BF16 for g in grads]
+        else:
+            self._grad[:] = list(map(torch.Tensor.data_ptr, grads))
+            self._grad_dtype[:] = F32 if f32 in kinds else BF16
         a = _AdamWArgs()
         a.beta1, a.beta2 = self.betas
         a.eps, a.seed = self.eps, self.seed
@@ -221,22 +229,27 @@ class AdamW:
         first = next((o[i] for o in (m_out, v_out) if o is not None for i in coded if o[i] is not None), None)
         if first is not None and first.dtype == bf16:
             kind = bf16
+        whole = len(coded) == count
         ms, vs = list(self.m), list(self.v)
+        pointers = []
         for name, outs, out in (("m_out", m_out, ms), ("v_out", v_out, vs)):
             if outs is None:
                 outs = [None] * count
-            elif len(coded) < count and any(x is not None and b != 8 for x, b in zip(outs, self.bits)):
+            elif not whole and any(x is not None and b != 8 for x, b in zip(outs, self.bits)):
                 raise ValueError(f"{name} is for moments in 8 bits: None elsewhere")
-            given = [outs[i] for i in coded]
-            if not self._fit(given, self._coded_shapes, {kind}):
+            given = list(outs) if whole else [outs[i] for i in coded]
+            if self._fit(given, self._coded_shapes) != {kind}:
                 for k, (i, x) in enumerate(zip(coded, given)):
                     given[k] = (torch.empty(self._shapes[i], dtype=kind, device=self.device) if x is None else
                                 _tensor(f"{name}[{i}]", x, kind, self._shapes[i], self.device))
-            for i, x in zip(coded, given):
-                out[i] = x
+            if whole:
+                out[:] = given
+            else:
+                for i, x in zip(coded, given):
+                    out[i] = x
+            pointers.append(np.array(list(map(torch.Tensor.data_ptr, given)), dtype=np.uint64))
         if coded:
-            table = self._table[coded]
-            pointers = [np.array([out[i].data_ptr() for i in coded], dtype=np.uint64) for out in (ms, vs)]
+            table = self._table if whole else self._table[coded]
             with _device(index):
                 _check(lib().bmoe_adamw_moments(table.ctypes.data, len(table), BF16 if kind == torch.bfloat16 else F32,
                                                 pointers[0].ctypes.data, pointers[1].ctypes.data, _raw_stream(self.params[0])))
