@@ -678,24 +678,24 @@ constexpr int gf_tile_side(GfTiling t) { return t == GF_64 ? 64 : t == GF_256 ? 
 // microseconds: rounds of workgroups over the CUs, a step of 64 by the lone workgroup of
 // a CU or by each of two, a tile's beginning and end; shares are written and read again in
 // fp32 by a launch behind.  Operands turned in LDS take longer, their reads being half as
-// wide.  The constants are fitted to 16 products of 0.6 to 1100 GFLOP, each with every
+// wide.  The constants are fitted to 31 products of 0.6 to 1100 GFLOP, each with every
 // tile and split forced (M x N x K, us: 16384 x 2048 x 8192 as x W^T, 256 405, 128_2 467, 128 516,
-// 64 777; 2736 x 512 x 4001 as dy^T x, 128_2 in 5 shares 27.5, 64 39.2; 4096 x 1024 x 4096 128 32.8,
+// 64 777; 2736 x 512 x 4001 as dy^T x, 128_2 in 5 shares 27.7, 64 40.8; 4096 x 1024 x 4096 128 32.8,
 // 128_2 in 2 shares 41.1, 64 46.2; 256 x 2048 x 8192 64 in 2 shares 17.7, 128 in 8 18.3); a
 // pick is within a tenth of the best of them.
+struct GfOption {
+  GfTiling tiling;
+  int per_cu;
+  double lone[2], shared[2], once;   // steps: plain, turned
+};
+constexpr GfOption gf_options[] = {{GF_64, 2, {0.2, 0.38}, {0.42, 0.53}, 3.0},
+                                   {GF_128, 1, {0.48, 0.73}, {0, 0}, 2.0},
+                                   {GF_128_2, 2, {0.66, 0.8}, {0.91, 1.0}, 3.0},
+                                   {GF_256, 1, {1.58, 1.71}, {0, 0}, 4.0}};
 GfTile gf_pick(int M, int N, int K, bool turned, bool may_split) {
-  struct Option {
-    GfTiling tiling;
-    int per_cu;
-    double lone[2], shared[2], once;   // steps: plain, turned
-  };
-  constexpr Option options[] = {{GF_64, 2, {0.2, 0.45}, {0.42, 0.62}, 3.0},
-                                {GF_128, 1, {0.48, 0.8}, {0, 0}, 2.0},
-                                {GF_128_2, 2, {0.66, 0.8}, {0.91, 1.1}, 3.0},
-                                {GF_256, 1, {1.58, 1.71}, {0, 0}, 4.0}};
   GfTile best{GF_64, 1, 0};
   const int steps = (K + 63) / 64;
-  for (const Option& o : options) {
+  for (const GfOption& o : gf_options) {
     const int side = gf_tile_side(o.tiling);
     const int64_t tiles = int64_t((M + side - 1) / side) * ((N + side - 1) / side);
     for (int split = 1; split <= (may_split ? GF_SPLIT : 1); ++split) {
@@ -807,9 +807,8 @@ void gf_three(int tokens, int d, int ff, int (&m)[3], int (&n)[3], int (&k)[3]) 
 }
 // By gf_pick's estimate, with the workgroups dealt out in order to whatever place is free first
 // (whole backward one by one and together, us: 4001 x 512 x 1368 94 and 69, 2354 x 1984 x 832 108
-// and 84, 4503 x 1536 x 5696 619 and 479, 677 x 1024 x 320 35 and 23; 16384 x 512 x 2048 315 and 294;
-// taken all the same: 8192 x 512 x 2048 161 and 174, 15899 x 1088 x 4096 1056 and 1067, which the
-// last 3 % leave out).
+// and 84, 4503 x 1536 x 5696 619 and 479, 677 x 1024 x 320 35 and 23; left one by one, by 3 %:
+// 15899 x 1088 x 4096 1056 and 1067).
 GfTogether gf_group_pick(int tokens, int d, int ff) {
   int m[3], n[3], k[3];
   gf_three(tokens, d, ff, m, n, k);
@@ -837,17 +836,18 @@ GfTogether gf_group_pick(int tokens, int d, int ff) {
         const int own = (steps[j] + split[j] - 1) / split[j];
         split[j] = (steps[j] + own - 1) / own;
         count += tiles[j] * split[j];
-        sums += 1.4 * double(m[j]) * n[j] * split[j] / 1e6;
+        sums += 1.6 * double(m[j]) * n[j] * split[j] / 1e6;
       }
       const bool parts = split[0] > 1 || split[1] > 1 || split[2] > 1;
       if (count > 8 * places) continue;
-      const double step = side == 256 ? 1.71 : count <= GF_CUS ? 0.8 : 1.1, once = side == 256 ? 4.0 : 3.0;
+      const GfOption& o = gf_options[side == 256 ? GF_256 : GF_128_2];
+      const double step = o.per_cu == 1 || count <= GF_CUS ? o.lone[1] : o.shared[1];
       // places by when they are free
       struct { double at; int64_t n; } free[8] = {{0, places}};
       int kinds = 1;
       double last = 0;
       for (int j = 0; j < 3; ++j) {
-        const double takes = ((steps[j] + split[j] - 1) / split[j]) * step + once;
+        const double takes = ((steps[j] + split[j] - 1) / split[j]) * step + o.once;
         for (int64_t left = tiles[j] * split[j]; left > 0;) {
           int f = 0;
           for (int q = 1; q < kinds; ++q)
