@@ -5,9 +5,9 @@
 // (dy, s, b, d_sum, db, dr), some 20 operations an element.  As in layer_norm.hip a row is
 // held in registers between its loads and its stores and a workgroup loops over rows, which
 // keeps the columns' weights and sums in registers.  Here that is five weights or four and
-// four sums a column, so a thread has one group of 8 columns up to width 8192 (two beyond)
-// and rows of more than 512 are shared by several waves,
-// those of up to 256 share a wave.
+// four sums a column, so a thread has one group of 8 columns up to width 8192 (two beyond, in
+// the backward from 4097 on), and rows of more than 512 are shared by several waves, those
+// of up to 256 share a wave.
 //
 // Every load is a whole group of 8 without a condition: where the width is no multiple
 // of 8 a row's last group is its last 8 columns, of which the group before has some
