@@ -194,6 +194,7 @@ __device__ __forceinline__ void aw_run(const AwTensor& t, int64_t base, int run,
       }
     }
     uint32_t top = 0;   // exponent fields of the largest m' (low half) and v'
+    float root[4], least = 1.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float g = b.g[j] * gs;
@@ -201,7 +202,17 @@ __device__ __forceinline__ void aw_run(const AwTensor& t, int64_t base, int run,
       b.v[j] = fmaf(s.beta2, b.v[j], s.rest2 * (g * g));
       // one unit in the last place of the hardware's root and reciprocal is far below
       // what p' is rounded by
-      const float den = fmaf(__builtin_amdgcn_sqrtf(b.v[j]), root2, s.eps);
+      root[j] = __builtin_amdgcn_sqrtf(b.v[j]);
+      least = fminf(least, b.v[j]);
+    }
+    if (least < 0x1p-126f) {   // the hardware's root takes subnormal numbers as 0
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (b.v[j] < 0x1p-126f) root[j] = __builtin_amdgcn_sqrtf(b.v[j] * 0x1p64f) * 0x1p-32f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float den = fmaf(root[j], root2, s.eps);
       b.p[j] = fmaf(-to * b.m[j], __builtin_amdgcn_rcpf(den), b.p[j] * stay);
       if constexpr (EIGHT) {
         const u16x2_t f = {(unsigned short)(aw_exp_field(b.m[j])), (unsigned short)(aw_exp_field(b.v[j]))};

@@ -10,7 +10,8 @@
  *     p' = (1 - lr_t decay) p - lr_t (m' / (1 - beta1^t)) / (sqrt(v' / (1 - beta2^t)) + eps)
  * where lr_t = lr lr_scale.  All in fp32; p, m, v are updated in place and `copy`,
  * where given, gets p' rounded to bf16.  Infinities and NaNs go through these
- * formulas as they are and stay in their value.
+ * formulas as they are and stay in their value.  With an eps of 0, a v' of 0 (g^2 below
+ * fp32's smallest number) makes p' infinite, or NaN where m' is 0 too.
  *
  * Moments in 8 bits.  Blocks of 256 consecutive values share a power of two for m and
  * one for v, and each value has a code of 8 steps to a factor of two:
@@ -65,7 +66,7 @@ typedef struct bmoe_adamw_tensor {
 typedef struct bmoe_adamw_args {
   double lr;                  /* finite; unused with lr_device */
   double beta1, beta2;        /* in [0, 1) */
-  double eps;                 /* 0 or in [2^-126, 2^126] (v' below 2^-126 may count as 0 beside it) */
+  double eps;                 /* 0 or in [2^-126, 2^126] */
   int64_t step;               /* t, at least 1; unused with step_device */
   int64_t* step_device;       /* 1 value on the device or NULL: the steps taken before,
                                  raised by 1 first; a captured call counts on in every replay */
