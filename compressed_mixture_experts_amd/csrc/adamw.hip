@@ -235,6 +235,13 @@ __device__ __forceinline__ void aw_run(const AwTensor& t, int64_t base, int run,
         b.cm |= (c | (um >> 24 & 128u)) << (8 * j);
         b.cv |= d << (8 * j);
       }
+      if (max(nm, nv) == 254) {   // what a largest value would be rounded up to is 2^128: its own code instead
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (nm == 254 && (b.cm >> (8 * j) & 127u) == 8 * AW_M_TOP + 16) b.cm -= 1u << (8 * j);
+          if (nv == 254 && (b.cv >> (8 * j) & 255u) == 8 * AW_V_TOP + 16) b.cv -= 1u << (8 * j);
+        }
+      }
       if ((threadIdx.x & 63) == 0 && 256 * block < t.n) {
         t.me[block] = uint8_t(nm);
         t.ve[block] = uint8_t(nv);

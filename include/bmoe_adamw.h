@@ -20,7 +20,8 @@
  * e the exponent of the block's largest finite value (2^e <= it < 2^(e + 1), e in
  * [-126, 127]), stored as the byte e + 127.  So m reaches 2^-17 of its block's largest
  * value and v 2^-33.  Codes 127 of m and 255 of v are NaN (and stand for
- * infinities).  A v that is not 0 never gets code 0: its value stays the divisor.
+ * infinities), and no finite value takes the code of 2^128.  A v that is not 0 never gets
+ * code 0: its value stays the divisor.
  * p' is that of m' and v' before they become codes.  A value between two codes takes the
  * upper one with a probability that makes the expected value right (v changes by
  * 1 - beta2 of itself a step, a hundredth of the codes' distance: rounded to the

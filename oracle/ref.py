@@ -651,11 +651,13 @@ def adamw_exponents(x):
 
 def adamw_codes(x, exps, top: int, r):
     """Codes of |x| at the blocks' stored exponents, rounded up by the fractions r (of
-    values only: signs, NaN codes and v's lowest code are the caller's)."""
+    values only: signs, NaN codes and v's lowest code are the caller's), but not to the
+    code of 2^128."""
     e = exps.astype(np.int64).repeat(ADAMW_BLOCK)[: len(x)] - 127 - top
     size = np.abs(x)
     k = np.where(size > 0, np.maximum(np.frexp(size)[1] - 1 - e, 0), 0)
-    return np.floor(np.ldexp(size, -(k + e - 3)) + r).astype(np.int64) + 8 * k
+    codes = np.floor(np.ldexp(size, -(k + e - 3)) + r).astype(np.int64) + 8 * k
+    return np.where(e + top == 127, np.minimum(codes, 8 * top + 15), codes)
 
 
 def adamw_values(codes, exps, top: int):

@@ -46,3 +46,25 @@ def test_subnormal_v_is_the_divisor(bits, eps):
         by = 1e-2 / (1 - B1 ** t) / (np.sqrt(v / (1 - B2 ** t)) + eps)
         tol = (16 * U + ev / v / 2) * np.abs(by * m) + by * em + 3 * U * (np.abs(p0) + np.abs(want))
         assert np.isfinite(p1).all() and (np.abs(p1 - want) <= tol).all()
+
+
+def test_finite_moments_stay_finite_in_8_bits():
+    """Moments in fp32's last eighth below 2^128, whose next code up would be that of 2^128:
+    with betas of 0 they are the gradient and its square, so all 2000 of them are known."""
+    import torch
+    r = np.random.default_rng(8)
+    for size, which, top, largest in ((2.0 ** 128, 0, ref.ADAMW_M_TOP, 119), (2.0 ** 64, 1, ref.ADAMW_V_TOP, 247)):
+        # m, or v's root, from the largest code's value (15/8 of 2^127) on
+        lowest = 15 / 16 if which == 0 else np.sqrt(15 / 16)
+        g = (size * r.uniform(lowest, 0.999999, 2000)).astype(np.float32) * (r.choice([-1, 1], 2000).astype(np.float32))
+        opt = bm.AdamW([torch.zeros(2000, device="cuda")], bits=8, betas=(0.0, 0.0), lr=1e-3)
+        opt.step([torch.from_numpy(g).cuda()])
+        code = (opt.m if which == 0 else opt.v)[0].cpu().numpy()
+        assert ((code & (127 if which == 0 else 255)) == largest).all()
+        got = opt.moments()[which][0]
+        assert torch.isfinite(got).all() and (got.abs().double() == 2.0 ** 127 * 15 / 8).all()
+        if which == 0:
+            assert ((got < 0).cpu().numpy() == (g < 0)).all()
+        else:
+            opt.step([torch.zeros(2000, device="cuda")])
+            assert torch.isfinite(opt.params[0]).all()

@@ -101,3 +101,15 @@ def test_gated_activations():
     assert np.allclose(a, [0, -0.2689414213699951, 0, 0.7310585786300049, 40]) and s[2] == 0.5 and np.isclose(s[4], 1)
     a, s = ref.gated_act(g, "gelu")
     assert np.allclose(a, [0, -0.15865525393145707, 0, 0.8413447460685429, 40]) and s[2] == 0.5 and np.isclose(s[4], 1)
+
+
+def test_adamw_codes_of_finite_values_are_finite():
+    """The largest exponent's codes stop below 2^128, whatever the fraction; one exponent lower
+    they go on to 2^127."""
+    x = np.array([2.0 ** 127 * 15 / 8, np.finfo(np.float32).max, 2.0 ** 127])
+    for top in (13, 29):
+        for r in (0.0, 0.5, 1 - 2.0 ** -16):
+            codes = ref.adamw_codes(x, np.array([254], dtype=np.uint8), top, r)
+            assert np.isfinite(ref.adamw_values(codes, np.array([254], dtype=np.uint8), top).astype(np.float32)).all()
+            assert list(codes) == [8 * top + 15, 8 * top + 15, 8 * top + 8]
+        assert ref.adamw_codes(x[1:2] / 2, np.array([253], dtype=np.uint8), top, 0.99)[0] == 8 * top + 16
