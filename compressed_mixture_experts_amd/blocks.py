@@ -132,10 +132,10 @@ class AdamW:
                     out.append(_tensor(f"{name}[{i}]", x, kind, shape, dev).detach())   # this memory, whatever x is given later
             if (given[0][i] is None) != (given[1][i] is None):
                 raise ValueError(f"m and v of parameter {i} go together")
-        # what its owner may give other memory (`tensor.data = ..`, a module's `.to`)
+        # what its owner may give other memory or another layout (`tensor.data = ..`, a module's `.to`)
         self._owned = [(f"{name}[{i}]", x, x.dtype, x.shape) for name, tensors in (("params", self.params), ("copies", self.copies))
                        for i, x in enumerate(tensors) if x is not None]
-        self._owned_tensors = [o[1] for o in self._owned]
+        self._owned_tensors, self._owned_kinds, self._owned_shapes = ([o[k] for o in self._owned] for k in (1, 2, 3))
         t = np.zeros(count, dtype=_ADAMW_TENSOR)
         self._table = t
         for name, tensors in (("m", self.m), ("v", self.v), ("m_exp", self.m_exp), ("v_exp", self.v_exp)):
@@ -181,8 +181,11 @@ class AdamW:
         if len(grads) != len(self.params):
             raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
         index = dev.index
-        if list(map(torch.Tensor.data_ptr, self._owned_tensors)) != self._addresses:   # taken where they are now
-            for name, x, kind, shape in self._owned:
+        t, own = torch.Tensor, self._owned_tensors
+        # (0.1 us a tensor for sizes, types and layouts beside the addresses: 45 -> 58 us at 120)
+        if (list(map(t.data_ptr, own)) != self._addresses or list(map(t.size, own)) != self._owned_shapes or
+                list(map(t.dtype.__get__, own)) != self._owned_kinds or not all(map(t.is_contiguous, own))):
+            for name, x, kind, shape in self._owned:   # taken where they are now
                 _tensor(name, x, kind, shape, dev)
             self._take_addresses()
         kinds = self._fit(grads, self._shapes)

@@ -1,0 +1,40 @@
+"""The tensors that an AdamW object holds: what their owner does to them between steps."""
+import pytest
+
+import compressed_mixture_experts_amd as bm
+from test_gpu_adamw import make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    bm.lib()
+    yield
+
+
+def test_a_layout_that_changed_at_the_same_address():
+    """Parameters and copies that are transposed, cut or read as another type in place."""
+    import torch
+    for bits in (32, 8):
+        for name, change in ((r"params\[1\]", lambda o: o.params[1].data.t()), (r"params\[1\]", lambda o: o.params[1].data[:8]),
+                             (r"params\[1\]", lambda o: o.params[1].data.view(8, 32)),
+                             (r"params\[1\]", lambda o: o.params[1].data.view(torch.bfloat16)[:, :16]),
+                             (r"copies\[1\]", lambda o: o.copies[1].data.t()), (r"copies\[1\]", lambda o: o.copies[1].data.view(torch.float16))):
+            ps = [torch.ones(40, device="cuda"), torch.arange(256.0, device="cuda").view(16, 16)]
+            opt = bm.AdamW(ps, bits=bits, copies=[None, torch.zeros(16, 16, dtype=torch.bfloat16, device="cuda")])
+            gs = [torch.ones(40, device="cuda"), torch.ones(16, 16, device="cuda")]
+            opt.step(gs)
+            held = opt.params[1] if name.startswith("params") else opt.copies[1]
+            whole, memory = held.data, held.data.clone()
+            held.data = change(opt)
+            assert held.data_ptr() == whole.data_ptr()
+            with pytest.raises(ValueError, match=name):
+                opt.step(gs)
+            torch.cuda.synchronize()
+            assert opt.steps == 1 and (whole == memory).all()
+            held.data = whole
+            opt.step(gs)
+            assert opt.steps == 2 and not (whole == memory).all()
