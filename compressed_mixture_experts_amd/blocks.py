@@ -68,7 +68,8 @@ class AdamW:
         opt = bmoe.AdamW([layer.theta[0], layer.phi[0], gamma], lr=1e-3, weight_decay=[0.0, 0.0, 0.0])
         opt.step([grads["theta"][0], grads["phi"][0], dgamma])
 
-    params           the tensors, updated in place by every step.
+    params           the tensors, updated in place by every step (autograd is told: a graph
+                     that saved one for its backward before refuses to run it).
     weight_decay, lr_scale, bits, copies   one for all tensors or a list of them: the
                      decoupled decay, a factor on lr, 32 or 8 bits for the moments (8:
                      bmoe_adamw.h's codes), a bf16 tensor that gets the new values.
@@ -218,6 +219,9 @@ class AdamW:
                 a.step = self._steps + 1
             _check(lib().bmoe_adamw_step(self._table_at, len(table), ctypes.byref(a), _raw_stream(self.params[0])))
         self._steps += 1
+        # autograd's count of changes, as torch's own updates in place raise it
+        torch.autograd.graph.increment_version(own if kinds is not None else [
+            x for tensors in (self.params, self.copies) for x, g in zip(tensors, grads) if x is not None and g is not None])
 
     def moments(self, m_out=None, v_out=None):
         """The moments' values as two lists: the fp32 tensors themselves, and for codes of

@@ -38,3 +38,32 @@ def test_a_layout_that_changed_at_the_same_address():
             held.data = whole
             opt.step(gs)
             assert opt.steps == 2 and not (whole == memory).all()
+
+
+def test_autograd_is_told():
+    """A step raises the version of what it changes, and of nothing else: a graph that saved a
+    parameter or a copy refuses its backward."""
+    import torch
+    g = torch.ones(8, device="cuda")
+    for kind in ("params", "copies"):
+        p = [torch.nn.Parameter(torch.ones(8, device="cuda")) for _ in range(3)]
+        c = [torch.zeros(8, dtype=torch.bfloat16, device="cuda", requires_grad=True), None, None]
+        opt = bm.AdamW(p, copies=c)
+        for grads, told in (([g, g, g], True), ([g, None, g], True), ([None, g, g], False), ([None, None, None], False)):
+            held = (opt.params if kind == "params" else opt.copies)[0]
+            x = torch.ones(8, device="cuda", dtype=held.dtype, requires_grad=True)
+            y = (x * held).sum()
+            before = [t._version for t in opt.params]
+            opt.step(grads)
+            assert [t._version > b for t, b in zip(opt.params, before)] == [q is not None for q in grads]
+            if told:
+                with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                    y.backward()
+            else:
+                y.backward()
+                assert torch.equal(x.grad, held.detach())
+    with torch.inference_mode():   # tensors without a version
+        p = torch.ones(8, device="cuda")
+        opt = bm.AdamW([p])
+        opt.step([g])
+        assert (p < 1).all()
