@@ -126,13 +126,11 @@ class AdamW:
                         raise ValueError(f"{name}[{i}] is for moments in 8 bits")
                     out.append(None)
                 elif x is None:
-                    if eight and (given[0][i] is None) != (have[i] is None):
-                        raise ValueError(f"m, v, m_exp and v_exp of parameter {i} go together")
                     out.append(torch.zeros(shape, dtype=kind, device=dev))
                 else:
                     out.append(_tensor(f"{name}[{i}]", x, kind, shape, dev).detach())   # this memory, whatever x is given later
-            if (given[0][i] is None) != (given[1][i] is None):
-                raise ValueError(f"m and v of parameter {i} go together")
+            if len({x[i] is None for x in (given if eight else given[:2])}) > 1:
+                raise ValueError(f"{'m, v, m_exp and v_exp' if eight else 'm and v'} of parameter {i} go together")
         # what its owner may give other memory or another layout (`tensor.data = ..`, a module's `.to`)
         self._owned = [(f"{name}[{i}]", x, x.dtype, x.shape) for name, tensors in (("params", self.params), ("copies", self.copies))
                        for i, x in enumerate(tensors) if x is not None]

@@ -67,3 +67,20 @@ def test_autograd_is_told():
         opt = bm.AdamW([p])
         opt.step([g])
         assert (p < 1).all()
+
+
+def test_moments_that_go_together():
+    """Some of m, v, m_exp and v_exp without the others: refused, whichever they are."""
+    import itertools
+    import torch
+    z = lambda n, kind=torch.uint8: torch.zeros(n, dtype=kind, device="cuda")  # noqa: E731
+    for keep in itertools.product((False, True), repeat=4):
+        kw = {k: [x] for k, x, on in zip(("m", "v", "m_exp", "v_exp"), (z(300), z(300), z(2), z(2)), keep) if on}
+        if all(keep) or not any(keep):
+            bm.AdamW([z(300, torch.float32)], bits=8, **kw).step([z(300, torch.float32)])
+        else:
+            with pytest.raises(ValueError, match="go together"):
+                bm.AdamW([z(300, torch.float32)], bits=8, **kw)
+    for kw in (dict(m=[z(300, torch.float32)]), dict(v=[z(300, torch.float32)])):
+        with pytest.raises(ValueError, match="m and v of parameter 0 go together"):
+            bm.AdamW([z(300, torch.float32)], **kw)
