@@ -232,7 +232,7 @@ class AdamW:
             if outs is not None and len(outs) != count:
                 raise ValueError(f"{name} has {len(outs)} entries for {count} parameters")
         first = next((o[i] for o in (m_out, v_out) if o is not None for i in coded if o[i] is not None), None)
-        if first is not None and first.dtype == bf16:
+        if getattr(first, "dtype", None) == bf16:
             kind = bf16
         whole = len(coded) == count
         ms, vs = list(self.m), list(self.v)

@@ -84,3 +84,13 @@ def test_moments_that_go_together():
     for kw in (dict(m=[z(300, torch.float32)]), dict(v=[z(300, torch.float32)])):
         with pytest.raises(ValueError, match="m and v of parameter 0 go together"):
             bm.AdamW([z(300, torch.float32)], **kw)
+
+
+def test_moments_into_what_is_no_tensor():
+    import torch
+    opt = bm.AdamW([torch.zeros(300, device="cuda")], bits=8)
+    for out in ([1.0], ["m"], [torch.zeros(300)], [torch.zeros(300, dtype=torch.float16, device="cuda")]):
+        with pytest.raises(ValueError, match=r"m_out\[0\]"):
+            opt.moments(m_out=out)
+        with pytest.raises(ValueError, match=r"v_out\[0\]"):
+            opt.moments(v_out=out)
