@@ -223,8 +223,10 @@ class AdamW:
 
     def moments(self, m_out=None, v_out=None):
         """The moments' values as two lists: the fp32 tensors themselves, and for codes of
-        8 bits new fp32 tensors, or those of m_out and v_out (lists of fp32 or of bf16
-        tensors, which hold the values exactly; not for moments of 32 bits)."""
+        8 bits those of m_out and v_out (lists of tensors, None for a new one; not for
+        moments of 32 bits) or new ones.  All of one type: that of the first given, fp32
+        without any, or bf16, which holds the values exactly too (from 2^-130 on; smaller
+        ones to the nearest of its numbers)."""
         torch = _torch()
         coded, kind, bf16 = self._coded, torch.float32, torch.bfloat16
         index, count = self.device.index, len(self.params)

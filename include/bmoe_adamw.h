@@ -85,8 +85,9 @@ typedef struct bmoe_adamw_args {
 bmoe_status bmoe_adamw_step(const bmoe_adamw_tensor* tensors, int32_t count, const bmoe_adamw_args* args,
                             hipStream_t stream);
 
-/* The values of 8-bit moments: m_out[i] and v_out[i] [n] of out_dtype (bmoe_dtype; the
- * codes' values are exact in either) for tensor i, either of them NULL if not wanted
+/* The values of 8-bit moments: m_out[i] and v_out[i] [n] of out_dtype (bmoe_dtype; a step's
+ * codes are exact in either, in bf16 from 2^-130 on, below which its numbers are 2^-133
+ * apart and take the nearest) for tensor i, either of them NULL if not wanted
  * (param, grad and copy are not used).  m_out and v_out are host arrays of `count`
  * device pointers.  Errors as above; BMOE_ERR_DTYPE for bits other than 8. */
 bmoe_status bmoe_adamw_moments(const bmoe_adamw_tensor* tensors, int32_t count, int32_t out_dtype, void* const* m_out,

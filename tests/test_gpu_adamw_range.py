@@ -68,3 +68,24 @@ def test_finite_moments_stay_finite_in_8_bits():
         else:
             opt.step([torch.zeros(2000, device="cuda")])
             assert torch.isfinite(opt.params[0]).all()
+
+
+def test_moments_in_bf16_down_to_its_smallest():
+    """The codes' values in fp32 are those of their definition, in bf16 the nearest to them,
+    also where bf16's numbers are further apart than codes."""
+    import torch
+    for size in (1.0, 1e-14, 1e-17, 1e-18):
+        r = np.random.default_rng(9)
+        g = (r.standard_normal(3000) * size * np.exp(2 * r.standard_normal(3000))).astype(np.float32)
+        opt = bm.AdamW([torch.zeros(3000, device="cuda")], bits=8)
+        opt.step([torch.from_numpy(g).cuda()])
+        _, m, v, _ = state64(opt, 0)
+        ms, vs = opt.moments()
+        assert np.array_equal(ms[0].cpu().double().numpy(), m) and np.array_equal(vs[0].cpu().double().numpy(), v)
+        m16, v16 = opt.moments(m_out=[torch.empty(3000, dtype=torch.bfloat16, device="cuda")])
+        assert m16[0].dtype == v16[0].dtype == torch.bfloat16   # the new one is of the given one's type
+        for x, y in ((ms[0], m16[0]), (vs[0], v16[0])):
+            assert torch.equal(x.cpu().to(torch.bfloat16), y.cpu())
+        exact = np.abs(v) >= 2.0 ** -130
+        assert np.array_equal(v16[0].cpu().double().numpy()[exact], v[exact])
+    assert ((v > 0) & ~exact).any()
