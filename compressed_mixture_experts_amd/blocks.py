@@ -451,9 +451,10 @@ def gated_ffn_forward_train(x, w_in, w_down, act: str = "silu", add=None, y=None
 def gated_ffn_backward(x, w_in, w_down, dy, state, act: str = "silu", dx_add=None, input_grad: bool = True, weight_grads: bool = True,
                        dx=None, dw_in=None, dw_down=None):
     """Gradients of sum(dy * y) at the state of gated_ffn_forward_train: (dx [tokens][d],
-    dw_in, dw_down like the weights), bf16, None for those not wanted.  dx_add [tokens][d]
-    fp32 is added into dx before its rounding (the input gradient of Layer.backward for the
-    same x).  The gradient of the forward's add is dy."""
+    dw_in, dw_down like the weights), bf16, None for those not wanted.  The activation is the
+    one that the state was made with, whichever act names.  dx_add [tokens][d] fp32 is added
+    into dx before its rounding (the input gradient of Layer.backward for the same x).  The
+    gradient of the forward's add is dy."""
     torch = _torch()
     tokens, d, ff, kind, bf16 = _ffn(x, w_in, w_down, act)
     dev = x.device

@@ -2099,8 +2099,7 @@ bmoe_status bmoe_gated_ffn_backward(int32_t tokens, int32_t d, int32_t ff, int32
   if (st != BMOE_OK) return st;
   auto u16 = [](const void* p) { return static_cast<const uint16_t*>(p); };
   auto w16 = [](void* p) { return static_cast<uint16_t*>(p); };
-  const GfBwdArgs a{u16(x), u16(w_in), u16(w_down), u16(dy), u16(state), dx_add, w16(dx), w16(dw_in), w16(dw_down), workspace, tokens, d, ff,
-                    act == BMOE_GATED_GELU};
+  const GfBwdArgs a{u16(x), u16(w_in), u16(w_down), u16(dy), u16(state), dx_add, w16(dx), w16(dw_in), w16(dw_down), workspace, tokens, d, ff};
   BMOE_HIP(launch_gated_ffn_backward(a, stream));
   return ok();
 }

@@ -741,6 +741,7 @@ hipError_t gf_go(GfGemm p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// F: of GF_GATE alone (what GF_GRAD needs of the activation is in the state).
 template <bool AT, bool BT, int EPI, int F = GF_SILU>
 hipError_t gf_tiled(const GfGemm& p, GfTiling t, hipStream_t s) {
   if (t == GF_64) return gf_go<AT, BT, EPI, F, 64, 64, 2, 2, 4>(p, s);
@@ -976,7 +977,7 @@ hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
     p.pa = const_cast<uint16_t*>(a.state);
     p.fine = reinterpret_cast<uint8_t*>(p.pa + size_t(M) * 3 * a.ff);
     const GfTiling tiling = gf_pick(M, p.N, p.K, true, false).tiling;
-    e = a.gelu ? gf_tiled<false, true, GF_GRAD, GF_GELU>(p, tiling, s) : gf_tiled<false, true, GF_GRAD, GF_SILU>(p, tiling, s);
+    e = gf_tiled<false, true, GF_GRAD>(p, tiling, s);
     if (e != hipSuccess) return e;
   }
   GfGroup g{};

@@ -161,7 +161,7 @@ struct GfBwdArgs {
   uint16_t* dw_in;          // [2 ff][d] or null
   uint16_t* dw_down;        // [d][ff] or null
   void* ws;
-  int32_t tokens, d, ff, gelu;
+  int32_t tokens, d, ff;
 };
 size_t gf_forward_workspace(int tokens, int d, int ff, bool with_state);
 size_t gf_backward_workspace(int tokens, int d, int ff);

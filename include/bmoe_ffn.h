@@ -50,6 +50,8 @@ bmoe_status bmoe_gated_ffn_forward(int32_t tokens, int32_t d, int32_t ff, int32_
                                    void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Backward of sum(dy y), at the forward's state, which is read only.
+ *   act      one of the activations; the gradients are those of the state's own, whose
+ *            slopes it holds, whichever is given here.
  *   dy       [tokens][d], read only.
  *   dx_add   [tokens][d] fp32 or NULL, read only: added into dx before it is rounded (the
  *            input gradient of bmoe_layer_backward for the same x).
