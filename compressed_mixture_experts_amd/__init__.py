@@ -28,7 +28,7 @@ import numpy as np
 
 __all__ = [
     "BmoeError", "lib", "library_path", "pack_ternary", "packed_words", "Layer",
-    "dbg_butterfly", "dbg_ternary_gemm", "dbg_ternary_gemm_fp4", "butterfly_backward", "substrate_grad",
+    "dbg_butterfly", "dbg_ternary_gemm", "dbg_ternary_gemm_fp4", "dbg_gated_ffn_plan", "butterfly_backward", "substrate_grad",
     "combine_backward", "router_backward", "gelu_backward", "substrate_input_grad",
     "layer_norm_forward", "layer_norm_backward", "orthogonalize", "substrate_step", "AdamW",
     "block_norm_forward", "block_norm_backward", "gated_ffn_forward", "gated_ffn_forward_train", "gated_ffn_backward", "STATUS",
@@ -69,7 +69,7 @@ EXPORTED_SYMBOLS = [
     "bmoe_gated_ffn_backward_workspace", "bmoe_gated_ffn_backward",
 ]
 # exported by libbmoe_debug.so only (include/bmoe_debug.h)
-DEBUG_SYMBOLS = ["bmoe_dbg_butterfly", "bmoe_dbg_ternary_gemm", "bmoe_dbg_ternary_gemm_fp4"]
+DEBUG_SYMBOLS = ["bmoe_dbg_butterfly", "bmoe_dbg_ternary_gemm", "bmoe_dbg_ternary_gemm_fp4", "bmoe_dbg_gated_ffn_plan"]
 
 
 class BmoeError(RuntimeError):
@@ -177,6 +177,7 @@ def _load(path: str, debug: bool) -> ctypes.CDLL:
         L.bmoe_dbg_butterfly.argtypes = [c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp]
         L.bmoe_dbg_ternary_gemm.argtypes = [c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_f, c_vp, c_vp]
         L.bmoe_dbg_ternary_gemm_fp4.argtypes = [c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_f, c_vp, c_vp]
+        L.bmoe_dbg_gated_ffn_plan.argtypes = [c_i32, c_i32, c_i32, ctypes.POINTER(c_i32 * 13)]
         ret += DEBUG_SYMBOLS
     for name in ret:
         getattr(L, name).restype = c_i32
@@ -808,6 +809,13 @@ def dbg_ternary_gemm_fp4(a, w_packed, n_out: int, alpha: float = 1.0):
     _check(D.bmoe_dbg_ternary_gemm_fp4(M, n_out, K, _ptr(a), _ptr(w_packed), _ptr(scratch),
                                        float(alpha), _ptr(z), _stream_handle()), D)
     return z
+
+
+def dbg_gated_ffn_plan(tokens: int, d: int, ff: int) -> dict:
+    """Test hook: which kernels the dense gated block takes (bmoe_dbg_gated_plan)."""
+    D, p = debug_lib(), (ctypes.c_int32 * 13)()
+    _check(D.bmoe_dbg_gated_ffn_plan(tokens, d, ff, ctypes.byref(p)), D)
+    return dict(zip(("few", "gate", "y", "y_shares", "grad", "joint", "joint_parts"), p[:7]), last=p[7:10], last_shares=p[10:13])
 
 
 from .blocks import (AdamW, block_norm_backward, block_norm_forward, gated_ffn_backward,  # noqa: E402

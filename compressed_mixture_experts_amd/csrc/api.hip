@@ -2104,4 +2104,16 @@ bmoe_status bmoe_gated_ffn_backward(int32_t tokens, int32_t d, int32_t ff, int32
   return ok();
 }
 
+#ifdef BMOE_DEBUG_EXPORTS
+bmoe_status bmoe_dbg_gated_ffn_plan(int32_t tokens, int32_t d, int32_t ff, bmoe_dbg_gated_plan* plan) {
+  if (!plan) return fail(BMOE_ERR_NULL, "plan is NULL");
+  const bmoe_status st = check_ffn(tokens, d, ff);
+  if (st != BMOE_OK) return st;
+  const GfPlan p = gated_ffn_plan(tokens, d, ff);
+  *plan = {p.few, p.gate, p.y, p.y_shares, p.grad, p.joint, p.joint_parts, {p.last[0], p.last[1], p.last[2]},
+           {p.last_shares[0], p.last_shares[1], p.last_shares[2]}};
+  return ok();
+}
+#endif  // BMOE_DEBUG_EXPORTS
+
 }  // extern "C"

@@ -712,6 +712,10 @@ GfTile gf_pick(int M, int N, int K, bool turned, bool may_split) {
   return best;
 }
 
+// g, u -> h, and dh -> dg, du: never in shares, whose sums the epilogue would lack.
+GfTiling gf_gate_tiling(int tokens, int d, int ff) { return gf_pick(tokens, 2 * ff, d, false, false).tiling; }
+GfTiling gf_grad_tiling(int tokens, int d, int ff) { return gf_pick(tokens, ff, d, true, false).tiling; }
+
 size_t gf_round(size_t bytes) { return (bytes + 255) / 256 * 256; }
 size_t gf_part_bytes(int M, int N, int split) { return gf_round(size_t(split) * M * N * 4); }
 size_t gf_pick_bytes(int M, int N, int K, bool turned) {
@@ -923,7 +927,7 @@ hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s) {
   p.pa = pa;
   p.fine = fine;
   p.ff = a.ff;
-  const GfTiling tiling = gf_pick(M, p.N, p.K, false, false).tiling;
+  const GfTiling tiling = gf_gate_tiling(M, a.d, a.ff);
   hipError_t e = a.gelu ? gf_tiled<false, false, GF_GATE, GF_GELU>(p, tiling, s) : gf_tiled<false, false, GF_GATE, GF_SILU>(p, tiling, s);
   if (e != hipSuccess) return e;
   p = GfGemm{};
@@ -976,7 +980,7 @@ hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
     p.out = dgu;
     p.pa = const_cast<uint16_t*>(a.state);
     p.fine = reinterpret_cast<uint8_t*>(p.pa + size_t(M) * 3 * a.ff);
-    const GfTiling tiling = gf_pick(M, p.N, p.K, true, false).tiling;
+    const GfTiling tiling = gf_grad_tiling(M, a.d, a.ff);
     e = gf_tiled<false, true, GF_GRAD>(p, tiling, s);
     if (e != hipSuccess) return e;
   }
@@ -1009,6 +1013,28 @@ hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s) {
   if (e == hipSuccess && a.dw_in) e = gf_product<true, true>(dw_in, part, s);
   if (e == hipSuccess && a.dw_down) e = gf_product<true, true>(dw_down, part, s);
   return e;
+}
+
+GfPlan gated_ffn_plan(int tokens, int d, int ff) {
+  GfPlan p{};
+  if (tokens == 0) return p;
+  p.few = tokens <= GF_FEW;
+  const GfTile y = gf_pick(tokens, d, ff, false, true);
+  p.gate = gf_gate_tiling(tokens, d, ff);
+  p.y = y.tiling;
+  p.y_shares = y.split;
+  p.grad = gf_grad_tiling(tokens, d, ff);
+  const GfTogether t = gf_group_pick(tokens, d, ff);
+  p.joint = t.side != 0;
+  p.joint_parts = t.parts;
+  int m[3], n[3], k[3];
+  gf_three(tokens, d, ff, m, n, k);
+  for (int j = 0; j < 3; ++j) {
+    const GfTile one = gf_pick(m[j], n[j], k[j], true, true);
+    p.last[j] = !t.side ? one.tiling : t.side == 128 ? GF_128_2 : GF_256;
+    p.last_shares[j] = t.side ? t.split[j] : one.split;
+  }
+  return p;
 }
 
 }  // namespace bmoe

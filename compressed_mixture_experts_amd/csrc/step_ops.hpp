@@ -167,5 +167,10 @@ size_t gf_forward_workspace(int tokens, int d, int ff, bool with_state);
 size_t gf_backward_workspace(int tokens, int d, int ff);
 hipError_t launch_gated_ffn_forward(const GfFwdArgs& a, hipStream_t s);
 hipError_t launch_gated_ffn_backward(const GfBwdArgs& a, hipStream_t s);
+// Which kernels those launch (bmoe_debug.h's numbers, in its order).
+struct GfPlan {
+  int32_t few, gate, y, y_shares, grad, joint, joint_parts, last[3], last_shares[3];
+};
+GfPlan gated_ffn_plan(int tokens, int d, int ff);
 
 }  // namespace bmoe

@@ -48,6 +48,22 @@ bmoe_status bmoe_dbg_ternary_gemm_fp4(int32_t M, int32_t N, int32_t K, const voi
                                       const uint32_t* w_packed, void* w_fp4, float alpha,
                                       void* z, hipStream_t stream);
 
+/* Which kernels the dense gated block (bmoe_ffn.h) takes at a size, so that tests can name
+ * sizes that reach each of them.  Nothing is launched.  A tile form is 0 (64 x 64), 1
+ * (128 x 128, eight waves), 2 (128 x 128, four waves, two to a CU) or 3 (256 x 256); a
+ * product in more than one share is written as partial sums. */
+typedef struct bmoe_dbg_gated_plan {
+  int32_t few;              /* 1: the forward takes the tokens one by one, without tiles */
+  int32_t gate;             /* tile form of g, u -> h */
+  int32_t y, y_shares;      /* of y = h Wd^T, and the shares of its depth */
+  int32_t grad;             /* of dh -> dg, du */
+  int32_t joint;            /* 1: dx, dW_in and dW_down in one launch */
+  int32_t joint_parts;      /* 1: all three as partial sums, also those in one share */
+  int32_t last[3];          /* tile forms of dx, dW_in, dW_down */
+  int32_t last_shares[3];
+} bmoe_dbg_gated_plan;
+bmoe_status bmoe_dbg_gated_ffn_plan(int32_t tokens, int32_t d, int32_t ff, bmoe_dbg_gated_plan* plan);
+
 #ifdef __cplusplus
 }
 #endif
