@@ -7,8 +7,11 @@
  * with act(g) = g / (1 + exp(-g)) (BMOE_GATED_SILU) or g Phi(g) (BMOE_GATED_GELU, the exact
  * GELU), Wg and Wu [ff][d], Wd [d][ff].  Both projections, the activation and the product
  * are one kernel.  All matrices are bf16 and row-major; products run on the matrix cores
- * with fp32 sums, g and u stay fp32 up to h, which is rounded to bf16 (with up to 4 tokens, which
- * do without matrix cores, only for the state), as are the backward's dg and du; their factors u act'(g) and act(g) are kept to 12 significant bits.
+ * with fp32 sums, g and u stay fp32 up to h, which is rounded to bf16 (with up to 4 tokens,
+ * which do without matrix cores, only for the state: the same token's y differs in its last
+ * bits between a batch of 4 and one of 5), as are the backward's dg and du; their factors
+ * u act'(g) and act(g) are kept to 12 significant bits.  Sums' orders, and with them last
+ * bits, go by the sizes of a call.
  *
  * tokens 0 .. 2^24; d and ff positive multiples of 8, d <= 16384, ff <= 65536, d ff <= 2^29,
  * tokens * max(d, ff) <= 2^36.  Memory rules as in bmoe.h: every pointer is caller-owned
